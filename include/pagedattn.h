@@ -338,6 +338,140 @@ PA_API pa_status pa_decode_split_noalloc(void *out, const void *q, const void *k
                                          int max_blocks_per_seq, int num_blocks, int q_len,
                                          pa_dtype dtype, void *stream);
 
+/*
+ * pa_rope_append -- rotary positions of one or several axes on q and on the new K
+ * rows, which go (with V, unrotated) straight into their cache slots.  With
+ *   theta(i, t) = positions[pair_axis[i]][t] * f_i
+ * pair i of every q and K head of token t becomes (a cos - b sin, b cos + a sin): its
+ * elements a, b are i and i + rotary_dim/2, or 2i and 2i + 1 when interleaved != 0.
+ * Elements from rotary_dim on are copied.  fp32 arithmetic, one rounding to the 16-bit
+ * type, or (k_scale and v_scale both non-NULL: FP8 cache, head_dim 128) to
+ * e4m3(x / scale[kv_head]) for the cache.  After pa_evict a token's cache row is no
+ * longer its position, so positions are always explicit.
+ *   positions     int32 [num_axes][n_tokens]  (e.g. time, height, width)
+ *   slot_mapping  int64 [n_tokens], as for pa_append_kv; a token with a negative slot,
+ *                 or one past the pool (PA_ERR_DEVICE_CHECK), has its q rotated only
+ *   turns         int64 [rotary_dim/2]: f_i in turns per position, units of 2^-64
+ *                 (round(2^64 f_i / (2 pi)) mod 2^64): the angle's fraction of a turn is
+ *                 then exact in integers at any position
+ *   pair_axis     int32 [rotary_dim/2], values in [0, num_axes) (others:
+ *                 PA_ERR_DEVICE_CHECK, axis 0)
+ *   q, q_out      [n_tokens][num_q_heads][head_dim], tokens q_stride / q_out_stride
+ *                 elements apart; q_out may be q itself (same stride)
+ *   k, v          [n_tokens][num_kv_heads][head_dim], tokens k_stride / v_stride apart
+ *                 (all strides multiples of 8, at least a token's width: slices of one
+ *                 fused projection need no copy)
+ * rotary_dim: a multiple of 16, at most head_dim.  Two tokens with the same slot:
+ * undefined which wins.  n_tokens == 0 is a no-op.
+ */
+PA_API pa_status pa_rope_append(void *q_out, const void *q, const void *k, const void *v,
+                                void *k_cache, void *v_cache, const int32_t *positions,
+                                const int64_t *slot_mapping, const int64_t *turns,
+                                const int32_t *pair_axis, int n_tokens, int num_q_heads,
+                                int num_kv_heads, int head_dim, int rotary_dim, int num_axes,
+                                int interleaved, int64_t q_out_stride, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, int block_size, int num_blocks,
+                                pa_dtype dtype, const float *k_scale, const float *v_scale,
+                                void *stream);
+
+/*
+ * pa_decode_scored -- pa_decode (16-bit cache) or pa_decode_fp8 (k_scale and v_scale
+ * both non-NULL), q_len 1..4096, that also keeps the ledger of accumulated attention
+ * weight that pa_evict goes by ([QA] Q4: the tokens that draw little attention).
+ * For cached row t of KV head h
+ *   share(t) = sum over the head's group and query tokens u that see t of the softmax
+ *              weight of (u, head) on t
+ *   scores[i][h][t] = scores[i][h][t] + share(t)   for rows that were there before
+ *                   = share(t)                     for this step's rows (the last q_len)
+ * and, with row_pos, row_pos[i][h][t] = seq_lens[i] - (context_lens[i] - t) for this
+ * step's rows: the token's position in its sequence.  seq_lens count the sequence's
+ * tokens, evicted ones included (equal to context_lens before any eviction).
+ * Rows t >= context_lens[i] of both ledgers are left as they were.
+ *   scores   fp32  [num_seqs][num_kv_heads][max_blocks_per_seq * block_size]
+ *   row_pos  int32, the same shape; NULL (with seq_lens NULL): no positions kept
+ * The sums have one order: results do not change from run to run.  num_splits as for
+ * pa_append_decode up to 16 query tokens; above, the call takes no partitions.
+ * Workspace: pa_decode_scored_workspace_size bytes, 256-byte aligned (up to 16 query
+ * tokens it holds 4 bytes per query row and table position); nothing in it has to
+ * start at zero.  Two calls that can overlap need workspaces of their own.
+ */
+PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_q_heads, int q_len,
+                                              int head_dim, int num_splits,
+                                              int max_blocks_per_seq, int block_size);
+PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, const void *q,
+                                  const void *k_cache, const void *v_cache, const float *k_scale,
+                                  const float *v_scale, const int32_t *block_tables,
+                                  const int32_t *context_lens, const int32_t *seq_lens,
+                                  int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, float scale, int max_blocks_per_seq,
+                                  int num_blocks, int q_len, pa_dtype dtype, int num_splits,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * pa_evict -- eviction by accumulated attention weight ([QA] Q4).  A sequence with
+ * context_lens[i] > budget keeps exactly `budget` rows, each KV head its own choice:
+ * rows of the first `sinks` positions (row_pos < sinks) and of the last `recent`
+ * (row_pos >= seq_lens[i] - recent), then by descending score; ties go to the lowest
+ * row; NaN ranks below every number.  (If more than `budget` rows are protected, the
+ * lowest rows of them stay.)  Kept rows below `budget` stay where they are; the i-th
+ * kept row at or past it is copied (K, V, score, position) into the i-th evicted row
+ * below it.  Attention over the shortened context needs nothing else: K rows carry
+ * their rotation, and the causal limit concerns only rows appended later.
+ * new_lens[i] = min(context_lens[i], budget).  The caller's allocator may take back
+ * the blocks past ceil(new_lens[i] / block_size).
+ * scores_out / row_pos_out: the ledgers themselves, updated in place, or both other
+ * arrays (not overlapping), rows below new_lens[i] written; rows from there on are
+ * left as they were.  With other arrays the call may be repeated with the same result.
+ * Blocks of a sequence longer than the budget must be its own (copy shared ones with
+ * pa_copy_blocks first).  A block id outside the pool: the row is not copied,
+ * PA_ERR_DEVICE_CHECK.
+ *   element_bytes  2 (16-bit cache) or 1 (FP8, head_dim 128): rows are moved bit for bit
+ *   new_lens       int32 [num_seqs], not context_lens itself
+ *   workspace      pa_evict_workspace_size bytes, 16-byte aligned
+ * budget >= sinks + recent, budget >= 1.
+ */
+PA_API size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int budget);
+PA_API pa_status pa_evict(void *k_cache, void *v_cache, float *scores_out, int32_t *row_pos_out,
+                          int32_t *new_lens, const float *scores, const int32_t *row_pos,
+                          const int32_t *block_tables, const int32_t *context_lens,
+                          const int32_t *seq_lens, int num_seqs, int num_kv_heads, int head_dim,
+                          int block_size, int max_blocks_per_seq, int num_blocks, int budget,
+                          int sinks, int recent, int element_bytes, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * pa_verify_drafts -- which drafted tokens stand, and the token after them ([ANIM] §3,
+ * [SB11] §11.7: accept with min(1, p/q), else resample from (p - q)+), from random
+ * numbers in [0, 1) that the caller gives.  For sequence i with m = draft_lens[i]
+ * drafts x_j, target rows p_j (j = 0..m) and draft rows q_j (j < m):
+ *   draft j stands while accept_u[i][j] * q_j(x_j) < p_j(x_j) and all before it stand;
+ *   a = num_accepted[i];
+ *   weights w(v) = max(p_a(v) - q_a(v), 0) if a < m, else p_m(v); if they sum to zero
+ *   (the two rows agree), w = p_a;
+ *   token = the first v with w(0) + .. + w(v) > sample_u[i] * sum w.
+ * out_tokens[i] = the a standing drafts, the token, then -1.  Products and sums are
+ * exact to fp64, so the choice is the formula's.  Weights that are negative, NaN or
+ * infinite count as zero.
+ * draft_probs NULL: drafts that were certain (q_j(x_j) = 1, 0 elsewhere).
+ * new_lens (may be NULL): context_lens[i] - (max_draft - a), the cache length after a
+ * step that appended 1 + max_draft rows per sequence (the last committed token, then
+ * the drafts, padded to max_draft); the next append overwrites the rejected rows.
+ *   target_probs  fp32 [num_seqs][max_draft + 1][target_stride], vocab used
+ *   draft_probs   fp32 [num_seqs][max_draft][draft_stride]
+ *   draft_tokens  int32 [num_seqs][max_draft]; draft_lens int32 [num_seqs] or NULL (all
+ *                 max_draft); accept_u fp32 [num_seqs][max_draft]; sample_u fp32 [num_seqs]
+ *   out_tokens    int32 [num_seqs][max_draft + 1]; num_accepted int32 [num_seqs]
+ * A draft id outside [0, vocab) is rejected, a draft_lens outside [0, max_draft] is
+ * clamped, a target row without any positive entry gives token -1: each sets
+ * PA_ERR_DEVICE_CHECK.  Pointers 4-byte aligned.
+ */
+PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *num_accepted, int32_t *new_lens,
+                                  const int32_t *context_lens, const float *target_probs,
+                                  const float *draft_probs, const int32_t *draft_tokens,
+                                  const int32_t *draft_lens, const float *accept_u,
+                                  const float *sample_u, int num_seqs, int max_draft, int vocab,
+                                  int64_t target_stride, int64_t draft_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

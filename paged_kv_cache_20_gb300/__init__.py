@@ -13,10 +13,12 @@ Layouts match ``include/pagedattn.h``:
   block_tables      int32 [num_seqs, max_blocks_per_seq]
   context_lens      int32 [num_seqs]       (count this step's new tokens)
   slot_mapping      int64 [n_tokens]
+  scores, row_pos   fp32, int32 [num_seqs, num_kv_heads, max_blocks_per_seq * block_size]
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -37,6 +39,7 @@ PA_FP16, PA_BF16 = 0, 1
 _DTYPE = {torch.float16: PA_FP16, torch.bfloat16: PA_BF16}
 
 _c_int, _c_float, _c_size, _c_vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+_c_i64 = ctypes.c_int64
 
 # name -> (restype, argtypes): mirrors include/pagedattn.h
 _SIGNATURES = {
@@ -71,6 +74,14 @@ _SIGNATURES = {
     "pa_decode_split_noalloc": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
                                          _c_int, _c_int, _c_int, _c_float, _c_int, _c_int,
                                          _c_int, _c_int, _c_int, _c_vp]),
+    "pa_rope_append": (_c_int, [_c_vp] * 10 + [_c_int] * 7 + [_c_i64] * 4 +
+                       [_c_int] * 3 + [_c_vp] * 3),
+    "pa_decode_scored_workspace_size": (_c_size, [_c_int] * 7),
+    "pa_decode_scored": (_c_int, [_c_vp] * 11 + [_c_int] * 5 + [_c_float] + [_c_int] * 5 +
+                         [_c_vp, _c_size, _c_vp]),
+    "pa_evict_workspace_size": (_c_size, [_c_int] * 3),
+    "pa_evict": (_c_int, [_c_vp] * 10 + [_c_int] * 10 + [_c_vp, _c_size, _c_vp]),
+    "pa_verify_drafts": (_c_int, [_c_vp] * 10 + [_c_int] * 3 + [_c_i64, _c_i64, _c_vp]),
 }
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # PA_NOALLOC_SCRATCH_BYTES
@@ -466,3 +477,299 @@ def pa_decode_split_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
         block_size, float(scale), num_splits, maxb, num_blocks, q_len, _elt(k_cache, "k_cache"),
         _stream(stream)))
     return out
+
+
+# ------------------------------------------------- rotary append, scored decode, eviction
+def _opt(t: torch.Tensor | None, name: str, dtype) -> int | None:
+    return None if t is None else _cuda(t, name, dtype)
+
+
+def _here(dev: int) -> None:
+    """The calls below launch on the current device: refuse tensors of another one."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _same_device(dev: int, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one CUDA device")
+
+
+def _tokens3(t: torch.Tensor, name: str, dtype) -> tuple[int, int]:
+    """Pointer and token stride of [n_tokens, heads, head_dim] with dense heads (a slice
+    of a fused projection's output is fine)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return t.data_ptr(), sn if n > 1 else max(sn, h * d) // 8 * 8
+
+
+def rope_table(head_dim: int, rotary_dim: int | None = None, base: float = 10000.0,
+               sections=None, inv_freq=None, device="cuda"):
+    """(turns, pair_axis) of pa_rope_append, made once per model.
+
+    inv_freq: rotary_dim / 2 angles per position (floats; default base ** (-2i /
+    rotary_dim)).  sections: how many consecutive pairs each position axis turns, in
+    order (default: one axis turns all).
+    """
+    rotary_dim = head_dim if rotary_dim is None else rotary_dim
+    half = rotary_dim // 2
+    if inv_freq is None:
+        inv_freq = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
+    inv_freq = [float(f) for f in inv_freq]
+    sections = [half] if sections is None else [int(n) for n in sections]
+    if len(inv_freq) != half or sum(sections) != half or min(sections) < 0:
+        raise ValueError("inv_freq and sections must cover rotary_dim / 2 pairs")
+    turns = [round(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for f in inv_freq]
+    turns = [x - (1 << 64) if x >= 1 << 63 else x for x in turns]
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    return (torch.tensor(turns, dtype=torch.int64, device=device),
+            torch.tensor(axis, dtype=torch.int32, device=device))
+
+
+def pa_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   k_cache: torch.Tensor, v_cache: torch.Tensor, positions: torch.Tensor,
+                   slot_mapping: torch.Tensor, turns: torch.Tensor, pair_axis: torch.Tensor,
+                   interleaved: bool = False, k_scale: torch.Tensor | None = None,
+                   v_scale: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotate q into q_out (which may be q) and k on its way into the cache, with v.
+
+    q, q_out [n_tokens, num_q_heads, head_dim]; k, v [n_tokens, num_kv_heads, head_dim];
+    tokens may be strided.  positions int32 [num_axes, n_tokens] (or [n_tokens] for one
+    axis); turns, pair_axis from rope_table.  k_scale, v_scale: FP8 caches.
+    """
+    num_blocks, h_kv, block_size, head_dim = _cache_dims(k_cache)
+    dev = q.get_device()
+    _here(dev)
+    _same_device(dev, q_out, k, v, k_cache, v_cache, positions, slot_mapping, turns, pair_axis,
+                 k_scale, v_scale)
+    dt = _elt(q, "q")
+    n_tokens, h_q = int(q.shape[0]), int(q.shape[1])
+    q_ptr, q_st = _tokens3(q, "q", q.dtype)
+    o_ptr, o_st = _tokens3(q_out, "q_out", q.dtype)
+    k_ptr, k_st = _tokens3(k, "k", q.dtype)
+    v_ptr, v_st = _tokens3(v, "v", q.dtype)
+    if q.shape[2] != head_dim or q_out.shape != q.shape:
+        raise ValueError("q and q_out must be [n_tokens, num_q_heads, head_dim]")
+    if k.shape != (n_tokens, h_kv, head_dim) or v.shape != k.shape:
+        raise ValueError("k and v must be [n_tokens, num_kv_heads, head_dim]")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must match k_cache")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("give both k_scale and v_scale, or neither")
+    if k_scale is None:
+        if k_cache.dtype != q.dtype:
+            raise TypeError(f"the caches must have q's dtype {q.dtype} (or e4m3 codes with scales)")
+        kc, vc = _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache")
+    else:
+        kc, vc = _fp8_cache(k_cache, "k_cache"), _fp8_cache(v_cache, "v_cache")
+        if k_scale.shape != (h_kv,) or v_scale.shape != (h_kv,):
+            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
+    axes = 1 if positions.dim() == 1 else int(positions.shape[0])
+    if positions.numel() != axes * n_tokens or slot_mapping.shape != (n_tokens,):
+        raise ValueError("positions must be [num_axes, n_tokens], slot_mapping [n_tokens]")
+    half = int(turns.shape[0])
+    if turns.dim() != 1 or pair_axis.shape != turns.shape:
+        raise ValueError("turns and pair_axis must be [rotary_dim / 2]")
+    if n_tokens == 0:
+        return q_out
+    _check("pa_rope_append", load().pa_rope_append(
+        o_ptr, q_ptr, k_ptr, v_ptr, kc, vc, _cuda(positions, "positions", torch.int32),
+        _cuda(slot_mapping, "slot_mapping", torch.int64), _cuda(turns, "turns", torch.int64),
+        _cuda(pair_axis, "pair_axis", torch.int32), n_tokens, h_q, h_kv, head_dim, 2 * half, axes,
+        1 if interleaved else 0, o_st, q_st, k_st, v_st, block_size, num_blocks, dt,
+        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
+        _stream(stream)))
+    return q_out
+
+
+def pa_decode_scored_workspace_size(num_seqs: int, num_q_heads: int, q_len: int, head_dim: int,
+                                    num_splits: int, max_blocks_per_seq: int,
+                                    block_size: int) -> int:
+    """Bytes of pa_decode_scored's workspace (0 for invalid sizes)."""
+    return int(load().pa_decode_scored_workspace_size(num_seqs, num_q_heads, q_len, head_dim,
+                                                      num_splits, max_blocks_per_seq, block_size))
+
+
+def pa_decode_scored(out: torch.Tensor, scores: torch.Tensor, q: torch.Tensor,
+                     k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, scale: float, q_len: int = 1, num_splits: int = 1,
+                     workspace: torch.Tensor | None = None, row_pos: torch.Tensor | None = None,
+                     seq_lens: torch.Tensor | None = None, k_scale: torch.Tensor | None = None,
+                     v_scale: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Paged attention that also adds every cached row's attention weight to scores
+    (and notes the positions of this step's rows in row_pos).  FP8 caches with scales."""
+    num_blocks, h_kv, block_size, head_dim, num_seqs, h_q, maxb = _decode_dims(
+        q, k_cache, block_tables, context_lens, q_len)
+    dev = q.get_device()
+    _here(dev)
+    _same_device(dev, out, scores, k_cache, v_cache, block_tables, context_lens, workspace, row_pos,
+                 seq_lens, k_scale, v_scale)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must match k_cache")
+    ledger = (num_seqs, h_kv, maxb * block_size)
+    if scores.shape != ledger or (row_pos is not None and row_pos.shape != ledger):
+        raise ValueError("scores and row_pos must be [num_seqs, num_kv_heads, "
+                         "max_blocks_per_seq * block_size]")
+    if (row_pos is None) != (seq_lens is None):
+        raise ValueError("give both row_pos and seq_lens, or neither")
+    if seq_lens is not None and seq_lens.shape != (num_seqs,):
+        raise ValueError("seq_lens must be [num_seqs]")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("give both k_scale and v_scale, or neither")
+    if k_scale is None:
+        if k_cache.dtype != q.dtype:
+            raise ValueError("q must have the cache dtype")
+        kc, vc = _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache")
+    else:
+        kc, vc = _fp8_cache(k_cache, "k_cache"), _fp8_cache(v_cache, "v_cache")
+        if k_scale.shape != (h_kv,) or v_scale.shape != (h_kv,):
+            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
+    if workspace is None:
+        nbytes = pa_decode_scored_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits, maxb,
+                                                 block_size)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    _check("pa_decode_scored", load().pa_decode_scored(
+        _cuda(out, "out"), _cuda(scores, "scores", torch.float32),
+        _opt(row_pos, "row_pos", torch.int32), _cuda(q, "q"), kc, vc,
+        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
+        _cuda(block_tables, "block_tables", torch.int32),
+        _cuda(context_lens, "context_lens", torch.int32), _opt(seq_lens, "seq_lens", torch.int32),
+        num_seqs, h_q, h_kv, head_dim, block_size, float(scale), maxb, num_blocks, q_len,
+        _elt(q, "q"), num_splits, _cuda(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def pa_evict_workspace_size(num_seqs: int, num_kv_heads: int, budget: int) -> int:
+    """Bytes of pa_evict's workspace (0 for invalid sizes)."""
+    return int(load().pa_evict_workspace_size(num_seqs, num_kv_heads, budget))
+
+
+def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Tensor,
+             row_pos: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+             seq_lens: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0,
+             scores_out: torch.Tensor | None = None, row_pos_out: torch.Tensor | None = None,
+             new_lens: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """Shorten every sequence longer than ``budget`` rows to it, each KV head keeping its
+    first ``sinks`` and last ``recent`` positions and its highest scores.  The ledgers are
+    updated in place unless both outputs are given.  Returns the new context lengths."""
+    num_blocks, h_kv, block_size, head_dim = _cache_dims(k_cache)
+    dev = k_cache.get_device()
+    _here(dev)
+    _same_device(dev, v_cache, scores, row_pos, block_tables, context_lens, seq_lens, scores_out,
+                 row_pos_out, new_lens, workspace)
+    num_seqs = int(context_lens.shape[0])
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must match k_cache")
+    if k_cache.dtype not in _DTYPE and k_cache.dtype not in _FP8_CACHE:
+        raise TypeError(f"k_cache must be 16-bit or hold e4m3 codes, got {k_cache.dtype}")
+    if block_tables.dim() != 2 or int(block_tables.shape[0]) != num_seqs:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    maxb = int(block_tables.shape[1])
+    if (scores_out is None) != (row_pos_out is None):
+        raise ValueError("give both scores_out and row_pos_out, or neither")
+    if scores_out is None:
+        scores_out, row_pos_out = scores, row_pos
+    for t, nm in ((scores, "scores"), (row_pos, "row_pos"), (scores_out, "scores_out"),
+                  (row_pos_out, "row_pos_out")):
+        if t.shape != (num_seqs, h_kv, maxb * block_size):
+            raise ValueError(f"{nm} must be [num_seqs, num_kv_heads, max_blocks_per_seq * block_size]")
+    if seq_lens.shape != (num_seqs,):
+        raise ValueError("seq_lens must be [num_seqs]")
+    if new_lens is None:
+        new_lens = torch.empty_like(context_lens)
+    elif new_lens.shape != (num_seqs,):
+        raise ValueError("new_lens must be [num_seqs]")
+    if workspace is None:
+        nbytes = pa_evict_workspace_size(num_seqs, h_kv, budget)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=k_cache.device)
+    _check("pa_evict", load().pa_evict(
+        _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"),
+        _cuda(scores_out, "scores_out", torch.float32),
+        _cuda(row_pos_out, "row_pos_out", torch.int32), _cuda(new_lens, "new_lens", torch.int32),
+        _cuda(scores, "scores", torch.float32), _cuda(row_pos, "row_pos", torch.int32),
+        _cuda(block_tables, "block_tables", torch.int32),
+        _cuda(context_lens, "context_lens", torch.int32), _cuda(seq_lens, "seq_lens", torch.int32),
+        num_seqs, h_kv, head_dim, block_size, maxb, num_blocks, budget, sinks, recent,
+        k_cache.element_size(), _cuda(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return new_lens
+
+
+def pa_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
+                     draft_tokens: torch.Tensor, accept_u: torch.Tensor, sample_u: torch.Tensor,
+                     draft_lens: torch.Tensor | None = None,
+                     context_lens: torch.Tensor | None = None,
+                     out_tokens: torch.Tensor | None = None,
+                     num_accepted: torch.Tensor | None = None,
+                     new_lens: torch.Tensor | None = None, stream=None):
+    """Accept drafted tokens and sample the one after them, from given uniforms.
+
+    target_probs fp32 [num_seqs, max_draft + 1, vocab]; draft_probs fp32 [num_seqs,
+    max_draft, vocab] or None (certain drafts); their rows may be padded (a slice of a
+    wider vocabulary).  Returns (out_tokens, num_accepted, new_lens or None): new_lens
+    is made when context_lens is given.
+    """
+    if draft_tokens.dim() != 2:
+        raise ValueError("draft_tokens must be [num_seqs, max_draft]")
+    n, k = (int(x) for x in draft_tokens.shape)
+    dev = target_probs.get_device()
+    _here(dev)
+    _same_device(dev, draft_probs, draft_tokens, accept_u, sample_u, draft_lens, context_lens,
+                 out_tokens, num_accepted, new_lens)
+
+    def rows(t, name, r):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
+            raise TypeError(f"{name} must be a float32 CUDA tensor")
+        if t.dim() != 3 or t.shape[0] != n or t.shape[1] != r:
+            raise ValueError(f"{name} must be [num_seqs, {r}, vocab]")
+        st = t.stride(1) if r > 1 or n == 1 else t.stride(0)
+        if (t.shape[2] > 1 and t.stride(2) != 1) or (n > 1 and t.stride(0) != r * st) or \
+                (r > 1 and t.stride(1) != st):
+            raise ValueError(f"{name}: rows must be dense and evenly spaced")
+        return t.data_ptr(), max(st, int(t.shape[2])) if r * n == 1 else st
+
+    p_ptr, p_st = rows(target_probs, "target_probs", k + 1)
+    vocab = int(target_probs.shape[2])
+    q_ptr, q_st = None, 0
+    if draft_probs is not None:
+        q_ptr, q_st = rows(draft_probs, "draft_probs", k)
+        if draft_probs.shape[2] != vocab:
+            raise ValueError("draft_probs must have target_probs' vocabulary")
+    if accept_u.shape != (n, k) or sample_u.shape != (n,):
+        raise ValueError("accept_u must be [num_seqs, max_draft], sample_u [num_seqs]")
+    for t, nm in ((draft_lens, "draft_lens"), (context_lens, "context_lens"),
+                  (num_accepted, "num_accepted"), (new_lens, "new_lens")):
+        if t is not None and t.shape != (n,):
+            raise ValueError(f"{nm} must be [num_seqs]")
+    if new_lens is not None and context_lens is None:
+        raise ValueError("new_lens needs context_lens")
+    if out_tokens is None:
+        out_tokens = torch.empty(n, k + 1, dtype=torch.int32, device=target_probs.device)
+    elif out_tokens.shape != (n, k + 1):
+        raise ValueError("out_tokens must be [num_seqs, max_draft + 1]")
+    if num_accepted is None:
+        num_accepted = torch.empty(n, dtype=torch.int32, device=target_probs.device)
+    if context_lens is not None and new_lens is None:
+        new_lens = torch.empty_like(context_lens)
+    _check("pa_verify_drafts", load().pa_verify_drafts(
+        _cuda(out_tokens, "out_tokens", torch.int32),
+        _cuda(num_accepted, "num_accepted", torch.int32), _opt(new_lens, "new_lens", torch.int32),
+        _opt(context_lens, "context_lens", torch.int32), p_ptr, q_ptr,
+        _cuda(draft_tokens, "draft_tokens", torch.int32),
+        _opt(draft_lens, "draft_lens", torch.int32), _cuda(accept_u, "accept_u", torch.float32),
+        _cuda(sample_u, "sample_u", torch.float32), n, k, vocab, p_st, q_st, _stream(stream)))
+    return out_tokens, num_accepted, new_lens

@@ -18,13 +18,17 @@
 
 #include "../../include/pagedattn.h"
 #include "pa_decode.cuh"
+#include "pa_host.h"
 #include "pa_launch.h"
+#include "pa_scored.h"
 
 namespace {
 
-// Block sizes the kernels take: a block of 32 tokens is read as two 16-token tiles,
-// a 16-token tile spans two blocks of 8
-bool supported_block(int b) { return b == 8 || b == 16 || b == 32; }
+using pa::aligned16;
+using pa::error_word;
+using pa::supported_block;
+using pa::supported_dtype;
+
 constexpr int kMaxDevices = 64;
 constexpr int kMaxQLen = 4096;       // query rows per sequence accepted by the ABI
 constexpr int kMaxDecodeQLen = 16;   // at most this many go to the decode kernel
@@ -281,6 +285,10 @@ void load_encode() {
 std::mutex g_err_mutex;
 unsigned *g_err_ptr[kMaxDevices] = {};
 
+}  // namespace
+
+namespace pa {
+
 // Device address of this device's error word (looked up once per device).
 unsigned *error_word() {
   int dev = 0;
@@ -294,9 +302,9 @@ unsigned *error_word() {
   return g_err_ptr[dev];
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace pa
 
-bool supported_dtype(pa_dtype d) { return d == PA_FP16 || d == PA_BF16; }
+namespace {
 
 // Tensor map over one cache: [num_blocks * num_kv_heads tiles][16 rows][head_dim],
 // box = 16 rows x 64 columns, 128-byte swizzle, zero fill outside.
@@ -398,6 +406,10 @@ struct Placement {
   const float *prior_ws = nullptr;
   const WsLayout *prior_lay = nullptr;
   int prior_splits = 0;
+  // scored attention: every score (decode kernel; the single pass writes its statistics
+  // to m and l), or the rows' statistics alone (many-row kernel; m and l)
+  float *raw_scores = nullptr;
+  float *stat_m = nullptr, *stat_l = nullptr;
 };
 
 // CTAs of a cascade's shared-prefix pass: a share of the SMs, so that the tail
@@ -476,6 +488,13 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
   } else {
     a.prior_acc = a.prior_m = a.prior_l = nullptr;
   }
+  const bool scored = place.raw_scores != nullptr || place.stat_m != nullptr;
+  a.raw_scores = place.raw_scores;
+  a.ws_lx = place.stat_l;
+  if (place.stat_m != nullptr) {
+    a.ws_m = place.stat_m;
+    a.ws_l = place.stat_l;
+  }
   a.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool partial = ws != nullptr;
@@ -533,10 +552,17 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
     } else {
       qmap = kmap;  // unused
     }
-    e = block_size == 16
+    if (scored)
+      e = pa::launch_prefill_stats(kmap, vmap, qmap, a, head_dim, dtype == PA_FP16, fp8, s);
+    else
+      e = block_size == 16
             ? pa::launch_prefill(kmap, vmap, qmap, a, head_dim, dtype == PA_FP16, partial, fp8, s)
             : pa::launch_prefill_bx(kmap, vmap, qmap, a, head_dim, dtype == PA_FP16, partial, fp8, s);
-  } else if (fp8 && block_size == 16)
+  } else if (scored)
+    e = dtype == PA_FP16
+            ? pa::launch_decode_scored_fp16(kmap, vmap, a, head_dim, fp8, partial, (int)units, s)
+            : pa::launch_decode_scored_bf16(kmap, vmap, a, head_dim, fp8, partial, (int)units, s);
+  else if (fp8 && block_size == 16)
     e = dtype == PA_FP16 ? pa::launch_decode8_fp16(kmap, vmap, a, partial, (int)units, s)
                          : pa::launch_decode8_bf16(kmap, vmap, a, partial, (int)units, s);
   else if (fp8)
@@ -897,6 +923,117 @@ PA_API pa_status pa_device_error(void *stream, int clear) {
   if (host & pa::kErrTimeout) return PA_ERR_DEVICE_TIMEOUT;
   if (host & pa::kErrCheck) return PA_ERR_DEVICE_CHECK;
   return PA_OK;
+}
+
+// Workspace of pa_decode_scored: the split-KV sections when num_splits > 1, else the
+// statistics alone (m, l per row); then, up to 16 query tokens, every score.
+struct ScoredLayout {
+  WsLayout split;
+  size_t m_off, l_off, raw_off, total;
+};
+
+static ScoredLayout scored_layout(int num_seqs, int num_q_heads, int q_len, int head_dim,
+                                  int num_splits, int max_blocks_per_seq, int block_size) {
+  ScoredLayout w;
+  const bool many = q_len > kMaxDecodeQLen;
+  const size_t rows = (size_t)num_seqs * q_len * num_q_heads;
+  w.split = ws_layout(num_seqs, num_q_heads, q_len, head_dim, num_splits);
+  if (!many && num_splits > 1) {
+    w.m_off = w.split.m_off;
+    w.l_off = w.split.l_off;
+    w.raw_off = w.split.total;
+  } else {
+    w.m_off = 0;
+    w.l_off = align256(rows * sizeof(float));
+    w.raw_off = w.l_off + align256(rows * sizeof(float));
+  }
+  const size_t tiles = ((size_t)max_blocks_per_seq * block_size + pa::kTileTokens - 1) / pa::kTileTokens;
+  w.total = w.raw_off + (many ? 0 : align256(rows * tiles * pa::kTileTokens * sizeof(float)));
+  return w;
+}
+
+PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_q_heads, int q_len,
+                                              int head_dim, int num_splits,
+                                              int max_blocks_per_seq, int block_size) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || q_len <= 0 || head_dim <= 0 || num_splits <= 0 ||
+      max_blocks_per_seq <= 0 || block_size <= 0)
+    return 0;
+  return scored_layout(num_seqs, num_q_heads, q_len, head_dim, num_splits, max_blocks_per_seq,
+                       block_size).total;
+}
+
+PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, const void *q,
+                                  const void *k_cache, const void *v_cache, const float *k_scale,
+                                  const float *v_scale, const int32_t *block_tables,
+                                  const int32_t *context_lens, const int32_t *seq_lens,
+                                  int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, float scale, int max_blocks_per_seq,
+                                  int num_blocks, int q_len, pa_dtype dtype, int num_splits,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+  if (!out || !aligned16(out) || !scores || !pa::aligned4(scores)) return PA_ERR_INVALID_ARG;
+  if ((row_pos == nullptr) != (seq_lens == nullptr)) return PA_ERR_INVALID_ARG;
+  if (!pa::aligned4(row_pos)) return PA_ERR_INVALID_ARG;
+  if ((k_scale == nullptr) != (v_scale == nullptr)) return PA_ERR_INVALID_ARG;
+  if (num_splits <= 0 || num_splits >= (1 << 20)) return PA_ERR_INVALID_ARG;
+  pa_status st = check_decode(q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+                              num_q_heads, num_kv_heads, head_dim, block_size, scale,
+                              max_blocks_per_seq, num_blocks, q_len, dtype);
+  if (st != PA_OK) return st;
+  if (k_scale && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PA_ERR_INVALID_ARG;
+  const bool many = q_len > kMaxDecodeQLen;
+  const ScoredLayout lay = scored_layout(num_seqs, num_q_heads, q_len, head_dim, num_splits,
+                                         max_blocks_per_seq, block_size);
+  if (workspace_bytes < lay.total) return PA_ERR_INVALID_ARG;
+  char *ws = static_cast<char *>(workspace);
+  // 1. the attention, leaving its scores (or, many query rows, its statistics)
+  Placement place;
+  if (!many) place.raw_scores = reinterpret_cast<float *>(ws + lay.raw_off);
+  const bool split = !many && num_splits > 1;
+  if (!split) {
+    place.stat_m = reinterpret_cast<float *>(ws + lay.m_off);
+    place.stat_l = reinterpret_cast<float *>(ws + lay.l_off);
+  }
+  st = decode_common(split ? nullptr : out, split ? static_cast<float *>(workspace) : nullptr,
+                     &lay.split, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, scale, split ? num_splits : 1,
+                     max_blocks_per_seq, num_blocks, q_len, dtype, stream, nullptr, nullptr, k_scale,
+                     v_scale, place);
+  if (st != PA_OK) return st;
+  if (split) {
+    st = pa_decode_combine(out, workspace, workspace_bytes, num_seqs, num_q_heads, head_dim, q_len,
+                           num_splits, dtype, stream);
+    if (st != PA_OK) return st;
+  }
+  // 2. the ledger
+  pa::LedgerArgs a;
+  a.scores = scores;
+  a.row_pos = row_pos;
+  a.seq_lens = seq_lens;
+  a.context_lens = context_lens;
+  a.block_tables = block_tables;
+  a.raw_scores = place.raw_scores;
+  a.ws_m = reinterpret_cast<const float *>(ws + lay.m_off);
+  a.ws_l = reinterpret_cast<const float *>(ws + lay.l_off);
+  a.q = q;
+  a.k_cache = k_cache;
+  a.k_scale = k_scale;
+  a.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+  a.num_seqs = num_seqs;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.q_len = q_len;
+  a.rows = a.group * q_len;
+  a.splits = split ? num_splits : 1;
+  a.max_rows = max_blocks_per_seq * block_size;
+  a.max_tiles = (int)(((int64_t)a.max_rows + pa::kTileTokens - 1) / pa::kTileTokens);
+  a.block_size = block_size;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = many ? pa::launch_mass(a, head_dim, dtype == PA_FP16, k_scale != nullptr, s)
+                             : pa::launch_ledger(a, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -105,6 +105,33 @@ struct DecodeArgs {
   // is partition 0.  prior_m == nullptr: none.
   const float *prior_acc, *prior_m, *prior_l;
   int prior_splits;
+  // Scored decode (paths built with SC): every score the pass computes, base-2 units,
+  // -inf where masked: [num_seqs][num_kv_heads][max_tiles][rows][16 tokens].  The
+  // single pass then also writes its statistics m and l (to ws_m, ws_l).
+  float *raw_scores;
+  // Scored prefill: the row sums of the unrounded weights [num_seqs][q_len * num_q_heads]
+  float *ws_lx;
+};
+
+// Where a path puts the scores of one tile (row r, token t at p[16 r + t]) for a
+// caller that needs every row's softmax weights once the row sums are known.  The
+// paths built without it hold an empty sink.
+template <bool SC>
+struct ScoreSink {
+  __device__ __forceinline__ void set(float *, int) {}
+  __device__ __forceinline__ void put(int, int, float) {}
+};
+template <>
+struct ScoreSink<true> {
+  float *p;
+  int rows;  // rows at or past it are padding
+  __device__ __forceinline__ void set(float *tile, int n) {
+    p = tile;
+    rows = n;
+  }
+  __device__ __forceinline__ void put(int r, int t, float v) {
+    if (r < rows) p[16 * r + t] = v;
+  }
 };
 
 constexpr int kLptMaxSeqs = 256;
@@ -206,8 +233,9 @@ __device__ __forceinline__ RowInfo row_info(const DecodeArgs &a, int kvh, int rh
 
 // ---------------------------------------------------------------------------------
 // CUDA-core path: R rows, K lanes per token.
-template <typename T, int D, int K, int R>
+template <typename T, int D, int K, int R, bool SC = false>
 struct FmaPath {
+  static constexpr bool kScored = SC;
   static constexpr int RPC = R;                    // rows per CTA
   static constexpr int TPP = 32 / K;               // tokens per pass
   static constexpr int PASSES = kTileTokens / TPP;  // passes per tile
@@ -225,6 +253,8 @@ struct FmaPath {
   float m[R], l[R];
   int lim[R];
   int part, tip, rot;
+  ScoreSink<SC> raw;
+  __device__ __forceinline__ ScoreSink<SC> &sink() { return raw; }
 
   __device__ __forceinline__ int chunk(int jj) const {
     return part * CH + (kRotate ? ((jj + rot) % CH) : jj);
@@ -295,6 +325,17 @@ struct FmaPath {
 #pragma unroll
         for (int r = 0; r < R; ++r)
           if (tg >= lim[r]) s[p][r] = -INFINITY;
+      }
+    }
+    if constexpr (SC) {
+      // the K lanes of a token hold the same score: lane part p stores pass p's
+      static_assert(PASSES <= K, "a lane for every pass");
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float v = s[0][r];
+#pragma unroll
+        for (int p = 1; p < PASSES; ++p) v = part == p ? s[p][r] : v;
+        if (part < PASSES) raw.put(r, part * TPP + tip, v);
       }
     }
     // online softmax, per lane group (tokens p*TPP + tip)
@@ -384,8 +425,9 @@ struct FmaPath {
 
 // ---------------------------------------------------------------------------------
 // Tensor-core path: up to 16 rows (padded), warp-level mma.sync m16n8k16.
-template <typename T, int D>
+template <typename T, int D, bool SC = false>
 struct MmaPath {
+  static constexpr bool kScored = SC;
   static constexpr int RPC = 16;
   static constexpr int KS = D / 16;  // k-steps of S = Q K^T
   static constexpr int NT = D / 8;   // n-tiles (8 dims) of O
@@ -395,6 +437,8 @@ struct MmaPath {
   float m[2], l[2];
   float rs[2];         // base-2 score scale of each of this lane's two rows
   int lim[2];
+  ScoreSink<SC> raw;
+  __device__ __forceinline__ ScoreSink<SC> &sink() { return raw; }
 
 
   // Row bookkeeping; returns this lane's two q rows (nullptr for padding rows).
@@ -489,6 +533,7 @@ struct MmaPath {
             if (tg >= lim[hr]) v = -INFINITY;
           }
           sc[nt][2 * hr + e] = v;
+          if constexpr (SC) raw.put((lane >> 2) + 8 * hr, nt * 8 + (lane & 3) * 2 + e, v);
         }
       mx[hr] = fmaxf(fmaxf(sc[0][2 * hr], sc[0][2 * hr + 1]), fmaxf(sc[1][2 * hr], sc[1][2 * hr + 1]));
       mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
@@ -592,8 +637,9 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 // [token][row]; one movmatrix transpose per block gives the B fragment of P^T.
 // Thread (g, c) = (lane / 4, lane % 4) holds rows 2c and 2c+1 (P, l, O^T columns) and
 // tokens g and g+8 of each tile.
-template <typename T, int D>
+template <typename T, int D, bool SC = false>
 struct MmaTPath {
+  static constexpr bool kScored = SC;
   static constexpr int RPC = 8;
   static constexpr int KS = D / 16;  // k-steps of S (16 dims each)
   static constexpr int MT = D / 16;  // m-tiles of O^T (16 dims each)
@@ -603,6 +649,8 @@ struct MmaTPath {
   float m[2], l[2];    // rows 2c + e
   float rs[2];
   int lim[2];
+  ScoreSink<SC> raw;
+  __device__ __forceinline__ ScoreSink<SC> &sink() { return raw; }
 
   // Rows 2c, 2c + 1 of this lane: causal limits, softmax state, O^T = 0.
   __device__ __forceinline__ void init_rows(const DecodeArgs &a, int kvh, int row0, int L,
@@ -677,6 +725,7 @@ struct MmaTPath {
         if (tg >= lim[i & 1]) v = -INFINITY;
       }
       sc[i] = v;
+      if constexpr (SC) raw.put(2 * (threadIdx.x & 3) + (i & 1), g + 8 * (i >> 1), v);
     }
     // online softmax per row (the 8 threads of a row differ in g: lanes c + 4g)
 #pragma unroll
@@ -805,12 +854,14 @@ __device__ __forceinline__ uint32_t e4m3_hi_f16x2(uint32_t w) {
 // Every load above is conflict-free under the 128-byte swizzle: the 8 lanes of a
 // shared-memory phase hit 8 distinct 16-byte bank groups.  Each q row is scaled by a
 // power of two into fp16's range and the score scale of its S^T column undoes it.
-template <typename T>
+template <typename T, bool SC = false>
 struct Mma8TPath {
+  static constexpr bool kScored = SC;
   static constexpr int D = 128;
   static constexpr int RPC = 8;
-  using Inner = MmaTPath<__half, D>;
+  using Inner = MmaTPath<__half, D, SC>;
   static constexpr int KS = Inner::KS;
+  __device__ __forceinline__ ScoreSink<SC> &sink() { return inner.raw; }
   Inner inner;  // inner.o[b][i]: O^T dim 16g + 2b + (i >> 1), row 2c + (i & 1)
 
   __device__ __forceinline__ void init(const DecodeArgs &a, int seq, int kvh, int row0, int L,
@@ -923,8 +974,9 @@ struct Mma8TPath {
 // FP8 (e4m3) cache, CUDA-core path: head_dim 128, one 128-byte row per token,
 // 4 lanes per token, each lane 2 chunks of 16 codes.  The K scale is folded into q,
 // the V scale into the output.
-template <typename T, int R>
+template <typename T, int R, bool SC = false>
 struct Fma8Path {
+  static constexpr bool kScored = SC;
   static constexpr int D = 128;
   static constexpr int RPC = R;
   static constexpr int K = 4;                        // lanes per token
@@ -939,6 +991,8 @@ struct Fma8Path {
   float m[R], l[R];
   int lim[R];
   int part, tip;
+  ScoreSink<SC> raw;
+  __device__ __forceinline__ ScoreSink<SC> &sink() { return raw; }
 
   __device__ __forceinline__ int chunk(int jj) const { return part * CH + jj; }
 
@@ -1006,6 +1060,17 @@ struct Fma8Path {
 #pragma unroll
         for (int r = 0; r < R; ++r)
           if (tg >= lim[r]) s[p][r] = -INFINITY;
+      }
+    }
+    if constexpr (SC) {
+      // the K lanes of a token hold the same score: lane part p stores pass p's
+      static_assert(PASSES <= K, "a lane for every pass");
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float v = s[0][r];
+#pragma unroll
+        for (int p = 1; p < PASSES; ++p) v = part == p ? s[p][r] : v;
+        if (part < PASSES) raw.put(r, part * TPP + tip, v);
       }
     }
 #pragma unroll
@@ -1100,12 +1165,14 @@ struct Fma8Path {
 // A bf16 q row is brought into fp16 range by an exact power-of-two factor 2^-e (e:
 // exponent of the row's largest |q|), and 2^e goes into that row's score scale.  P
 // is then fp16 too: no hi/lo split is needed.
-template <typename T>
+template <typename T, bool SC = false>
 struct Mma8Path {
+  static constexpr bool kScored = SC;
   static constexpr int D = 128;
   static constexpr int RPC = 16;
-  using Inner = MmaPath<__half, D>;
+  using Inner = MmaPath<__half, D, SC>;
   static constexpr int KS = Inner::KS;
+  __device__ __forceinline__ ScoreSink<SC> &sink() { return inner.raw; }
   Inner inner;
 
   __device__ __forceinline__ void init(const DecodeArgs &a, int seq, int kvh, int row0, int L,
@@ -1443,6 +1510,10 @@ __global__ void __launch_bounds__(NW * 32)
     const int j = tile_of(n);
     const uint32_t kt = my_stages + s * kStageBytes;
     const uint32_t vt = kt + kTileBytes;
+    if constexpr (Path::kScored)
+      path.sink().set(a.raw_scores + (((size_t)(seq * a.num_kv_heads + kvh) * a.max_tiles + j) * a.rows +
+                                      row0) * kTileTokens,
+                      a.rows - row0);
     if (j >= first_masked) {
       const int nvalid = L - j * kTileTokens;  // rows >= nvalid are past the context
       if (nvalid < kTileTokens) {
@@ -1503,6 +1574,10 @@ __global__ void __launch_bounds__(NW * 32)
       }
     } else {
       const size_t orow = (size_t)(seq * a.q_len + ri.u) * a.num_q_heads + ri.h;
+      if (Path::kScored && d8 == 0) {
+        a.ws_m[orow] = M;
+        a.ws_l[orow] = den;
+      }
       float inv = den > 0.f ? vscale / den : 0.f;
       float o[8];
 #pragma unroll

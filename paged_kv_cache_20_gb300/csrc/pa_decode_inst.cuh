@@ -120,65 +120,66 @@ static cudaError_t launch_few_units(const CUtensorMap &kmap, const CUtensorMap &
   return launch_one<BS, T, 128, Path, false, KV8>(kmap, vmap, a, units, 1, st, WAVE4_NUM, WAVE4_DEN);
 }
 
-template <int BS, typename T, int D, bool PARTIAL>
+// SC: the paths also write every score (scored decode).
+template <int BS, typename T, int D, bool PARTIAL, bool SC>
 static cudaError_t launch_paths(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                 const DecodeArgs &a, int units, cudaStream_t st) {
   if constexpr (!PARTIAL && D == 128) {
-    if (a.rows == 1) return launch_few_units<BS, T, FmaPath<T, D, 4, 1>, false, 2, 1>(kmap, vmap, a, units, st);
-    if (a.rows == 2) return launch_few_units<BS, T, FmaPath<T, D, 8, 2>, false, 2, 1>(kmap, vmap, a, units, st);
+    if (a.rows == 1) return launch_few_units<BS, T, FmaPath<T, D, 4, 1, SC>, false, 2, 1>(kmap, vmap, a, units, st);
+    if (a.rows == 2) return launch_few_units<BS, T, FmaPath<T, D, 8, 2, SC>, false, 2, 1>(kmap, vmap, a, units, st);
   }
-  if (a.rows == 1) return launch_one<BS, T, D, FmaPath<T, D, 4, 1>, PARTIAL>(kmap, vmap, a, units, 1, st);
-  if (a.rows == 2) return launch_one<BS, T, D, FmaPath<T, D, 8, 2>, PARTIAL>(kmap, vmap, a, units, 1, st);
+  if (a.rows == 1) return launch_one<BS, T, D, FmaPath<T, D, 4, 1, SC>, PARTIAL>(kmap, vmap, a, units, 1, st);
+  if (a.rows == 2) return launch_one<BS, T, D, FmaPath<T, D, 8, 2, SC>, PARTIAL>(kmap, vmap, a, units, 1, st);
   if (a.rows <= 8) {
     if constexpr (!PARTIAL && D == 128)
-      return launch_few_units<BS, T, MmaTPath<T, D>, false, 2, 1>(kmap, vmap, a, units, st);
-    return launch_one<BS, T, D, MmaTPath<T, D>, PARTIAL>(kmap, vmap, a, units, 1, st);
+      return launch_few_units<BS, T, MmaTPath<T, D, SC>, false, 2, 1>(kmap, vmap, a, units, st);
+    return launch_one<BS, T, D, MmaTPath<T, D, SC>, PARTIAL>(kmap, vmap, a, units, 1, st);
   }
   const int groups = (a.rows + 15) / 16;
   if constexpr (!PARTIAL && D == 128)
-    if (groups == 1) return launch_few_units<BS, T, MmaPath<T, D>, false, 2, 1>(kmap, vmap, a, units, st);
-  return launch_one<BS, T, D, MmaPath<T, D>, PARTIAL>(kmap, vmap, a, units, groups, st);
+    if (groups == 1) return launch_few_units<BS, T, MmaPath<T, D, SC>, false, 2, 1>(kmap, vmap, a, units, st);
+  return launch_one<BS, T, D, MmaPath<T, D, SC>, PARTIAL>(kmap, vmap, a, units, groups, st);
 }
 
-template <int BS, typename T, bool PARTIAL>
+template <int BS, typename T, bool PARTIAL, bool SC>
 static cudaError_t launch_paths8(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                  const DecodeArgs &a, int units, cudaStream_t st) {
   if constexpr (!PARTIAL) {
-    if (a.rows == 1) return launch_few_units<BS, T, Fma8Path<T, 1>, true, 2, 1>(kmap, vmap, a, units, st);
-    if (a.rows == 2) return launch_few_units<BS, T, Fma8Path<T, 2>, true, 2, 1>(kmap, vmap, a, units, st);
+    if (a.rows == 1) return launch_few_units<BS, T, Fma8Path<T, 1, SC>, true, 2, 1>(kmap, vmap, a, units, st);
+    if (a.rows == 2) return launch_few_units<BS, T, Fma8Path<T, 2, SC>, true, 2, 1>(kmap, vmap, a, units, st);
   }
-  if (a.rows == 1) return launch_one<BS, T, 128, Fma8Path<T, 1>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
-  if (a.rows == 2) return launch_one<BS, T, 128, Fma8Path<T, 2>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
+  if (a.rows == 1) return launch_one<BS, T, 128, Fma8Path<T, 1, SC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
+  if (a.rows == 2) return launch_one<BS, T, 128, Fma8Path<T, 2, SC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
   if (a.rows <= 8) {
-    if constexpr (!PARTIAL) return launch_few_units<BS, T, Mma8TPath<T>, true, 3, 2>(kmap, vmap, a, units, st);
-    return launch_one<BS, T, 128, Mma8TPath<T>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
+    if constexpr (!PARTIAL) return launch_few_units<BS, T, Mma8TPath<T, SC>, true, 3, 2>(kmap, vmap, a, units, st);
+    return launch_one<BS, T, 128, Mma8TPath<T, SC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
   }
   const int groups = (a.rows + 15) / 16;
   if constexpr (!PARTIAL)
-    if (groups == 1) return launch_few_units<BS, T, Mma8Path<T>, true, 2, 1>(kmap, vmap, a, units, st);
-  return launch_one<BS, T, 128, Mma8Path<T>, PARTIAL, true>(kmap, vmap, a, units, groups, st);
+    if (groups == 1) return launch_few_units<BS, T, Mma8Path<T, SC>, true, 2, 1>(kmap, vmap, a, units, st);
+  return launch_one<BS, T, 128, Mma8Path<T, SC>, PARTIAL, true>(kmap, vmap, a, units, groups, st);
 }
 
 // FP8 (e4m3) cache, head_dim 128; T is the type of q and out.
 // BS = 16: kernels built for 16-token blocks; BS = 0: kernels that read the block
 // size (8 or 32) from the arguments.
-template <int BS, typename T>
+template <int BS, typename T, bool SC = false>
 static cudaError_t launch_decode8_t(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                     const DecodeArgs &a, bool partial, int units, cudaStream_t st) {
-  return partial ? launch_paths8<BS, T, true>(kmap, vmap, a, units, st)
-                 : launch_paths8<BS, T, false>(kmap, vmap, a, units, st);
+  return partial ? launch_paths8<BS, T, true, SC>(kmap, vmap, a, units, st)
+                 : launch_paths8<BS, T, false, SC>(kmap, vmap, a, units, st);
 }
 
-template <int BS, typename T>
+template <int BS, typename T, bool SC = false>
 static cudaError_t launch_decode_t(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                    const DecodeArgs &a, int head_dim, bool partial, int units,
                                    cudaStream_t st) {
   if (head_dim == 128)
-    return partial ? launch_paths<BS, T, 128, true>(kmap, vmap, a, units, st)
-                   : launch_paths<BS, T, 128, false>(kmap, vmap, a, units, st);
+    return partial ? launch_paths<BS, T, 128, true, SC>(kmap, vmap, a, units, st)
+                   : launch_paths<BS, T, 128, false, SC>(kmap, vmap, a, units, st);
   if (head_dim == 64)
-    return partial ? launch_paths<BS, T, 64, true>(kmap, vmap, a, units, st)
-                   : launch_paths<BS, T, 64, false>(kmap, vmap, a, units, st);
+    return partial ? launch_paths<BS, T, 64, true, SC>(kmap, vmap, a, units, st)
+                   : launch_paths<BS, T, 64, false, SC>(kmap, vmap, a, units, st);
   return cudaErrorInvalidValue;
 }
 

@@ -22,13 +22,13 @@ namespace {
 template <int D> constexpr int kRingK = D == 128 ? 3 : 4;
 template <int D> constexpr int kRingV = D == 128 ? 2 : 4;
 
-template <typename T, int D, bool PARTIAL, bool KV8, bool BS16>
+template <typename T, int D, bool PARTIAL, bool KV8, bool BS16, bool STATS = false>
 cudaError_t launch_prefill_t(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap,
                              const DecodeArgs &a, cudaStream_t st) {
   // the MMA operands are fp16 over an FP8 cache; the layout's sizes match either way
   using TM = typename TcPick<KV8, __half, T>::type;
   constexpr int kSmem = TcLayout<TM, D>::smem_bytes(kRingK<D>, kRingV<D>);
-  auto kern = paged_prefill_tc_kernel<T, D, kRingK<D>, kRingV<D>, PARTIAL, KV8, BS16>;
+  auto kern = paged_prefill_tc_kernel<T, D, kRingK<D>, kRingV<D>, PARTIAL, KV8, BS16, STATS>;
   static std::atomic<unsigned long long> opted{0};  // bit per device: smem opt-in done
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -93,6 +93,18 @@ cudaError_t dispatch(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUt
   if (head_dim == 64)
     return partial ? launch_prefill_t<T, 64, true, false, BS16>(kmap, vmap, qmap, a, st)
                    : launch_prefill_t<T, 64, false, false, BS16>(kmap, vmap, qmap, a, st);
+  return cudaErrorInvalidValue;
+}
+
+// Single pass with the rows' statistics (scored attention).
+template <bool BS16, typename T>
+cudaError_t dispatch_stats(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap,
+                           const DecodeArgs &a, int head_dim, bool kv8, cudaStream_t st) {
+  if (kv8)
+    return head_dim == 128 ? launch_prefill_t<T, 128, false, true, BS16, true>(kmap, vmap, qmap, a, st)
+                           : cudaErrorInvalidValue;
+  if (head_dim == 128) return launch_prefill_t<T, 128, false, false, BS16, true>(kmap, vmap, qmap, a, st);
+  if (head_dim == 64) return launch_prefill_t<T, 64, false, false, BS16, true>(kmap, vmap, qmap, a, st);
   return cudaErrorInvalidValue;
 }
 

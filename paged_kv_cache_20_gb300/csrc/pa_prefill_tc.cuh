@@ -318,7 +318,9 @@ __device__ __forceinline__ void tc_widen_e4m3_rows(uint32_t st, int r0, int rows
 
 // BS16: the cache's blocks are 16 tokens (fixed at compile time); otherwise the
 // block size (8 or 32) is read from the arguments.
-template <typename T, int D, int NK, int NV, bool PARTIAL, bool KV8, bool BS16>
+// STATS (single pass only): also write each row's maximum and the sum of its weights
+// before their rounding for P V, for a second pass that needs the weights themselves.
+template <typename T, int D, int NK, int NV, bool PARTIAL, bool KV8, bool BS16, bool STATS = false>
 __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap,
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
   const int kBsz = BS16 ? 16 : a.block_size;
   constexpr int kOCols = D / 2;  // O columns per softmax warp
   static_assert(NK >= 2 && NV >= 2, "ring depth");
+  static_assert(!(PARTIAL && STATS), "statistics of a single pass");
   static_assert(D == 64 || D == 128, "head_dim");
 
   extern __shared__ uint8_t smem_raw[];
@@ -853,6 +856,8 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
     bool pend = false;
     int pend_gl = 0;
     float pend_sc = 0.f, pend_m = 0.f, pend_vs = 1.f;
+    // STATS: the sum of the unrounded weights (bf16 P keeps it in l already)
+    constexpr bool kExactSum = STATS && !Lay::kSplitP;
     long long pend_roff = -1;
 
     int g = 0;   // chunks of this CTA so far (all units)
@@ -866,7 +871,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
     for (int k = 0; ok && cu.valid; ++k) {
       unit_scales(cu, e_cur);
       const int lim_row = cu.rvalid ? min(cu.vis, cu.te * kTileTokens) : 0;  // padding rows: 0
-      float m_run = -INFINITY, l = 0.f;
+      float m_run = -INFINITY, l = 0.f, lx = 0.f;
       for (int j = 0; j < cu.nch; ++j) {
         const int gg = g + j;
         const int b = gg % 3;
@@ -907,11 +912,13 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         const float f = need ? ex2_ftz(m_run - m_new) : 1.f;  // 0 when m_run = -inf
         if (need) {
           l *= f;
+          if constexpr (kExactSum) lx *= f;
           m_run = m_new;
         }
         const float mb = (m_run == -INFINITY) ? 0.f : m_run;
         const uint64_t nmb2 = tc::f2pack(-mb, -mb);
         uint64_t ps2[2] = {0ull, 0ull};  // packed partial sums (+0.0f, +0.0f)
+        uint64_t px2[2] = {0ull, 0ull};  // the same of the unrounded weights
         {
           // P over these S columns: hi words in the first 32, lo words (bf16) next
           uint32_t hw[32];
@@ -931,6 +938,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
               ps2[e & 1] = tc::fadd2(ps2[e & 1], pp);
             } else {
               hw[e] = Elt<TM>::from_f2(p0, p1);
+              if constexpr (kExactSum) px2[e & 1] = tc::fadd2(px2[e & 1], tc::f2pack(p0, p1));
               // the sum of the rounded weights P V is taken with: the quotient O / l
               // is then an exact convex combination of V rows (a dominant weight's
               // rounding cancels)
@@ -950,6 +958,11 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
           tc::f2unpack(ps2[0], a0, a1);
           tc::f2unpack(ps2[1], b0, b1);
           l += (a0 + a1) + (b0 + b1);
+          if constexpr (kExactSum) {
+            tc::f2unpack(px2[0], a0, a1);
+            tc::f2unpack(px2[1], b0, b1);
+            lx += (a0 + a1) + (b0 + b1);
+          }
         }
         // O rescale: P_{j-1} V_{j-1} (and with it every earlier P V) must be complete.
         // S_j's completion implies P_{j-3} V_{j-3}'s and P_j V_j is not issued yet, so
@@ -1051,7 +1064,12 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
                        : (long long)((size_t)(cu.rseq * a.q_len + cu.ru) * a.num_q_heads + cu.rh);
       if (cu.nch > 0) {
         l = exchange(l, false);  // the row sum over both column halves
+        if constexpr (kExactSum) lx = exchange(lx, false);
         if (!ok) break;
+        if (STATS && hc == 0 && roff >= 0) {
+          a.ws_m[roff] = m_run;
+          a.ws_lx[roff] = kExactSum ? lx : l;
+        }
         pend = true;
         pend_gl = g + cu.nch - 1;
         pend_sc = PARTIAL ? l : (l > 0.f ? vs_u / l : 0.f);
@@ -1060,6 +1078,10 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         pend_roff = roff;
       } else {
         // no position in this unit's partition: zeros (empty statistics)
+        if (STATS && hc == 0 && roff >= 0) {
+          a.ws_m[roff] = -INFINITY;
+          a.ws_lx[roff] = 0.f;
+        }
         if (pend) {
           if (!epilogue(true, pend_gl, pend_sc, pend_m, pend_roff, pend_vs)) {
             ok = false;

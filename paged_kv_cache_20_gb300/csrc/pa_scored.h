@@ -1,0 +1,46 @@
+// pa_scored.h -- launch entry points of scored attention (host code only).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace pa {
+
+struct DecodeArgs;
+
+// The second part of scored attention: weights from the scores and the rows'
+// statistics, added to the ledger.
+struct LedgerArgs {
+  float *scores;              // [num_seqs][num_kv_heads][max_rows]
+  int32_t *row_pos;           // the same shape, or nullptr
+  const int32_t *seq_lens;    // [num_seqs] (with row_pos)
+  const int32_t *context_lens, *block_tables;
+  const float *raw_scores;    // [num_seqs][num_kv_heads][max_tiles][rows][16]
+  const float *ws_m, *ws_l;   // [num_seqs][splits][q_len * num_q_heads]
+  // the scores again from K and q (more than 16 query tokens)
+  const void *q, *k_cache;
+  const float *k_scale;
+  float scale_log2;
+  int num_seqs, num_kv_heads, group, q_len, rows, splits;  // rows = group * q_len
+  int max_rows, max_tiles, block_size, max_blocks_per_seq, num_blocks;
+};
+
+cudaError_t launch_ledger(const LedgerArgs &args, cudaStream_t stream);
+cudaError_t launch_mass(const LedgerArgs &args, int head_dim, bool fp16, bool kv8,
+                        cudaStream_t stream);
+
+// The decode kernels with their scores written to args.raw_scores; the single pass
+// also writes its statistics.
+cudaError_t launch_decode_scored_fp16(const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                      const DecodeArgs &args, int head_dim, bool kv8, bool partial,
+                                      int units, cudaStream_t stream);
+cudaError_t launch_decode_scored_bf16(const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                      const DecodeArgs &args, int head_dim, bool kv8, bool partial,
+                                      int units, cudaStream_t stream);
+// The many-row kernel, single pass, writing its rows' statistics (ws_m, ws_lx).
+cudaError_t launch_prefill_stats(const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const CUtensorMap &qmap, const DecodeArgs &args, int head_dim,
+                                 bool fp16, bool kv8, cudaStream_t stream);
+
+}  // namespace pa
