@@ -480,37 +480,80 @@ def pa_decode_split_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
 
 
 # ------------------------------------------------- rotary append, scored decode, eviction
-def _opt(t: torch.Tensor | None, name: str, dtype) -> int | None:
-    return None if t is None else _cuda(t, name, dtype)
+# These calls are short on the GPU (a few microseconds for a decode step's tokens), so
+# their checks are written for the host's time: one test per tensor on the way that
+# passes, and the reason worked out only on the way that fails.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _here(dev: int) -> None:
-    """The calls below launch on the current device: refuse tensors of another one."""
+def _device_of(t) -> int:
+    """Device of the call's first tensor: the calls launch on the current device, so
+    tensors of another one are refused."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("tensors must be CUDA tensors")
+    dev = t.get_device()
     if dev != torch.cuda.current_device():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _same_device(dev: int, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors must be on one CUDA device")
+def _stream_on(stream, dev: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
-def _tokens3(t: torch.Tensor, name: str, dtype) -> tuple[int, int]:
+def _refuse(t, name: str, dtype, dev: int):
+    _cuda(t, name, dtype)
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the others on cuda:{dev}")
+
+
+def _ptr(t, name: str, dtype, dev: int) -> int:
+    """Pointer of a contiguous tensor of this type on this device."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev \
+            or not t.is_contiguous():
+        _refuse(t, name, dtype, dev)
+    return t.data_ptr()
+
+
+def _shape(t, name: str, want: tuple) -> None:
+    if t.shape != want:
+        raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+
+
+def _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, h_kv: int, dev: int):
+    """Pointers of the caches and their scales (None, None: 16-bit caches of type elt)."""
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("give both k_scale and v_scale, or neither")
+    _shape(v_cache, "v_cache", k_cache.shape)
+    if k_scale is None:
+        return _ptr(k_cache, "k_cache", elt, dev), _ptr(v_cache, "v_cache", elt, dev), None, None
+    dt = k_cache.dtype
+    if dt not in _FP8_CACHE:
+        raise TypeError(f"k_cache must hold e4m3 codes (uint8 or float8_e4m3fn), got {dt}")
+    _shape(k_scale, "k_scale", (h_kv,))
+    _shape(v_scale, "v_scale", (h_kv,))
+    return (_ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+            _ptr(k_scale, "k_scale", torch.float32, dev), _ptr(v_scale, "v_scale", torch.float32, dev))
+
+
+def _tokens3(t, name: str, dtype, dev: int, shape) -> tuple[int, int]:
     """Pointer and token stride of [n_tokens, heads, head_dim] with dense heads (a slice
     of a fused projection's output is fine)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [n_tokens, heads, head_dim]")
-    n, h, d = t.shape
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev:
+        _cuda(t, name, dtype)
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    _shape(t, name, shape)
+    n, h, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
     sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return t.data_ptr(), sn if n > 1 else max(sn, h * d) // 8 * 8
+    return t.data_ptr(), sn if n > 1 else h * d
 
 
 def rope_table(head_dim: int, rotary_dim: int | None = None, base: float = 10000.0,
@@ -547,48 +590,41 @@ def pa_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     tokens may be strided.  positions int32 [num_axes, n_tokens] (or [n_tokens] for one
     axis); turns, pair_axis from rope_table.  k_scale, v_scale: FP8 caches.
     """
+    dev = _device_of(q)
     num_blocks, h_kv, block_size, head_dim = _cache_dims(k_cache)
-    dev = q.get_device()
-    _here(dev)
-    _same_device(dev, q_out, k, v, k_cache, v_cache, positions, slot_mapping, turns, pair_axis,
-                 k_scale, v_scale)
+    elt = q.dtype
     dt = _elt(q, "q")
-    n_tokens, h_q = int(q.shape[0]), int(q.shape[1])
-    q_ptr, q_st = _tokens3(q, "q", q.dtype)
-    o_ptr, o_st = _tokens3(q_out, "q_out", q.dtype)
-    k_ptr, k_st = _tokens3(k, "k", q.dtype)
-    v_ptr, v_st = _tokens3(v, "v", q.dtype)
-    if q.shape[2] != head_dim or q_out.shape != q.shape:
-        raise ValueError("q and q_out must be [n_tokens, num_q_heads, head_dim]")
-    if k.shape != (n_tokens, h_kv, head_dim) or v.shape != k.shape:
-        raise ValueError("k and v must be [n_tokens, num_kv_heads, head_dim]")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("v_cache must match k_cache")
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("give both k_scale and v_scale, or neither")
-    if k_scale is None:
-        if k_cache.dtype != q.dtype:
-            raise TypeError(f"the caches must have q's dtype {q.dtype} (or e4m3 codes with scales)")
-        kc, vc = _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache")
-    else:
-        kc, vc = _fp8_cache(k_cache, "k_cache"), _fp8_cache(v_cache, "v_cache")
-        if k_scale.shape != (h_kv,) or v_scale.shape != (h_kv,):
-            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
-    axes = 1 if positions.dim() == 1 else int(positions.shape[0])
-    if positions.numel() != axes * n_tokens or slot_mapping.shape != (n_tokens,):
-        raise ValueError("positions must be [num_axes, n_tokens], slot_mapping [n_tokens]")
-    half = int(turns.shape[0])
-    if turns.dim() != 1 or pair_axis.shape != turns.shape:
-        raise ValueError("turns and pair_axis must be [rotary_dim / 2]")
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tokens, num_q_heads, head_dim]")
+    q_shape = q.shape
+    n_tokens, h_q, q_dim = q_shape
+    if q_dim != head_dim:
+        raise ValueError("q must have the cache's head_dim")
+    kv_shape = (n_tokens, h_kv, head_dim)
+    q_ptr, q_st = _tokens3(q, "q", elt, dev, q_shape)
+    o_ptr, o_st = _tokens3(q_out, "q_out", elt, dev, q_shape)
+    k_ptr, k_st = _tokens3(k, "k", elt, dev, kv_shape)
+    v_ptr, v_st = _tokens3(v, "v", elt, dev, kv_shape)
+    kc, vc, ks, vs = _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, h_kv, dev)
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.numel() != axes * n_tokens:
+        raise ValueError("positions must be [num_axes, n_tokens]")
+    _shape(slot_mapping, "slot_mapping", (n_tokens,))
+    if turns.dim() != 1:
+        raise ValueError("turns must be [rotary_dim / 2]")
+    half = turns.shape[0]
+    _shape(pair_axis, "pair_axis", (half,))
+    args = (_ptr(positions, "positions", torch.int32, dev),
+            _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
+            _ptr(turns, "turns", torch.int64, dev), _ptr(pair_axis, "pair_axis", torch.int32, dev))
     if n_tokens == 0:
         return q_out
-    _check("pa_rope_append", load().pa_rope_append(
-        o_ptr, q_ptr, k_ptr, v_ptr, kc, vc, _cuda(positions, "positions", torch.int32),
-        _cuda(slot_mapping, "slot_mapping", torch.int64), _cuda(turns, "turns", torch.int64),
-        _cuda(pair_axis, "pair_axis", torch.int32), n_tokens, h_q, h_kv, head_dim, 2 * half, axes,
-        1 if interleaved else 0, o_st, q_st, k_st, v_st, block_size, num_blocks, dt,
-        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
-        _stream(stream)))
+    st = (_lib or load()).pa_rope_append(
+        o_ptr, q_ptr, k_ptr, v_ptr, kc, vc, *args, n_tokens, h_q, h_kv, head_dim, 2 * half, axes,
+        interleaved, o_st, q_st, k_st, v_st, block_size, num_blocks, dt, ks, vs,
+        _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_rope_append", st)
     return q_out
 
 
@@ -608,47 +644,35 @@ def pa_decode_scored(out: torch.Tensor, scores: torch.Tensor, q: torch.Tensor,
                      v_scale: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Paged attention that also adds every cached row's attention weight to scores
     (and notes the positions of this step's rows in row_pos).  FP8 caches with scales."""
+    dev = _device_of(q)
     num_blocks, h_kv, block_size, head_dim, num_seqs, h_q, maxb = _decode_dims(
         q, k_cache, block_tables, context_lens, q_len)
-    dev = q.get_device()
-    _here(dev)
-    _same_device(dev, out, scores, k_cache, v_cache, block_tables, context_lens, workspace, row_pos,
-                 seq_lens, k_scale, v_scale)
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must match q")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("v_cache must match k_cache")
+    elt = q.dtype
+    dt = _elt(q, "q")
+    _shape(out, "out", q.shape)
     ledger = (num_seqs, h_kv, maxb * block_size)
-    if scores.shape != ledger or (row_pos is not None and row_pos.shape != ledger):
-        raise ValueError("scores and row_pos must be [num_seqs, num_kv_heads, "
-                         "max_blocks_per_seq * block_size]")
+    _shape(scores, "scores", ledger)
     if (row_pos is None) != (seq_lens is None):
         raise ValueError("give both row_pos and seq_lens, or neither")
-    if seq_lens is not None and seq_lens.shape != (num_seqs,):
-        raise ValueError("seq_lens must be [num_seqs]")
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("give both k_scale and v_scale, or neither")
-    if k_scale is None:
-        if k_cache.dtype != q.dtype:
-            raise ValueError("q must have the cache dtype")
-        kc, vc = _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache")
-    else:
-        kc, vc = _fp8_cache(k_cache, "k_cache"), _fp8_cache(v_cache, "v_cache")
-        if k_scale.shape != (h_kv,) or v_scale.shape != (h_kv,):
-            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
+    rp = sl = None
+    if row_pos is not None:
+        _shape(row_pos, "row_pos", ledger)
+        _shape(seq_lens, "seq_lens", (num_seqs,))
+        rp, sl = _ptr(row_pos, "row_pos", torch.int32, dev), _ptr(seq_lens, "seq_lens", torch.int32, dev)
+    kc, vc, ks, vs = _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, h_kv, dev)
     if workspace is None:
         nbytes = pa_decode_scored_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits, maxb,
                                                  block_size)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _check("pa_decode_scored", load().pa_decode_scored(
-        _cuda(out, "out"), _cuda(scores, "scores", torch.float32),
-        _opt(row_pos, "row_pos", torch.int32), _cuda(q, "q"), kc, vc,
-        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
-        _cuda(block_tables, "block_tables", torch.int32),
-        _cuda(context_lens, "context_lens", torch.int32), _opt(seq_lens, "seq_lens", torch.int32),
-        num_seqs, h_q, h_kv, head_dim, block_size, float(scale), maxb, num_blocks, q_len,
-        _elt(q, "q"), num_splits, _cuda(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    st = (_lib or load()).pa_decode_scored(
+        _ptr(out, "out", elt, dev), _ptr(scores, "scores", torch.float32, dev), rp,
+        _ptr(q, "q", elt, dev), kc, vc, ks, vs, _ptr(block_tables, "block_tables", torch.int32, dev),
+        _ptr(context_lens, "context_lens", torch.int32, dev), sl, num_seqs, h_q, h_kv, head_dim,
+        block_size, scale, maxb, num_blocks, q_len, dt, num_splits,
+        _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
+        _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_decode_scored", st)
     return out
 
 
@@ -666,47 +690,64 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Tensor,
     """Shorten every sequence longer than ``budget`` rows to it, each KV head keeping its
     first ``sinks`` and last ``recent`` positions and its highest scores.  The ledgers are
     updated in place unless both outputs are given.  Returns the new context lengths."""
+    dev = _device_of(k_cache)
     num_blocks, h_kv, block_size, head_dim = _cache_dims(k_cache)
-    dev = k_cache.get_device()
-    _here(dev)
-    _same_device(dev, v_cache, scores, row_pos, block_tables, context_lens, seq_lens, scores_out,
-                 row_pos_out, new_lens, workspace)
-    num_seqs = int(context_lens.shape[0])
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("v_cache must match k_cache")
-    if k_cache.dtype not in _DTYPE and k_cache.dtype not in _FP8_CACHE:
-        raise TypeError(f"k_cache must be 16-bit or hold e4m3 codes, got {k_cache.dtype}")
-    if block_tables.dim() != 2 or int(block_tables.shape[0]) != num_seqs:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    maxb = int(block_tables.shape[1])
+    elt = k_cache.dtype
+    if elt not in _DTYPE and elt not in _FP8_CACHE:
+        raise TypeError(f"k_cache must be 16-bit or hold e4m3 codes, got {elt}")
+    _shape(v_cache, "v_cache", k_cache.shape)
+    if block_tables.dim() != 2 or context_lens.dim() != 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq], context_lens [num_seqs]")
+    num_seqs, maxb = block_tables.shape
+    per_seq, ledger = (num_seqs,), (num_seqs, h_kv, maxb * block_size)
+    _shape(context_lens, "context_lens", per_seq)
+    _shape(seq_lens, "seq_lens", per_seq)
+    _shape(scores, "scores", ledger)
+    _shape(row_pos, "row_pos", ledger)
+    sc, rp = _ptr(scores, "scores", torch.float32, dev), _ptr(row_pos, "row_pos", torch.int32, dev)
+    so, po = sc, rp
     if (scores_out is None) != (row_pos_out is None):
         raise ValueError("give both scores_out and row_pos_out, or neither")
-    if scores_out is None:
-        scores_out, row_pos_out = scores, row_pos
-    for t, nm in ((scores, "scores"), (row_pos, "row_pos"), (scores_out, "scores_out"),
-                  (row_pos_out, "row_pos_out")):
-        if t.shape != (num_seqs, h_kv, maxb * block_size):
-            raise ValueError(f"{nm} must be [num_seqs, num_kv_heads, max_blocks_per_seq * block_size]")
-    if seq_lens.shape != (num_seqs,):
-        raise ValueError("seq_lens must be [num_seqs]")
+    if scores_out is not None:
+        _shape(scores_out, "scores_out", ledger)
+        _shape(row_pos_out, "row_pos_out", ledger)
+        so = _ptr(scores_out, "scores_out", torch.float32, dev)
+        po = _ptr(row_pos_out, "row_pos_out", torch.int32, dev)
     if new_lens is None:
         new_lens = torch.empty_like(context_lens)
-    elif new_lens.shape != (num_seqs,):
-        raise ValueError("new_lens must be [num_seqs]")
+    _shape(new_lens, "new_lens", per_seq)
     if workspace is None:
         nbytes = pa_evict_workspace_size(num_seqs, h_kv, budget)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=k_cache.device)
-    _check("pa_evict", load().pa_evict(
-        _cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache"),
-        _cuda(scores_out, "scores_out", torch.float32),
-        _cuda(row_pos_out, "row_pos_out", torch.int32), _cuda(new_lens, "new_lens", torch.int32),
-        _cuda(scores, "scores", torch.float32), _cuda(row_pos, "row_pos", torch.int32),
-        _cuda(block_tables, "block_tables", torch.int32),
-        _cuda(context_lens, "context_lens", torch.int32), _cuda(seq_lens, "seq_lens", torch.int32),
-        num_seqs, h_kv, head_dim, block_size, maxb, num_blocks, budget, sinks, recent,
-        k_cache.element_size(), _cuda(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    st = (_lib or load()).pa_evict(
+        _ptr(k_cache, "k_cache", elt, dev), _ptr(v_cache, "v_cache", elt, dev), so, po,
+        _ptr(new_lens, "new_lens", torch.int32, dev), sc, rp,
+        _ptr(block_tables, "block_tables", torch.int32, dev),
+        _ptr(context_lens, "context_lens", torch.int32, dev),
+        _ptr(seq_lens, "seq_lens", torch.int32, dev), num_seqs, h_kv, head_dim, block_size, maxb,
+        num_blocks, budget, sinks, recent, 2 if elt in _DTYPE else 1,
+        _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
+        _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_evict", st)
     return new_lens
+
+
+def _prob_rows(t, name: str, n: int, r: int, dev: int) -> tuple[int, int]:
+    """Pointer and row stride of fp32 [n, r, vocab], rows dense and evenly spaced (a
+    slice of a padded vocabulary is fine)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.get_device() != dev:
+        raise TypeError(f"{name} must be a float32 tensor on cuda:{dev}")
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != r:
+        raise ValueError(f"{name} must be [{n}, {r}, vocab]")
+    vocab = t.shape[2]
+    if t.is_contiguous():
+        return t.data_ptr(), vocab
+    s0, s1, s2 = t.stride()
+    row = s1 if r > 1 else s0 if n > 1 else vocab
+    if (vocab > 1 and s2 != 1) or (n > 1 and s0 != r * row):
+        raise ValueError(f"{name}: rows must be dense and evenly spaced")
+    return t.data_ptr(), row
 
 
 def pa_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
@@ -723,53 +764,45 @@ def pa_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | Non
     wider vocabulary).  Returns (out_tokens, num_accepted, new_lens or None): new_lens
     is made when context_lens is given.
     """
+    dev = _device_of(target_probs)
     if draft_tokens.dim() != 2:
         raise ValueError("draft_tokens must be [num_seqs, max_draft]")
-    n, k = (int(x) for x in draft_tokens.shape)
-    dev = target_probs.get_device()
-    _here(dev)
-    _same_device(dev, draft_probs, draft_tokens, accept_u, sample_u, draft_lens, context_lens,
-                 out_tokens, num_accepted, new_lens)
-
-    def rows(t, name, r):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
-            raise TypeError(f"{name} must be a float32 CUDA tensor")
-        if t.dim() != 3 or t.shape[0] != n or t.shape[1] != r:
-            raise ValueError(f"{name} must be [num_seqs, {r}, vocab]")
-        st = t.stride(1) if r > 1 or n == 1 else t.stride(0)
-        if (t.shape[2] > 1 and t.stride(2) != 1) or (n > 1 and t.stride(0) != r * st) or \
-                (r > 1 and t.stride(1) != st):
-            raise ValueError(f"{name}: rows must be dense and evenly spaced")
-        return t.data_ptr(), max(st, int(t.shape[2])) if r * n == 1 else st
-
-    p_ptr, p_st = rows(target_probs, "target_probs", k + 1)
-    vocab = int(target_probs.shape[2])
+    n, k = draft_tokens.shape
+    i32, per_seq = torch.int32, (n,)
+    p_ptr, p_st = _prob_rows(target_probs, "target_probs", n, k + 1, dev)
+    vocab = target_probs.shape[2]
     q_ptr, q_st = None, 0
     if draft_probs is not None:
-        q_ptr, q_st = rows(draft_probs, "draft_probs", k)
+        q_ptr, q_st = _prob_rows(draft_probs, "draft_probs", n, k, dev)
         if draft_probs.shape[2] != vocab:
             raise ValueError("draft_probs must have target_probs' vocabulary")
-    if accept_u.shape != (n, k) or sample_u.shape != (n,):
-        raise ValueError("accept_u must be [num_seqs, max_draft], sample_u [num_seqs]")
-    for t, nm in ((draft_lens, "draft_lens"), (context_lens, "context_lens"),
-                  (num_accepted, "num_accepted"), (new_lens, "new_lens")):
-        if t is not None and t.shape != (n,):
-            raise ValueError(f"{nm} must be [num_seqs]")
-    if new_lens is not None and context_lens is None:
-        raise ValueError("new_lens needs context_lens")
+    _shape(accept_u, "accept_u", (n, k))
+    _shape(sample_u, "sample_u", per_seq)
+    dl = cl = nl = None
+    if draft_lens is not None:
+        _shape(draft_lens, "draft_lens", per_seq)
+        dl = _ptr(draft_lens, "draft_lens", i32, dev)
+    if context_lens is not None:
+        _shape(context_lens, "context_lens", per_seq)
+        cl = _ptr(context_lens, "context_lens", i32, dev)
+        if new_lens is None:
+            new_lens = torch.empty_like(context_lens)
+    if new_lens is not None:
+        if context_lens is None:
+            raise ValueError("new_lens needs context_lens")
+        _shape(new_lens, "new_lens", per_seq)
+        nl = _ptr(new_lens, "new_lens", i32, dev)
     if out_tokens is None:
-        out_tokens = torch.empty(n, k + 1, dtype=torch.int32, device=target_probs.device)
-    elif out_tokens.shape != (n, k + 1):
-        raise ValueError("out_tokens must be [num_seqs, max_draft + 1]")
+        out_tokens = torch.empty(n, k + 1, dtype=i32, device=target_probs.device)
+    _shape(out_tokens, "out_tokens", (n, k + 1))
     if num_accepted is None:
-        num_accepted = torch.empty(n, dtype=torch.int32, device=target_probs.device)
-    if context_lens is not None and new_lens is None:
-        new_lens = torch.empty_like(context_lens)
-    _check("pa_verify_drafts", load().pa_verify_drafts(
-        _cuda(out_tokens, "out_tokens", torch.int32),
-        _cuda(num_accepted, "num_accepted", torch.int32), _opt(new_lens, "new_lens", torch.int32),
-        _opt(context_lens, "context_lens", torch.int32), p_ptr, q_ptr,
-        _cuda(draft_tokens, "draft_tokens", torch.int32),
-        _opt(draft_lens, "draft_lens", torch.int32), _cuda(accept_u, "accept_u", torch.float32),
-        _cuda(sample_u, "sample_u", torch.float32), n, k, vocab, p_st, q_st, _stream(stream)))
+        num_accepted = torch.empty(n, dtype=i32, device=target_probs.device)
+    _shape(num_accepted, "num_accepted", per_seq)
+    st = (_lib or load()).pa_verify_drafts(
+        _ptr(out_tokens, "out_tokens", i32, dev), _ptr(num_accepted, "num_accepted", i32, dev), nl, cl,
+        p_ptr, q_ptr, _ptr(draft_tokens, "draft_tokens", i32, dev), dl,
+        _ptr(accept_u, "accept_u", torch.float32, dev), _ptr(sample_u, "sample_u", torch.float32, dev),
+        n, k, vocab, p_st, q_st, _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_verify_drafts", st)
     return out_tokens, num_accepted, new_lens

@@ -333,15 +333,16 @@ pa_status make_map(CUtensorMap *map, const void *cache, pa_dtype dtype, int head
 }
 
 // Tensor map over q [tokens][num_q_heads][head_dim] as [head_dim, num_q_heads,
-// tokens], box = 64 columns x `group` heads x 128/group tokens: the 128 query rows
-// (token, head) of one KV head's row block, 128-byte swizzle, zero fill outside.
+// tokens], box = 64 columns x `heads` heads x `toks` tokens (a KV head's group x 128 /
+// group: the 128 query rows (token, head) of one row block), 128-byte swizzle, zero
+// fill outside.
 pa_status make_q_map(CUtensorMap *map, const void *q, pa_dtype dtype, int head_dim,
-                     int num_q_heads, int64_t tokens, int group) {
+                     int num_q_heads, int64_t tokens, int heads, int toks) {
   std::call_once(g_encode_once, load_encode);
   if (g_encode == nullptr) return PA_ERR_CUDA;
   cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads, (cuuint64_t)tokens};
   cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_q_heads * head_dim * 2};
-  cuuint32_t box[3] = {64u, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+  cuuint32_t box[3] = {64u, (cuuint32_t)heads, (cuuint32_t)toks};
   cuuint32_t elem_strides[3] = {1, 1, 1};
   CUresult r = g_encode(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         3, const_cast<void *>(q), dims, strides, box, elem_strides,
@@ -547,7 +548,8 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
     // (over an FP8 cache a bf16 q is converted to fp16 by the softmax threads)
     a.q_tma = (128 % a.group == 0 && !(fp8 && dtype == PA_BF16)) ? 1 : 0;
     if (a.q_tma) {
-      st = make_q_map(&qmap, q, dtype, head_dim, num_q_heads, (int64_t)num_seqs * q_len, a.group);
+      st = make_q_map(&qmap, q, dtype, head_dim, num_q_heads, (int64_t)num_seqs * q_len, a.group,
+                      128 / a.group);
       if (st != PA_OK) return st;
     } else {
       qmap = kmap;  // unused
@@ -1030,10 +1032,32 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
   a.block_size = block_size;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
+  a.err = error_word();
+  if (a.err == nullptr) return PA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = many ? pa::launch_mass(a, head_dim, dtype == PA_FP16, k_scale != nullptr, s)
-                             : pa::launch_ledger(a, s);
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (!many) return pa::launch_ledger(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  int heads = 0, toks = 0;
+  pa::mass_q_box(a.group, &heads, &toks);
+  // (a launch takes a bounded number of sequences)
+  const int step = pa::mass_max_seqs();
+  for (int i = 0; i < num_seqs; i += step) {
+    pa::LedgerArgs b = a;
+    b.num_seqs = std::min(step, num_seqs - i);
+    const size_t led = (size_t)i * num_kv_heads * a.max_rows, row = (size_t)i * q_len * num_q_heads;
+    b.scores += led;
+    if (row_pos) b.row_pos += led, b.seq_lens += i;
+    b.context_lens += i;
+    b.block_tables += (size_t)i * max_blocks_per_seq;
+    b.ws_m += row;
+    b.ws_l += row;
+    b.q = static_cast<const uint16_t *>(q) + row * head_dim;
+    CUtensorMap qmap;
+    st = make_q_map(&qmap, b.q, dtype, head_dim, num_q_heads, (int64_t)b.num_seqs * q_len, heads, toks);
+    if (st != PA_OK) return st;
+    if (pa::launch_mass(qmap, b, head_dim, dtype == PA_FP16, k_scale != nullptr, s) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
+  return PA_OK;
 }
 
 }  // extern "C"

@@ -9,15 +9,18 @@
 //   * up to 16 query tokens: the decode pass leaves its scores in the workspace
 //     (ledger_kernel reads them back: 4 bytes per row and head against the 2 head_dim
 //     16-bit values per row of reading K again and V);
-//   * more: the scores would outgrow the cache, so mass_kernel computes them again
-//     from K and q.
+//   * more: the scores would outgrow the cache, so mass_tc_kernel (pa_mass_tc.cuh)
+//     computes them again from K and q.
 // Rows that this step appended (the last q_len) start their scores here, and their
 // positions are noted; a row's score is written by one thread, so the sums have one
 // order.
 #include <cuda_runtime.h>
 
-#include "pa_decode.cuh"
+#include <algorithm>
+#include <atomic>
+
 #include "pa_launch.h"
+#include "pa_mass_tc.cuh"
 #include "pa_scored.h"
 
 namespace pa {
@@ -78,95 +81,45 @@ __global__ void __launch_bounds__(kLedgerThreads) ledger_kernel(const LedgerArgs
   if (t < L) ledger_write(a, seq, (int64_t)unit * a.max_rows + t, t, Lc, share);
 }
 
-// Element (two of them) of a cached row as the MMA operand of type T: 16-bit as it
-// is, e4m3 widened (exact in fp16 and bf16).
-template <typename T, bool KV8>
-__device__ __forceinline__ uint32_t load_pair(const void *cache, int64_t at) {
-  if constexpr (KV8) {
-    const uint32_t h2 = e4m3x2_to_f16x2(__ldg(reinterpret_cast<const uint16_t *>(
-        static_cast<const uint8_t *>(cache) + at)));
-    const float2 f = Elt<__half>::to_f2(h2);
-    return Elt<T>::from_f2(f.x, f.y);
-  } else {
-    return __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(cache) + at));
-  }
-}
-
-// Many query rows: S^T = K q^T again, 16 cached rows a warp (the MMA's M, its K
-// fragments in registers) by 8 query rows at a time.
 template <typename T, int D, bool KV8>
-__global__ void __launch_bounds__(256) mass_kernel(const LedgerArgs a) {
-  constexpr int KS = D / 16;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  const int groups = (a.max_tiles + 7) / 8;
-  const int unit = blockIdx.x / groups, tile = (blockIdx.x % groups) * 8 + warp;
-  const int seq = unit / a.num_kv_heads, kvh = unit % a.num_kv_heads;
-  const int Lc = max(0, __ldg(a.context_lens + seq)), L = min(Lc, a.max_rows);
-  const int t0 = tile * kTileTokens;
-  if (t0 >= L) return;
-  const int heads = a.group * a.num_kv_heads;
-  uint32_t ka[KS][4];
-#pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    const int t = t0 + g + 8 * hh;
-    int64_t row = -1;
-    if (t < L) {
-      const int id = __ldg(a.block_tables + (size_t)seq * a.max_blocks_per_seq + t / a.block_size);
-      if (id >= 0 && id < a.num_blocks)  // (a bad id reads as zeros; the attention pass reports it)
-        row = (((int64_t)id * a.num_kv_heads + kvh) * a.block_size + t % a.block_size) * D;
-    }
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      ka[ks][hh] = row < 0 ? 0u : load_pair<T, KV8>(a.k_cache, row + ks * 16 + 2 * c);
-      ka[ks][hh + 2] = row < 0 ? 0u : load_pair<T, KV8>(a.k_cache, row + ks * 16 + 2 * c + 8);
-    }
+cudaError_t launch_mass_t(const CUtensorMap &qmap, const LedgerArgs &a, cudaStream_t st) {
+  auto kern = mass_tc_kernel<T, D, KV8>;
+  static std::atomic<unsigned long long> opted{0};  // bit per device: smem opt-in done
+  static std::atomic<int> sm_count[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!(opted.load(std::memory_order_acquire) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             MassLayout<D>::smem_bytes(kMassMaxSeqs));
+    if (e != cudaSuccess) return e;
+    int sms = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    sm_count[dev].store(sms, std::memory_order_relaxed);
+    opted.fetch_or(1ull << dev, std::memory_order_acq_rel);
   }
-  const float scale = a.scale_log2 * (KV8 ? __ldg(a.k_scale + kvh) : 1.f);
-  // query tokens before u0 see none of these rows
-  const int u0 = max(0, t0 - (Lc - a.q_len));
-  float share[2] = {0.f, 0.f};
-  for (int r0 = u0 * a.group; r0 < a.rows; r0 += 8) {
-    const int rq = r0 + g;  // the query row whose elements this lane loads
-    const int uq = rq / a.group, hq = kvh * a.group + rq % a.group;
-    const T *q = static_cast<const T *>(a.q) + ((size_t)(seq * a.q_len + uq) * heads + hq) * D;
-    float sc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      uint32_t b0 = 0u, b1 = 0u;
-      if (rq < a.rows) {
-        b0 = __ldg(reinterpret_cast<const uint32_t *>(q + ks * 16 + 2 * c));
-        b1 = __ldg(reinterpret_cast<const uint32_t *>(q + ks * 16 + 2 * c + 8));
-      }
-      Elt<T>::mma16816(sc, ka[ks], b0, b1);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 2 * c + (i & 1), t = t0 + g + 8 * (i >> 1);
-      if (r >= a.rows) continue;
-      const int u = r / a.group;
-      if (t > Lc - a.q_len + u) continue;
-      const size_t row = (size_t)(seq * a.q_len + u) * heads + kvh * a.group + r % a.group;
-      const float l = a.ws_l[row];
-      share[i >> 1] += l > 0.f ? fast_exp2(sc[i] * scale - a.ws_m[row]) / l : 0.f;
-    }
-  }
-#pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    share[hh] += __shfl_xor_sync(0xffffffffu, share[hh], 1);
-    share[hh] += __shfl_xor_sync(0xffffffffu, share[hh], 2);
-    const int t = t0 + g + 8 * hh;
-    if (c == 0 && t < L) ledger_write(a, seq, (int64_t)unit * a.max_rows + t, t, Lc, share[hh]);
-  }
+  const long long most = (long long)a.num_seqs * a.num_kv_heads * ((a.max_rows + kMassUnit - 1) / kMassUnit);
+  if (most > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(most, sm_count[dev].load(std::memory_order_relaxed)), 1, 1);
+  cfg.blockDim = dim3(kMassThreads, 1, 1);
+  cfg.dynamicSmemBytes = MassLayout<D>::smem_bytes(a.num_seqs);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, qmap, a);
 }
 
 template <typename T>
-cudaError_t mass_t(const LedgerArgs &a, int head_dim, bool kv8, unsigned blocks, cudaStream_t s) {
-  if (kv8) return launch_dependent(mass_kernel<T, 128, true>, blocks, 256, s, a);
-  if (head_dim == 128) return launch_dependent(mass_kernel<T, 128, false>, blocks, 256, s, a);
-  return launch_dependent(mass_kernel<T, 64, false>, blocks, 256, s, a);
+cudaError_t mass_t(const CUtensorMap &qmap, const LedgerArgs &a, int head_dim, bool kv8, cudaStream_t s) {
+  if (kv8) return launch_mass_t<T, 128, true>(qmap, a, s);
+  if (head_dim == 128) return launch_mass_t<T, 128, false>(qmap, a, s);
+  return launch_mass_t<T, 64, false>(qmap, a, s);
 }
 
 }  // namespace
@@ -178,11 +131,18 @@ cudaError_t launch_ledger(const LedgerArgs &a, cudaStream_t s) {
   return launch_dependent(ledger_kernel, (unsigned)blocks, kLedgerThreads, s, a);
 }
 
-cudaError_t launch_mass(const LedgerArgs &a, int head_dim, bool fp16, bool kv8, cudaStream_t s) {
-  const long long blocks = (long long)a.num_seqs * a.num_kv_heads * ((a.max_tiles + 7) / 8);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return fp16 ? mass_t<__half>(a, head_dim, kv8, (unsigned)blocks, s)
-              : mass_t<__nv_bfloat16>(a, head_dim, kv8, (unsigned)blocks, s);
+cudaError_t launch_mass(const CUtensorMap &qmap, const LedgerArgs &a, int head_dim, bool fp16,
+                        bool kv8, cudaStream_t s) {
+  return fp16 ? mass_t<__half>(qmap, a, head_dim, kv8, s)
+              : mass_t<__nv_bfloat16>(qmap, a, head_dim, kv8, s);
 }
+
+void mass_q_box(int group, int *heads, int *tokens) {
+  const MassGeo g = mass_geo(group);
+  *heads = g.hb;
+  *tokens = g.tb;
+}
+
+int mass_max_seqs() { return kMassMaxSeqs; }
 
 }  // namespace pa

@@ -24,11 +24,17 @@ struct LedgerArgs {
   float scale_log2;
   int num_seqs, num_kv_heads, group, q_len, rows, splits;  // rows = group * q_len
   int max_rows, max_tiles, block_size, max_blocks_per_seq, num_blocks;
+  unsigned *err;
 };
 
 cudaError_t launch_ledger(const LedgerArgs &args, cudaStream_t stream);
-cudaError_t launch_mass(const LedgerArgs &args, int head_dim, bool fp16, bool kv8,
-                        cudaStream_t stream);
+// Many query rows: the scores again from K and q on the tensor cores.  qmap: tensor map
+// over q with a box of 64 columns x the heads x the tokens that mass_q_box names.  At
+// most mass_max_seqs() sequences per launch.
+cudaError_t launch_mass(const CUtensorMap &qmap, const LedgerArgs &args, int head_dim, bool fp16,
+                        bool kv8, cudaStream_t stream);
+void mass_q_box(int group, int *heads, int *tokens);
+int mass_max_seqs();
 
 // The decode kernels with their scores written to args.raw_scores; the single pass
 // also writes its statistics.

@@ -137,6 +137,9 @@ MANY = [
     ([513, 129], 100, 4, 2, 128, 8, "fp16", False),
     ([700], 300, 5, 1, 128, 32, "bf16", False),
     ([257, 64], 64, 3, 3, 64, 8, "bf16", False),
+    ([300, 20], 17, 135, 1, 64, 16, "bf16", False),        # more heads than a block of rows
+    ([600, 511], 150, 8, 8, 128, 16, "fp16", False),
+    ([520, 256, 257], 90, 7, 1, 128, 16, "bf16", False),
     ([200, 50], 33, 6, 2, 128, 16, "fp16", True),
     ([150, 290], 129, 4, 1, 128, 32, "bf16", True),
 ]
@@ -155,6 +158,13 @@ def test_many_query_tokens(pa, shape):
     c = make(12, *shape)
     check(c, run(pa, c), shape[6], str(shape))
     assert pa.pa_device_error() == 0
+
+
+def test_many_sequences(pa):
+    """More sequences than one launch of the many-row pass takes."""
+    lens = [17 + i % 3 for i in range(4099)]
+    c = make(22, lens, 17, 1, 1, 64, 32, "fp16", False, spare=0)
+    check(c, run(pa, c), "fp16")
 
 
 def test_agrees_with_the_plain_calls(pa):
