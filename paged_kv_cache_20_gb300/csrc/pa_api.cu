@@ -408,9 +408,10 @@ struct Placement {
   const WsLayout *prior_lay = nullptr;
   int prior_splits = 0;
   // scored attention: every score (decode kernel; the single pass writes its statistics
-  // to m and l), or the rows' statistics alone (many-row kernel; m and l)
+  // to m and l), or the rows' statistics alone (many-row kernel)
   float *raw_scores = nullptr;
   float *stat_m = nullptr, *stat_l = nullptr;
+  float *row_nlse = nullptr;
 };
 
 // CTAs of a cascade's shared-prefix pass: a share of the SMs, so that the tail
@@ -489,9 +490,9 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
   } else {
     a.prior_acc = a.prior_m = a.prior_l = nullptr;
   }
-  const bool scored = place.raw_scores != nullptr || place.stat_m != nullptr;
+  const bool scored = place.raw_scores != nullptr || place.row_nlse != nullptr;
   a.raw_scores = place.raw_scores;
-  a.ws_lx = place.stat_l;
+  a.row_nlse = place.row_nlse;
   if (place.stat_m != nullptr) {
     a.ws_m = place.stat_m;
     a.ws_l = place.stat_l;
@@ -927,8 +928,9 @@ PA_API pa_status pa_device_error(void *stream, int clear) {
   return PA_OK;
 }
 
-// Workspace of pa_decode_scored: the split-KV sections when num_splits > 1, else the
-// statistics alone (m, l per row); then, up to 16 query tokens, every score.
+// Workspace of pa_decode_scored up to 16 query tokens: the split-KV sections when
+// num_splits > 1, else the statistics alone (m, l per row); then every score.  Above:
+// one statistic per row.
 struct ScoredLayout {
   WsLayout split;
   size_t m_off, l_off, raw_off, total;
@@ -947,7 +949,7 @@ static ScoredLayout scored_layout(int num_seqs, int num_q_heads, int q_len, int 
   } else {
     w.m_off = 0;
     w.l_off = align256(rows * sizeof(float));
-    w.raw_off = w.l_off + align256(rows * sizeof(float));
+    w.raw_off = w.l_off + (many ? 0 : align256(rows * sizeof(float)));
   }
   const size_t tiles = ((size_t)max_blocks_per_seq * block_size + pa::kTileTokens - 1) / pa::kTileTokens;
   w.total = w.raw_off + (many ? 0 : align256(rows * tiles * pa::kTileTokens * sizeof(float)));
@@ -992,7 +994,9 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
   Placement place;
   if (!many) place.raw_scores = reinterpret_cast<float *>(ws + lay.raw_off);
   const bool split = !many && num_splits > 1;
-  if (!split) {
+  if (many) {
+    place.row_nlse = reinterpret_cast<float *>(ws + lay.m_off);
+  } else if (!split) {
     place.stat_m = reinterpret_cast<float *>(ws + lay.m_off);
     place.stat_l = reinterpret_cast<float *>(ws + lay.l_off);
   }
@@ -1017,6 +1021,7 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
   a.raw_scores = place.raw_scores;
   a.ws_m = reinterpret_cast<const float *>(ws + lay.m_off);
   a.ws_l = reinterpret_cast<const float *>(ws + lay.l_off);
+  a.row_nlse = place.row_nlse;
   a.q = q;
   a.k_cache = k_cache;
   a.k_scale = k_scale;
@@ -1048,8 +1053,7 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
     if (row_pos) b.row_pos += led, b.seq_lens += i;
     b.context_lens += i;
     b.block_tables += (size_t)i * max_blocks_per_seq;
-    b.ws_m += row;
-    b.ws_l += row;
+    b.row_nlse += row;
     b.q = static_cast<const uint16_t *>(q) + row * head_dim;
     CUtensorMap qmap;
     st = make_q_map(&qmap, b.q, dtype, head_dim, num_q_heads, (int64_t)b.num_seqs * q_len, heads, toks);

@@ -109,8 +109,8 @@ struct DecodeArgs {
   // -inf where masked: [num_seqs][num_kv_heads][max_tiles][rows][16 tokens].  The
   // single pass then also writes its statistics m and l (to ws_m, ws_l).
   float *raw_scores;
-  // Scored prefill: the row sums of the unrounded weights [num_seqs][q_len * num_q_heads]
-  float *ws_lx;
+  // Scored prefill: -(m + log2 l) of every query row [num_seqs][num_kv_heads][rows]
+  float *row_nlse;
 };
 
 // Where a path puts the scores of one tile (row r, token t at p[16 r + t]) for a

@@ -318,7 +318,7 @@ __device__ __forceinline__ void tc_widen_e4m3_rows(uint32_t st, int r0, int rows
 
 // BS16: the cache's blocks are 16 tokens (fixed at compile time); otherwise the
 // block size (8 or 32) is read from the arguments.
-// STATS (single pass only): also write each row's maximum and the sum of its weights
+// STATS (single pass only): also write each row's -(m + log2 l), l the sum of its weights
 // before their rounding for P V, for a second pass that needs the weights themselves.
 template <typename T, int D, int NK, int NV, bool PARTIAL, bool KV8, bool BS16, bool STATS = false>
 __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
@@ -1056,6 +1056,10 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
       }
 
       // ---- the unit's results: deferred to the next unit's first chunk ----
+      auto stat_row = [&]() -> size_t {  // the KV head's rows together
+        return ((size_t)cu.rseq * a.num_kv_heads + cu.kvh) * a.rows + (size_t)cu.ru * a.group +
+               (cu.rh - cu.kvh * a.group);
+      };
       long long roff = -1;
       if (cu.rvalid)
         roff = PARTIAL ? (long long)(((size_t)cu.rseq * a.ws_splits + a.ws_split0 + cu.split) *
@@ -1066,10 +1070,8 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         l = exchange(l, false);  // the row sum over both column halves
         if constexpr (kExactSum) lx = exchange(lx, false);
         if (!ok) break;
-        if (STATS && hc == 0 && roff >= 0) {
-          a.ws_m[roff] = m_run;
-          a.ws_lx[roff] = kExactSum ? lx : l;
-        }
+        if (STATS && hc == 0 && roff >= 0)
+          a.row_nlse[stat_row()] = -(m_run + log2f(kExactSum ? lx : l));
         pend = true;
         pend_gl = g + cu.nch - 1;
         pend_sc = PARTIAL ? l : (l > 0.f ? vs_u / l : 0.f);
@@ -1078,10 +1080,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         pend_roff = roff;
       } else {
         // no position in this unit's partition: zeros (empty statistics)
-        if (STATS && hc == 0 && roff >= 0) {
-          a.ws_m[roff] = -INFINITY;
-          a.ws_lx[roff] = 0.f;
-        }
+        if (STATS && hc == 0 && roff >= 0) a.row_nlse[stat_row()] = 0.f;  // (sees nothing)
         if (pend) {
           if (!epilogue(true, pend_gl, pend_sc, pend_m, pend_roff, pend_vs)) {
             ok = false;

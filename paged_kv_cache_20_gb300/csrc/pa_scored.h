@@ -18,7 +18,9 @@ struct LedgerArgs {
   const int32_t *context_lens, *block_tables;
   const float *raw_scores;    // [num_seqs][num_kv_heads][max_tiles][rows][16]
   const float *ws_m, *ws_l;   // [num_seqs][splits][q_len * num_q_heads]
-  // the scores again from K and q (more than 16 query tokens)
+  // the scores again from K and q (more than 16 query tokens), with the rows'
+  // -(m + log2 l) [num_seqs][num_kv_heads][rows]
+  const float *row_nlse;
   const void *q, *k_cache;
   const float *k_scale;
   float scale_log2;
@@ -44,7 +46,7 @@ cudaError_t launch_decode_scored_fp16(const CUtensorMap &kmap, const CUtensorMap
 cudaError_t launch_decode_scored_bf16(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                       const DecodeArgs &args, int head_dim, bool kv8, bool partial,
                                       int units, cudaStream_t stream);
-// The many-row kernel, single pass, writing its rows' statistics (ws_m, ws_lx).
+// The many-row kernel, single pass, writing its rows' statistics (row_nlse).
 cudaError_t launch_prefill_stats(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                  const CUtensorMap &qmap, const DecodeArgs &args, int head_dim,
                                  bool fp16, bool kv8, cudaStream_t stream);

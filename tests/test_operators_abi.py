@@ -63,7 +63,7 @@ def test_decode_scored_workspace(lib):  # noqa: F811
     rows = 3 * 2 * 8
     assert size(3, 8, 2, 128, 1, 5, 8) == 2 * al(rows * 4) + al(rows * 48 * 4)  # 40 rows: 3 tiles
     assert size(3, 8, 2, 128, 4, 5, 8) == lib.pa_decode_workspace_size(3, 8, 2, 128, 4) + al(rows * 48 * 4)
-    assert size(3, 8, 17, 128, 4, 5, 8) == 2 * al(3 * 17 * 8 * 4)  # many rows: statistics only
+    assert size(3, 8, 17, 128, 4, 5, 8) == al(3 * 17 * 8 * 4)  # many rows: a statistic each
     for bad in ((0, 8, 2, 128, 1, 5, 8), (3, 8, 2, 128, 0, 5, 8), (3, 8, 2, 128, 1, 0, 8)):
         assert size(*bad) == 0
 
