@@ -10,14 +10,24 @@
 //
 // Keys.  A row's score as an unsigned integer whose order is the floats' order; NaN
 // below every number; a protected position above all.  Kept = the `budget` largest
-// (key, then lower row).  The budget-th largest key is found by a radix select, eight
-// bits at a time, over keys held in shared memory.
+// (key, then lower row).  Two ways to find them, by how many rows are over budget:
+//   * up to kFew (a serving step appends one row, or a few with drafts): that many
+//     times the smallest (key, then higher row) that is larger than the last one found;
+//   * more: the budget-th largest key by a radix select, eight bits at a time, then the
+//     rows in order.  (One row over 1024: 17.5 us by the radix select, 6.9 by the first.)
+// Keys are held in shared memory.
 //
 // Moves.  Attention does not depend on the order of cached rows (K rows carry their
 // rotation), so nothing is shifted: with m rows evicted below `budget`, exactly m kept
 // rows lie at or past it, and the i-th of these is copied into the i-th hole.  Sources
 // are never written and holes never read, so the copies need no order, and repeating
-// the call repeats the same copies.
+// the call repeats the same copies.  They are latency-bound one by one (302 us for 128
+// heads of 1800 rows): a warp works out 32 pairs at once, one per lane, and keeps eight
+// rows' loads in flight.
+//
+// A (sequence, KV head) is one thread block, or a cluster of them that shares its rows
+// when there are fewer than the GPU holds: counts and sums then meet through distributed
+// shared memory.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -28,10 +38,11 @@
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kKeyCap = 48 * 1024;  // keys held in shared memory (192 KiB)
+constexpr int kKeyCap = 44 * 1024;  // keys a CTA can hold in shared memory (176 KiB)
 constexpr uint32_t kProtected = 0xffffffffu;
+constexpr int kFew = 8;
+constexpr int kListCap = 512;  // moves a single CTA lists in shared memory
+constexpr int kMaxCluster = 8;
 
 struct EvictArgs {
   uint8_t *k_cache, *v_cache;
@@ -40,10 +51,10 @@ struct EvictArgs {
   float *scores_out;
   int32_t *row_pos_out, *new_lens;
   const int32_t *block_tables, *context_lens, *seq_lens;
-  int32_t *moves;  // workspace: (hole, source) pairs, list_cap per (sequence, head)
-  int num_kv_heads, block_size, max_blocks_per_seq, num_blocks, max_rows;
-  int budget, sinks, recent, list_cap, key_cap;
-  int row_chunks;  // 16-byte chunks of a cached row
+  int2 *moves;  // workspace: (hole, source) pairs, `budget` per (sequence, head)
+  int num_kv_heads, block_shift, max_blocks_per_seq, num_blocks, max_rows;
+  int budget, sinks, recent, key_cap;
+  int row_chunks;  // 16-byte chunks of a cached row: 8 or 16
   unsigned *err;
 };
 
@@ -54,78 +65,241 @@ __device__ __forceinline__ uint32_t key_of(float score, int pos, int sinks, int6
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Exclusive prefix of per-warp values x (all lanes of a warp hold the same x) over the
-// CTA's warps; *total = their sum.
-__device__ __forceinline__ int warps_before(int x, int *buf, int *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  if (lane == 0) buf[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
+__device__ __forceinline__ uint64_t warp_min(uint64_t x) {
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int y = buf[w];
-    before += w < warp ? y : 0;
-    all += y;
-  }
-  *total = all;
-  return before;
+  for (int o = 16; o > 0; o >>= 1) x = min(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
 
-// One CTA per (sequence, KV head).
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
+__device__ __forceinline__ uint64_t dsmem_ld_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// All threads of the cluster (or of the CTA that is one).
+__device__ __forceinline__ void group_sync(int csize) {
+  if (csize > 1)
+    pa::cluster_sync_all();
+  else
+    __syncthreads();
+}
+
+// Rows of a contiguous range: above the border key and equal to it, below the budget and
+// from it on.
+struct Counts {
+  int gt_lo, gt_hi, eq_lo, eq_hi, n_lo;
+  // with `t` equal rows before the range, of which `left` stay in all: holes and sources
+  __device__ __forceinline__ int kept_lo(int t, int left) const {
+    return gt_lo + min(eq_lo, max(0, left - t));
+  }
+  __device__ __forceinline__ int holes(int t, int left) const { return n_lo - kept_lo(t, left); }
+  __device__ __forceinline__ int sources(int t, int left) const {
+    return gt_hi + min(eq_hi, max(0, left - t - eq_lo));
+  }
+};
+
+// Copy the cached rows of cnt <= 32 pairs: lane l holds pair l's row indices (in rows of
+// the pool; rt < 0: nothing to copy).
+__device__ __forceinline__ void copy_rows(const EvictArgs &a, int64_t rt, int64_t rf, int cnt) {
+  const int lane = threadIdx.x & 31;
+  const int per = 2 * a.row_chunks;             // chunks of a pair, K then V
+  const int side = 32 / per;                    // pairs per step of the warp: 1 or 2
+  const int sub = lane / per, c = lane % per;
+  uint4 *cache = reinterpret_cast<uint4 *>(c < a.row_chunks ? a.k_cache : a.v_cache);
+  const int cc = c < a.row_chunks ? c : c - a.row_chunks;
+  constexpr int kUnroll = 8;
+  for (int j0 = 0; j0 < cnt; j0 += kUnroll * side) {
+    uint4 x[kUnroll];
+    int64_t to[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * side + sub;
+      const int64_t from = __shfl_sync(0xffffffffu, rf, j & 31);
+      to[u] = __shfl_sync(0xffffffffu, rt, j & 31);
+      if (j >= cnt) to[u] = -1;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (to[u] >= 0) x[u] = cache[from * a.row_chunks + cc];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (to[u] >= 0) cache[to[u] * a.row_chunks + cc] = x[u];
+  }
+}
+
+// (64 registers a thread: 32 warps per SM)
+template <int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a) {
+  constexpr int NW = NT / 32;
+  constexpr int kUnroll = 8;
   extern __shared__ uint32_t s_keys[];
-  __shared__ int hist[256];
-  __shared__ int s_warp[kWarps];
+  __shared__ int hist[4][256];
+  __shared__ Counts s_cnt[NW];        // by warp
+  __shared__ Counts s_pub;            // of this CTA, read by its peers
+  __shared__ uint64_t s_min[kFew][NW];
+  __shared__ uint64_t s_cta_min[kFew];
+  __shared__ int2 s_moves[kListCap];
   __shared__ int s_digit, s_left;
   pa::griddep_wait();
   pa::griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seq = blockIdx.x / a.num_kv_heads, head = blockIdx.x % a.num_kv_heads;
+  const int csize = (int)pa::cluster_nctarank(), crank = (int)pa::cluster_ctarank();
+  const int unit = blockIdx.x / csize;
+  const int seq = unit / a.num_kv_heads, head = unit % a.num_kv_heads;
   int L = max(0, __ldg(a.context_lens + seq));
+  const int64_t recent_from = (int64_t)__ldg(a.seq_lens + seq) - a.recent;
   if (L > a.max_rows) {  // context longer than its table
-    if (tid == 0 && head == 0) pa::record_error(a.err, pa::kErrCheck);
+    if (tid == 0 && head == 0 && crank == 0) pa::record_error(a.err, pa::kErrCheck);
     L = a.max_rows;
   }
-  if (tid == 0 && head == 0) a.new_lens[seq] = min(L, a.budget);
-  const int64_t led = ((int64_t)seq * a.num_kv_heads + head) * a.max_rows;
+  if (tid == 0 && head == 0 && crank == 0) a.new_lens[seq] = min(L, a.budget);
+  const int64_t led = (int64_t)unit * a.max_rows;
   const float *scores = a.scores + led;
   const int32_t *row_pos = a.row_pos + led;
   float *scores_out = a.scores_out + led;
   int32_t *row_pos_out = a.row_pos_out + led;
-  const bool in_place = a.scores == a.scores_out;
-  if (L <= a.budget) {
-    if (!in_place)
-      for (int r = tid; r < L; r += kThreads) {
-        scores_out[r] = scores[r];
-        row_pos_out[r] = row_pos[r];
+  const bool apart = a.scores != a.scores_out;
+  const int over = L - a.budget;  // rows to evict
+  if (over <= 0 && !apart) return;  // (all CTAs of the cluster)
+
+  // this CTA's rows [lo, hi), of which each warp takes a contiguous range [w0, w1).  Keys
+  // into shared memory; with ledgers apart, the rows below the budget are copied as they
+  // are (every evicted one of them is written again below).
+  const int slice = ((L + csize - 1) / csize + 31) & ~31;
+  const int lo = min(L, crank * slice), hi = min(L, lo + slice);
+  const int held = min(hi - lo, a.key_cap);
+  const int per = ((hi - lo + NW - 1) / NW + 31) & ~31;
+  const int w0 = min(hi, lo + warp * per), w1 = min(hi, w0 + per);
+  uint64_t least = ~0ull;
+  auto rank_of = [](uint32_t key, int r) -> uint64_t {  // smallest: evicted first
+    return ((uint64_t)key << 32) | (uint32_t)~r;
+  };
+  for (int i = tid; i < 4 * 256; i += NT) (&hist[0][0])[i] = 0;
+  for (int r0 = w0 + lane; r0 < w1; r0 += 32 * kUnroll) {
+    float sc[kUnroll];
+    int ps[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = min(r0 + 32 * u, w1 - 1);
+      sc[u] = __ldcg(scores + r);
+      ps[u] = __ldcg(row_pos + r);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + 32 * u;
+      if (r < w1) {
+        if (apart && r < a.budget) {
+          scores_out[r] = sc[u];
+          row_pos_out[r] = ps[u];
+        }
+        const uint32_t k = key_of(sc[u], ps[u], a.sinks, recent_from);
+        if (r - lo < held) s_keys[r - lo] = k;
+        least = min(least, rank_of(k, r));
       }
+    }
+  }
+  if (over <= 0) return;
+  auto key = [&](int r) {
+    return r - lo < held ? s_keys[r - lo]
+                         : key_of(__ldcg(scores + r), __ldcg(row_pos + r), a.sinks, recent_from);
+  };
+  const unsigned below = (1u << lane) - 1u;
+  const int32_t *table = a.block_tables + (int64_t)seq * a.max_blocks_per_seq;
+  // move pair p: the ledgers here; the row indices of its copy (-1: no such block)
+  auto start_move = [&](int2 p, int64_t &rt, int64_t &rf) {
+    scores_out[p.x] = __ldcg(scores + p.y);
+    row_pos_out[p.x] = __ldcg(row_pos + p.y);
+    const int sh = a.block_shift, mask = (1 << sh) - 1;
+    const int bt = __ldg(table + (p.x >> sh)), bf = __ldg(table + (p.y >> sh));
+    rt = rf = -1;
+    if (bt < 0 || bt >= a.num_blocks || bf < 0 || bf >= a.num_blocks) {
+      pa::record_error(a.err, pa::kErrCheck);
+      return;
+    }
+    rt = (((int64_t)bt * a.num_kv_heads + head) << sh) + (p.x & mask);
+    rf = (((int64_t)bf * a.num_kv_heads + head) << sh) + (p.y & mask);
+  };
+
+  if (over <= kFew) {
+    // the `over` smallest, one at a time; every warp ends up with all of them
+    int evicted = -1;  // lane i < over: the i-th
+    uint64_t last = 0ull;
+    for (int e = 0; e < over; ++e) {
+      if (e > 0) {
+        least = ~0ull;
+        for (int r = w0 + lane; r < w1; r += 32) {
+          const uint64_t x = rank_of(key(r), r);
+          if (x > last) least = min(least, x);
+        }
+      }
+      const uint64_t w = warp_min(least);
+      if (lane == 0) s_min[e][warp] = w;
+      __syncthreads();
+      uint64_t m = warp_min(lane < NW ? s_min[e][lane] : ~0ull);
+      if (csize > 1) {
+        if (tid == 0) s_cta_min[e] = m;
+        pa::cluster_sync_all();
+        m = warp_min(lane < csize ? dsmem_ld_u64(pa::dsmem_map(pa::smem_u32(&s_cta_min[e]), lane)) : ~0ull);
+      }
+      last = m;
+      if (lane == e) evicted = (int)~(uint32_t)m;
+    }
+    // no CTA leaves, and no copied ledger row is written again, before all are done
+    group_sync(csize);
+    if (crank != 0 || warp != 0) return;
+    // holes: evicted rows below the budget, in order; sources: rows past it that stay
+    const bool is_hole = lane < over && evicted < a.budget;
+    int hole_rank = 0;
+    bool gone = false;  // row budget + lane is evicted
+    for (int e = 0; e < over; ++e) {
+      const int x = __shfl_sync(0xffffffffu, evicted, e);
+      hole_rank += x < evicted;
+      gone |= x == a.budget + lane;
+    }
+    const bool is_src = lane < over && !gone;
+    const unsigned srcs = __ballot_sync(0xffffffffu, is_src);
+    if (is_hole) s_moves[hole_rank].x = evicted;
+    if (is_src) s_moves[__popc(srcs & below)].y = a.budget + lane;
+    __syncwarp();
+    const int m = __popc(srcs);
+    int64_t rt = -1, rf = -1;
+    if (lane < m) start_move(s_moves[lane], rt, rf);
+    copy_rows(a, rt, rf, m);
     return;
   }
-  const int64_t recent_from = (int64_t)__ldg(a.seq_lens + seq) - a.recent;
-  auto load_key = [&](int r) { return key_of(scores[r], row_pos[r], a.sinks, recent_from); };
-  const int held = min(L, a.key_cap);
-  for (int r = tid; r < held; r += kThreads) s_keys[r] = load_key(r);
-  auto key = [&](int r) { return r < held ? s_keys[r] : load_key(r); };
 
   // radix select of the budget-th largest key, from the top byte down: `prefix` holds
   // the bytes known so far, `left` how many rows with that prefix are still to keep
   uint32_t prefix = 0;
   int left = a.budget;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int r = tid; r < L; r += kThreads) {
+  __syncthreads();  // zeroed counts
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    const uint32_t mask = pass == 0 ? 0u : ~0u << (shift + 8);
+#pragma unroll 4
+    for (int r = w0 + lane; r < w1; r += 32) {
       const uint32_t k = key(r);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+      if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & 255u], 1);
     }
-    __syncthreads();
+    group_sync(csize);
     if (warp == 0) {
       // lane l takes digits 255 - 8 l .. 248 - 8 l, highest first
-      int part = 0;
+      int cnt[8], part = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) part += hist[255 - 8 * lane - i];
+      for (int i = 0; i < 8; ++i) {
+        const int d = 255 - 8 * lane - i;
+        cnt[i] = hist[pass][d];
+      }
+      if (csize > 1) {
+        for (int c = 1; c < csize; ++c) {
+          const int peer = crank + c < csize ? crank + c : crank + c - csize;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            cnt[i] += pa::dsmem_ld_s32(pa::dsmem_map(pa::smem_u32(&hist[pass][255 - 8 * lane - i]), peer));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part += cnt[i];
       int incl = part;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -136,12 +310,11 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
       if (run < left && incl >= left) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int d = 255 - 8 * lane - i, n = hist[d];
-          if (run < left && run + n >= left) {
-            s_digit = d;
+          if (run < left && run + cnt[i] >= left) {
+            s_digit = 255 - 8 * lane - i;
             s_left = left - run;
           }
-          run += n;
+          run += cnt[i];
         }
       }
     }
@@ -152,69 +325,122 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
   }
   const uint32_t border = prefix;  // rows above it are kept, and the first `left` equal to it
 
-  // each warp takes a contiguous range of rows, in order
-  const int per = ((L + kWarps - 1) / kWarps + 31) & ~31;
-  const int lo = min(L, warp * per), hi = min(L, lo + per);
-  int ties = 0;
-  for (int r = lo; r < hi; r += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, r + lane < hi && key(r + lane) == border));
-  int all;
-  const int ties_before = warps_before(ties, s_warp, &all);
-  const unsigned below = (1u << lane) - 1u;
-  // holes (evicted rows below the budget) and sources (kept rows from there on)
-  int32_t *moves = a.moves + ((int64_t)seq * a.num_kv_heads + head) * a.list_cap * 2;
-  int holes_at = 0, srcs_at = 0, m = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int t = ties_before, nh = holes_at, ns = srcs_at;
-    for (int r0 = lo; r0 < hi; r0 += 32) {
-      const int r = r0 + lane;
-      const uint32_t k = r < hi ? key(r) : 0u;
-      const unsigned eq = __ballot_sync(0xffffffffu, r < hi && k == border);
-      const bool kept = r < hi && (k > border || (k == border && t + __popc(eq & below) < left));
-      t += __popc(eq);
-      const unsigned hb = __ballot_sync(0xffffffffu, r < hi && !kept && r < a.budget);
-      const unsigned sb = __ballot_sync(0xffffffffu, kept && r >= a.budget);
-      if (pass == 1) {
-        if ((hb >> lane) & 1u) moves[2 * (nh + __popc(hb & below))] = r;
-        if ((sb >> lane) & 1u) moves[2 * (ns + __popc(sb & below)) + 1] = r;
-        if (!in_place && kept && r < a.budget) {
-          scores_out[r] = scores[r];
-          row_pos_out[r] = row_pos[r];
-        }
-      }
-      nh += __popc(hb);
-      ns += __popc(sb);
-    }
-    if (pass == 0) {
-      holes_at = warps_before(nh, s_warp, &all);
-      srcs_at = warps_before(ns, s_warp, &m);
-    }
+  // how many rows of each kind every warp holds; from those, where its holes (evicted rows
+  // below the budget) and sources (kept rows from there on) stand in the lists
+  Counts mine = {0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int r = w0 + lane; r < w1; r += 32) {
+    const uint32_t k = key(r);
+    const bool low = r < a.budget;
+    mine.gt_lo += k > border && low;
+    mine.gt_hi += k > border && !low;
+    mine.eq_lo += k == border && low;
+    mine.eq_hi += k == border && !low;
   }
+  mine.gt_lo = __reduce_add_sync(0xffffffffu, mine.gt_lo);
+  mine.gt_hi = __reduce_add_sync(0xffffffffu, mine.gt_hi);
+  mine.eq_lo = __reduce_add_sync(0xffffffffu, mine.eq_lo);
+  mine.eq_hi = __reduce_add_sync(0xffffffffu, mine.eq_hi);
+  mine.n_lo = max(0, min(w1, a.budget) - w0);
+  if (lane == 0) s_cnt[warp] = mine;
   __syncthreads();
-
-  // the copies: a warp per pair, lanes over its chunks (K, then V)
-  const int rc = a.row_chunks;
-  const int32_t *table = a.block_tables + (int64_t)seq * a.max_blocks_per_seq;
-  for (int i = warp; i < m; i += kWarps) {
-    const int to = moves[2 * i], from = moves[2 * i + 1];
-    if (lane == 0) {
-      scores_out[to] = scores[from];
-      row_pos_out[to] = row_pos[from];
+  if (csize > 1 && tid == 0) {
+    Counts all = {0, 0, 0, 0, 0};
+    for (int w = 0; w < NW; ++w) {
+      all.gt_lo += s_cnt[w].gt_lo;
+      all.gt_hi += s_cnt[w].gt_hi;
+      all.eq_lo += s_cnt[w].eq_lo;
+      all.eq_hi += s_cnt[w].eq_hi;
+      all.n_lo += s_cnt[w].n_lo;
     }
-    const int bt = __ldg(table + to / a.block_size), bf = __ldg(table + from / a.block_size);
-    if (bt < 0 || bt >= a.num_blocks || bf < 0 || bf >= a.num_blocks) {
-      if (lane == 0) pa::record_error(a.err, pa::kErrCheck);
-      continue;
-    }
-    const int64_t rt = ((int64_t)bt * a.num_kv_heads + head) * a.block_size + to % a.block_size;
-    const int64_t rf = ((int64_t)bf * a.num_kv_heads + head) * a.block_size + from % a.block_size;
-    for (int c = lane; c < 2 * rc; c += 32) {
-      uint8_t *cache = c < rc ? a.k_cache : a.v_cache;
-      const int cc = c < rc ? c : c - rc;
-      const uint4 x = *(reinterpret_cast<const uint4 *>(cache) + rf * rc + cc);
-      *(reinterpret_cast<uint4 *>(cache) + rt * rc + cc) = x;
+    s_pub = all;
+  }
+  if (csize > 1) pa::cluster_sync_all();
+  int t = 0, nh = 0, ns = 0, m = 0;  // equal rows, holes, sources before this warp; sources in all
+  {
+    int tt = 0;
+    for (int c = 0; c < csize; ++c) {
+      if (c == crank) {
+        t = tt;
+        for (int w = 0; w < NW; ++w) {
+          const Counts x = s_cnt[w];
+          if (w < warp) {
+            nh += x.holes(tt, left);
+            ns += x.sources(tt, left);
+            t += x.eq_lo + x.eq_hi;
+          }
+          m += x.sources(tt, left);
+          tt += x.eq_lo + x.eq_hi;
+        }
+      } else {
+        Counts x;
+        const uint32_t at = pa::dsmem_map(pa::smem_u32(&s_pub), c);
+        x.gt_lo = pa::dsmem_ld_s32(at);
+        x.gt_hi = pa::dsmem_ld_s32(at + 4);
+        x.eq_lo = pa::dsmem_ld_s32(at + 8);
+        x.eq_hi = pa::dsmem_ld_s32(at + 12);
+        x.n_lo = pa::dsmem_ld_s32(at + 16);
+        if (c < crank) {
+          nh += x.holes(tt, left);
+          ns += x.sources(tt, left);
+        }
+        m += x.sources(tt, left);
+        tt += x.eq_lo + x.eq_hi;
+      }
     }
   }
+  int2 *moves = csize == 1 && m <= kListCap ? s_moves : a.moves + (int64_t)unit * a.budget;
+  for (int r0 = w0; r0 < w1; r0 += 32) {
+    const int r = r0 + lane;
+    const uint32_t k = r < w1 ? key(r) : 0u;
+    const unsigned eq = __ballot_sync(0xffffffffu, r < w1 && k == border);
+    const bool kept = r < w1 && (k > border || (k == border && t + __popc(eq & below) < left));
+    t += __popc(eq);
+    const unsigned hb = __ballot_sync(0xffffffffu, r < w1 && !kept && r < a.budget);
+    const unsigned sb = __ballot_sync(0xffffffffu, kept && r >= a.budget);
+    if ((hb >> lane) & 1u) moves[nh + __popc(hb & below)].x = r;
+    if ((sb >> lane) & 1u) moves[ns + __popc(sb & below)].y = r;
+    nh += __popc(hb);
+    ns += __popc(sb);
+  }
+  group_sync(csize);  // the whole list, and every read of the old ledgers, before the moves
+
+  const int warps = csize * NW;
+  const int batch = min(32, (m + warps - 1) / warps);
+  for (int i0 = (crank * NW + warp) * batch; i0 < m; i0 += warps * batch) {
+    const int cnt = min(batch, m - i0);
+    int64_t rt = -1, rf = -1;
+    if (lane < cnt) start_move(moves[i0 + lane], rt, rf);
+    copy_rows(a, rt, rf, cnt);
+  }
+  // (distributed shared memory was last read before the barrier above)
+}
+
+// Tables of at most so many rows: CTAs of 256 threads; longer ones: 512.
+constexpr int kSmallRows = 4096;
+
+template <int NT>
+cudaError_t launch_evict(const EvictArgs &a, unsigned units, int cluster, int smem, cudaStream_t s) {
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(evict_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kKeyCap * (int)sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * cluster, 1, 1);
+  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<NT>, a);
 }
 
 }  // namespace
@@ -262,34 +488,33 @@ extern "C" PA_API pa_status pa_evict(
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.seq_lens = seq_lens;
-  a.moves = static_cast<int32_t *>(workspace);
+  a.moves = static_cast<int2 *>(workspace);
   a.num_kv_heads = num_kv_heads;
-  a.block_size = block_size;
+  a.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
   a.max_rows = max_blocks_per_seq * block_size;
   a.budget = budget;
   a.sinks = sinks;
   a.recent = recent;
-  a.list_cap = budget;
-  a.key_cap = std::min(a.max_rows, kKeyCap);
   a.row_chunks = head_dim * element_bytes / 16;
   a.err = pa::error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
-  const int smem = a.key_cap * (int)sizeof(uint32_t);
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kKeyCap * (int)sizeof(uint32_t)) != cudaSuccess)
+  // few units: a cluster each, while the clusters' CTAs fill at most about two per SM
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(num_seqs * num_kv_heads), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_kernel, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const long long units = (long long)num_seqs * num_kv_heads;
+  int cluster = 1;
+  if (a.max_rows > kSmallRows)
+    while (cluster < kMaxCluster && units * cluster * 2 <= 2LL * sms) cluster *= 2;
+  if (units * cluster >= 1LL << 31) return PA_ERR_INVALID_ARG;
+  const int slice = ((a.max_rows + cluster - 1) / cluster + 31) & ~31;
+  a.key_cap = std::min(slice, kKeyCap);
+  const int smem = a.key_cap * (int)sizeof(uint32_t);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a.max_rows > kSmallRows ? launch_evict<512>(a, (unsigned)units, cluster, smem, s)
+                                                : launch_evict<256>(a, (unsigned)units, cluster, smem, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

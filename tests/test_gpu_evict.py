@@ -102,6 +102,11 @@ CASES = [
     ([2000, 1999], 2, 128, 8, 1, 700, 3, 200),
     ([513], 8, 64, 16, 2, 512, 4, 256),
     ([4100, 700], 2, 64, 32, 2, 1024, 4, 256),
+    ([9001, 8998, 8995, 3], 2, 128, 16, 1, 8994, 4, 30),  # 7, 4, 1 and no rows over
+    ([9001, 5000], 1, 64, 8, 2, 8993, 0, 8000),           # 8 over
+    ([9001], 1, 64, 8, 2, 8992, 2, 100),                  # 9 over
+    ([30, 27, 24, 23, 22], 3, 128, 8, 2, 22, 1, 3),
+    ([12000, 40], 1, 128, 32, 2, 6000, 4, 64),            # many moves in a cluster
 ]
 
 
@@ -147,6 +152,13 @@ def test_long_context(pa):
     c = make(5, [52000, 700], 1, 64, 32, zeros=0.5)
     check(c, run(pa, c, 5000, 4, 1000, True), 5000, 4, 1000, True)
     check(c, run(pa, c, 49999, 4, 1000, False), 49999, 4, 1000, False)
+
+
+def test_more_rows_than_keys_held(pa):
+    """So many units that each is one CTA, and a context longer than its shared memory."""
+    c = make(10, [46000] + [40] * 159, 1, 64, 32, zeros=0.3)
+    check(c, run(pa, c, 20000, 4, 1000, True), 20000, 4, 1000, True)
+    check(c, run(pa, c, 45997, 4, 1000, False), 45997, 4, 1000, False)
 
 
 def test_again_with_other_ledgers_gives_the_same(pa):
