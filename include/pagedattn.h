@@ -427,7 +427,7 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
  * PA_ERR_DEVICE_CHECK.
  *   element_bytes  2 (16-bit cache) or 1 (FP8, head_dim 128): rows are moved bit for bit
  *   new_lens       int32 [num_seqs], not context_lens itself
- *   workspace      pa_evict_workspace_size bytes, 16-byte aligned
+ *   workspace      pa_evict_workspace_size bytes
  * budget >= sinks + recent, budget >= 1.
  */
 PA_API size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int budget);

@@ -131,7 +131,7 @@ __device__ __forceinline__ void copy_rows(const EvictArgs &a, int64_t rt, int64_
 template <int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a) {
   constexpr int NW = NT / 32;
-  constexpr int kUnroll = 8;
+  constexpr int kUnroll = 3;
   extern __shared__ uint32_t s_keys[];
   __shared__ int hist[4][256];
   __shared__ Counts s_cnt[NW];        // by warp
@@ -175,33 +175,70 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a)
     return ((uint64_t)key << 32) | (uint32_t)~r;
   };
   for (int i = tid; i < 4 * 256; i += NT) (&hist[0][0])[i] = 0;
-  for (int r0 = w0 + lane; r0 < w1; r0 += 32 * kUnroll) {
-    float sc[kUnroll];
-    int ps[kUnroll];
+  // four rows a thread and load (ranges begin at multiples of 32 rows, and a table holds a
+  // multiple of 8)
+  for (int r0 = w0 + 4 * lane; r0 < w1; r0 += 128 * kUnroll) {
+    float4 sc[kUnroll];
+    int4 ps[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int r = min(r0 + 32 * u, w1 - 1);
-      sc[u] = __ldcg(scores + r);
-      ps[u] = __ldcg(row_pos + r);
+      const int r = r0 + 128 * u < w1 ? r0 + 128 * u : r0;
+      sc[u] = __ldcg(reinterpret_cast<const float4 *>(scores + r));
+      ps[u] = __ldcg(reinterpret_cast<const int4 *>(row_pos + r));
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + 32 * u;
-      if (r < w1) {
-        if (apart && r < a.budget) {
-          scores_out[r] = sc[u];
-          row_pos_out[r] = ps[u];
-        }
-        const uint32_t k = key_of(sc[u], ps[u], a.sinks, recent_from);
-        if (r - lo < held) s_keys[r - lo] = k;
-        least = min(least, rank_of(k, r));
+      const int r = r0 + 128 * u;
+      if (r >= w1) break;
+      const int n = min(4, w1 - r);
+      if (apart && r + 3 < min(a.budget, w1)) {
+        *reinterpret_cast<float4 *>(scores_out + r) = sc[u];
+        *reinterpret_cast<int4 *>(row_pos_out + r) = ps[u];
+      } else if (apart) {
+        const float f[4] = {sc[u].x, sc[u].y, sc[u].z, sc[u].w};
+        const int p[4] = {ps[u].x, ps[u].y, ps[u].z, ps[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < n && r + i < a.budget) {
+            scores_out[r + i] = f[i];
+            row_pos_out[r + i] = p[i];
+          }
       }
+      const uint4 k = make_uint4(key_of(sc[u].x, ps[u].x, a.sinks, recent_from),
+                                 key_of(sc[u].y, ps[u].y, a.sinks, recent_from),
+                                 key_of(sc[u].z, ps[u].z, a.sinks, recent_from),
+                                 key_of(sc[u].w, ps[u].w, a.sinks, recent_from));
+      // (held is a multiple of 4 wherever it is less than the slice, and the rows of a
+      // slice are padded to 32 in shared memory)
+      if (r - lo < held) *reinterpret_cast<uint4 *>(s_keys + (r - lo)) = k;
+      least = min(least, rank_of(k.x, r));
+      if (n > 1) least = min(least, rank_of(k.y, r + 1));
+      if (n > 2) least = min(least, rank_of(k.z, r + 2));
+      if (n > 3) least = min(least, rank_of(k.w, r + 3));
     }
   }
+  __syncwarp();  // (a warp's later passes read its rows' keys in another order)
   if (over <= 0) return;
   auto key = [&](int r) {
     return r - lo < held ? s_keys[r - lo]
                          : key_of(__ldcg(scores + r), __ldcg(row_pos + r), a.sinks, recent_from);
+  };
+  // f(key, row) for every row of this warp, four at a time
+  auto each_row = [&](auto f) {
+#pragma unroll 2
+    for (int r = w0 + 4 * lane; r < w1; r += 128) {
+      uint32_t k[4];
+      if (r - lo < held) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(s_keys + (r - lo));
+        k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = key(min(r + i, w1 - 1));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r + i < w1) f(k[i], r + i);
+    }
   };
   const unsigned below = (1u << lane) - 1u;
   const int32_t *table = a.block_tables + (int64_t)seq * a.max_blocks_per_seq;
@@ -227,10 +264,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a)
     for (int e = 0; e < over; ++e) {
       if (e > 0) {
         least = ~0ull;
-        for (int r = w0 + lane; r < w1; r += 32) {
-          const uint64_t x = rank_of(key(r), r);
+        each_row([&](uint32_t k, int r) {
+          const uint64_t x = rank_of(k, r);
           if (x > last) least = min(least, x);
-        }
+        });
       }
       const uint64_t w = warp_min(least);
       if (lane == 0) s_min[e][warp] = w;
@@ -276,11 +313,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a)
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     const uint32_t mask = pass == 0 ? 0u : ~0u << (shift + 8);
-#pragma unroll 4
-    for (int r = w0 + lane; r < w1; r += 32) {
-      const uint32_t k = key(r);
+    each_row([&](uint32_t k, int) {
       if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & 255u], 1);
-    }
+    });
     group_sync(csize);
     if (warp == 0) {
       // lane l takes digits 255 - 8 l .. 248 - 8 l, highest first
@@ -328,15 +363,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a)
   // how many rows of each kind every warp holds; from those, where its holes (evicted rows
   // below the budget) and sources (kept rows from there on) stand in the lists
   Counts mine = {0, 0, 0, 0, 0};
-#pragma unroll 4
-  for (int r = w0 + lane; r < w1; r += 32) {
-    const uint32_t k = key(r);
+  each_row([&](uint32_t k, int r) {
     const bool low = r < a.budget;
     mine.gt_lo += k > border && low;
     mine.gt_hi += k > border && !low;
     mine.eq_lo += k == border && low;
     mine.eq_hi += k == border && !low;
-  }
+  });
   mine.gt_lo = __reduce_add_sync(0xffffffffu, mine.gt_lo);
   mine.gt_hi = __reduce_add_sync(0xffffffffu, mine.gt_hi);
   mine.eq_lo = __reduce_add_sync(0xffffffffu, mine.eq_lo);
@@ -467,8 +500,9 @@ extern "C" PA_API pa_status pa_evict(
   // the ledgers are both updated in place or both written elsewhere
   if ((scores == scores_out) != (row_pos == row_pos_out)) return PA_ERR_INVALID_ARG;
   if (new_lens == context_lens) return PA_ERR_INVALID_ARG;  // (every KV head reads the old lengths)
-  if (!pa::aligned16(k_cache) || !pa::aligned16(v_cache) || !pa::aligned16(workspace))
-    return PA_ERR_INVALID_ARG;
+  const void *ptrs[7] = {k_cache, v_cache, workspace, scores, row_pos, scores_out, row_pos_out};
+  for (const void *p : ptrs)
+    if (!pa::aligned16(p)) return PA_ERR_INVALID_ARG;
   if (element_bytes != 1 && element_bytes != 2) return PA_ERR_UNSUPPORTED;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (element_bytes == 1 && head_dim != 128) return PA_ERR_UNSUPPORTED;

@@ -77,6 +77,7 @@ EVICT = dict(k=FAKE, v=FAKE, so=FAKE, po=FAKE + 64, nl=FAKE, sc=FAKE, rp=FAKE + 
     ({"wsb": 2 * 2 * 32 * 8 - 1}, INVALID), ({"ws": None}, INVALID), ({"ws": FAKE + 8}, INVALID),
     ({"k": None}, INVALID), ({"so": None}, INVALID), ({"nl": None}, INVALID), ({"rp": None}, INVALID),
     ({"sl": None}, INVALID), ({"k": FAKE + 8}, INVALID), ({"nl": FAKE + 16}, INVALID),
+    ({"sc": FAKE + 4, "so": FAKE + 4}, INVALID), ({"rp": FAKE + 8, "po": FAKE + 8}, INVALID),
     ({"so": FAKE + 256}, INVALID),  # one ledger in place, the other not
     ({"budget": 0}, INVALID), ({"sinks": -1}, INVALID), ({"recent": -1}, INVALID),
     ({"sinks": 30, "recent": 3}, INVALID), ({"n": 0}, INVALID), ({"nb": 0}, INVALID),
