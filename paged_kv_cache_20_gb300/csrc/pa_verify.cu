@@ -18,10 +18,15 @@
 // summed as fp32 pairs (value, rounding error; Knuth's two-sum) and reduced in fp64;
 // u q < p is compared in fp64, where the product of two fp32 is exact.
 //
+// The fp64 rate of GB300 is two operations a clock and SM, so fp64 appears only where a
+// warp reduces once.
+//
 // A sequence reads the drafted tokens' entries, then one vocabulary row of p and one
 // of q.  One thread-block cluster per sequence: its CTAs sum a slice of the row each,
 // exchange their sums through distributed shared memory, and the CTA whose slice
-// holds the border searches it (the slice is in L2 by then).
+// holds the border searches it (the slice is in L2 by then): its CTAs' and warps' sums,
+// then 1024 entries at a time through shared memory, so that the loads are coalesced and
+// each lane still adds up 32 neighbours.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -32,9 +37,10 @@
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 8;  // loads of each row in flight per thread
+constexpr int kSearch = 1024;  // entries searched at once
 
 struct VerifyArgs {
   int32_t *out_tokens, *num_accepted, *new_lens;
@@ -77,10 +83,6 @@ struct Row {
     if (v == skip) return Weight{0.f, 0.f};
     return weight_of(__ldg(p + v), q ? __ldg(q + v) : 0.f);
   }
-  __device__ __forceinline__ double value(int v) const {
-    const Weight w = at(v);
-    return (double)w.d + (double)w.e;
-  }
 };
 
 __device__ __forceinline__ double warp_sum(double x) {
@@ -119,9 +121,49 @@ __device__ __forceinline__ double dsmem_ld_f64(uint32_t addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+// fp32 pair sum of the weights of entries [lo, hi), lane by lane (lo + lane, + 32, ...).
+template <bool Q>
+__device__ __forceinline__ void sum_range(const Row &row, int lo, int hi, float &s, float &c) {
+  const int lane = threadIdx.x & 31;
+  int v = lo + lane;
+  for (; v + 32 * (kUnroll - 1) < hi; v += 32 * kUnroll) {
+    float p[kUnroll], q[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      p[u] = __ldg(row.p + v + 32 * u);
+      if (Q) q[u] = __ldg(row.q + v + 32 * u);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (Q) {
+        const Weight w = weight_of(p[u], q[u]);
+        two_sum(s, c, w.d);
+        c += w.e;
+      } else {
+        two_sum(s, c, v + 32 * u == row.skip ? 0.f : weight_of(p[u], 0.f).d);
+      }
+    }
+  }
+  float p[kUnroll], q[kUnroll];  // the rest
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const bool in = v + 32 * u < hi;
+    p[u] = in ? __ldg(row.p + v + 32 * u) : 0.f;
+    q[u] = (Q && in) ? __ldg(row.q + v + 32 * u) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    Weight w = weight_of(p[u], q[u]);
+    if (v + 32 * u == row.skip) w.d = w.e = 0.f;
+    two_sum(s, c, w.d);
+    c += w.e;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
   __shared__ double warp_part[kWarps];
   __shared__ double cta_part;
+  __shared__ Weight s_w[32 * 33];  // 1024 searched weights, 32 a row
   __shared__ int s_count, s_given, s_skip;
   pa::griddep_wait();
   pa::griddep_launch_dependents();
@@ -183,22 +225,10 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     const int64_t lo64 = (int64_t)(crank * kWarps + warp) * per_warp;
     const int lo = (int)min((int64_t)a.vocab, lo64), hi = (int)min((int64_t)a.vocab, lo64 + per_warp);
     float s = 0.f, c = 0.f;
-    for (int v = lo + lane; v < hi; v += 32 * kUnroll) {
-      float p[kUnroll], q[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int w = v + 32 * u;
-        p[u] = w < hi ? __ldg(row.p + w) : 0.f;
-        q[u] = (w < hi && row.q) ? __ldg(row.q + w) : 0.f;
-        if (w == row.skip) p[u] = 0.f;
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const Weight w = weight_of(p[u], q[u]);
-        two_sum(s, c, w.d);
-        c += w.e;
-      }
-    }
+    if (row.q)
+      sum_range<true>(row, lo, hi, s, c);
+    else
+      sum_range<false>(row, lo, hi, s, c);
     const double part = warp_sum((double)s + (double)c);
     if (lane == 0) warp_part[warp] = part;
     __syncthreads();
@@ -220,41 +250,47 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
           const int64_t l64 = (int64_t)(crank * kWarps + w) * per_warp;
           const int wlo = (int)min((int64_t)a.vocab, l64);
           const int whi = (int)min((int64_t)a.vocab, l64 + per_warp);
-          // lane l sums entries [wlo + l k, wlo + (l + 1) k), k = per_warp / 32
-          const int k = per_warp / 32;
-          double sum = 0.0;
-          for (int j = 0; j < k; ++j) {
-            const int v = wlo + lane * k + j;
-            if (v < whi) sum += row.value(v);
-          }
-          const int part_lane = find_part(sum, before, border, &before);
-          for (int j0 = 0; part_lane >= 0 && j0 < k; j0 += 32) {
-            const int v = wlo + part_lane * k + j0 + lane;
-            const double wv = (j0 + lane < k && v < whi) ? row.value(v) : 0.0;
+          for (int g0 = wlo; g0 < whi; g0 += kSearch) {
+            const int g1 = min(whi, g0 + kSearch);
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {
+              const int v = g0 + 32 * j + lane;
+              s_w[33 * j + lane] = v < g1 ? row.at(v) : Weight{0.f, 0.f};
+            }
+            __syncwarp();
+            float ls = 0.f, lc = 0.f;  // entries [g0 + 32 lane, + 32)
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {
+              const Weight x = s_w[33 * lane + j];
+              two_sum(ls, lc, x.d);
+              lc += x.e;
+            }
+            const double sum = (double)ls + (double)lc;
             const double base = before;
-            const int e = find_part(wv, base, border, &before);
-            if (e >= 0) token = wlo + part_lane * k + j0 + e;
-            const double next = base + warp_sum(wv);
-            if (next > border) break;
-            before = next;
+            double at;
+            const int part = find_part(sum, base, border, &at);
+            if (part >= 0) {
+              const Weight x = s_w[33 * part + lane];
+              const int e = find_part((double)x.d + (double)x.e, at, border, &at);
+              if (e >= 0) token = g0 + 32 * part + e;
+            }
+            before = base + warp_sum(sum);
+            __syncwarp();
+            if (before > border) break;  // else the border lies further on, or in rounding
           }
         }
+      }
+      const bool none = who < 0 && round == 1;  // no weight anywhere: no token
+      if (who == crank || (none && crank == 0)) {
+        int32_t *out = a.out_tokens + (int64_t)seq * (a.max_draft + 1);
+        for (int j = lane; j <= a.max_draft; j += 32)
+          out[j] = j < count ? __ldg(x + j) : j == count ? token : -1;
         if (lane == 0) {
-          int32_t *out = a.out_tokens + (int64_t)seq * (a.max_draft + 1);
-          for (int j = 0; j <= a.max_draft; ++j)
-            out[j] = j < count ? __ldg(x + j) : j == count ? token : -1;
+          if (none) pa::record_error(a.err, pa::kErrCheck);
           a.num_accepted[seq] = count;
           if (a.new_lens)
             a.new_lens[seq] = max(0, __ldg(a.context_lens + seq) - (a.max_draft - count));
         }
-      } else if (who < 0 && round == 1 && crank == 0 && lane == 0) {
-        // no weight anywhere: no token
-        pa::record_error(a.err, pa::kErrCheck);
-        int32_t *out = a.out_tokens + (int64_t)seq * (a.max_draft + 1);
-        for (int j = 0; j <= a.max_draft; ++j) out[j] = j < count ? __ldg(x + j) : -1;
-        a.num_accepted[seq] = count;
-        if (a.new_lens)
-          a.new_lens[seq] = max(0, __ldg(a.context_lens + seq) - (a.max_draft - count));
       }
       if (lane == 0) s_given = who;
     }
