@@ -14,19 +14,17 @@
 //
 // The answer is a token id, so sums decide at borders: with a vocabulary of 10^5
 // tokens an fp32 sum of the weights (error ~1e-7 of the total) lands on the wrong side
-// of one of the borders in about one call in a hundred.  The weights are therefore
-// summed as fp32 pairs (value, rounding error; Knuth's two-sum) and reduced in fp64;
-// u q < p is compared in fp64, where the product of two fp32 is exact.
-//
-// The fp64 rate of GB300 is two operations a clock and SM, so fp64 appears only where a
-// warp reduces once.
+// of one of the borders in about one call in a hundred.  All sums here are pairs of
+// fp32 (the rounded sum and the rounding errors it dropped, by Knuth's two-sum), good to
+// about 2^-46 of the total; the fp64 rate of GB300 is two operations a clock and SM
+// (scans in fp64 made the search 17 us of 35 in a batch of 64).  u q < p is compared in
+// fp64, where the product of two fp32 is exact.
 //
 // A sequence reads the drafted tokens' entries, then one vocabulary row of p and one
 // of q.  One thread-block cluster per sequence: its CTAs sum a slice of the row each,
 // exchange their sums through distributed shared memory, and the CTA whose slice
-// holds the border searches it (the slice is in L2 by then): its CTAs' and warps' sums,
-// then 1024 entries at a time through shared memory, so that the loads are coalesced and
-// each lane still adds up 32 neighbours.
+// holds the border searches it (the slice is in L2 by then): by its warps' ranges, then
+// 2048 entries at a time with 256 a warp, each lane's eight loads in flight at once.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,7 +38,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 8;  // loads of each row in flight per thread
-constexpr int kSearch = 1024;  // entries searched at once
+constexpr int kCluster = 8;
+constexpr int kPiece = 32 * kUnroll;        // entries a warp searches at once
+constexpr int kSearch = kWarps * kPiece;    // and the CTA
 
 struct VerifyArgs {
   int32_t *out_tokens, *num_accepted, *new_lens;
@@ -53,25 +53,54 @@ struct VerifyArgs {
   unsigned *err;
 };
 
-// (s, c) += x: s the running fp32 sum, c the rounding errors it has dropped.
-__device__ __forceinline__ void two_sum(float &s, float &c, float x) {
-  const float t = __fadd_rn(s, x);
-  const float z = __fsub_rn(t, s);
-  c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
-  s = t;
+// s the rounded sum, c the rounding errors it has dropped.
+struct Pair {
+  float s, c;
+  __device__ __forceinline__ bool positive() const { return s > 0.f; }  // (weights are >= 0)
+};
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair r;
+  r.s = __fadd_rn(a.s, b.s);
+  const float z = __fsub_rn(r.s, a.s);
+  r.c = __fadd_rn(__fadd_rn(a.c, b.c), __fadd_rn(__fsub_rn(a.s, __fsub_rn(r.s, z)), __fsub_rn(b.s, z)));
+  return r;
 }
 
-// A weight as value + error: p - q split exactly, zero where it is not positive (or
+// a > b: where the rounded sums are close their difference is exact
+__device__ __forceinline__ bool greater(Pair a, Pair b) {
+  return __fadd_rn(__fsub_rn(a.s, b.s), __fsub_rn(a.c, b.c)) > 0.f;
+}
+
+// u * a
+__device__ __forceinline__ Pair scaled(float u, Pair a) {
+  Pair r;
+  r.s = __fmul_rn(u, a.s);
+  r.c = __fadd_rn(__fmaf_rn(u, a.s, -r.s), __fmul_rn(u, a.c));
+  return r;
+}
+
+__device__ __forceinline__ Pair shfl(Pair a, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, a.s, lane), __shfl_sync(0xffffffffu, a.c, lane)};
+}
+
+// Sum over groups of N lanes.
+template <int N>
+__device__ __forceinline__ Pair group_sum(Pair x) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1)
+    x = add(x, Pair{__shfl_xor_sync(0xffffffffu, x.s, o), __shfl_xor_sync(0xffffffffu, x.c, o)});
+  return x;
+}
+
+// A weight: p - q split exactly into value and error, zero where it is not positive (or
 // not finite).
-struct Weight {
-  float d, e;
-};
-__device__ __forceinline__ Weight weight_of(float p, float q) {
-  Weight w;
-  w.d = __fsub_rn(p, q);
-  const float z = __fsub_rn(w.d, p);
-  w.e = __fsub_rn(__fsub_rn(p, __fsub_rn(w.d, z)), __fadd_rn(q, z));
-  if (!(w.d > 0.f && w.d <= 3.4028234e38f)) w.d = w.e = 0.f;
+__device__ __forceinline__ Pair weight_of(float p, float q) {
+  Pair w;
+  w.s = __fsub_rn(p, q);
+  const float z = __fsub_rn(w.s, p);
+  w.c = __fsub_rn(__fsub_rn(p, __fsub_rn(w.s, z)), __fadd_rn(q, z));
+  if (!(w.s > 0.f && w.s <= 3.4028234e38f)) w.s = w.c = 0.f;
   return w;
 }
 
@@ -79,54 +108,38 @@ __device__ __forceinline__ Weight weight_of(float p, float q) {
 struct Row {
   const float *p, *q;
   int skip;
-  __device__ __forceinline__ Weight at(int v) const {
-    if (v == skip) return Weight{0.f, 0.f};
-    return weight_of(__ldg(p + v), q ? __ldg(q + v) : 0.f);
-  }
 };
 
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// Inclusive prefix sum over the warp.
-__device__ __forceinline__ double warp_scan(double x) {
+// Among the parts x of lanes 0 .. N-1 (in order; other lanes hold zeros), `base` the sum
+// before them: the first part whose running sum exceeds `border`, else the last positive
+// one (rounding at the end of the row), else -1.  *before = the running sum before it,
+// *over = whether the border was exceeded.
+template <int N>
+__device__ __forceinline__ int find_part(Pair x, Pair base, Pair border, Pair *before, bool *over) {
   const int lane = threadIdx.x & 31;
+  Pair incl = x;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+  for (int o = 1; o < N; o <<= 1) {
+    const Pair y = {__shfl_up_sync(0xffffffffu, incl.s, o), __shfl_up_sync(0xffffffffu, incl.c, o)};
+    if (lane >= o) incl = add(y, incl);
   }
-  return x;
-}
-
-// Among 32 consecutive parts of sum x (one per lane), base the sum before them: the
-// first whose running sum exceeds `border`, else the last with x > 0 (rounding at the
-// end of the row), else -1.  *before = the running sum before it.
-__device__ __forceinline__ int find_part(double x, double base, double border, double *before) {
-  const double incl = base + warp_scan(x);
-  const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && incl > border);
-  const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
-  const int k = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
-  const double prev = __shfl_sync(0xffffffffu, incl - x, k < 0 ? 0 : k);
-  *before = prev;
+  incl = add(base, incl);
+  const unsigned past = __ballot_sync(0xffffffffu, lane < N && x.positive() && greater(incl, border));
+  const unsigned some = __ballot_sync(0xffffffffu, lane < N && x.positive());
+  const int k = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : -1;
+  *over = past != 0u;
+  const Pair prev = shfl(incl, k > 0 ? k - 1 : 0);
+  *before = k > 0 ? prev : base;
   return k;
 }
 
-__device__ __forceinline__ double dsmem_ld_f64(uint32_t addr) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-// fp32 pair sum of the weights of entries [lo, hi), lane by lane (lo + lane, + 32, ...).
+// fp32 pair sum of the weights of this lane's entries of [lo, hi): lo + lane, + 32, ...
 template <bool Q>
-__device__ __forceinline__ void sum_range(const Row &row, int lo, int hi, float &s, float &c) {
+__device__ __forceinline__ Pair sum_range(const Row &row, int lo, int hi) {
   const int lane = threadIdx.x & 31;
+  Pair sum = {0.f, 0.f};
   int v = lo + lane;
-  for (; v + 32 * (kUnroll - 1) < hi; v += 32 * kUnroll) {
+  for (; v + 32 * (kUnroll - 1) < hi; v += kPiece) {
     float p[kUnroll], q[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -135,36 +148,27 @@ __device__ __forceinline__ void sum_range(const Row &row, int lo, int hi, float 
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (Q) {
-        const Weight w = weight_of(p[u], q[u]);
-        two_sum(s, c, w.d);
-        c += w.e;
-      } else {
-        two_sum(s, c, v + 32 * u == row.skip ? 0.f : weight_of(p[u], 0.f).d);
-      }
+      Pair w = weight_of(p[u], Q ? q[u] : 0.f);
+      if (!Q && v + 32 * u == row.skip) w = Pair{0.f, 0.f};
+      sum = add(sum, w);
     }
   }
-  float p[kUnroll], q[kUnroll];  // the rest
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const bool in = v + 32 * u < hi;
-    p[u] = in ? __ldg(row.p + v + 32 * u) : 0.f;
-    q[u] = (Q && in) ? __ldg(row.q + v + 32 * u) : 0.f;
+  for (; v < hi; v += 32) {
+    Pair w = weight_of(__ldg(row.p + v), Q ? __ldg(row.q + v) : 0.f);
+    if (v == row.skip) w = Pair{0.f, 0.f};
+    sum = add(sum, w);
   }
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    Weight w = weight_of(p[u], q[u]);
-    if (v + 32 * u == row.skip) w.d = w.e = 0.f;
-    two_sum(s, c, w.d);
-    c += w.e;
-  }
+  return sum;
+}
+
+__device__ __forceinline__ Pair dsmem_ld_pair(uint32_t addr) {
+  return Pair{pa::dsmem_ld_f32(addr), pa::dsmem_ld_f32(addr + 4)};
 }
 
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
-  __shared__ double warp_part[kWarps];
-  __shared__ double cta_part;
-  __shared__ Weight s_w[32 * 33];  // 1024 searched weights, 32 a row
-  __shared__ int s_count, s_given, s_skip;
+  __shared__ Pair warp_part[kWarps], piece_part[kWarps];
+  __shared__ Pair cta_part;
+  __shared__ int s_count, s_given, s_skip, s_token;
   pa::griddep_wait();
   pa::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -218,84 +222,95 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
 
   // slice of this CTA, ranges of its warps: whole multiples of 32 entries
   const int per_warp = ((a.vocab + csize * kWarps - 1) / (csize * kWarps) + 31) & ~31;
-  int token = -1;
   // round 0: the weights above; round 1 (their sum is zero: the distributions agree to
   // rounding, or the row is empty): the target row itself
   for (int round = 0; round < 2; ++round) {
     const int64_t lo64 = (int64_t)(crank * kWarps + warp) * per_warp;
     const int lo = (int)min((int64_t)a.vocab, lo64), hi = (int)min((int64_t)a.vocab, lo64 + per_warp);
-    float s = 0.f, c = 0.f;
-    if (row.q)
-      sum_range<true>(row, lo, hi, s, c);
-    else
-      sum_range<false>(row, lo, hi, s, c);
-    const double part = warp_sum((double)s + (double)c);
+    const Pair part = group_sum<32>(row.q ? sum_range<true>(row, lo, hi) : sum_range<false>(row, lo, hi));
     if (lane == 0) warp_part[warp] = part;
     __syncthreads();
+    const Pair none = {0.f, 0.f};
+    const Pair parts = lane < kWarps ? warp_part[lane] : none;
     if (warp == 0) {
-      const double all = warp_sum(lane < kWarps ? warp_part[lane] : 0.0);
-      if (lane == 0) cta_part = all;
+      const Pair all = group_sum<kWarps>(parts);
+      if (lane == 0) {
+        cta_part = all;
+        s_token = -1;
+      }
     }
     pa::cluster_sync_all();
-    if (warp == 0) {
-      // every CTA finds the CTA whose slice holds the border; that one goes on
-      const double mine = lane < csize ? dsmem_ld_f64(pa::dsmem_map(pa::smem_u32(&cta_part), lane)) : 0.0;
-      const double total = warp_sum(mine);
-      const double border = (double)__ldg(a.sample_u + seq) * total;
-      double before;
-      const int who = find_part(mine, 0.0, border, &before);
-      if (who == crank) {
-        const int w = find_part(lane < kWarps ? warp_part[lane] : 0.0, before, border, &before);
-        if (w >= 0) {
-          const int64_t l64 = (int64_t)(crank * kWarps + w) * per_warp;
-          const int wlo = (int)min((int64_t)a.vocab, l64);
-          const int whi = (int)min((int64_t)a.vocab, l64 + per_warp);
-          for (int g0 = wlo; g0 < whi; g0 += kSearch) {
-            const int g1 = min(whi, g0 + kSearch);
-#pragma unroll 8
-            for (int j = 0; j < 32; ++j) {
-              const int v = g0 + 32 * j + lane;
-              s_w[33 * j + lane] = v < g1 ? row.at(v) : Weight{0.f, 0.f};
-            }
-            __syncwarp();
-            float ls = 0.f, lc = 0.f;  // entries [g0 + 32 lane, + 32)
-#pragma unroll 8
-            for (int j = 0; j < 32; ++j) {
-              const Weight x = s_w[33 * lane + j];
-              two_sum(ls, lc, x.d);
-              lc += x.e;
-            }
-            const double sum = (double)ls + (double)lc;
-            const double base = before;
-            double at;
-            const int part = find_part(sum, base, border, &at);
-            if (part >= 0) {
-              const Weight x = s_w[33 * part + lane];
-              const int e = find_part((double)x.d + (double)x.e, at, border, &at);
-              if (e >= 0) token = g0 + 32 * part + e;
-            }
-            before = base + warp_sum(sum);
-            __syncwarp();
-            if (before > border) break;  // else the border lies further on, or in rounding
+    // every warp of every CTA finds the CTA whose slice holds the border
+    const Pair slices = lane < csize ? dsmem_ld_pair(pa::dsmem_map(pa::smem_u32(&cta_part), lane)) : none;
+    const Pair border = scaled(__ldg(a.sample_u + seq), shfl(group_sum<kCluster>(slices), 0));
+    Pair before;
+    bool over;
+    const int who = find_part<kCluster>(slices, none, border, &before, &over);
+    if (who == crank) {
+      const int w = find_part<kWarps>(parts, before, border, &before, &over);
+      const int64_t l64 = (int64_t)(crank * kWarps + w) * per_warp;
+      const int wlo = (int)min((int64_t)a.vocab, l64), whi = (int)min((int64_t)a.vocab, l64 + per_warp);
+      over = false;
+      for (int g0 = wlo; g0 < whi && !over; g0 += kSearch) {
+        // each warp weighs its piece of 256 entries, entry 32 j + lane in register j
+        const int v0 = g0 + warp * kPiece + lane;
+        float p[kUnroll], q[kUnroll];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          const bool in = v0 + 32 * j < whi;
+          p[j] = in ? __ldg(row.p + v0 + 32 * j) : 0.f;
+          q[j] = (in && row.q) ? __ldg(row.q + v0 + 32 * j) : 0.f;
+        }
+        Pair x[kUnroll], sum = none;
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          x[j] = weight_of(p[j], q[j]);
+          if (v0 + 32 * j == row.skip) x[j] = none;
+          sum = add(sum, x[j]);
+        }
+        sum = group_sum<32>(sum);
+        if (lane == 0) piece_part[warp] = sum;
+        __syncthreads();
+        const Pair pieces = lane < kWarps ? piece_part[lane] : none;
+        const Pair all = add(before, shfl(group_sum<kWarps>(pieces), 0));
+        Pair at;
+        const int piece = find_part<kWarps>(pieces, before, border, &at, &over);
+        if (piece == warp) {
+          // its eight rows of 32 entries: their sums (lane j keeps row j's), then the entry
+          Pair rows = none;
+#pragma unroll
+          for (int j = 0; j < kUnroll; ++j) {
+            const Pair r = group_sum<32>(x[j]);
+            if (lane == j) rows = r;
           }
+          bool o;
+          const int j = find_part<kUnroll>(rows, at, border, &at, &o);
+          Pair mine = none;
+#pragma unroll
+          for (int i = 0; i < kUnroll; ++i)
+            if (i == j) mine = x[i];
+          const int e = find_part<32>(mine, at, border, &at, &o);
+          if (lane == 0 && e >= 0) s_token = g0 + piece * kPiece + 32 * j + e;
         }
+        before = all;
+        __syncthreads();  // (over is the same in every warp: the border is found, or further on)
       }
-      const bool none = who < 0 && round == 1;  // no weight anywhere: no token
-      if (who == crank || (none && crank == 0)) {
-        int32_t *out = a.out_tokens + (int64_t)seq * (a.max_draft + 1);
-        for (int j = lane; j <= a.max_draft; j += 32)
-          out[j] = j < count ? __ldg(x + j) : j == count ? token : -1;
-        if (lane == 0) {
-          if (none) pa::record_error(a.err, pa::kErrCheck);
-          a.num_accepted[seq] = count;
-          if (a.new_lens)
-            a.new_lens[seq] = max(0, __ldg(a.context_lens + seq) - (a.max_draft - count));
-        }
+    }
+    const bool empty = who < 0 && round == 1;  // no weight anywhere: no token
+    if (warp == 0 && (who == crank || (empty && crank == 0))) {
+      const int token = s_token;
+      int32_t *out = a.out_tokens + (int64_t)seq * (a.max_draft + 1);
+      for (int j = lane; j <= a.max_draft; j += 32)
+        out[j] = j < count ? __ldg(x + j) : j == count ? token : -1;
+      if (lane == 0) {
+        if (empty) pa::record_error(a.err, pa::kErrCheck);
+        a.num_accepted[seq] = count;
+        if (a.new_lens)
+          a.new_lens[seq] = max(0, __ldg(a.context_lens + seq) - (a.max_draft - count));
       }
-      if (lane == 0) s_given = who;
     }
     pa::cluster_sync_all();  // the sums have been read: they may be written again, or the CTA exit
-    if (s_given >= 0) break;
+    if (who >= 0) break;
     row.q = nullptr;
     row.skip = -1;
   }
@@ -340,7 +355,7 @@ extern "C" PA_API pa_status pa_verify_drafts(
   a.vocab = vocab;
   a.err = pa::error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
-  const int cluster = 8;
+  const int cluster = kCluster;
   if ((int64_t)num_seqs * cluster >= (int64_t)1 << 31) return PA_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(num_seqs * cluster), 1, 1);
