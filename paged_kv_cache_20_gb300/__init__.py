@@ -484,6 +484,7 @@ def pa_decode_split_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
 # their checks are written for the host's time: one test per tensor on the way that
 # passes, and the reason worked out only on the way that fails.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _device_of(t) -> int:
@@ -492,9 +493,8 @@ def _device_of(t) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("tensors must be CUDA tensors")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if dev != _raw_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_raw_device()}")
     return dev
 
 
@@ -511,12 +511,19 @@ def _refuse(t, name: str, dtype, dev: int):
 
 def _ptr(t, name: str, dtype, dev: int) -> int:
     """Pointer of a contiguous tensor of this type on this device."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev \
-            or not t.is_contiguous():
-        _refuse(t, name, dtype, dev)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    _refuse(t, name, dtype, dev)
+
+
+def _cache_shape(k_cache) -> tuple:
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    return shape
 
 
 def _shape(t, name: str, want: tuple) -> None:
@@ -524,18 +531,18 @@ def _shape(t, name: str, want: tuple) -> None:
         raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
 
 
-def _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, h_kv: int, dev: int):
+def _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, shape, dev: int):
     """Pointers of the caches and their scales (None, None: 16-bit caches of type elt)."""
     if (k_scale is None) != (v_scale is None):
         raise ValueError("give both k_scale and v_scale, or neither")
-    _shape(v_cache, "v_cache", k_cache.shape)
+    _shape(v_cache, "v_cache", shape)
     if k_scale is None:
         return _ptr(k_cache, "k_cache", elt, dev), _ptr(v_cache, "v_cache", elt, dev), None, None
     dt = k_cache.dtype
     if dt not in _FP8_CACHE:
         raise TypeError(f"k_cache must hold e4m3 codes (uint8 or float8_e4m3fn), got {dt}")
-    _shape(k_scale, "k_scale", (h_kv,))
-    _shape(v_scale, "v_scale", (h_kv,))
+    _shape(k_scale, "k_scale", (shape[1],))
+    _shape(v_scale, "v_scale", (shape[1],))
     return (_ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
             _ptr(k_scale, "k_scale", torch.float32, dev), _ptr(v_scale, "v_scale", torch.float32, dev))
 
@@ -543,7 +550,7 @@ def _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, h_kv: int, dev: int):
 def _tokens3(t, name: str, dtype, dev: int, shape) -> tuple[int, int]:
     """Pointer and token stride of [n_tokens, heads, head_dim] with dense heads (a slice
     of a fused projection's output is fine)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
         _cuda(t, name, dtype)
         raise ValueError(f"{name} must be on cuda:{dev}")
     _shape(t, name, shape)
@@ -591,7 +598,7 @@ def pa_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     axis); turns, pair_axis from rope_table.  k_scale, v_scale: FP8 caches.
     """
     dev = _device_of(q)
-    num_blocks, h_kv, block_size, head_dim = _cache_dims(k_cache)
+    num_blocks, h_kv, block_size, head_dim = cache = _cache_shape(k_cache)
     elt = q.dtype
     dt = _elt(q, "q")
     if q.dim() != 3:
@@ -605,7 +612,7 @@ def pa_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     o_ptr, o_st = _tokens3(q_out, "q_out", elt, dev, q_shape)
     k_ptr, k_st = _tokens3(k, "k", elt, dev, kv_shape)
     v_ptr, v_st = _tokens3(v, "v", elt, dev, kv_shape)
-    kc, vc, ks, vs = _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, h_kv, dev)
+    kc, vc, ks, vs = _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, cache, dev)
     axes = positions.shape[0] if positions.dim() == 2 else 1
     if positions.numel() != axes * n_tokens:
         raise ValueError("positions must be [num_axes, n_tokens]")
@@ -645,11 +652,18 @@ def pa_decode_scored(out: torch.Tensor, scores: torch.Tensor, q: torch.Tensor,
     """Paged attention that also adds every cached row's attention weight to scores
     (and notes the positions of this step's rows in row_pos).  FP8 caches with scales."""
     dev = _device_of(q)
-    num_blocks, h_kv, block_size, head_dim, num_seqs, h_q, maxb = _decode_dims(
-        q, k_cache, block_tables, context_lens, q_len)
+    num_blocks, h_kv, block_size, head_dim = cache = _cache_shape(k_cache)
     elt = q.dtype
     dt = _elt(q, "q")
-    _shape(out, "out", q.shape)
+    q_shape, tables = q.shape, block_tables.shape
+    if len(tables) != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    num_seqs, maxb = tables
+    h_q = q_shape[-2]
+    if q_shape != (num_seqs, q_len, h_q, head_dim) and (q_len != 1 or q_shape != (num_seqs, h_q, head_dim)):
+        raise ValueError("q must be [num_seqs, q_len, num_q_heads, head_dim]")
+    _shape(context_lens, "context_lens", (num_seqs,))
+    _shape(out, "out", q_shape)
     ledger = (num_seqs, h_kv, maxb * block_size)
     _shape(scores, "scores", ledger)
     if (row_pos is None) != (seq_lens is None):
@@ -659,7 +673,7 @@ def pa_decode_scored(out: torch.Tensor, scores: torch.Tensor, q: torch.Tensor,
         _shape(row_pos, "row_pos", ledger)
         _shape(seq_lens, "seq_lens", (num_seqs,))
         rp, sl = _ptr(row_pos, "row_pos", torch.int32, dev), _ptr(seq_lens, "seq_lens", torch.int32, dev)
-    kc, vc, ks, vs = _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, h_kv, dev)
+    kc, vc, ks, vs = _cache_pair(k_cache, v_cache, k_scale, v_scale, elt, cache, dev)
     if workspace is None:
         nbytes = pa_decode_scored_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits, maxb,
                                                  block_size)
@@ -691,11 +705,11 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Tensor,
     first ``sinks`` and last ``recent`` positions and its highest scores.  The ledgers are
     updated in place unless both outputs are given.  Returns the new context lengths."""
     dev = _device_of(k_cache)
-    num_blocks, h_kv, block_size, head_dim = _cache_dims(k_cache)
+    num_blocks, h_kv, block_size, head_dim = cache = _cache_shape(k_cache)
     elt = k_cache.dtype
     if elt not in _DTYPE and elt not in _FP8_CACHE:
         raise TypeError(f"k_cache must be 16-bit or hold e4m3 codes, got {elt}")
-    _shape(v_cache, "v_cache", k_cache.shape)
+    _shape(v_cache, "v_cache", cache)
     if block_tables.dim() != 2 or context_lens.dim() != 1:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq], context_lens [num_seqs]")
     num_seqs, maxb = block_tables.shape

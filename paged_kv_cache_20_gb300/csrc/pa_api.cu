@@ -32,6 +32,7 @@ using pa::supported_dtype;
 constexpr int kMaxDevices = 64;
 constexpr int kMaxQLen = 4096;       // query rows per sequence accepted by the ABI
 constexpr int kMaxDecodeQLen = 16;   // at most this many go to the decode kernel
+constexpr int kMaxDecodeRows = 16;   // query rows of a KV head in one row group of it
 // Share of the SMs a cascade's shared-prefix pass runs on (num / den); the rest
 // serve the tail pass that overlaps it.  Measured on 128 sequences sharing a
 // 1024-token prefix (q_len 4, 32/8 heads): 152, 128, 96, 76, 64, 48 and 38 prefix
@@ -412,6 +413,10 @@ struct Placement {
   float *raw_scores = nullptr;
   float *stat_m = nullptr, *stat_l = nullptr;
   float *row_nlse = nullptr;
+  // ... the decode kernel's single pass also updating the ledger itself
+  float *scores = nullptr;
+  int32_t *row_pos = nullptr;
+  const int32_t *seq_lens = nullptr;
 };
 
 // CTAs of a cascade's shared-prefix pass: a share of the SMs, so that the tail
@@ -493,6 +498,10 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
   const bool scored = place.raw_scores != nullptr || place.row_nlse != nullptr;
   a.raw_scores = place.raw_scores;
   a.row_nlse = place.row_nlse;
+  a.scores = place.scores;
+  a.row_pos = place.row_pos;
+  a.seq_lens = place.seq_lens;
+  a.max_rows = max_blocks_per_seq * block_size;
   if (place.stat_m != nullptr) {
     a.ws_m = place.stat_m;
     a.ws_l = place.stat_l;
@@ -996,6 +1005,11 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
   const bool split = !many && num_splits > 1;
   if (many) {
     place.row_nlse = reinterpret_cast<float *>(ws + lay.m_off);
+  } else if (!split && (int64_t)(num_q_heads / num_kv_heads) * q_len <= kMaxDecodeRows) {
+    // one row group holds every query row of a KV head: its CTAs update the ledger
+    place.scores = scores;
+    place.row_pos = row_pos;
+    place.seq_lens = seq_lens;
   } else if (!split) {
     place.stat_m = reinterpret_cast<float *>(ws + lay.m_off);
     place.stat_l = reinterpret_cast<float *>(ws + lay.l_off);
@@ -1011,6 +1025,7 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
                            num_splits, dtype, stream);
     if (st != PA_OK) return st;
   }
+  if (place.scores != nullptr) return PA_OK;
   // 2. the ledger
   pa::LedgerArgs a;
   a.scores = scores;

@@ -107,11 +107,27 @@ struct DecodeArgs {
   int prior_splits;
   // Scored decode (paths built with SC): every score the pass computes, base-2 units,
   // -inf where masked: [num_seqs][num_kv_heads][max_tiles][rows][16 tokens].  The
-  // single pass then also writes its statistics m and l (to ws_m, ws_l).
+  // single pass then also writes its statistics m and l (to ws_m, ws_l, if given).
   float *raw_scores;
+  // Scored single pass with one row group: the ledger is brought up to date by the CTAs
+  // that hold a unit's row sums (scores == nullptr: the caller does it afterwards)
+  float *scores;               // [num_seqs][num_kv_heads][max_rows]
+  int32_t *row_pos;            // the same, or nullptr
+  const int32_t *seq_lens;     // (with row_pos)
+  int max_rows;
   // Scored prefill: -(m + log2 l) of every query row [num_seqs][num_kv_heads][rows]
   float *row_nlse;
 };
+
+// The ledger's entry at `at` (cached row t of a sequence of Lc tokens) gains `share`; rows
+// of this step (the last q_len) start with it, and their position is noted.
+__device__ __forceinline__ void ledger_write(float *scores, int32_t *row_pos, const int32_t *seq_lens,
+                                             int seq, int64_t at, int t, int Lc, int q_len, float old,
+                                             float share) {
+  const bool fresh = t >= Lc - q_len;
+  scores[at] = fresh ? share : old + share;
+  if (fresh && row_pos) row_pos[at] = __ldg(seq_lens + seq) - Lc + t;
+}
 
 // Where a path puts the scores of one tile (row r, token t at p[16 r + t]) for a
 // caller that needs every row's softmax weights once the row sums are known.  The
@@ -1313,6 +1329,8 @@ __global__ void __launch_bounds__(NW * 32)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[NW * NSTAGE];
   __shared__ int s_failed;
+  constexpr bool kLedger = Path::kScored && !PARTIAL;
+  __shared__ float s_row[2][kLedger ? RPC : 1];  // scored: the rows' maxima and 1 / sums
 
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
@@ -1574,7 +1592,7 @@ __global__ void __launch_bounds__(NW * 32)
       }
     } else {
       const size_t orow = (size_t)(seq * a.q_len + ri.u) * a.num_q_heads + ri.h;
-      if (Path::kScored && d8 == 0) {
+      if (Path::kScored && d8 == 0 && a.ws_m != nullptr) {
         a.ws_m[orow] = M;
         a.ws_l[orow] = den;
       }
@@ -1608,6 +1626,49 @@ __global__ void __launch_bounds__(NW * 32)
     }
   };
 
+  // Scored: each warp turns the scores of its own tiles into weights, now that the rows'
+  // sums are known (s_row), and adds them to the ledger.  16 lanes take a tile's tokens;
+  // 2 kTiles tiles' loads are in flight.
+  auto ledger = [&]() {
+    constexpr int kTiles = 4;
+    const size_t unit_id = (size_t)seq * a.num_kv_heads + kvh;
+    const float *raw = a.raw_scores + unit_id * a.max_tiles * a.rows * kTileTokens;
+    const int64_t led = (int64_t)unit_id * a.max_rows;
+    const int Lr = min(L, a.max_rows), tok = lane & 15;
+    for (int n0 = 0; n0 < n_my; n0 += 2 * kTiles) {
+      const float *src[kTiles];
+      float share[kTiles], old[kTiles];
+      int t[kTiles];
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
+        const int nn = n0 + 2 * u + (lane >> 4);
+        const int j = tile_of(min(nn, n_my - 1));
+        t[u] = nn < n_my ? j * kTileTokens + tok : Lr;
+        src[u] = raw + (size_t)j * a.rows * kTileTokens + tok;
+        share[u] = old[u] = 0.f;
+        if (t[u] < Lr) old[u] = a.scores[led + t[u]];
+      }
+      for (int r = 0; r < a.rows; ++r) {
+        const float m = s_row[0][r], inv = s_row[1][r];
+        float x[kTiles];
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) x[u] = src[u][r * kTileTokens];
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) share[u] += fast_exp2(x[u] - m) * inv;
+      }
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u)
+        if (t[u] < Lr)
+          ledger_write(a.scores, a.row_pos, a.seq_lens, seq, led + t[u], t[u], L, a.q_len, old[u], share[u]);
+    }
+  };
+  // (a row that sees nothing has no weights: its scores are -inf, its maximum counts as 0)
+  auto set_row = [&](int r, float M, float den) {
+    s_row[0][r] = M == -INFINITY ? 0.f : M;
+    s_row[1][r] = den > 0.f ? 1.f / den : 0.f;
+  };
+  const bool with_ledger = kLedger && a.scores != nullptr;
+
   // level 1: merge this CTA's warps, item = (row, 8 dims)
   if (!cta_failed) {
     for (int item = threadIdx.x; item < RPC * (D / 8); item += NW * 32) {
@@ -1629,6 +1690,7 @@ __global__ void __launch_bounds__(NW * 32)
       }
       if (csize == 1) {
         emit(r, d8, M, den, num);
+        if (kLedger && d8 == 0) set_row(r, M, den);
       } else {
         float4 *dst = reinterpret_cast<float4 *>(cta_acc + r * kStride + d8 * 8);
         dst[0] = make_float4(num[0], num[1], num[2], num[3]);
@@ -1640,7 +1702,15 @@ __global__ void __launch_bounds__(NW * 32)
       }
     }
   }
-  if (csize == 1) return;
+  if (csize == 1) {
+    if constexpr (kLedger) {
+      if (with_ledger && !cta_failed) {
+        __syncthreads();
+        ledger();
+      }
+    }
+    return;
+  }
 
   // level 2: merge the cluster's CTAs through distributed shared memory; CTA crank
   // takes every csize-th item.  Every CTA reaches both cluster barriers.
@@ -1665,6 +1735,23 @@ __global__ void __launch_bounds__(NW * 32)
         num[4] += wt * x1.x; num[5] += wt * x1.y; num[6] += wt * x1.z; num[7] += wt * x1.w;
       }
       emit(r, d8, M, den, num);
+    }
+    if constexpr (kLedger) {
+      if (with_ledger) {
+        for (int r = threadIdx.x; r < RPC; r += NW * 32) {
+          float M = -INFINITY, den = 0.f;
+          for (int c = 0; c < csize; ++c)
+            M = fmaxf(M, dsmem_ld_f32(dsmem_map(smem_u32(cta_m + r), c)));
+          for (int c = 0; c < csize; ++c) {
+            const float mc = dsmem_ld_f32(dsmem_map(smem_u32(cta_m + r), c));
+            if (mc != -INFINITY)
+              den += fast_exp2(mc - M) * dsmem_ld_f32(dsmem_map(smem_u32(cta_l + r), c));
+          }
+          set_row(r, M, den);
+        }
+        __syncthreads();
+        ledger();
+      }
     }
   }
   cluster_sync_all();  // peers' shared memory stays alive until every read is done

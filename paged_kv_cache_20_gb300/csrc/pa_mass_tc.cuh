@@ -470,9 +470,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&h_free[pair]));
         if (pos < t.L) {
           const int64_t at = ((int64_t)t.seq * a.num_kv_heads + t.kvh) * a.max_rows + pos;
-          const bool fresh = pos >= t.Lc - a.q_len;
-          a.scores[at] = fresh ? share : a.scores[at] + share;
-          if (fresh && a.row_pos) a.row_pos[at] = __ldg(a.seq_lens + t.seq) - t.Lc + pos;
+          ledger_write(a.scores, a.row_pos, a.seq_lens, t.seq, at, pos, t.Lc, a.q_len, a.scores[at], share);
         }
       }
     }

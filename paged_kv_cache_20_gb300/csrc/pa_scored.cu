@@ -6,9 +6,10 @@
 //              2^(s_rt - m_r) / l_r                 (s in base-2 units)
 // with m_r and l_r the row's softmax maximum and sum.  These are known only after the
 // attention pass, so the weights take a second look at the scores:
-//   * up to 16 query tokens: the decode pass leaves its scores in the workspace
-//     (ledger_kernel reads them back: 4 bytes per row and head against the 2 head_dim
-//     16-bit values per row of reading K again and V);
+//   * up to 16 query tokens: the decode pass leaves its scores in the workspace, 4 bytes
+//     per query row and cached row against the 2 head_dim 16-bit values per cached row of
+//     K and V.  They are read back from L2, by the same CTAs where those hold all of a
+//     KV head's rows (pa_decode.cuh), else by ledger_kernel;
 //   * more: the scores would outgrow the cache, so mass_tc_kernel (pa_mass_tc.cuh)
 //     computes them again from K and q.
 // Rows that this step appended (the last q_len) start their scores here, and their
@@ -30,15 +31,6 @@ namespace {
 constexpr int kLedgerThreads = 256;
 constexpr int kRowBatch = 256;  // rows whose statistics are in shared memory at once
 
-// Score and position of cached row t (Lc: the context length as given, which may
-// exceed the table).
-__device__ __forceinline__ void ledger_write(const LedgerArgs &a, int seq, int64_t at, int t, int Lc,
-                                             float share) {
-  const bool fresh = t >= Lc - a.q_len;
-  a.scores[at] = fresh ? share : a.scores[at] + share;
-  if (fresh && a.row_pos) a.row_pos[at] = __ldg(a.seq_lens + seq) - Lc + t;
-}
-
 // A CTA takes 256 cached rows of one (sequence, KV head).
 __global__ void __launch_bounds__(kLedgerThreads) ledger_kernel(const LedgerArgs a) {
   __shared__ float s_m[kRowBatch], s_inv[kRowBatch];
@@ -54,31 +46,42 @@ __global__ void __launch_bounds__(kLedgerThreads) ledger_kernel(const LedgerArgs
                      t % kTileTokens;
   const int heads = a.group * a.num_kv_heads;
   float share = 0.f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t at = (int64_t)unit * a.max_rows + t;
+  const float old = t < L ? a.scores[at] : 0.f;
   for (int r0 = 0; r0 < a.rows; r0 += kRowBatch) {
     const int n = min(kRowBatch, a.rows - r0);
     __syncthreads();
-    for (int r = threadIdx.x; r < n; r += kLedgerThreads) {
-      // merge the partitions' statistics of query token u, head h
+    for (int r = warp; r < n; r += kLedgerThreads / 32) {
+      // a warp merges the partitions' statistics of query token u, head h
       const int u = (r0 + r) / a.group, h = kvh * a.group + (r0 + r) % a.group;
       const size_t base = (size_t)seq * a.splits * a.q_len * heads + (size_t)u * heads + h;
-      float m = -INFINITY, l = 0.f;
-      for (int p = 0; p < a.splits; ++p) {
-        const float mp = a.ws_m[base + (size_t)p * a.q_len * heads];
-        const float lp = a.ws_l[base + (size_t)p * a.q_len * heads];
-        if (!(lp > 0.f)) continue;
-        const float mn = fmaxf(m, mp);
-        l = l * fast_exp2(m - mn) + lp * fast_exp2(mp - mn);
-        m = mn;
+      const size_t step = (size_t)a.q_len * heads;
+      float m = -INFINITY;
+      for (int p = lane; p < a.splits; p += 32)
+        if (a.ws_l[base + p * step] > 0.f) m = fmaxf(m, a.ws_m[base + p * step]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float l = 0.f;
+      for (int p = lane; p < a.splits; p += 32) {
+        const float lp = a.ws_l[base + p * step];
+        if (lp > 0.f) l += lp * fast_exp2(a.ws_m[base + p * step] - m);
       }
-      s_m[r] = m == -INFINITY ? 0.f : m;
-      s_inv[r] = l > 0.f ? 1.f / l : 0.f;  // a row that sees nothing has no weights
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        s_m[r] = m == -INFINITY ? 0.f : m;
+        s_inv[r] = l > 0.f ? 1.f / l : 0.f;  // a row that sees nothing has no weights
+      }
     }
     __syncthreads();
-    if (t < L)
+    if (t < L) {
+#pragma unroll 4
       for (int r = 0; r < n; ++r)
-        share += fast_exp2(raw[(size_t)(r0 + r) * kTileTokens] - s_m[r]) * s_inv[r];
+        share += fast_exp2(__ldcs(raw + (size_t)(r0 + r) * kTileTokens) - s_m[r]) * s_inv[r];
+    }
   }
-  if (t < L) ledger_write(a, seq, (int64_t)unit * a.max_rows + t, t, Lc, share);
+  if (t < L) ledger_write(a.scores, a.row_pos, a.seq_lens, seq, at, t, Lc, a.q_len, old, share);
 }
 
 template <typename T, int D, bool KV8>
