@@ -368,6 +368,20 @@ WsLayout ws_layout(int num_seqs, int num_q_heads, int q_len, int head_dim, int n
   return w;
 }
 
+pa::CombineArgs combine_args(void *out, const void *workspace, const WsLayout &lay, int num_seqs,
+                             int rows_per_seq, int num_splits) {
+  const char *base = static_cast<const char *>(workspace);
+  pa::CombineArgs a;
+  a.out = out;
+  a.ws_acc = reinterpret_cast<const float *>(base + lay.acc_off);
+  a.ws_m = reinterpret_cast<const float *>(base + lay.m_off);
+  a.ws_l = reinterpret_cast<const float *>(base + lay.l_off);
+  a.num_seqs = num_seqs;
+  a.rows_per_seq = rows_per_seq;
+  a.num_splits = num_splits;
+  return a;
+}
+
 // Checks shared by pa_decode and pa_decode_partial.
 pa_status check_decode(const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *block_tables, const int32_t *context_lens, int num_seqs,
@@ -901,15 +915,7 @@ PA_API pa_status pa_decode_combine(void *out, const void *workspace, size_t work
   if ((int64_t)num_seqs * q_len * num_q_heads >= (int64_t)1 << 31) return PA_ERR_INVALID_ARG;
   const WsLayout lay = ws_layout(num_seqs, num_q_heads, q_len, head_dim, num_splits);
   if (workspace_bytes < lay.total) return PA_ERR_INVALID_ARG;
-  const char *base = static_cast<const char *>(workspace);
-  pa::CombineArgs a;
-  a.out = out;
-  a.ws_acc = reinterpret_cast<const float *>(base + lay.acc_off);
-  a.ws_m = reinterpret_cast<const float *>(base + lay.m_off);
-  a.ws_l = reinterpret_cast<const float *>(base + lay.l_off);
-  a.num_seqs = num_seqs;
-  a.rows_per_seq = q_len * num_q_heads;
-  a.num_splits = num_splits;
+  const pa::CombineArgs a = combine_args(out, workspace, lay, num_seqs, q_len * num_q_heads, num_splits);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = dtype == PA_FP16 ? pa::launch_combine_fp16(a, head_dim, s)
                                    : pa::launch_combine_bf16(a, head_dim, s);
@@ -983,9 +989,9 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
                                   int block_size, float scale, int max_blocks_per_seq,
                                   int num_blocks, int q_len, pa_dtype dtype, int num_splits,
                                   void *workspace, size_t workspace_bytes, void *stream) {
-  if (!out || !aligned16(out) || !scores || !pa::aligned4(scores)) return PA_ERR_INVALID_ARG;
+  if (!out || !aligned16(out) || !scores || !aligned16(scores)) return PA_ERR_INVALID_ARG;
   if ((row_pos == nullptr) != (seq_lens == nullptr)) return PA_ERR_INVALID_ARG;
-  if (!pa::aligned4(row_pos)) return PA_ERR_INVALID_ARG;
+  if (!aligned16(row_pos)) return PA_ERR_INVALID_ARG;
   if ((k_scale == nullptr) != (v_scale == nullptr)) return PA_ERR_INVALID_ARG;
   if (num_splits <= 0 || num_splits >= (1 << 20)) return PA_ERR_INVALID_ARG;
   pa_status st = check_decode(q, k_cache, v_cache, block_tables, context_lens, num_seqs,
@@ -1020,13 +1026,8 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
                      max_blocks_per_seq, num_blocks, q_len, dtype, stream, nullptr, nullptr, k_scale,
                      v_scale, place);
   if (st != PA_OK) return st;
-  if (split) {
-    st = pa_decode_combine(out, workspace, workspace_bytes, num_seqs, num_q_heads, head_dim, q_len,
-                           num_splits, dtype, stream);
-    if (st != PA_OK) return st;
-  }
   if (place.scores != nullptr) return PA_OK;
-  // 2. the ledger
+  // 2. the ledger (and the merge of the partitions)
   pa::LedgerArgs a;
   a.scores = scores;
   a.row_pos = row_pos;
@@ -1055,7 +1056,13 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
   a.err = error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!many) return pa::launch_ledger(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (!many) {
+    const pa::CombineArgs c = combine_args(out, workspace, lay.split, num_seqs, q_len * num_q_heads,
+                                           num_splits);
+    return pa::launch_finish(a, split ? &c : nullptr, head_dim, dtype == PA_FP16, s) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+  }
   int heads = 0, toks = 0;
   pa::mass_q_box(a.group, &heads, &toks);
   // (a launch takes a bounded number of sequences)

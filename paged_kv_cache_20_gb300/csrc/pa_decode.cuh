@@ -1766,14 +1766,11 @@ struct CombineArgs {
   int num_seqs, rows_per_seq, num_splits;
 };
 
+// Row gw (of num_seqs * rows_per_seq) by the calling warp.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) split_combine_kernel(const CombineArgs a) {
+__device__ __forceinline__ void combine_row(const CombineArgs &a, int gw) {
   constexpr int PER = D / 32;  // dims per lane
-  const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (gw >= a.num_seqs * a.rows_per_seq) return;
-  griddep_wait();  // the workspace comes from the partial pass just before
-  griddep_launch_dependents();
   const int seq = gw / a.rows_per_seq, r = gw % a.rows_per_seq;
   const size_t base = (size_t)seq * a.num_splits * a.rows_per_seq + r;
   const size_t pstride = a.rows_per_seq;
@@ -1821,19 +1818,24 @@ __global__ void __launch_bounds__(128) split_combine_kernel(const CombineArgs a)
     *reinterpret_cast<uint32_t *>(o + k) = Elt<T>::from_f2(num[k] * inv, num[k + 1] * inv);
 }
 
+template <typename T, int D>
+__global__ void __launch_bounds__(128) split_combine_kernel(const CombineArgs a) {
+  const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (gw >= a.num_seqs * a.rows_per_seq) return;
+  griddep_wait();  // the workspace comes from the partial pass just before
+  griddep_launch_dependents();
+  combine_row<T, D>(a, gw);
+}
+
 // With few rows and many partitions the warps of the form above are too few to
 // hide the partitions' load latency: this form gives each row D / 32 warps, one
 // dimension per lane, every partition's load of that dimension in flight at once.
 // The partitions are summed in the same order, so both forms give the same bits.
+// Dimensions 32 part .. 32 part + 31 of row row_id by the calling warp.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) split_combine_spread_kernel(const CombineArgs a) {
-  constexpr int kWarpsPerRow = D / 32;
-  const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+__device__ __forceinline__ void combine_row_part(const CombineArgs &a, int row_id, int part) {
   const int lane = threadIdx.x & 31;
-  const int row_id = gw / kWarpsPerRow, dim = (gw % kWarpsPerRow) * 32 + lane;
-  if (row_id >= a.num_seqs * a.rows_per_seq) return;
-  griddep_wait();  // the workspace comes from the partial pass just before
-  griddep_launch_dependents();
+  const int dim = part * 32 + lane;
   const int seq = row_id / a.rows_per_seq, r = row_id % a.rows_per_seq;
   const size_t base = (size_t)seq * a.num_splits * a.rows_per_seq + r;
   const size_t pstride = a.rows_per_seq;
@@ -1868,5 +1870,21 @@ __global__ void __launch_bounds__(128) split_combine_spread_kernel(const Combine
   static_cast<uint16_t *>(a.out)[((size_t)seq * a.rows_per_seq + r) * D + dim] =
       Elt<T>::from_f(num * inv);
 }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(128) split_combine_spread_kernel(const CombineArgs a) {
+  constexpr int kWarpsPerRow = D / 32;
+  const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (gw / kWarpsPerRow >= a.num_seqs * a.rows_per_seq) return;
+  griddep_wait();  // the workspace comes from the partial pass just before
+  griddep_launch_dependents();
+  combine_row_part<T, D>(a, gw / kWarpsPerRow, gw % kWarpsPerRow);
+}
+
+// Which form a combine of so many partitions and rows takes: one dimension per lane for
+// more than 8 partitions of at most 512 rows.  Measured on GB300: 4 x 32 rows of 16
+// partitions, 92.5 -> 90.5 us per step; 8 x 32 rows of 8 partitions and 64 x 32 rows of
+// 4 partitions were slower spread.
+inline bool combine_spread(int num_splits, long long rows) { return num_splits > 8 && rows <= 512; }
 
 }  // namespace pa

@@ -9,7 +9,7 @@
 //   * up to 16 query tokens: the decode pass leaves its scores in the workspace, 4 bytes
 //     per query row and cached row against the 2 head_dim 16-bit values per cached row of
 //     K and V.  They are read back from L2, by the same CTAs where those hold all of a
-//     KV head's rows (pa_decode.cuh), else by ledger_kernel;
+//     KV head's rows (pa_decode.cuh), else by finish_kernel;
 //   * more: the scores would outgrow the cache, so mass_tc_kernel (pa_mass_tc.cuh)
 //     computes them again from K and q.
 // Rows that this step appended (the last q_len) start their scores here, and their
@@ -29,26 +29,53 @@ namespace pa {
 namespace {
 
 constexpr int kLedgerThreads = 256;
-constexpr int kRowBatch = 256;  // rows whose statistics are in shared memory at once
+constexpr int kLedgerRows = 4 * kLedgerThreads;  // cached rows of a CTA, four a thread
+constexpr int kRowBatch = 64;   // query rows whose statistics are in shared memory at once
+constexpr int kAhead = 4;       // scores loaded before the statistics are known
 
-// A CTA takes 256 cached rows of one (sequence, KV head).
-__global__ void __launch_bounds__(kLedgerThreads) ledger_kernel(const LedgerArgs a) {
+// What follows the decode pass when its CTAs do not hold a KV head's row sums: CTAs below
+// combine_blocks merge the partitions into the output (SPREAD: one dimension per lane),
+// the others take kLedgerRows cached rows of one (sequence, KV head) each.  One launch
+// for both: neither is long (6.6 and 20 us as two launches over 4 x 32768 tokens in 16
+// partitions), and both wait on loads.
+template <typename T, int D, bool SPREAD>
+__global__ void __launch_bounds__(kLedgerThreads) finish_kernel(const LedgerArgs a, const CombineArgs c,
+                                                                int combine_blocks) {
   __shared__ float s_m[kRowBatch], s_inv[kRowBatch];
   griddep_wait();
   griddep_launch_dependents();
-  const int chunks = (a.max_rows + kLedgerThreads - 1) / kLedgerThreads;
-  const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int)blockIdx.x < combine_blocks) {
+    constexpr int kParts = SPREAD ? D / 32 : 1;
+    const int gw = blockIdx.x * (kLedgerThreads / 32) + warp;
+    if (gw / kParts >= c.num_seqs * c.rows_per_seq) return;
+    if constexpr (SPREAD)
+      combine_row_part<T, D>(c, gw / kParts, gw % kParts);
+    else
+      combine_row<T, D>(c, gw);
+    return;
+  }
+  const int id = blockIdx.x - combine_blocks;
+  const int chunks = (a.max_rows + kLedgerRows - 1) / kLedgerRows;
+  const int unit = id / chunks, chunk = id % chunks;
   const int seq = unit / a.num_kv_heads, kvh = unit % a.num_kv_heads;
   const int Lc = max(0, __ldg(a.context_lens + seq)), L = min(Lc, a.max_rows);
-  if (chunk * kLedgerThreads >= L) return;
-  const int t = chunk * kLedgerThreads + threadIdx.x;
-  const float *raw = a.raw_scores + ((size_t)unit * a.max_tiles + t / kTileTokens) * a.rows * kTileTokens +
-                     t % kTileTokens;
-  const int heads = a.group * a.num_kv_heads;
-  float share = 0.f;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (chunk * kLedgerRows >= L) return;
+  const int t = chunk * kLedgerRows + 4 * threadIdx.x;  // this thread's rows t .. t + 3
+  const float4 *raw = reinterpret_cast<const float4 *>(
+      a.raw_scores + ((size_t)unit * a.max_tiles + t / kTileTokens) * a.rows * kTileTokens + t % kTileTokens);
+  constexpr int kStep = kTileTokens / 4;  // float4s between query rows
   const int64_t at = (int64_t)unit * a.max_rows + t;
-  const float old = t < L ? a.scores[at] : 0.f;
+  const bool in = t < L;  // (a table holds a multiple of 8 rows)
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f), x[kAhead];
+  if (in) old = *reinterpret_cast<const float4 *>(a.scores + at);
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r) {
+    x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in && r < a.rows) x[r] = raw[r * kStep];
+  }
+  const int heads = a.group * a.num_kv_heads;
+  float4 share = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int r0 = 0; r0 < a.rows; r0 += kRowBatch) {
     const int n = min(kRowBatch, a.rows - r0);
     __syncthreads();
@@ -57,15 +84,18 @@ __global__ void __launch_bounds__(kLedgerThreads) ledger_kernel(const LedgerArgs
       const int u = (r0 + r) / a.group, h = kvh * a.group + (r0 + r) % a.group;
       const size_t base = (size_t)seq * a.splits * a.q_len * heads + (size_t)u * heads + h;
       const size_t step = (size_t)a.q_len * heads;
-      float m = -INFINITY;
-      for (int p = lane; p < a.splits; p += 32)
-        if (a.ws_l[base + p * step] > 0.f) m = fmaxf(m, a.ws_m[base + p * step]);
+      float m = -INFINITY, l = 0.f;
+      for (int p0 = 0; p0 < a.splits; p0 += 32) {
+        const int p = p0 + lane;
+        const float lp = p < a.splits ? a.ws_l[base + p * step] : 0.f;
+        const float mp = p < a.splits ? a.ws_m[base + p * step] : -INFINITY;
+        float mx = lp > 0.f ? mp : -INFINITY;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float l = 0.f;
-      for (int p = lane; p < a.splits; p += 32) {
-        const float lp = a.ws_l[base + p * step];
-        if (lp > 0.f) l += lp * fast_exp2(a.ws_m[base + p * step] - m);
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(mx, m);
+        if (mx == -INFINITY) continue;
+        l = l * fast_exp2(m - mx) + (lp > 0.f ? lp * fast_exp2(mp - mx) : 0.f);
+        m = mx;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -75,13 +105,47 @@ __global__ void __launch_bounds__(kLedgerThreads) ledger_kernel(const LedgerArgs
       }
     }
     __syncthreads();
-    if (t < L) {
+    auto add = [&](const float4 &v, int r) {
+      const float m = s_m[r], inv = s_inv[r];
+      share.x += fast_exp2(v.x - m) * inv;
+      share.y += fast_exp2(v.y - m) * inv;
+      share.z += fast_exp2(v.z - m) * inv;
+      share.w += fast_exp2(v.w - m) * inv;
+    };
+    int r = 0;
+    if (r0 == 0) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < n) add(x[i], i);
+      r = kAhead;
+    }
+    if (in) {
 #pragma unroll 4
-      for (int r = 0; r < n; ++r)
-        share += fast_exp2(__ldcs(raw + (size_t)(r0 + r) * kTileTokens) - s_m[r]) * s_inv[r];
+      for (; r < n; ++r) add(raw[(size_t)(r0 + r) * kStep], r);
     }
   }
-  if (t < L) ledger_write(a.scores, a.row_pos, a.seq_lens, seq, at, t, Lc, a.q_len, old, share);
+  const float s[4] = {share.x, share.y, share.z, share.w}, o[4] = {old.x, old.y, old.z, old.w};
+  if (in && t + 4 <= Lc - a.q_len) {
+    *reinterpret_cast<float4 *>(a.scores + at) = make_float4(o[0] + s[0], o[1] + s[1], o[2] + s[2], o[3] + s[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t + i < L)
+        ledger_write(a.scores, a.row_pos, a.seq_lens, seq, at + i, t + i, Lc, a.q_len, o[i], s[i]);
+  }
+}
+
+template <typename T, int D>
+cudaError_t finish_t(const LedgerArgs &a, const CombineArgs &c, bool combine, cudaStream_t st) {
+  const long long ledger = (long long)a.num_seqs * a.num_kv_heads * ((a.max_rows + kLedgerRows - 1) / kLedgerRows);
+  const long long rows = combine ? (long long)c.num_seqs * c.rows_per_seq : 0;
+  const bool spread = combine && combine_spread(c.num_splits, rows);
+  const long long warps = spread ? rows * (D / 32) : rows;
+  const long long blocks = (warps + kLedgerThreads / 32 - 1) / (kLedgerThreads / 32);
+  if (ledger + blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(ledger + blocks), 1, 1);
+  return spread ? launch_dependent(finish_kernel<T, D, true>, grid, kLedgerThreads, st, a, c, (int)blocks)
+                : launch_dependent(finish_kernel<T, D, false>, grid, kLedgerThreads, st, a, c, (int)blocks);
 }
 
 template <typename T, int D, bool KV8>
@@ -127,11 +191,14 @@ cudaError_t mass_t(const CUtensorMap &qmap, const LedgerArgs &a, int head_dim, b
 
 }  // namespace
 
-cudaError_t launch_ledger(const LedgerArgs &a, cudaStream_t s) {
-  const long long blocks = (long long)a.num_seqs * a.num_kv_heads *
-                           ((a.max_rows + kLedgerThreads - 1) / kLedgerThreads);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_dependent(ledger_kernel, (unsigned)blocks, kLedgerThreads, s, a);
+cudaError_t launch_finish(const LedgerArgs &a, const CombineArgs *c, int head_dim, bool fp16,
+                          cudaStream_t s) {
+  const CombineArgs cc = c ? *c : CombineArgs();
+  if (head_dim == 128)
+    return fp16 ? finish_t<__half, 128>(a, cc, c != nullptr, s)
+                : finish_t<__nv_bfloat16, 128>(a, cc, c != nullptr, s);
+  return fp16 ? finish_t<__half, 64>(a, cc, c != nullptr, s)
+              : finish_t<__nv_bfloat16, 64>(a, cc, c != nullptr, s);
 }
 
 cudaError_t launch_mass(const CUtensorMap &qmap, const LedgerArgs &a, int head_dim, bool fp16,

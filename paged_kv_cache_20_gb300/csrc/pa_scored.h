@@ -8,6 +8,7 @@
 namespace pa {
 
 struct DecodeArgs;
+struct CombineArgs;
 
 // The second part of scored attention: weights from the scores and the rows'
 // statistics, added to the ledger.
@@ -29,7 +30,10 @@ struct LedgerArgs {
   unsigned *err;
 };
 
-cudaError_t launch_ledger(const LedgerArgs &args, cudaStream_t stream);
+// After a decode pass that left its scores: the ledger, and with `combine` the merge of
+// the partitions into the output, in one launch.
+cudaError_t launch_finish(const LedgerArgs &args, const CombineArgs *combine, int head_dim, bool fp16,
+                          cudaStream_t stream);
 // Many query rows: the scores again from K and q on the tensor cores.  qmap: tensor map
 // over q with a box of 64 columns x the heads x the tokens that mass_q_box names.  At
 // most mass_max_seqs() sequences per launch.

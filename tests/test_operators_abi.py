@@ -44,8 +44,8 @@ SCORED = dict(out=FAKE, scores=FAKE, pos=FAKE, q=FAKE, k=FAKE, v=FAKE, ks=None, 
 @pytest.mark.parametrize("kw,status", [
     ({}, INVALID),  # no room in the workspace
     ({"ws": None}, INVALID), ({"ws": FAKE + 16}, INVALID), ({"out": None}, INVALID),
-    ({"scores": None}, INVALID), ({"scores": FAKE + 2}, INVALID), ({"pos": None}, INVALID),
-    ({"sl": None}, INVALID), ({"pos": FAKE + 1}, INVALID), ({"ks": FAKE}, INVALID),
+    ({"scores": None}, INVALID), ({"scores": FAKE + 4}, INVALID), ({"pos": None}, INVALID),
+    ({"sl": None}, INVALID), ({"pos": FAKE + 8}, INVALID), ({"ks": FAKE}, INVALID),
     ({"splits": 0}, INVALID), ({"splits": 1 << 20}, INVALID), ({"hq": 9}, INVALID), ({"u": 0}, INVALID),
     ({"scale": float("inf")}, INVALID), ({"u": 4097}, UNSUPPORTED), ({"d": 80}, UNSUPPORTED),
     ({"bs": 64}, UNSUPPORTED), ({"dtype": 2}, UNSUPPORTED),
