@@ -348,7 +348,7 @@ PA_API pa_status pa_decode_split_noalloc(void *out, const void *q, const void *k
  * type, or (k_scale and v_scale both non-NULL: FP8 cache, head_dim 128) to
  * e4m3(x / scale[kv_head]) for the cache.  After pa_evict a token's cache row is no
  * longer its position, so positions are always explicit.
- *   positions     int32 [num_axes][n_tokens]  (e.g. time, height, width)
+ *   positions     int32 [num_axes][n_tokens]  (e.g. time, height, width; at most 32 axes)
  *   slot_mapping  int64 [n_tokens], as for pa_append_kv; a token with a negative slot,
  *                 or one past the pool (PA_ERR_DEVICE_CHECK), has its q rotated only
  *   turns         int64 [rotary_dim/2]: f_i in turns per position, units of 2^-64

@@ -14,6 +14,12 @@
 // product position * F_i modulo 2^64 is the fraction of a turn, exact in integer
 // arithmetic up to |position| * 2^-65 turns from F_i's own rounding.  Its upper 32
 // bits, as a signed number of half turns in [-1, 1), go to sincospif.
+//
+// Bound by DRAM: every byte of q, k, v once in and once out.  A CTA walks tokens, each
+// thread on the same items of every token, with the next token's loads and angles under
+// way while it rotates and stores the current one; a barrier per token hands the angles
+// over.  8192 tokens of 32/8 heads: MEASURED us; with one CTA per token, whose first load
+// or first store waits for the angles, 42.5 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,41 +40,50 @@ struct RopeArgs {
   const int32_t *pair_axis;     // [rotary_dim / 2]
   int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
   int64_t num_slots;
-  int n_tokens, num_q_heads, num_kv_heads, half, num_axes, block_size;
+  int n_tokens, num_q_heads, num_kv_heads, half, num_axes, block_shift;
   const float *k_scale, *v_scale;
   unsigned *err;
 };
 
-// Eight rotated pairs: a (16 bytes of first elements) and b (of second elements),
-// cs[0..7] their (cos, sin); fp32 results in x (a') and y (b').
+// The angles of a token in shared memory, (cos, sin) a pair, placed so that the eight
+// lanes of a 16-byte read phase, which hold consecutive chunks, fall on eight different
+// bank groups (pair after pair they would share two or four): halves apart, pairs
+// 8 c + 2 q and + 1 at [q][c]; adjacent, pairs 4 j + 2 q and + 1 at [q][j].
+template <bool ADJ>
+__device__ __forceinline__ int angle_at(int pair) {
+  return ADJ ? 2 * (16 * ((pair >> 1) & 1) + (pair >> 2)) + (pair & 1)
+             : 2 * (8 * ((pair >> 1) & 3) + (pair >> 3)) + (pair & 1);
+}
+
+// Eight rotated pairs, 8 c .. 8 c + 7: a (16 bytes of first elements) and b (of second
+// elements); fp32 results in x (a') and y (b').
 template <typename T>
-__device__ __forceinline__ void rotate8(const uint4 a, const uint4 b, const float2 *cs,
+__device__ __forceinline__ void rotate8(const uint4 a, const uint4 b, const float2 *cs, int c,
                                         float (&x)[8], float (&y)[8]) {
   const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 fa = pa::Elt<T>::to_f2(wa[i]), fb = pa::Elt<T>::to_f2(wb[i]);
-    const float4 c = *reinterpret_cast<const float4 *>(cs + 2 * i);  // cos, sin of two pairs
-    x[2 * i] = fmaf(fa.x, c.x, -fb.x * c.y);
-    y[2 * i] = fmaf(fb.x, c.x, fa.x * c.y);
-    x[2 * i + 1] = fmaf(fa.y, c.z, -fb.y * c.w);
-    y[2 * i + 1] = fmaf(fb.y, c.z, fa.y * c.w);
+    const float4 t = *reinterpret_cast<const float4 *>(cs + 2 * (8 * i + c));  // of two pairs
+    x[2 * i] = fmaf(fa.x, t.x, -fb.x * t.y);
+    y[2 * i] = fmaf(fb.x, t.x, fa.x * t.y);
+    x[2 * i + 1] = fmaf(fa.y, t.z, -fb.y * t.w);
+    y[2 * i + 1] = fmaf(fb.y, t.z, fa.y * t.w);
   }
 }
 
-// Eight adjacent pairs in 32 bytes a, b: the same with the pairs' elements adjacent;
-// x holds the results for a's elements, y for b's.
+// Four adjacent pairs, chunk j of a head (elements 8 j .. 8 j + 7).
 template <typename T>
-__device__ __forceinline__ void rotate8_adjacent(const uint4 a, const uint4 b, const float2 *cs,
-                                                 float (&x)[8], float (&y)[8]) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void rotate4_adjacent(const uint4 a, const float2 *cs, int j, float (&x)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = pa::Elt<T>::to_f2(w[i]);
-    const float2 c = cs[i];
-    float *o = i < 4 ? x + 2 * i : y + 2 * (i - 4);
-    o[0] = fmaf(f.x, c.x, -f.y * c.y);
-    o[1] = fmaf(f.y, c.x, f.x * c.y);
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = pa::Elt<T>::to_f2(w[2 * i]), g = pa::Elt<T>::to_f2(w[2 * i + 1]);
+    const float4 t = *reinterpret_cast<const float4 *>(cs + 2 * (16 * i + j));
+    x[4 * i] = fmaf(f.x, t.x, -f.y * t.y);
+    x[4 * i + 1] = fmaf(f.y, t.x, f.x * t.y);
+    x[4 * i + 2] = fmaf(g.x, t.z, -g.y * t.w);
+    x[4 * i + 3] = fmaf(g.y, t.z, g.x * t.w);
   }
 }
 
@@ -89,109 +104,225 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
                     pa::Elt<T>::from_f2(x[4], x[5]), pa::Elt<T>::from_f2(x[6], x[7]));
 }
 
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
+// x / scale, correctly rounded, for a head's many x: with r = 1 / scale rounded,
+// q = x r and the exact remainder x - q scale, q + remainder r is the rounded quotient
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990), where nothing underflows: a scale within 2^+-60 keeps every quotient
+// that is not far below e4m3's smallest step clear of that.  Quotients beyond 2^60
+// saturate as they are, zeros keep their sign; other scales divide.
+struct Divisor {
+  float scale, r;
+  bool near;
+  __device__ __forceinline__ void set(float s) {
+    scale = s;
+    r = 1.f / s;
+    near = fabsf(s) >= 0x1p-60f && fabsf(s) <= 0x1p60f;
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    const float q = x * r;
+    const float p = fmaf(fmaf(-q, scale, x), r, q);
+    return fabsf(q) <= 0x1p60f && q != 0.f ? p : q;
+  }
+};
+
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], const Divisor &d) {
   uint32_t c[4];
+  if (d.near) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = pa::f32x2_to_e4m3x2(x[2 * i] / scale, x[2 * i + 1] / scale);
+    for (int i = 0; i < 4; ++i) c[i] = pa::f32x2_to_e4m3x2(d(x[2 * i]), d(x[2 * i + 1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = pa::f32x2_to_e4m3x2(x[2 * i] / d.scale, x[2 * i + 1] / d.scale);
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 constexpr int kMaxHalf = 64;  // rotary pairs per head at most (head_dim 128)
+constexpr int kMaxAxes = 32;
+constexpr int kThreads = 384;  // at most
 
-// CTA t takes token t.  An item is 16 elements of one head: the two 16-byte chunks
-// of eight rotated pairs, or two adjacent chunks that are copied (V, and elements
-// past rotary_dim).  Heads are numbered q, then K, then V.
-template <typename T, int D, bool ADJ, bool KV8>
-__global__ void rope_append_kernel(const RopeArgs a) {
+// An item is two 16-byte chunks of one head.  The chunks that are rotated (and, apart from
+// them, those that are copied: V, and elements past rotary_dim) are paired first half with
+// second half, so that consecutive lanes read and write consecutive chunks, and with the
+// halves apart a pair's two elements are in one item.  A token's heads are numbered q,
+// then K, then V.  Thread i of block row y takes items (y IPT + u) blockDim + i
+// of tokens blockIdx.x, + gridDim.x, ...
+template <typename T, int D, bool ADJ, bool KV8, int IPT>
+__global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs a) {
   constexpr int kItems = D / 16;  // items of a head
-  __shared__ __align__(16) float2 cs[kMaxHalf];
+  __shared__ __align__(16) float2 cs[2][kMaxHalf];
+  __shared__ int64_t s_turn[kMaxHalf];
+  __shared__ int s_axis[kMaxHalf], s_pos[2][kMaxAxes];
+  __shared__ int64_t s_slot[3];
   pa::griddep_wait();
   pa::griddep_launch_dependents();
-  const int64_t t = blockIdx.x;
-  for (int i = threadIdx.x; i < a.half; i += blockDim.x) {
+  const int tid = threadIdx.x;
+  const int hq = a.num_q_heads, hkv = a.num_kv_heads;
+  const int64_t G = gridDim.x;
+
+  // this thread's items, the same of every token: where they come from and go to (bytes,
+  // the token's own offset apart), kind 0 q, 1 K, 2 V, 3 none
+  const int64_t q_step = G * a.q_stride * 2, k_step = G * a.k_stride * 2, v_step = G * a.v_stride * 2;
+  const char *src[IPT];
+  char *dst[IPT];
+  int kind[IPT], d0[IPT], d1[IPT], pairs[IPT];  // d0, d1: the chunks' elements; pairs: < 0 copied
+  Divisor div[IPT];
+#pragma unroll
+  for (int u = 0; u < IPT; ++u) {
+    const int it = (blockIdx.y * IPT + u) * blockDim.x + tid;
+    const int h = it / kItems, c = it % kItems;
+    kind[u] = h < hq ? 0 : h < hq + hkv ? 1 : h < hq + 2 * hkv ? 2 : 3;
+    const int64_t hh = kind[u] == 0 ? h : kind[u] == 1 ? h - hq : h - hq - hkv;
+    const int rot_items = kind[u] < 2 ? a.half / 8 : 0;
+    const bool rot = c < rot_items;
+    const int chunk = rot ? c : rot_items + c;  // (copied: 2 rot_items + (c - rot_items))
+    d0[u] = 8 * chunk;
+    d1[u] = 8 * (chunk + (rot ? rot_items : kItems - rot_items));
+    pairs[u] = rot ? c : -1;
+    const int64_t t0 = blockIdx.x;
+    src[u] = reinterpret_cast<const char *>(kind[u] == 0   ? a.q + t0 * a.q_stride + hh * D
+                                            : kind[u] == 1 ? a.k + t0 * a.k_stride + hh * D
+                                                           : a.v + t0 * a.v_stride + hh * D);
+    dst[u] = kind[u] == 0 ? reinterpret_cast<char *>(a.q_out + hh * D)
+                          : static_cast<char *>(kind[u] == 1 ? a.k_cache : a.v_cache) +
+                                (hh << a.block_shift) * (D * (KV8 ? 1 : 2));
+    if (KV8) div[u].set(kind[u] == 1 ? __ldg(a.k_scale + hh) : kind[u] == 2 ? __ldg(a.v_scale + hh) : 1.f);
+  }
+  // the items of the token that src stands at, and on to this CTA's next one
+  auto load = [&](uint4 (&x)[IPT][2]) {
+#pragma unroll
+    for (int u = 0; u < IPT; ++u) {
+      if (kind[u] != 3) {
+        x[u][0] = *reinterpret_cast<const uint4 *>(src[u] + 2 * d0[u]);
+        x[u][1] = *reinterpret_cast<const uint4 *>(src[u] + 2 * d1[u]);
+      }
+      src[u] += kind[u] == 0 ? q_step : kind[u] == 1 ? k_step : v_step;
+    }
+  };
+  auto angles = [&](int buf) {
+    for (int i = tid; i < a.half; i += blockDim.x) {
+      const uint64_t turn = (uint64_t)(int64_t)s_pos[buf][s_axis[i]] * (uint64_t)s_turn[i];
+      const float h = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // half turns
+      float s, c;
+      sincospif(h, &s, &c);
+      cs[buf][angle_at<ADJ>(i)] = make_float2(c, s);
+    }
+  };
+  auto position = [&](int64_t t) {
+    return tid < a.num_axes && t < a.n_tokens ? __ldg(a.positions + (int64_t)tid * a.n_tokens + t) : 0;
+  };
+  auto slot_of = [&](int64_t t) -> int64_t {
+    if (tid != 0 || t >= a.n_tokens) return -1;
+    const int64_t slot = __ldg(a.slot_mapping + t);
+    if (slot >= a.num_slots) {
+      pa::record_error(a.err, pa::kErrCheck);
+      return -1;
+    }
+    return slot;
+  };
+
+  int64_t t = blockIdx.x;
+  uint4 x[IPT][2];
+  load(x);
+  for (int i = tid; i < a.half; i += blockDim.x) {
     int axis = __ldg(a.pair_axis + i);
     if (axis < 0 || axis >= a.num_axes) {
       pa::record_error(a.err, pa::kErrCheck);
       axis = 0;
     }
-    const int64_t pos = __ldg(a.positions + (int64_t)axis * a.n_tokens + t);
-    const uint64_t turn = (uint64_t)pos * (uint64_t)__ldg(a.turns + i);
-    const float h = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // half turns
-    float s, c;
-    sincospif(h, &s, &c);
-    cs[i] = make_float2(c, s);
+    s_axis[i] = axis;
+    s_turn[i] = __ldg(a.turns + i);
   }
-  int64_t blk = -1;
-  int off = 0;
-  const int64_t slot = __ldg(a.slot_mapping + t);
-  if (slot >= a.num_slots) {
-    if (threadIdx.x == 0) pa::record_error(a.err, pa::kErrCheck);
-  } else if (slot >= 0) {
-    blk = slot / a.block_size;
-    off = (int)(slot - blk * a.block_size);
+  {
+    const int p0 = position(t), p1 = position(t + G);
+    const int64_t l0 = slot_of(t), l1 = slot_of(t + G);
+    if (tid < a.num_axes) {
+      s_pos[0][tid] = p0;
+      s_pos[1][tid] = p1;
+    }
+    if (tid == 0) {
+      s_slot[0] = l0;
+      s_slot[1] = l1;
+    }
   }
   __syncthreads();
+  angles(0);
+  __syncthreads();
 
-  const int hq = a.num_q_heads, hkv = a.num_kv_heads;
-  const int rot_items = a.half / 8;
-  const int heads = blk < 0 ? hq : hq + 2 * hkv;  // without a slot only q is rotated
-  for (int it = threadIdx.x; it < heads * kItems; it += blockDim.x) {
-    const int h = it / kItems, c = it % kItems;
-    const bool is_q = h < hq, is_k = !is_q && h < hq + hkv;
-    const uint16_t *src = is_q ? a.q + t * a.q_stride + (int64_t)h * D
-                         : is_k ? a.k + t * a.k_stride + (int64_t)(h - hq) * D
-                                : a.v + t * a.v_stride + (int64_t)(h - hq - hkv) * D;
-    const bool rot = (is_q || is_k) && c < rot_items;
-    const int e0 = (rot && !ADJ) ? 8 * c : 16 * c;
-    const int e1 = (rot && !ADJ) ? 8 * c + a.half : 16 * c + 8;
-    const uint4 u0 = *reinterpret_cast<const uint4 *>(src + e0);
-    const uint4 u1 = *reinterpret_cast<const uint4 *>(src + e1);
-    float x[8], y[8];
-    if (rot) {
-      if (ADJ)
-        rotate8_adjacent<T>(u0, u1, cs + 8 * c, x, y);
-      else
-        rotate8<T>(u0, u1, cs + 8 * c, x, y);
-    }
-    if (is_q) {
-      uint16_t *dst = a.q_out + t * a.q_out_stride + (int64_t)h * D;
-      *reinterpret_cast<uint4 *>(dst + e0) = rot ? narrow8<T>(x) : u0;
-      *reinterpret_cast<uint4 *>(dst + e1) = rot ? narrow8<T>(y) : u1;
-    } else {
-      const int hh = is_k ? h - hq : h - hq - hkv;
-      const int64_t row = ((blk * hkv + hh) * a.block_size + off) * D;
-      void *cache = is_k ? a.k_cache : a.v_cache;
-      if constexpr (KV8) {
-        if (!rot) {
-          widen8<T>(u0, x);
-          widen8<T>(u1, y);
-        }
-        const float scale = __ldg((is_k ? a.k_scale : a.v_scale) + hh);
-        uint8_t *dst = static_cast<uint8_t *>(cache) + row;
-        *reinterpret_cast<uint2 *>(dst + e0) = quantise8(x, scale);
-        *reinterpret_cast<uint2 *>(dst + e1) = quantise8(y, scale);
-      } else {
-        uint16_t *dst = static_cast<uint16_t *>(cache) + row;
-        *reinterpret_cast<uint4 *>(dst + e0) = rot ? narrow8<T>(x) : u0;
-        *reinterpret_cast<uint4 *>(dst + e1) = rot ? narrow8<T>(y) : u1;
+  int at = 0;  // of the token in s_slot
+  for (int k = 0; t < a.n_tokens; ++k, t += G) {
+    const bool more = t + G < a.n_tokens;
+    uint4 y[IPT][2];
+    if (more) load(y);
+    const int pos2 = position(t + 2 * G);
+    const int64_t slot2 = slot_of(t + 2 * G);
+    const int64_t slot = s_slot[at];
+    const int64_t q_off = t * a.q_out_stride * 2;
+    const int64_t kv_off = ((((slot >> a.block_shift) * hkv) << a.block_shift) +
+                            (slot & ((1 << a.block_shift) - 1))) * (D * (KV8 ? 1 : 2));
+#pragma unroll
+    for (int u = 0; u < IPT; ++u) {
+      if (kind[u] == 3 || (kind[u] != 0 && slot < 0)) continue;  // without a slot only q is rotated
+      float p[8], r[8];
+      if (pairs[u] >= 0) {
+        if (ADJ) {
+          rotate4_adjacent<T>(x[u][0], cs[k & 1], pairs[u], p);
+          rotate4_adjacent<T>(x[u][1], cs[k & 1], d1[u] / 8, r);
+        } else
+          rotate8<T>(x[u][0], x[u][1], cs[k & 1], pairs[u], p, r);
       }
+      char *to = dst[u] + (kind[u] == 0 ? q_off : kv_off);
+      if (kind[u] == 0 || !KV8) {
+        *reinterpret_cast<uint4 *>(to + 2 * d0[u]) = pairs[u] >= 0 ? narrow8<T>(p) : x[u][0];
+        *reinterpret_cast<uint4 *>(to + 2 * d1[u]) = pairs[u] >= 0 ? narrow8<T>(r) : x[u][1];
+      } else {
+        if (pairs[u] < 0) {
+          widen8<T>(x[u][0], p);
+          widen8<T>(x[u][1], r);
+        }
+        *reinterpret_cast<uint2 *>(to + d0[u]) = quantise8(p, div[u]);
+        *reinterpret_cast<uint2 *>(to + d1[u]) = quantise8(r, div[u]);
+      }
+    }
+    if (!more) break;
+    // the next token's angles (its positions were put there an iteration ago); what the
+    // one after it needs goes where nobody reads in this iteration
+    angles((k + 1) & 1);
+    if (tid < a.num_axes) s_pos[k & 1][tid] = pos2;
+    at = at == 2 ? 0 : at + 1;
+    if (tid == 0) s_slot[at == 2 ? 0 : at + 1] = slot2;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < IPT; ++u) {
+      x[u][0] = y[u][0];
+      x[u][1] = y[u][1];
     }
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_rope(const RopeArgs &a, bool adj, bool kv8, cudaStream_t s) {
+template <typename T, int D, bool ADJ, bool KV8>
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s) {
+  constexpr int IPT = 2;
   const int items = (a.num_q_heads + 2 * a.num_kv_heads) * (D / 16);
-  const unsigned threads = (unsigned)std::min(256, (items + 31) / 32 * 32);
-  const dim3 grid((unsigned)a.n_tokens, 1, 1);
-  if (kv8) {
-    if constexpr (D == 128)
-      return adj ? pa::launch_dependent(rope_append_kernel<T, D, true, true>, grid, threads, s, a)
-                 : pa::launch_dependent(rope_append_kernel<T, D, false, true>, grid, threads, s, a);
-    return cudaErrorInvalidValue;
-  }
-  return adj ? pa::launch_dependent(rope_append_kernel<T, D, true, false>, grid, threads, s, a)
-             : pa::launch_dependent(rope_append_kernel<T, D, false, false>, grid, threads, s, a);
+  const int rows = (items + IPT * kThreads - 1) / (IPT * kThreads);
+  const int each = (items + rows * IPT - 1) / (rows * IPT);
+  const unsigned threads = (unsigned)((each + 31) / 32 * 32);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // as many CTAs as are resident (up to 85 registers a thread: 768 threads an SM)
+  const int resident = sms * std::min(32, 768 / (int)threads);
+  const dim3 grid((unsigned)std::min(a.n_tokens, std::max(1, resident / rows)), (unsigned)rows, 1);
+  return pa::launch_dependent(rope_append_kernel<T, D, ADJ, KV8, IPT>, grid, threads, s, a);
+}
+
+template <typename T, int D>
+cudaError_t dispatch_rope(const RopeArgs &a, bool adj, bool kv8, cudaStream_t s) {
+  if constexpr (D == 128)
+    if (kv8) return adj ? launch_rope<T, D, true, true>(a, s) : launch_rope<T, D, false, true>(a, s);
+  if (kv8) return cudaErrorInvalidValue;
+  return adj ? launch_rope<T, D, true, false>(a, s) : launch_rope<T, D, false, false>(a, s);
 }
 
 }  // namespace
@@ -220,6 +351,7 @@ extern "C" PA_API pa_status pa_rope_append(
   if (rotary_dim > head_dim) return PA_ERR_INVALID_ARG;
   if (rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
   if (num_q_heads > 65536 || num_kv_heads > 65536) return PA_ERR_INVALID_ARG;
+  if (num_axes > kMaxAxes) return PA_ERR_UNSUPPORTED;
   // a token's heads are dense; tokens are any multiple of 16 bytes apart that keeps
   // them from overlapping
   const int64_t wq = (int64_t)num_q_heads * head_dim, wkv = (int64_t)num_kv_heads * head_dim;
@@ -250,7 +382,7 @@ extern "C" PA_API pa_status pa_rope_append(
   a.num_kv_heads = num_kv_heads;
   a.half = rotary_dim / 2;
   a.num_axes = num_axes;
-  a.block_size = block_size;
+  a.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.err = pa::error_word();
@@ -259,10 +391,10 @@ extern "C" PA_API pa_status pa_rope_append(
   const bool kv8 = k_scale != nullptr, adj = interleaved != 0;
   cudaError_t e;
   if (head_dim == 128)
-    e = dtype == PA_FP16 ? launch_rope<__half, 128>(a, adj, kv8, s)
-                         : launch_rope<__nv_bfloat16, 128>(a, adj, kv8, s);
+    e = dtype == PA_FP16 ? dispatch_rope<__half, 128>(a, adj, kv8, s)
+                         : dispatch_rope<__nv_bfloat16, 128>(a, adj, kv8, s);
   else
-    e = dtype == PA_FP16 ? launch_rope<__half, 64>(a, adj, kv8, s)
-                         : launch_rope<__nv_bfloat16, 64>(a, adj, kv8, s);
+    e = dtype == PA_FP16 ? dispatch_rope<__half, 64>(a, adj, kv8, s)
+                         : dispatch_rope<__nv_bfloat16, 64>(a, adj, kv8, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -115,6 +115,8 @@ SHAPES = [
     (9, 32, 8, 128, 16, "bf16", 3, 128, False, True, True),
     (65, 5, 5, 128, 32, "fp16", 1, 64, True, True, False),
     (1030, 16, 2, 64, 16, "fp16", 2, 48, False, False, False),
+    (3, 300, 20, 128, 16, "bf16", 1, 128, False, False, False),   # more items than a pass
+    (77, 1, 1, 128, 8, "bf16", 2, 112, True, True, False),        # several tokens a CTA
 ]
 
 
@@ -156,6 +158,33 @@ def test_zero_position_is_the_identity(pa):
     c = make(4, 20, 4, 4, 64, 16, "fp16", 1, 64, True, False, False)
     c["pos"].zero_()
     assert torch.equal(run(pa, c), c["q"])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_codes_are_those_of_the_plain_append(pa, dtype):
+    """V rows of every 16-bit pattern under scales from tiny to huge: the codes of
+    pa_append_kv_fp8, which divides."""
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(DTYPES[dtype])
+    scales = [1.0, 0.037, 3.3e-3, 448.0, 2.0 ** -60, 2.0 ** -61, 1e-30, 7e-39, 1.7e18, 1.3e19, 3e38, 0.0,
+              -0.25, float("inf"), float("nan"), 1.1754944e-38]
+    hkv, tokens = len(scales), (1 << 16) // 128
+    v = bits.view(tokens, 1, 128).expand(tokens, hkv, 128).contiguous().to(DEV)
+    k = torch.zeros_like(v)
+    sc = torch.tensor(scales, device=DEV)
+    slots = torch.arange(tokens, device=DEV)
+    shape = (tokens // 16, hkv, 16, 128)
+    a = [torch.full(shape, 0x55, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    pa.pa_append_kv_fp8(a[0], a[1], k, v, slots, sc, sc)
+    turns, axis = pa.rope_table(128, device=DEV)
+    q = torch.zeros(tokens, 1, 128, dtype=v.dtype, device=DEV)
+    pos = torch.zeros(1, tokens, dtype=torch.int32, device=DEV)
+    pa.pa_rope_append(q, q, k, v, a[2], a[3], pos, slots, turns, axis, k_scale=sc, v_scale=sc)
+    torch.cuda.synchronize()
+    same = a[1] == a[3]
+    # (0 / 0 and the like: a NaN code of either sign is a NaN)
+    nan = (a[1] & 0x7F == 0x7F) & (a[3] & 0x7F == 0x7F)
+    assert (same | nan).all(), [(scales[int(h)], int((~(same | nan))[:, h].sum())) for h in range(hkv)]
+    assert torch.equal(a[0][:, :4], a[2][:, :4])
 
 
 def test_bad_slots_and_axes_are_reported(pa):

@@ -28,7 +28,7 @@ ROPE = dict(q_out=FAKE, q=FAKE, k=FAKE, v=FAKE, kc=FAKE, vc=FAKE, pos=FAKE, slot
     ({"axes": 0}, INVALID), ({"nb": 0}, INVALID), ({"q": FAKE + 2}, INVALID),
     ({"k": FAKE + 8}, INVALID), ({"vc": FAKE + 4}, INVALID), ({"so": 1016}, INVALID),
     ({"sk": 255}, INVALID), ({"sk": 260}, INVALID), ({"sv": -256}, INVALID),
-    ({"rot": 144}, INVALID), ({"rot": 0}, INVALID), ({"rot": 24}, UNSUPPORTED),
+    ({"rot": 144}, INVALID), ({"rot": 0}, INVALID), ({"rot": 24}, UNSUPPORTED), ({"axes": 33}, UNSUPPORTED),
     ({"d": 96, "rot": 96}, UNSUPPORTED), ({"bs": 24}, UNSUPPORTED), ({"dtype": 7}, UNSUPPORTED),
     ({"d": 64, "rot": 64, "ks": FAKE, "vs": FAKE}, UNSUPPORTED),
 ])
