@@ -104,36 +104,41 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
                     pa::Elt<T>::from_f2(x[4], x[5]), pa::Elt<T>::from_f2(x[6], x[7]));
 }
 
-// x / scale, correctly rounded, for a head's many x: with r = 1 / scale rounded,
-// q = x r and the exact remainder x - q scale, q + remainder r is the rounded quotient
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990), where nothing underflows: a scale within 2^+-60 keeps every quotient
-// that is not far below e4m3's smallest step clear of that.  Quotients beyond 2^60
-// saturate as they are, zeros keep their sign; other scales divide.
+// Eight e4m3 codes of x / scale.  With r = 1 / scale rounded, q = x r and the exact
+// remainder q scale - x, q - remainder r is the correctly rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990)
+// where nothing overflows or underflows: a positive scale within 2^+-60 and |x| up to
+// 2^60 scale leave only quotients far below e4m3's smallest step to underflow, and those
+// keep their sign.  Everything else is divided.  (Three operations a value against about
+// twenty: the quantising of 33 M values bounded the kernel.)
 struct Divisor {
-  float scale, r;
-  bool near;
+  float scale, r, most;  // most: largest |x| of the short way
   __device__ __forceinline__ void set(float s) {
     scale = s;
     r = 1.f / s;
-    near = fabsf(s) >= 0x1p-60f && fabsf(s) <= 0x1p60f;
-  }
-  __device__ __forceinline__ float operator()(float x) const {
-    const float q = x * r;
-    const float p = fmaf(fmaf(-q, scale, x), r, q);
-    return fabsf(q) <= 0x1p60f && q != 0.f ? p : q;
+    most = s >= 0x1p-60f && s <= 0x1p60f ? s * 0x1p60f : -1.f;
   }
 };
 
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], const Divisor &d) {
-  uint32_t c[4];
-  if (d.near) {
+  // (NaN passes the test: it stays NaN either way)
+  float m = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = pa::f32x2_to_e4m3x2(d(x[2 * i]), d(x[2 * i + 1]));
+  for (int i = 2; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+  float y[8];
+  if (m <= d.most) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = x[i] * d.r;
+      y[i] = fmaf(-fmaf(q, d.scale, -x[i]), d.r, q);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = pa::f32x2_to_e4m3x2(x[2 * i] / d.scale, x[2 * i + 1] / d.scale);
+    for (int i = 0; i < 8; ++i) y[i] = x[i] / d.scale;
   }
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = pa::f32x2_to_e4m3x2(y[2 * i], y[2 * i + 1]);
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
@@ -144,8 +149,9 @@ constexpr int kThreads = 384;  // at most
 // An item is two 16-byte chunks of one head.  The chunks that are rotated (and, apart from
 // them, those that are copied: V, and elements past rotary_dim) are paired first half with
 // second half, so that consecutive lanes read and write consecutive chunks, and with the
-// halves apart a pair's two elements are in one item.  A token's heads are numbered q,
-// then K, then V.  Thread i of block row y takes items (y IPT + u) blockDim + i
+// halves apart a pair's two elements are in one item.  A token's items in order: rotated
+// ones of q and of K, copied ones of q, K and V (so that a warp's lanes do the same).
+// Thread i of block row y takes items (y IPT + u) blockDim + i
 // of tokens blockIdx.x, + gridDim.x, ...
 template <typename T, int D, bool ADJ, bool KV8, int IPT>
 __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs a) {
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
   __shared__ __align__(16) float2 cs[2][kMaxHalf];
   __shared__ int64_t s_turn[kMaxHalf];
   __shared__ int s_axis[kMaxHalf], s_pos[2][kMaxAxes];
-  __shared__ int64_t s_slot[3];
+  __shared__ int64_t s_kv[3];  // the token's byte offset in the caches, -1: none
   pa::griddep_wait();
   pa::griddep_launch_dependents();
   const int tid = threadIdx.x;
@@ -169,15 +175,28 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
   Divisor div[IPT];
 #pragma unroll
   for (int u = 0; u < IPT; ++u) {
-    const int it = (blockIdx.y * IPT + u) * blockDim.x + tid;
-    const int h = it / kItems, c = it % kItems;
-    kind[u] = h < hq ? 0 : h < hq + hkv ? 1 : h < hq + 2 * hkv ? 2 : 3;
-    const int64_t hh = kind[u] == 0 ? h : kind[u] == 1 ? h - hq : h - hq - hkv;
-    const int rot_items = kind[u] < 2 ? a.half / 8 : 0;
-    const bool rot = c < rot_items;
-    const int chunk = rot ? c : rot_items + c;  // (copied: 2 rot_items + (c - rot_items))
+    int it = (blockIdx.y * IPT + u) * blockDim.x + tid;
+    const int rot_items = a.half / 8, copied = kItems - rot_items;
+    const bool rot = it < (hq + hkv) * rot_items;
+    int64_t hh = 0;
+    int c = 0, n = rot_items;  // item c of n of its kind in head hh
+    kind[u] = 3;
+    if (rot) {
+      hh = it / rot_items, c = it % rot_items;
+      kind[u] = hh < hq ? 0 : 1;
+    } else if ((it -= (hq + hkv) * rot_items) < (hq + hkv) * copied) {
+      n = copied;
+      hh = it / copied, c = it % copied;
+      kind[u] = hh < hq ? 0 : 1;
+    } else if ((it -= (hq + hkv) * copied) < hkv * kItems) {
+      n = kItems;
+      hh = it / kItems, c = it % kItems;
+      kind[u] = 2;
+    }
+    if (kind[u] == 1) hh -= hq;
+    const int chunk = rot || kind[u] == 2 ? c : 2 * rot_items + c;
     d0[u] = 8 * chunk;
-    d1[u] = 8 * (chunk + (rot ? rot_items : kItems - rot_items));
+    d1[u] = 8 * (chunk + n);
     pairs[u] = rot ? c : -1;
     const int64_t t0 = blockIdx.x;
     src[u] = reinterpret_cast<const char *>(kind[u] == 0   ? a.q + t0 * a.q_stride + hh * D
@@ -208,17 +227,19 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
       cs[buf][angle_at<ADJ>(i)] = make_float2(c, s);
     }
   };
-  auto position = [&](int64_t t) {
-    return tid < a.num_axes && t < a.n_tokens ? __ldg(a.positions + (int64_t)tid * a.n_tokens + t) : 0;
-  };
-  auto slot_of = [&](int64_t t) -> int64_t {
-    if (tid != 0 || t >= a.n_tokens) return -1;
-    const int64_t slot = __ldg(a.slot_mapping + t);
-    if (slot >= a.num_slots) {
-      pa::record_error(a.err, pa::kErrCheck);
-      return -1;
+  // token t's positions (lane i: axis i) and place in the caches (lane 0), by warp 0
+  auto token = [&](int64_t t, int &pos, int64_t &kv) {
+    pos = 0;
+    kv = -1;
+    if (t >= a.n_tokens) return;
+    if (tid < a.num_axes) pos = __ldg(a.positions + (int64_t)tid * a.n_tokens + t);
+    if (tid == 0) {
+      const int64_t slot = __ldg(a.slot_mapping + t);
+      if (slot >= a.num_slots) pa::record_error(a.err, pa::kErrCheck);
+      if (slot >= 0 && slot < a.num_slots)
+        kv = ((((slot >> a.block_shift) * hkv) << a.block_shift) + (slot & ((1 << a.block_shift) - 1))) *
+             (D * (KV8 ? 1 : 2));
     }
-    return slot;
   };
 
   int64_t t = blockIdx.x;
@@ -233,36 +254,36 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
     s_axis[i] = axis;
     s_turn[i] = __ldg(a.turns + i);
   }
-  {
-    const int p0 = position(t), p1 = position(t + G);
-    const int64_t l0 = slot_of(t), l1 = slot_of(t + G);
-    if (tid < a.num_axes) {
-      s_pos[0][tid] = p0;
-      s_pos[1][tid] = p1;
-    }
+  if (tid < 32) {
+    int p0, p1;
+    int64_t kv0, kv1;
+    token(t, p0, kv0);
+    token(t + G, p1, kv1);
+    s_pos[0][tid] = p0;
+    s_pos[1][tid] = p1;
     if (tid == 0) {
-      s_slot[0] = l0;
-      s_slot[1] = l1;
+      s_kv[0] = kv0;
+      s_kv[1] = kv1;
     }
   }
   __syncthreads();
   angles(0);
   __syncthreads();
 
-  int at = 0;  // of the token in s_slot
+  int at = 0;  // of the token in s_kv
+  int64_t q_off = t * a.q_out_stride * 2;
+  const int64_t q_out_step = G * a.q_out_stride * 2;
   for (int k = 0; t < a.n_tokens; ++k, t += G) {
     const bool more = t + G < a.n_tokens;
     uint4 y[IPT][2];
     if (more) load(y);
-    const int pos2 = position(t + 2 * G);
-    const int64_t slot2 = slot_of(t + 2 * G);
-    const int64_t slot = s_slot[at];
-    const int64_t q_off = t * a.q_out_stride * 2;
-    const int64_t kv_off = ((((slot >> a.block_shift) * hkv) << a.block_shift) +
-                            (slot & ((1 << a.block_shift) - 1))) * (D * (KV8 ? 1 : 2));
+    int pos2 = 0;
+    int64_t kv2 = -1;
+    if (tid < 32) token(t + 2 * G, pos2, kv2);
+    const int64_t kv = s_kv[at];
 #pragma unroll
     for (int u = 0; u < IPT; ++u) {
-      if (kind[u] == 3 || (kind[u] != 0 && slot < 0)) continue;  // without a slot only q is rotated
+      if (kind[u] == 3 || (kind[u] != 0 && kv < 0)) continue;  // without a slot only q is rotated
       float p[8], r[8];
       if (pairs[u] >= 0) {
         if (ADJ) {
@@ -271,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
         } else
           rotate8<T>(x[u][0], x[u][1], cs[k & 1], pairs[u], p, r);
       }
-      char *to = dst[u] + (kind[u] == 0 ? q_off : kv_off);
+      char *to = dst[u] + (kind[u] == 0 ? q_off : kv);
       if (kind[u] == 0 || !KV8) {
         *reinterpret_cast<uint4 *>(to + 2 * d0[u]) = pairs[u] >= 0 ? narrow8<T>(p) : x[u][0];
         *reinterpret_cast<uint4 *>(to + 2 * d1[u]) = pairs[u] >= 0 ? narrow8<T>(r) : x[u][1];
@@ -288,10 +309,11 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
     // the next token's angles (its positions were put there an iteration ago); what the
     // one after it needs goes where nobody reads in this iteration
     angles((k + 1) & 1);
-    if (tid < a.num_axes) s_pos[k & 1][tid] = pos2;
+    if (tid < 32) s_pos[k & 1][tid] = pos2;
     at = at == 2 ? 0 : at + 1;
-    if (tid == 0) s_slot[at == 2 ? 0 : at + 1] = slot2;
+    if (tid == 0) s_kv[at == 2 ? 0 : at + 1] = kv2;
     __syncthreads();
+    q_off += q_out_step;
 #pragma unroll
     for (int u = 0; u < IPT; ++u) {
       x[u][0] = y[u][0];
