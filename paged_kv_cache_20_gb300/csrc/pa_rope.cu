@@ -16,13 +16,16 @@
 // bits, as a signed number of half turns in [-1, 1), go to sincospif.
 //
 // Bound by DRAM: every byte of q, k, v once in and once out.  A CTA walks tokens, each
-// thread on the same items of every token, with the next token's loads and angles under
-// way while it rotates and stores the current one; a barrier per token hands the angles
-// over.  8192 tokens of 32/8 heads: MEASURED us; with one CTA per token, whose first load
-// or first store waits for the angles, 42.5 us.
+// thread on the same items of every token.  A token's q, k and v rows come by three bulk
+// copies into a ring of stages in shared memory, so that two to four tokens a CTA are in
+// flight without registers; the next token's angles are worked out while the current one
+// is rotated and stored, and one barrier per token hands them over and the stage back.
+// 8192 tokens of 32/8 heads 35.5 us, 4099 of 32/32 into an FP8 cache 33.8; with
+// loads to registers a token ahead 34.3 and 38.3; with one CTA per token 42.5 and 37.6.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pa_decode.cuh"
 #include "pa_host.h"
@@ -40,7 +43,9 @@ struct RopeArgs {
   const int32_t *pair_axis;     // [rotary_dim / 2]
   int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
   int64_t num_slots;
-  int n_tokens, num_q_heads, num_kv_heads, half, num_axes, block_shift;
+  // heads of this launch (the pointers stand at its first ones); KV heads of a cache block
+  int num_q_heads, num_kv_heads, cache_heads;
+  int n_tokens, half, num_axes, block_shift, stages;
   const float *k_scale, *v_scale;
   unsigned *err;
 };
@@ -145,79 +150,94 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], const Divisor &d
 constexpr int kMaxHalf = 64;  // rotary pairs per head at most (head_dim 128)
 constexpr int kMaxAxes = 32;
 constexpr int kThreads = 384;  // at most
+constexpr int kPer = 2;        // items of a thread
+constexpr int kMaxHeads = kThreads * kPer / 8;  // of a launch, at head_dim 128: 96
+constexpr int kMaxStages = 4;
+constexpr int kStageMemory = 208 * 1024;  // of an SM's shared memory, for stages
+constexpr int kResident = 768;            // threads an SM holds (up to 85 registers each)
 
 // An item is two 16-byte chunks of one head.  The chunks that are rotated (and, apart from
 // them, those that are copied: V, and elements past rotary_dim) are paired first half with
 // second half, so that consecutive lanes read and write consecutive chunks, and with the
 // halves apart a pair's two elements are in one item.  A token's items in order: rotated
 // ones of q and of K, copied ones of q, K and V (so that a warp's lanes do the same).
-// Thread i of block row y takes items (y IPT + u) blockDim + i
-// of tokens blockIdx.x, + gridDim.x, ...
-template <typename T, int D, bool ADJ, bool KV8, int IPT>
+// Thread i takes items u blockDim + i of tokens blockIdx.x,
+// + gridDim.x, ...
+template <typename T, int D, bool ADJ, bool KV8>
 __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs a) {
   constexpr int kItems = D / 16;  // items of a head
+  extern __shared__ __align__(128) uint8_t s_stage[];
+  __shared__ __align__(8) uint64_t s_full[kMaxStages];
   __shared__ __align__(16) float2 cs[2][kMaxHalf];
   __shared__ int64_t s_turn[kMaxHalf];
   __shared__ int s_axis[kMaxHalf], s_pos[2][kMaxAxes];
   __shared__ int64_t s_kv[3];  // the token's byte offset in the caches, -1: none
-  pa::griddep_wait();
-  pa::griddep_launch_dependents();
+  __shared__ int s_failed;
   const int tid = threadIdx.x;
   const int hq = a.num_q_heads, hkv = a.num_kv_heads;
   const int64_t G = gridDim.x;
+  const uint32_t q_bytes = (uint32_t)hq * (D * 2), kv_bytes = (uint32_t)hkv * (D * 2);
+  const uint32_t stage_bytes = q_bytes + 2 * kv_bytes;
+  if (tid == 0) {
+    s_failed = 0;
+    for (int i = 0; i < a.stages; ++i) pa::mbar_init(pa::smem_u32(&s_full[i]), 1);
+    pa::fence_mbar_init();
+  }
+  pa::griddep_wait();
+  pa::griddep_launch_dependents();
 
-  // this thread's items, the same of every token: where they come from and go to (bytes,
-  // the token's own offset apart), kind 0 q, 1 K, 2 V, 3 none
-  const int64_t q_step = G * a.q_stride * 2, k_step = G * a.k_stride * 2, v_step = G * a.v_stride * 2;
-  const char *src[IPT];
-  char *dst[IPT];
-  int kind[IPT], d0[IPT], d1[IPT], pairs[IPT];  // d0, d1: the chunks' elements; pairs: < 0 copied
-  Divisor div[IPT];
+  // token t into stage i (thread 0)
+  auto fetch = [&](int64_t t, int i) {
+    const uint32_t bar = pa::smem_u32(&s_full[i]);
+    const uint32_t to = pa::smem_u32(s_stage) + i * stage_bytes;
+    pa::mbar_arrive_expect_tx(bar, stage_bytes);
+    if (q_bytes) pa::bulk_load(to, a.q + t * a.q_stride, q_bytes, bar);
+    if (kv_bytes) {
+      pa::bulk_load(to + q_bytes, a.k + t * a.k_stride, kv_bytes, bar);
+      pa::bulk_load(to + q_bytes + kv_bytes, a.v + t * a.v_stride, kv_bytes, bar);
+    }
+  };
+  int64_t t = blockIdx.x;
+  if (tid == 0)
+    for (int i = 0; i < a.stages; ++i)
+      if (t + i * G < a.n_tokens) fetch(t + i * G, i);
+
+  // this thread's items, the same of every token: where they lie in a stage and where they
+  // go to (bytes, the token's own offset apart), kind 0 q, 1 K, 2 V, 3 none
+  uint32_t src[kPer];
+  char *dst[kPer];
+  int kind[kPer], d0[kPer], d1[kPer], pairs[kPer];  // d0, d1: the chunks' elements; pairs: < 0 copied
+  Divisor div[kPer];
 #pragma unroll
-  for (int u = 0; u < IPT; ++u) {
-    int it = (blockIdx.y * IPT + u) * blockDim.x + tid;
+  for (int u = 0; u < kPer; ++u) {
+    int it = u * blockDim.x + tid;
     const int rot_items = a.half / 8, copied = kItems - rot_items;
     const bool rot = it < (hq + hkv) * rot_items;
-    int64_t hh = 0;
-    int c = 0, n = rot_items;  // item c of n of its kind in head hh
+    int h = 0, c = 0, n = rot_items;  // item c of n of its kind in head h
     kind[u] = 3;
     if (rot) {
-      hh = it / rot_items, c = it % rot_items;
-      kind[u] = hh < hq ? 0 : 1;
+      h = it / rot_items, c = it % rot_items;
+      kind[u] = h < hq ? 0 : 1;
     } else if ((it -= (hq + hkv) * rot_items) < (hq + hkv) * copied) {
       n = copied;
-      hh = it / copied, c = it % copied;
-      kind[u] = hh < hq ? 0 : 1;
+      h = it / copied, c = it % copied;
+      kind[u] = h < hq ? 0 : 1;
     } else if ((it -= (hq + hkv) * copied) < hkv * kItems) {
       n = kItems;
-      hh = it / kItems, c = it % kItems;
+      h = it / kItems, c = it % kItems;
       kind[u] = 2;
     }
-    if (kind[u] == 1) hh -= hq;
     const int chunk = rot || kind[u] == 2 ? c : 2 * rot_items + c;
     d0[u] = 8 * chunk;
     d1[u] = 8 * (chunk + n);
     pairs[u] = rot ? c : -1;
-    const int64_t t0 = blockIdx.x;
-    src[u] = reinterpret_cast<const char *>(kind[u] == 0   ? a.q + t0 * a.q_stride + hh * D
-                                            : kind[u] == 1 ? a.k + t0 * a.k_stride + hh * D
-                                                           : a.v + t0 * a.v_stride + hh * D);
-    dst[u] = kind[u] == 0 ? reinterpret_cast<char *>(a.q_out + hh * D)
+    src[u] = pa::smem_u32(s_stage) + (kind[u] == 2 ? q_bytes + kv_bytes : 0u) + (uint32_t)h * (D * 2);
+    if (kind[u] == 1) h -= hq;
+    dst[u] = kind[u] == 0 ? reinterpret_cast<char *>(a.q_out + (int64_t)h * D)
                           : static_cast<char *>(kind[u] == 1 ? a.k_cache : a.v_cache) +
-                                (hh << a.block_shift) * (D * (KV8 ? 1 : 2));
-    if (KV8) div[u].set(kind[u] == 1 ? __ldg(a.k_scale + hh) : kind[u] == 2 ? __ldg(a.v_scale + hh) : 1.f);
+                                ((int64_t)h << a.block_shift) * (D * (KV8 ? 1 : 2));
+    if (KV8) div[u].set(kind[u] == 1 ? __ldg(a.k_scale + h) : kind[u] == 2 ? __ldg(a.v_scale + h) : 1.f);
   }
-  // the items of the token that src stands at, and on to this CTA's next one
-  auto load = [&](uint4 (&x)[IPT][2]) {
-#pragma unroll
-    for (int u = 0; u < IPT; ++u) {
-      if (kind[u] != 3) {
-        x[u][0] = *reinterpret_cast<const uint4 *>(src[u] + 2 * d0[u]);
-        x[u][1] = *reinterpret_cast<const uint4 *>(src[u] + 2 * d1[u]);
-      }
-      src[u] += kind[u] == 0 ? q_step : kind[u] == 1 ? k_step : v_step;
-    }
-  };
   auto angles = [&](int buf) {
     for (int i = tid; i < a.half; i += blockDim.x) {
       const uint64_t turn = (uint64_t)(int64_t)s_pos[buf][s_axis[i]] * (uint64_t)s_turn[i];
@@ -237,14 +257,12 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
       const int64_t slot = __ldg(a.slot_mapping + t);
       if (slot >= a.num_slots) pa::record_error(a.err, pa::kErrCheck);
       if (slot >= 0 && slot < a.num_slots)
-        kv = ((((slot >> a.block_shift) * hkv) << a.block_shift) + (slot & ((1 << a.block_shift) - 1))) *
+        kv = ((((slot >> a.block_shift) * a.cache_heads) << a.block_shift) +
+              (slot & ((1 << a.block_shift) - 1))) *
              (D * (KV8 ? 1 : 2));
     }
   };
 
-  int64_t t = blockIdx.x;
-  uint4 x[IPT][2];
-  load(x);
   for (int i = tid; i < a.half; i += blockDim.x) {
     int axis = __ldg(a.pair_axis + i);
     if (axis < 0 || axis >= a.num_axes) {
@@ -266,40 +284,51 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
       s_kv[1] = kv1;
     }
   }
-  __syncthreads();
+  __syncthreads();  // (the stages' barriers are initialised, too)
   angles(0);
   __syncthreads();
 
-  int at = 0;  // of the token in s_kv
+  volatile int *failed = &s_failed;
+  int at = 0;     // of the token in s_kv
+  int stage = 0, parity = 0;
   int64_t q_off = t * a.q_out_stride * 2;
   const int64_t q_out_step = G * a.q_out_stride * 2;
   for (int k = 0; t < a.n_tokens; ++k, t += G) {
     const bool more = t + G < a.n_tokens;
-    uint4 y[IPT][2];
-    if (more) load(y);
     int pos2 = 0;
     int64_t kv2 = -1;
-    if (tid < 32) token(t + 2 * G, pos2, kv2);
+    if (more && tid < 32) token(t + 2 * G, pos2, kv2);
     const int64_t kv = s_kv[at];
+    // a wait that gives up is reported, and nothing more is waited for or stored; every
+    // thread still comes to every barrier
+    bool ok = !*failed;
+    if (ok && !pa::mbar_wait_bounded(pa::smem_u32(&s_full[stage]), parity)) {
+      pa::record_error(a.err, pa::kErrTimeout);
+      *failed = 1;
+      ok = false;
+    }
+    const uint32_t from = stage * stage_bytes;
 #pragma unroll
-    for (int u = 0; u < IPT; ++u) {
-      if (kind[u] == 3 || (kind[u] != 0 && kv < 0)) continue;  // without a slot only q is rotated
+    for (int u = 0; u < kPer; ++u) {
+      if (!ok || kind[u] == 3 || (kind[u] != 0 && kv < 0)) continue;  // without a slot only q is rotated
+      const uint4 x = pa::lds128(src[u] + from + 2 * d0[u]), y = pa::lds128(src[u] + from + 2 * d1[u]);
       float p[8], r[8];
       if (pairs[u] >= 0) {
         if (ADJ) {
-          rotate4_adjacent<T>(x[u][0], cs[k & 1], pairs[u], p);
-          rotate4_adjacent<T>(x[u][1], cs[k & 1], d1[u] / 8, r);
-        } else
-          rotate8<T>(x[u][0], x[u][1], cs[k & 1], pairs[u], p, r);
+          rotate4_adjacent<T>(x, cs[k & 1], pairs[u], p);
+          rotate4_adjacent<T>(y, cs[k & 1], d1[u] / 8, r);
+        } else {
+          rotate8<T>(x, y, cs[k & 1], pairs[u], p, r);
+        }
       }
       char *to = dst[u] + (kind[u] == 0 ? q_off : kv);
       if (kind[u] == 0 || !KV8) {
-        *reinterpret_cast<uint4 *>(to + 2 * d0[u]) = pairs[u] >= 0 ? narrow8<T>(p) : x[u][0];
-        *reinterpret_cast<uint4 *>(to + 2 * d1[u]) = pairs[u] >= 0 ? narrow8<T>(r) : x[u][1];
+        *reinterpret_cast<uint4 *>(to + 2 * d0[u]) = pairs[u] >= 0 ? narrow8<T>(p) : x;
+        *reinterpret_cast<uint4 *>(to + 2 * d1[u]) = pairs[u] >= 0 ? narrow8<T>(r) : y;
       } else {
         if (pairs[u] < 0) {
-          widen8<T>(x[u][0], p);
-          widen8<T>(x[u][1], r);
+          widen8<T>(x, p);
+          widen8<T>(y, r);
         }
         *reinterpret_cast<uint2 *>(to + d0[u]) = quantise8(p, div[u]);
         *reinterpret_cast<uint2 *>(to + d1[u]) = quantise8(r, div[u]);
@@ -313,30 +342,55 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs
     at = at == 2 ? 0 : at + 1;
     if (tid == 0) s_kv[at == 2 ? 0 : at + 1] = kv2;
     __syncthreads();
+    if (tid == 0 && t + a.stages * G < a.n_tokens && !*failed) {
+      pa::fence_proxy_async_smem();  // the stage's reads before the copy writes it again
+      fetch(t + a.stages * G, stage);
+    }
     q_off += q_out_step;
-#pragma unroll
-    for (int u = 0; u < IPT; ++u) {
-      x[u][0] = y[u][0];
-      x[u][1] = y[u][1];
+    if (++stage == a.stages) {
+      stage = 0;
+      parity ^= 1;
     }
   }
+  if (*failed && tid == 0)  // copies still in flight land (bounded) before the CTA ends
+    for (int i = 0; i < a.stages; ++i)
+      for (int b = 0; b < 2; ++b) (void)pa::mbar_wait_bounded(pa::smem_u32(&s_full[i]), b);
 }
 
 template <typename T, int D, bool ADJ, bool KV8>
-cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s) {
-  constexpr int IPT = 2;
-  const int items = (a.num_q_heads + 2 * a.num_kv_heads) * (D / 16);
-  const int rows = (items + IPT * kThreads - 1) / (IPT * kThreads);
-  const int each = (items + rows * IPT - 1) / (rows * IPT);
-  const unsigned threads = (unsigned)((each + 31) / 32 * 32);
-  int dev = 0, sms = 0;
+cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
+  auto kern = rope_append_kernel<T, D, ADJ, KV8>;
+  const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+  const int each = (heads * (D / 16) + kPer - 1) / kPer;
+  const int threads = (each + 31) / 32 * 32;
+  static std::atomic<int> sm_count[64];
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // as many CTAs as are resident (up to 85 registers a thread: 768 threads an SM)
-  const int resident = sms * std::min(32, 768 / (int)threads);
-  const dim3 grid((unsigned)std::min(a.n_tokens, std::max(1, resident / rows)), (unsigned)rows, 1);
-  return pa::launch_dependent(rope_append_kernel<T, D, ADJ, KV8, IPT>, grid, threads, s, a);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int sms = sm_count[dev].load(std::memory_order_acquire);
+  if (sms <= 0) {  // first call on this device: the shared-memory opt-in, too
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMemory);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    sm_count[dev].store(sms, std::memory_order_release);
+  }
+  // CTAs an SM holds by its threads, and the stages that fit beside each other
+  const int bytes = heads * D * 2;
+  int ctas = std::max(1, std::min(32, kResident / threads));
+  while (ctas > 1 && kStageMemory / ctas / bytes < 2) --ctas;
+  a.stages = std::max(2, std::min(kMaxStages, kStageMemory / ctas / bytes));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min(a.n_tokens, sms * ctas), 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)a.stages * bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <typename T, int D>
@@ -402,6 +456,7 @@ extern "C" PA_API pa_status pa_rope_append(
   a.n_tokens = n_tokens;
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
+  a.cache_heads = num_kv_heads;
   a.half = rotary_dim / 2;
   a.num_axes = num_axes;
   a.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
@@ -411,12 +466,33 @@ extern "C" PA_API pa_status pa_rope_append(
   if (a.err == nullptr) return PA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool kv8 = k_scale != nullptr, adj = interleaved != 0;
-  cudaError_t e;
-  if (head_dim == 128)
-    e = dtype == PA_FP16 ? dispatch_rope<__half, 128>(a, adj, kv8, s)
-                         : dispatch_rope<__nv_bfloat16, 128>(a, adj, kv8, s);
-  else
-    e = dtype == PA_FP16 ? dispatch_rope<__half, 64>(a, adj, kv8, s)
-                         : dispatch_rope<__nv_bfloat16, 64>(a, adj, kv8, s);
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  // A launch takes at most kMaxHeads heads of a token (twice as many at head_dim 64), K
+  // and V together with as many q heads as fit beside them; usually one does all
+  const int most = head_dim == 128 ? kMaxHeads : 2 * kMaxHeads;
+  const int kv_step = std::min(num_kv_heads, most / 3);
+  const int q_step = most - 2 * kv_step;
+  const int launches = std::max((num_q_heads + q_step - 1) / q_step, (num_kv_heads + kv_step - 1) / kv_step);
+  for (int i = 0; i < launches; ++i) {
+    RopeArgs b = a;
+    const int q0 = std::min(num_q_heads, i * q_step), kv0 = std::min(num_kv_heads, i * kv_step);
+    b.num_q_heads = std::min(q_step, num_q_heads - q0);
+    b.num_kv_heads = std::min(kv_step, num_kv_heads - kv0);
+    b.q += (int64_t)q0 * head_dim;
+    b.q_out += (int64_t)q0 * head_dim;
+    b.k += (int64_t)kv0 * head_dim;
+    b.v += (int64_t)kv0 * head_dim;
+    const int64_t skip = (int64_t)kv0 * block_size * head_dim * (kv8 ? 1 : 2);
+    b.k_cache = static_cast<char *>(k_cache) + skip;
+    b.v_cache = static_cast<char *>(v_cache) + skip;
+    if (kv8) b.k_scale += kv0, b.v_scale += kv0;
+    cudaError_t e;
+    if (head_dim == 128)
+      e = dtype == PA_FP16 ? dispatch_rope<__half, 128>(b, adj, kv8, s)
+                           : dispatch_rope<__nv_bfloat16, 128>(b, adj, kv8, s);
+    else
+      e = dtype == PA_FP16 ? dispatch_rope<__half, 64>(b, adj, kv8, s)
+                           : dispatch_rope<__nv_bfloat16, 64>(b, adj, kv8, s);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  }
+  return PA_OK;
 }

@@ -116,7 +116,9 @@ SHAPES = [
     (65, 5, 5, 128, 32, "fp16", 1, 64, True, True, False),
     (1030, 16, 2, 64, 16, "fp16", 2, 48, False, False, False),
     (3, 300, 20, 128, 16, "bf16", 1, 128, False, False, False),   # more items than a pass
-    (77, 1, 1, 128, 8, "bf16", 2, 112, True, True, False),        # several tokens a CTA
+    (77, 1, 1, 128, 8, "bf16", 2, 112, True, True, False),
+    (9, 2, 50, 64, 16, "fp16", 1, 64, False, False, True),        # more KV heads than a launch
+    (3000, 2, 1, 128, 32, "fp16", 3, 128, False, True, True),     # many tokens a CTA
 ]
 
 
