@@ -389,6 +389,10 @@ PA_API pa_status pa_rope_append(void *q_out, const void *q, const void *k, const
  * Rows t >= context_lens[i] of both ledgers are left as they were.
  *   scores   fp32  [num_seqs][num_kv_heads][max_blocks_per_seq * block_size]
  *   row_pos  int32, the same shape; NULL (with seq_lens NULL): no positions kept
+ * out, bad blocks and non-finite values are as in pa_decode; with several query tokens an
+ * infinite or NaN V row of this step therefore also reaches the step's earlier tokens
+ * (their weight on it is 0, and 0 times it is NaN).  The ledger is free of that: a row
+ * gains nothing from query tokens that do not see it.
  * The sums have one order: results do not change from run to run.  num_splits as for
  * pa_append_decode up to 16 query tokens; above, the call takes no partitions.
  * Workspace: pa_decode_scored_workspace_size bytes, 256-byte aligned (up to 16 query
@@ -426,8 +430,9 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
  * pa_copy_blocks first).  A block id outside the pool: the row is not copied,
  * PA_ERR_DEVICE_CHECK.
  *   element_bytes  2 (16-bit cache) or 1 (FP8, head_dim 128): rows are moved bit for bit
- *   new_lens       int32 [num_seqs], not context_lens itself
- *   workspace      pa_evict_workspace_size bytes
+ *   new_lens       int32 [num_seqs], neither context_lens nor seq_lens itself
+ *   workspace      pa_evict_workspace_size bytes; two calls that can overlap need
+ *                  workspaces of their own
  * budget >= sinks + recent, budget >= 1.
  */
 PA_API size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int budget);
@@ -453,7 +458,8 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, float *scores_out, int32
  * exact to fp64, so the choice is the formula's.  Weights that are negative, NaN or
  * infinite count as zero.
  * draft_probs NULL: drafts that were certain (q_j(x_j) = 1, 0 elsewhere).
- * new_lens (may be NULL): context_lens[i] - (max_draft - a), the cache length after a
+ * new_lens (may be NULL, or context_lens itself): context_lens[i] - (max_draft - a), the
+ * cache length after a
  * step that appended 1 + max_draft rows per sequence (the last committed token, then
  * the drafts, padded to max_draft); the next append overwrites the rejected rows.
  *   target_probs  fp32 [num_seqs][max_draft + 1][target_stride], vocab used

@@ -499,7 +499,8 @@ extern "C" PA_API pa_status pa_evict(
     return PA_ERR_INVALID_ARG;
   // the ledgers are both updated in place or both written elsewhere
   if ((scores == scores_out) != (row_pos == row_pos_out)) return PA_ERR_INVALID_ARG;
-  if (new_lens == context_lens) return PA_ERR_INVALID_ARG;  // (every KV head reads the old lengths)
+  // (every KV head reads the old lengths while one writes the new)
+  if (new_lens == context_lens || new_lens == seq_lens) return PA_ERR_INVALID_ARG;
   const void *ptrs[7] = {k_cache, v_cache, workspace, scores, row_pos, scores_out, row_pos_out};
   for (const void *p : ptrs)
     if (!pa::aligned16(p)) return PA_ERR_INVALID_ARG;

@@ -17,11 +17,13 @@
 //
 // Bound by DRAM: every byte of q, k, v once in and once out.  A CTA walks tokens, each
 // thread on the same items of every token.  A token's q, k and v rows come by three bulk
-// copies into a ring of stages in shared memory, so that two to four tokens a CTA are in
-// flight without registers; the next token's angles are worked out while the current one
-// is rotated and stored, and one barrier per token hands them over and the stage back.
-// 8192 tokens of 32/8 heads 35.5 us, 4099 of 32/32 into an FP8 cache 33.8; with
-// loads to registers a token ahead 34.3 and 38.3; with one CTA per token 42.5 and 37.6.
+// copies into a ring of stages in shared memory, so that two tokens a CTA are in flight
+// without registers (which lets three 384-thread CTAs share an SM; two measured 2 %
+// slower, four spill); the next token's angles are worked out while the current one is
+// rotated and stored, and one barrier per token hands them over and the stage back.
+// 8192 tokens of 32/8 heads 33.8 us (6.0 TB/s), 4099 of 32/32 into an FP8 cache 31.7
+// (5.3 TB/s); with loads to registers a token ahead 34.3 and 38.3; with one CTA per token
+// 42.5 and 37.6.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -152,9 +154,9 @@ constexpr int kMaxAxes = 32;
 constexpr int kThreads = 384;  // at most
 constexpr int kPer = 2;        // items of a thread
 constexpr int kMaxHeads = kThreads * kPer / 8;  // of a launch, at head_dim 128: 96
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 2;  // (3 and 4 measured the same and 3 % slower)
 constexpr int kStageMemory = 208 * 1024;  // of an SM's shared memory, for stages
-constexpr int kResident = 768;            // threads an SM holds (up to 85 registers each)
+constexpr int kResident = 1152;           // threads an SM holds (56 registers each)
 
 // An item is two 16-byte chunks of one head.  The chunks that are rotated (and, apart from
 // them, those that are copied: V, and elements past rotary_dim) are paired first half with
@@ -164,7 +166,7 @@ constexpr int kResident = 768;            // threads an SM holds (up to 85 regis
 // Thread i takes items u blockDim + i of tokens blockIdx.x,
 // + gridDim.x, ...
 template <typename T, int D, bool ADJ, bool KV8>
-__global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const RopeArgs a) {
   constexpr int kItems = D / 16;  // items of a head
   extern __shared__ __align__(128) uint8_t s_stage[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages];
@@ -436,6 +438,8 @@ extern "C" PA_API pa_status pa_rope_append(
   for (int i = 0; i < 4; ++i)
     if (strides[i] < widths[i] || strides[i] % 8 != 0 || strides[i] > ((int64_t)1 << 40))
       return PA_ERR_INVALID_ARG;
+  // (over its own input, each token's rows over themselves)
+  if (q_out == q && q_out_stride != q_stride) return PA_ERR_INVALID_ARG;
   if (n_tokens == 0) return PA_OK;
   RopeArgs a;
   a.q_out = static_cast<uint16_t *>(q_out);

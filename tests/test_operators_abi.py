@@ -21,7 +21,7 @@ ROPE = dict(q_out=FAKE, q=FAKE, k=FAKE, v=FAKE, kc=FAKE, vc=FAKE, pos=FAKE, slot
 
 
 @pytest.mark.parametrize("kw,status", [
-    ({}, 0), ({"ks": FAKE, "vs": FAKE}, 0), ({"sq": 1536, "sk": 1536, "sv": 1536}, 0),
+    ({}, 0), ({"ks": FAKE, "vs": FAKE}, 0), ({"so": 1536, "sq": 1536, "sk": 1536, "sv": 1536}, 0),
     ({"q_out": None}, INVALID), ({"v": None}, INVALID), ({"pos": None}, INVALID),
     ({"slots": None}, INVALID), ({"turns": None}, INVALID), ({"axis": None}, INVALID),
     ({"ks": FAKE}, INVALID), ({"n": -1}, INVALID), ({"hq": 0}, INVALID), ({"hkv": 0}, INVALID),
@@ -31,6 +31,8 @@ ROPE = dict(q_out=FAKE, q=FAKE, k=FAKE, v=FAKE, kc=FAKE, vc=FAKE, pos=FAKE, slot
     ({"rot": 144}, INVALID), ({"rot": 0}, INVALID), ({"rot": 24}, UNSUPPORTED), ({"axes": 33}, UNSUPPORTED),
     ({"d": 96, "rot": 96}, UNSUPPORTED), ({"bs": 24}, UNSUPPORTED), ({"dtype": 7}, UNSUPPORTED),
     ({"d": 64, "rot": 64, "ks": FAKE, "vs": FAKE}, UNSUPPORTED),
+    ({"so": 1032}, INVALID),  # over its own input with another stride
+    ({"so": 1032, "q_out": FAKE + 64}, 0),
 ])
 def test_rope_append(lib, kw, status):  # noqa: F811
     assert _call(lib, "pa_rope_append", ROPE, kw) == status
@@ -69,7 +71,7 @@ def test_decode_scored_workspace(lib):  # noqa: F811
 
 
 EVICT = dict(k=FAKE, v=FAKE, so=FAKE, po=FAKE + 64, nl=FAKE, sc=FAKE, rp=FAKE + 64, bt=FAKE,
-             cl=FAKE + 16, sl=FAKE, n=2, hkv=2, d=128, bs=16, maxb=4, nb=8, budget=32, sinks=2,
+             cl=FAKE + 16, sl=FAKE + 48, n=2, hkv=2, d=128, bs=16, maxb=4, nb=8, budget=32, sinks=2,
              recent=8, eb=2, ws=FAKE, wsb=2 * 2 * 32 * 8, stream=None)
 
 
@@ -77,6 +79,7 @@ EVICT = dict(k=FAKE, v=FAKE, so=FAKE, po=FAKE + 64, nl=FAKE, sc=FAKE, rp=FAKE + 
     ({"wsb": 2 * 2 * 32 * 8 - 1}, INVALID), ({"ws": None}, INVALID), ({"ws": FAKE + 8}, INVALID),
     ({"k": None}, INVALID), ({"so": None}, INVALID), ({"nl": None}, INVALID), ({"rp": None}, INVALID),
     ({"sl": None}, INVALID), ({"k": FAKE + 8}, INVALID), ({"nl": FAKE + 16}, INVALID),
+    ({"nl": FAKE + 32, "sl": FAKE + 32}, INVALID),
     ({"sc": FAKE + 4, "so": FAKE + 4}, INVALID), ({"rp": FAKE + 8, "po": FAKE + 8}, INVALID),
     ({"so": FAKE + 256}, INVALID),  # one ledger in place, the other not
     ({"budget": 0}, INVALID), ({"sinks": -1}, INVALID), ({"recent": -1}, INVALID),
