@@ -106,7 +106,8 @@ struct DecodeArgs {
   const float *prior_acc, *prior_m, *prior_l;
   int prior_splits;
   // Scored decode (paths built with SC): every score the pass computes, base-2 units,
-  // -inf where masked: [num_seqs][num_kv_heads][max_tiles][rows][16 tokens].  The
+  // -inf where masked: [num_seqs][num_kv_heads][max_tiles][rows][16 tokens], the tokens
+  // of a tile's row in the order of score_slot.  The
   // single pass then also writes its statistics m and l (to ws_m, ws_l, if given).
   float *raw_scores;
   // Scored single pass with one row group: the ledger is brought up to date by the CTAs
@@ -129,24 +130,44 @@ __device__ __forceinline__ void ledger_write(float *scores, int32_t *row_pos, co
   if (fresh && row_pos) row_pos[at] = __ldg(seq_lens + seq) - Lc + t;
 }
 
-// Where a path puts the scores of one tile (row r, token t at p[16 r + t]) for a
-// caller that needs every row's softmax weights once the row sums are known.  The
-// paths built without it hold an empty sink.
+// Where a path puts the scores of one tile, for a caller that needs every row's softmax
+// weights once the row sums are known: row r of a tile holds its 16 tokens' scores in the
+// order the path's threads have them, so that each stores its own with few wide stores.
+// score_slot: the place of token t in a row, by the path that a number of rows takes.
+// The paths built without it hold an empty sink.
+__host__ __device__ __forceinline__ int score_slot(int rows, int t) {
+  if (rows <= 2) return t;                                 // CUDA cores: by token
+  if (rows <= 8) return 2 * (t & 7) + (t >> 3);            // swapped operands: t, t + 8
+  return 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1);      // t, t + 1, t + 8, t + 9
+}
+__host__ __device__ __forceinline__ int score_token(int rows, int slot) {  // its inverse
+  if (rows <= 2) return slot;
+  if (rows <= 8) return (slot >> 1) + 8 * (slot & 1);
+  return 2 * (slot >> 2) + 8 * ((slot >> 1) & 1) + (slot & 1);
+}
 template <bool SC>
 struct ScoreSink {
-  __device__ __forceinline__ void set(float *, int) {}
-  __device__ __forceinline__ void put(int, int, float) {}
+  __device__ __forceinline__ void unit(float *, int, int) {}
+  __device__ __forceinline__ void tile(int) {}
 };
 template <>
 struct ScoreSink<true> {
-  float *p;
-  int rows;  // rows at or past it are padding
-  __device__ __forceinline__ void set(float *tile, int n) {
-    p = tile;
+  float *base, *p;
+  int stride, rows;  // floats between tiles; rows at or past `rows` are padding
+  __device__ __forceinline__ void unit(float *first, int step, int n) {
+    base = first;
+    stride = step;
     rows = n;
   }
-  __device__ __forceinline__ void put(int r, int t, float v) {
-    if (r < rows) p[16 * r + t] = v;
+  __device__ __forceinline__ void tile(int j) { p = base + (int64_t)j * stride; }
+  __device__ __forceinline__ void put(int r, int slot, float v) {
+    if (r < rows) p[16 * r + slot] = v;
+  }
+  __device__ __forceinline__ void put2(int r, int slot, float a, float b) {
+    if (r < rows) *reinterpret_cast<float2 *>(p + 16 * r + slot) = make_float2(a, b);
+  }
+  __device__ __forceinline__ void put4(int r, int slot, float4 v) {
+    if (r < rows) *reinterpret_cast<float4 *>(p + 16 * r + slot) = v;
   }
 };
 
@@ -549,8 +570,10 @@ struct MmaPath {
             if (tg >= lim[hr]) v = -INFINITY;
           }
           sc[nt][2 * hr + e] = v;
-          if constexpr (SC) raw.put((lane >> 2) + 8 * hr, nt * 8 + (lane & 3) * 2 + e, v);
         }
+      if constexpr (SC)
+        raw.put4((lane >> 2) + 8 * hr, 4 * (lane & 3),
+                 make_float4(sc[0][2 * hr], sc[0][2 * hr + 1], sc[1][2 * hr], sc[1][2 * hr + 1]));
       mx[hr] = fmaxf(fmaxf(sc[0][2 * hr], sc[0][2 * hr + 1]), fmaxf(sc[1][2 * hr], sc[1][2 * hr + 1]));
       mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
       mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
@@ -741,7 +764,11 @@ struct MmaTPath {
         if (tg >= lim[i & 1]) v = -INFINITY;
       }
       sc[i] = v;
-      if constexpr (SC) raw.put(2 * (threadIdx.x & 3) + (i & 1), g + 8 * (i >> 1), v);
+    }
+    if constexpr (SC) {
+      const int r = 2 * (threadIdx.x & 3);
+      raw.put2(r, 2 * g, sc[0], sc[2]);
+      raw.put2(r + 1, 2 * g, sc[1], sc[3]);
     }
     // online softmax per row (the 8 threads of a row differ in g: lanes c + 4g)
 #pragma unroll
@@ -1460,6 +1487,10 @@ __global__ void __launch_bounds__(NW * 32)
   if (n_my > 0) load_window(0);
   Path path;
   path.init(a, seq, kvh, row0, L, sscale);
+  if constexpr (Path::kScored)
+    path.sink().unit(a.raw_scores + ((size_t)(seq * a.num_kv_heads + kvh) * a.max_tiles * a.rows + row0) *
+                                        kTileTokens,
+                     a.rows * kTileTokens, a.rows - row0);
 
   // Fused append: every CTA that reads a tile holding a new position writes all of
   // this unit's new rows itself (CTAs of one row group or neighbouring split that
@@ -1528,10 +1559,7 @@ __global__ void __launch_bounds__(NW * 32)
     const int j = tile_of(n);
     const uint32_t kt = my_stages + s * kStageBytes;
     const uint32_t vt = kt + kTileBytes;
-    if constexpr (Path::kScored)
-      path.sink().set(a.raw_scores + (((size_t)(seq * a.num_kv_heads + kvh) * a.max_tiles + j) * a.rows +
-                                      row0) * kTileTokens,
-                      a.rows - row0);
+    if constexpr (Path::kScored) path.sink().tile(j);
     if (j >= first_masked) {
       const int nvalid = L - j * kTileTokens;  // rows >= nvalid are past the context
       if (nvalid < kTileTokens) {
@@ -1628,25 +1656,30 @@ __global__ void __launch_bounds__(NW * 32)
 
   // Scored: each warp turns the scores of its own tiles into weights, now that the rows'
   // sums are known (s_row), and adds them to the ledger.  16 lanes take a tile's tokens;
-  // 2 kTiles tiles' loads are in flight.
+  // 2 kTiles tiles' loads are in flight.  The old score is not read: a reduction without
+  // an answer adds to it in L2 (each address by one thread, so the sum has one order), which
+  // leaves one wait per round, for scores that this CTA wrote (32 x 32 heads over FP8:
+  // 106.9 us; with the old scores read and half as many tiles a round 111.6, without the
+  // ledger 99.4, the plain attention 91.2).
   auto ledger = [&]() {
-    constexpr int kTiles = 4;
+    constexpr int kTiles = 8;
     const size_t unit_id = (size_t)seq * a.num_kv_heads + kvh;
-    const float *raw = a.raw_scores + unit_id * a.max_tiles * a.rows * kTileTokens;
-    const int64_t led = (int64_t)unit_id * a.max_rows;
-    const int Lr = min(L, a.max_rows), tok = lane & 15;
+    const int tok = lane & 15;
+    const int step = a.rows * kTileTokens;  // floats between tiles
+    const float *raw = a.raw_scores + unit_id * a.max_tiles * step + score_slot(a.rows, tok);
+    float *sc = a.scores + (int64_t)unit_id * a.max_rows;
+    const int Lr = min(L, a.max_rows);
     for (int n0 = 0; n0 < n_my; n0 += 2 * kTiles) {
-      const float *src[kTiles];
-      float share[kTiles], old[kTiles];
+      float share[kTiles];
       int t[kTiles];
+      const float *src[kTiles];
 #pragma unroll
       for (int u = 0; u < kTiles; ++u) {
         const int nn = n0 + 2 * u + (lane >> 4);
         const int j = tile_of(min(nn, n_my - 1));
         t[u] = nn < n_my ? j * kTileTokens + tok : Lr;
-        src[u] = raw + (size_t)j * a.rows * kTileTokens + tok;
-        share[u] = old[u] = 0.f;
-        if (t[u] < Lr) old[u] = a.scores[led + t[u]];
+        src[u] = raw + (int64_t)j * step;
+        share[u] = 0.f;
       }
       for (int r = 0; r < a.rows; ++r) {
         const float m = s_row[0][r], inv = s_row[1][r];
@@ -1657,9 +1690,14 @@ __global__ void __launch_bounds__(NW * 32)
         for (int u = 0; u < kTiles; ++u) share[u] += fast_exp2(x[u] - m) * inv;
       }
 #pragma unroll
-      for (int u = 0; u < kTiles; ++u)
-        if (t[u] < Lr)
-          ledger_write(a.scores, a.row_pos, a.seq_lens, seq, led + t[u], t[u], L, a.q_len, old[u], share[u]);
+      for (int u = 0; u < kTiles; ++u) {
+        if (t[u] >= Lr) continue;
+        if (t[u] >= L - a.q_len)
+          ledger_write(a.scores, a.row_pos, a.seq_lens, seq, (int64_t)unit_id * a.max_rows + t[u], t[u], L,
+                       a.q_len, 0.f, share[u]);
+        else
+          atomicAdd(sc + t[u], share[u]);
+      }
     }
   };
   // (a row that sees nothing has no weights: its scores are -inf, its maximum counts as 0)

@@ -61,14 +61,22 @@ __global__ void __launch_bounds__(kLedgerThreads) finish_kernel(const LedgerArgs
   const int seq = unit / a.num_kv_heads, kvh = unit % a.num_kv_heads;
   const int Lc = max(0, __ldg(a.context_lens + seq)), L = min(Lc, a.max_rows);
   if (chunk * kLedgerRows >= L) return;
-  const int t = chunk * kLedgerRows + 4 * threadIdx.x;  // this thread's rows t .. t + 3
+  // this thread's four cached rows: slots 4 i .. 4 i + 3 of a tile
+  const int tile = chunk * (kLedgerRows / kTileTokens) + threadIdx.x / 4;
+  const int slot = 4 * (threadIdx.x % 4);
   const float4 *raw = reinterpret_cast<const float4 *>(
-      a.raw_scores + ((size_t)unit * a.max_tiles + t / kTileTokens) * a.rows * kTileTokens + t % kTileTokens);
+      a.raw_scores + ((size_t)unit * a.max_tiles + tile) * a.rows * kTileTokens + slot);
   constexpr int kStep = kTileTokens / 4;  // float4s between query rows
-  const int64_t at = (int64_t)unit * a.max_rows + t;
-  const bool in = t < L;  // (a table holds a multiple of 8 rows)
-  float4 old = make_float4(0.f, 0.f, 0.f, 0.f), x[kAhead];
-  if (in) old = *reinterpret_cast<const float4 *>(a.scores + at);
+  const int64_t led = (int64_t)unit * a.max_rows;
+  int t[4];
+  float o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[i] = tile * kTileTokens + score_token(a.rows, slot + i);
+    o[i] = t[i] < L ? a.scores[led + t[i]] : 0.f;
+  }
+  const bool in = tile * kTileTokens < L;
+  float4 x[kAhead];
 #pragma unroll
   for (int r = 0; r < kAhead; ++r) {
     x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -124,15 +132,11 @@ __global__ void __launch_bounds__(kLedgerThreads) finish_kernel(const LedgerArgs
       for (; r < n; ++r) add(raw[(size_t)(r0 + r) * kStep], r);
     }
   }
-  const float s[4] = {share.x, share.y, share.z, share.w}, o[4] = {old.x, old.y, old.z, old.w};
-  if (in && t + 4 <= Lc - a.q_len) {
-    *reinterpret_cast<float4 *>(a.scores + at) = make_float4(o[0] + s[0], o[1] + s[1], o[2] + s[2], o[3] + s[3]);
-  } else {
+  const float s[4] = {share.x, share.y, share.z, share.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (t + i < L)
-        ledger_write(a.scores, a.row_pos, a.seq_lens, seq, at + i, t + i, Lc, a.q_len, o[i], s[i]);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (t[i] < L)
+      ledger_write(a.scores, a.row_pos, a.seq_lens, seq, led + t[i], t[i], Lc, a.q_len, o[i], s[i]);
 }
 
 template <typename T, int D>
