@@ -18,6 +18,7 @@ Layouts match ``include/pagedattn.h``:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import threading
@@ -88,6 +89,7 @@ NOALLOC_SCRATCH_BYTES = 8 << 20   # PA_NOALLOC_SCRATCH_BYTES
 
 _lock = threading.Lock()
 _lib = None
+_fast = None   # the checked calls of csrc/pa_calls.cpp, once the library is loaded
 
 
 class PagedAttnError(RuntimeError):
@@ -98,7 +100,7 @@ class PagedAttnError(RuntimeError):
 
 def load(path: str = LIBRARY) -> ctypes.CDLL:
     """Load the library (once).  Raises RuntimeError when it has not been built."""
-    global _lib
+    global _lib, _fast
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -109,6 +111,8 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
+            if path == LIBRARY:
+                _fast = importlib.import_module("._calls", __package__)  # (links the same library)
             _lib = lib
         return _lib
 
@@ -480,9 +484,11 @@ def pa_decode_split_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
 
 
 # ------------------------------------------------- rotary append, scored decode, eviction
-# These calls are short on the GPU (a few microseconds for a decode step's tokens), so
-# their checks are written for the host's time: one test per tensor on the way that
-# passes, and the reason worked out only on the way that fails.
+# These calls are short on the GPU (a few microseconds for a decode step's tokens), so a
+# call on the current stream goes through csrc/pa_calls.cpp, which makes the checks below
+# in compiled code and answers None where one fails.  What it does not take (another
+# stream, buffers to be made, padded vocabularies, anything wrong) comes here; the checks
+# too are written for the host's time, with the reason worked out only where one fails.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -597,6 +603,13 @@ def pa_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     tokens may be strided.  positions int32 [num_axes, n_tokens] (or [n_tokens] for one
     axis); turns, pair_axis from rope_table.  k_scale, v_scale: FP8 caches.
     """
+    if stream is None and _fast is not None:
+        st = _fast.rope_append(q_out, q, k, v, k_cache, v_cache, positions, slot_mapping, turns,
+                                pair_axis, interleaved, k_scale, v_scale)
+        if st == PA_OK:
+            return q_out
+        if st is not None:
+            raise PagedAttnError("pa_rope_append", st)
     dev = _device_of(q)
     num_blocks, h_kv, block_size, head_dim = cache = _cache_shape(k_cache)
     elt = q.dtype
@@ -651,6 +664,13 @@ def pa_decode_scored(out: torch.Tensor, scores: torch.Tensor, q: torch.Tensor,
                      v_scale: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Paged attention that also adds every cached row's attention weight to scores
     (and notes the positions of this step's rows in row_pos).  FP8 caches with scales."""
+    if stream is None and _fast is not None:
+        st = _fast.decode_scored(out, scores, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                  q_len, num_splits, workspace, row_pos, seq_lens, k_scale, v_scale)
+        if st == PA_OK:
+            return out
+        if st is not None:
+            raise PagedAttnError("pa_decode_scored", st)
     dev = _device_of(q)
     num_blocks, h_kv, block_size, head_dim = cache = _cache_shape(k_cache)
     elt = q.dtype
@@ -704,6 +724,13 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Tensor,
     """Shorten every sequence longer than ``budget`` rows to it, each KV head keeping its
     first ``sinks`` and last ``recent`` positions and its highest scores.  The ledgers are
     updated in place unless both outputs are given.  Returns the new context lengths."""
+    if stream is None and _fast is not None:
+        st = _fast.evict(k_cache, v_cache, scores, row_pos, block_tables, context_lens, seq_lens, budget,
+                          sinks, recent, scores_out, row_pos_out, new_lens, workspace)
+        if st == PA_OK:
+            return new_lens
+        if st is not None:
+            raise PagedAttnError("pa_evict", st)
     dev = _device_of(k_cache)
     num_blocks, h_kv, block_size, head_dim = cache = _cache_shape(k_cache)
     elt = k_cache.dtype
@@ -778,6 +805,13 @@ def pa_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | Non
     wider vocabulary).  Returns (out_tokens, num_accepted, new_lens or None): new_lens
     is made when context_lens is given.
     """
+    if stream is None and _fast is not None:
+        st = _fast.verify_drafts(target_probs, draft_probs, draft_tokens, accept_u, sample_u, draft_lens,
+                                  context_lens, out_tokens, num_accepted, new_lens)
+        if st == PA_OK:
+            return out_tokens, num_accepted, new_lens
+        if st is not None:
+            raise PagedAttnError("pa_verify_drafts", st)
     dev = _device_of(target_probs)
     if draft_tokens.dim() != 2:
         raise ValueError("draft_tokens must be [num_seqs, max_draft]")

@@ -2,7 +2,9 @@
 
 Each .cu file compiles to an object in parallel, then one link step produces
 ``paged_kv_cache_20_gb300/libpagedattn.so``.  The library links the shared CUDA
-runtime so it shares one runtime instance with PyTorch in the same process.
+runtime so it shares one runtime instance with PyTorch in the same process.  The
+binding's checked calls (``csrc/pa_calls.cpp``, host code against torch's headers) go
+into ``paged_kv_cache_20_gb300/_calls.so`` beside it.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libpagedattn.so")
+CALLS = os.path.join(HERE, "_calls.so")   # the binding's checked calls (host code only)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -42,10 +45,24 @@ def _deps() -> list[str]:
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIBRARY):
+    if not os.path.exists(LIBRARY) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIBRARY)
+    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(CALLS))
     return any(os.path.getmtime(f) > t for f in _deps())
+
+
+def calls_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+            os.path.join(CSRC, "pa_calls.cpp"), "-o", out, "-L", os.path.join(root, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", HERE, "-l:libpagedattn.so",
+            "-Wl,-rpath,$ORIGIN"]
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -72,6 +89,11 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{res.stdout}{res.stderr}")
     os.replace(tmp, LIBRARY)
+    tmp = CALLS + ".tmp"
+    res = subprocess.run(calls_command(tmp), capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed: {' '.join(calls_command(tmp))}\n{res.stdout}{res.stderr}")
+    os.replace(tmp, CALLS)
     return LIBRARY
 
 

@@ -132,3 +132,43 @@ def test_verify_drafts_over_its_own_lengths(pa):
     lens = torch.tensor([9, 7], dtype=I32, device=DEV)
     got = pa.pa_verify_drafts(**a, context_lens=lens, new_lens=lens)
     assert got[2] is lens and lens.tolist() == [9, 5] and got[1].tolist() == [3, 1]
+
+
+def test_both_ways_of_calling_agree(pa):
+    """A call on the current stream goes through compiled checks, one on a stream that is
+    named through the binding's own: the same results, strided arguments among them."""
+    assert pa._fast is not None
+    here = torch.cuda.current_stream()
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g).half().to(DEV)  # noqa: E731
+    qkv = rnd(20, 8, 64)
+    turns, axis = pa.rope_table(64, device=DEV)
+    got = []
+    for stream in (None, here):
+        r = rope_args() | dict(q_out=z(20, 4, 64), q=qkv[:, :4], k=qkv[:, 4:6], v=qkv[:, 6:],
+                               positions=torch.arange(20, dtype=I32, device=DEV),
+                               slot_mapping=torch.arange(20, device=DEV), turns=turns, pair_axis=axis)
+        pa.pa_rope_append(**r, stream=stream)
+        tables = torch.tensor([[0, 1], [1, 0]], dtype=I32, device=DEV)
+        lens = torch.tensor([20, 17], dtype=I32, device=DEV)
+        out, scores = z(2, 1, 4, 64), z(2, 2, 32, dtype=F32)
+        ws = z(pa.pa_decode_scored_workspace_size(2, 4, 1, 64, 1, 2, 16), dtype=torch.uint8)
+        pa.pa_decode_scored(out, scores, r["q_out"][:2].view(2, 1, 4, 64).contiguous(), r["k_cache"], r["v_cache"],
+                            tables, lens, 0.125, workspace=ws, stream=stream)
+        pos = torch.arange(32, dtype=I32, device=DEV).repeat(2, 2, 1)
+        new = z(2, dtype=I32)
+        we = z(pa.pa_evict_workspace_size(2, 2, 12), dtype=torch.uint8)
+        pa.pa_evict(r["k_cache"], r["v_cache"], scores, pos, tables[:, :].contiguous(), lens.clamp_max(12), lens, 12,
+                    1, 2, new_lens=new, workspace=we, stream=stream)
+        v = verify_args()
+        v["target_probs"] = torch.softmax(torch.arange(80, device=DEV).view(2, 4, 10) / 7.0, -1)
+        v["sample_u"].fill_(0.4)
+        v["accept_u"].fill_(0.9)
+        toks, acc = z(2, 4, dtype=I32), z(2, dtype=I32)
+        pa.pa_verify_drafts(**v, out_tokens=toks, num_accepted=acc, stream=stream)
+        got.append([r["q_out"], r["k_cache"], r["v_cache"], out, scores, pos, new, toks, acc])
+    torch.cuda.synchronize()
+    assert pa.pa_device_error() == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert got[0][3].abs().sum() > 0 and got[0][7].min() >= -1
