@@ -14,6 +14,12 @@ Layouts match ``include/pagedattn.h``:
   context_lens      int32 [num_seqs]       (count this step's new tokens)
   slot_mapping      int64 [n_tokens]
   scores, row_pos   fp32, int32 [num_seqs, num_kv_heads, max_blocks_per_seq * block_size]
+
+Streams: a call runs on the current stream, or on the one named by ``stream`` (a
+``torch.cuda.Stream`` or a raw handle; ordering it after the work that makes the
+arguments is the caller's).  Workspaces and outputs that are not given are made from that
+stream's memory pool, as under ``torch.cuda.stream(stream)``: an output that is then used
+on another stream wants ``record_stream`` before it is dropped.
 """
 from __future__ import annotations
 
@@ -132,6 +138,25 @@ def _stream(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made(shape, dtype, device, stream) -> torch.Tensor:
+    """A workspace or output that the caller did not give, from the memory pool of the
+    stream that the call runs on: memory of another stream's pool may be given out again
+    once the call has returned, with its kernels still to come."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle = _stream(stream)
+    if handle == 2:  # cudaStreamPerThread: one handle, a stream in every thread
+        raise ValueError("on the per-thread default stream give every workspace and output")
+    if not (hasattr(stream, "cuda_stream") and hasattr(stream, "device")):
+        # (handles 0 and 1 both name the legacy default stream)
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
+    elif stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _cuda(t: torch.Tensor, name: str, dtype=None) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -160,7 +185,7 @@ def pa_slot_mapping(block_tables: torch.Tensor, context_lens: torch.Tensor, bloc
     """Slots of each sequence's last q_len positions -> int64 [num_seqs * q_len]."""
     n, maxb = (int(x) for x in block_tables.shape)
     if out is None:
-        out = torch.empty(n * q_len, dtype=torch.int64, device=block_tables.device)
+        out = _made((n * q_len,), torch.int64, block_tables.device, stream)
     _check("pa_slot_mapping", load().pa_slot_mapping(
         _cuda(out, "out", torch.int64), _cuda(block_tables, "block_tables", torch.int32),
         _cuda(context_lens, "context_lens", torch.int32), n, maxb, block_size, q_len,
@@ -248,7 +273,7 @@ def pa_decode_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     if num_splits > 1:
         if workspace is None:
             nbytes = pa_decode_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _made((nbytes,), torch.uint8, q.device, stream)
         ws_ptr, ws_bytes = _cuda(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _check("pa_decode_fp8", load().pa_decode_fp8(
         _cuda(out, "out"), _cuda(q, "q"), kn, vn, _fp8_cache(k_cache, "k_cache"),
@@ -372,7 +397,7 @@ def pa_append_decode(out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor,
     if num_splits > 1:
         if workspace is None:
             nbytes = pa_decode_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _made((nbytes,), torch.uint8, q.device, stream)
         ws_ptr, ws_bytes = _cuda(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _check("pa_append_decode", load().pa_append_decode(
         _cuda(out, "out"), _cuda(q, "q"), _cuda(k_new, "k_new"), _cuda(v_new, "v_new"),
@@ -407,7 +432,7 @@ def pa_decode_cascade(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                 raise TypeError(f"{nm} must have the cache dtype {k_cache.dtype}")
     if workspace is None:
         nbytes = pa_decode_workspace_size(num_seqs, h_q, q_len, head_dim, 1 + tail_splits)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _made((nbytes,), torch.uint8, q.device, stream)
     _check("pa_decode_cascade", load().pa_decode_cascade(
         _cuda(out, "out"), _cuda(q, "q"),
         None if k_new is None else _cuda(k_new, "k_new"),
@@ -438,7 +463,7 @@ def paged_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     """
     if fused:
         if out is None:
-            out = torch.empty_like(q)
+            out = _made(q.shape, q.dtype, q.device, stream)
         return pa_append_decode(out, q, k_new, v_new, k_cache, v_cache, block_tables,
                                 context_lens, scale, q_len, num_splits, workspace, stream)
     block_size = int(k_cache.shape[2])
@@ -446,14 +471,14 @@ def paged_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                                    out=slot_mapping, stream=stream)
     pa_append_kv(k_cache, v_cache, k_new, v_new, slot_mapping, stream=stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(q.shape, q.dtype, q.device, stream)
     if num_splits <= 1:
         return pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, q_len,
                          stream=stream)
     if workspace is None:
         num_seqs, h_q, head_dim = int(q.shape[0]), int(q.shape[-2]), int(q.shape[-1])
         nbytes = pa_decode_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _made((nbytes,), torch.uint8, q.device, stream)
     pa_decode_partial(workspace, q, k_cache, v_cache, block_tables, context_lens, scale,
                       num_splits, q_len, stream=stream)
     return pa_decode_combine(out, workspace, num_splits, stream=stream)
@@ -697,7 +722,7 @@ def pa_decode_scored(out: torch.Tensor, scores: torch.Tensor, q: torch.Tensor,
     if workspace is None:
         nbytes = pa_decode_scored_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits, maxb,
                                                  block_size)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _made((nbytes,), torch.uint8, q.device, stream)
     st = (_lib or load()).pa_decode_scored(
         _ptr(out, "out", elt, dev), _ptr(scores, "scores", torch.float32, dev), rp,
         _ptr(q, "q", elt, dev), kc, vc, ks, vs, _ptr(block_tables, "block_tables", torch.int32, dev),
@@ -755,11 +780,11 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, scores: torch.Tensor,
         so = _ptr(scores_out, "scores_out", torch.float32, dev)
         po = _ptr(row_pos_out, "row_pos_out", torch.int32, dev)
     if new_lens is None:
-        new_lens = torch.empty_like(context_lens)
+        new_lens = _made(per_seq, torch.int32, context_lens.device, stream)
     _shape(new_lens, "new_lens", per_seq)
     if workspace is None:
         nbytes = pa_evict_workspace_size(num_seqs, h_kv, budget)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=k_cache.device)
+        workspace = _made((nbytes,), torch.uint8, k_cache.device, stream)
     st = (_lib or load()).pa_evict(
         _ptr(k_cache, "k_cache", elt, dev), _ptr(v_cache, "v_cache", elt, dev), so, po,
         _ptr(new_lens, "new_lens", torch.int32, dev), sc, rp,
@@ -834,17 +859,17 @@ def pa_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | Non
         _shape(context_lens, "context_lens", per_seq)
         cl = _ptr(context_lens, "context_lens", i32, dev)
         if new_lens is None:
-            new_lens = torch.empty_like(context_lens)
+            new_lens = _made(per_seq, torch.int32, context_lens.device, stream)
     if new_lens is not None:
         if context_lens is None:
             raise ValueError("new_lens needs context_lens")
         _shape(new_lens, "new_lens", per_seq)
         nl = _ptr(new_lens, "new_lens", i32, dev)
     if out_tokens is None:
-        out_tokens = torch.empty(n, k + 1, dtype=i32, device=target_probs.device)
+        out_tokens = _made((n, k + 1), i32, target_probs.device, stream)
     _shape(out_tokens, "out_tokens", (n, k + 1))
     if num_accepted is None:
-        num_accepted = torch.empty(n, dtype=i32, device=target_probs.device)
+        num_accepted = _made(per_seq, i32, target_probs.device, stream)
     _shape(num_accepted, "num_accepted", per_seq)
     st = (_lib or load()).pa_verify_drafts(
         _ptr(out_tokens, "out_tokens", i32, dev), _ptr(num_accepted, "num_accepted", i32, dev), nl, cl,
