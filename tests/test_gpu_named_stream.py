@@ -22,17 +22,18 @@ def pa():
     return pa
 
 
-def meanwhile(call):
-    """call(stream) on a stream that is still busy, the current stream taking and filling
-    whatever memory it is given; then again by the stream's raw handle."""
-    torch.cuda.synchronize()
+def meanwhile(setup, call):
+    """call(stream, *setup()) on a stream that is still busy, the current stream taking and
+    filling whatever memory it is given; then again by the stream's raw handle."""
     torch.cuda.empty_cache()
     got = []
     side = torch.cuda.Stream()
     for stream in (side, side.cuda_stream):
+        state = setup()
+        torch.cuda.synchronize()
         with torch.cuda.stream(side):
             torch.cuda._sleep(20_000_000)  # about 10 ms
-        out = call(stream)
+        out = call(stream, *state)
         pools = {s["stream"] for s in torch.cuda.memory_snapshot()}
         assert side.cuda_stream in pools
         hogs = [torch.full((n,), 255, dtype=torch.uint8, device=DEV)
@@ -51,15 +52,15 @@ def test_evict(pa, few):
     c = evicts.make(31, lens, 2, 64, 16)
     want = evicts.run(pa, c, budget, 4, 100, False)[:5]
 
-    def call(stream):
-        k, v = (c[x].to(DEV).view(torch.bfloat16) for x in ("k", "v"))
-        scores, pos, table = c["scores"].to(DEV), c["pos"].to(DEV), c["table"].to(DEV)
-        cl, sl = (torch.tensor(c[x], dtype=torch.int32, device=DEV) for x in ("lens", "sl"))
-        torch.cuda.synchronize()
+    def setup():
+        return (*(c[x].to(DEV).view(torch.bfloat16) for x in ("k", "v")), c["scores"].to(DEV), c["pos"].to(DEV),
+                c["table"].to(DEV), *(torch.tensor(c[x], dtype=torch.int32, device=DEV) for x in ("lens", "sl")))
+
+    def call(stream, k, v, scores, pos, table, cl, sl):
         new = pa.pa_evict(k, v, scores, pos, table, cl, sl, budget, 4, 100, stream=stream)
         return k, v, scores, pos, new, (table, cl, sl)
 
-    for got in meanwhile(call):
+    for got in meanwhile(setup, call):
         for x, y in zip(got[:5], want):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     assert pa.pa_device_error() == 0
@@ -70,14 +71,15 @@ def test_decode_scored(pa, u, splits):
     c = scoreds.make(32, [900, 500], u, 16, 2, 128, 16, "bf16", False)
     want = scoreds.run(pa, c, splits)
 
-    def call(stream):
-        out, scores, pos = torch.empty_like(c["q"]), c["scores"].clone(), c["pos"].clone()
-        torch.cuda.synchronize()
+    def setup():
+        return torch.empty_like(c["q"]), c["scores"].clone(), c["pos"].clone()
+
+    def call(stream, out, scores, pos):
         pa.pa_decode_scored(out, scores, c["q"], c["k"], c["v"], c["table"], c["cl"], c["scale"], q_len=u,
                             num_splits=splits, row_pos=pos, seq_lens=c["sl"], stream=stream)
         return out, scores, pos
 
-    for got in meanwhile(call):
+    for got in meanwhile(setup, call):
         for x, y in zip(got, want):
             assert torch.equal(x, y)
     assert pa.pa_device_error() == 0
@@ -89,8 +91,8 @@ def test_verify_drafts(pa):
     want = verifies.both(pa, c, lens=lens)
     d = {a: b.to(DEV) for a, b in c.items()}
     cl = torch.tensor(lens, dtype=torch.int32, device=DEV)
-    for got in meanwhile(lambda s: pa.pa_verify_drafts(d["p"], d["q"], d["x"], d["au"], d["su"],
-                                                       context_lens=cl, stream=s)):
+    for got in meanwhile(tuple, lambda s: pa.pa_verify_drafts(d["p"], d["q"], d["x"], d["au"], d["su"],
+                                                              context_lens=cl, stream=s)):
         for x, y in zip(got, want):
             assert torch.equal(x, y)
 
@@ -111,9 +113,10 @@ def test_attention(pa, how):
                  for s in ((n, 1, hq, d), (n, hkv, d), (n, hkv, d)))
     sc = torch.full((hkv,), 0.03, device=DEV)
 
-    def call(stream):
-        kc, vc, out = k.clone(), v.clone(), torch.empty_like(q)
-        torch.cuda.synchronize()
+    def setup():
+        return k.clone(), v.clone(), torch.empty_like(q)
+
+    def call(stream, kc, vc, out):
         if fp8:
             pa.pa_decode_fp8(out, q, kc, vc, sc, sc, tables, lens, 0.09, num_splits=3, k_new=kn, v_new=vn,
                              stream=stream)
@@ -126,9 +129,9 @@ def test_attention(pa, how):
                                        num_splits=1 if how == "step" else 3, stream=stream)
         return out, kc, vc
 
-    want = call(None)
+    want = call(None, *setup())
     torch.cuda.synchronize()
-    for got in meanwhile(call):
+    for got in meanwhile(setup, call):
         for x, y in zip(got, want):
             assert torch.equal(x, y)
     assert pa.pa_device_error() == 0
