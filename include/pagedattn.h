@@ -394,7 +394,8 @@ PA_API pa_status pa_rope_append(void *q_out, const void *q, const void *k, const
  * (their weight on it is 0, and 0 times it is NaN).  The ledger is free of that: a row
  * gains nothing from query tokens that do not see it.
  * The sums have one order: results do not change from run to run.  num_splits as for
- * pa_append_decode up to 16 query tokens; above, the call takes no partitions.
+ * pa_append_decode up to 16 query tokens; above, the call takes no partitions, and out
+ * must not overlap q (the ledger's pass reads q after out is written).
  * Workspace: pa_decode_scored_workspace_size bytes, 256-byte aligned (up to 16 query
  * tokens it holds 4 bytes per query row and table position); nothing in it has to
  * start at zero.  Two calls that can overlap need workspaces of their own.

@@ -1001,6 +1001,9 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
   if (k_scale && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PA_ERR_INVALID_ARG;
   const bool many = q_len > kMaxDecodeQLen;
+  // (many query rows: the weights' pass reads q again, after the attention has written out)
+  const size_t q_bytes = (size_t)num_seqs * q_len * num_q_heads * head_dim * 2;
+  if (many && pa::overlap(out, q_bytes, q, q_bytes)) return PA_ERR_INVALID_ARG;
   const ScoredLayout lay = scored_layout(num_seqs, num_q_heads, q_len, head_dim, num_splits,
                                          max_blocks_per_seq, block_size);
   if (workspace_bytes < lay.total) return PA_ERR_INVALID_ARG;

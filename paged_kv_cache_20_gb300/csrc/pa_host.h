@@ -2,6 +2,7 @@
 // C ABI.
 #pragma once
 
+#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/pagedattn.h"
@@ -14,6 +15,12 @@ unsigned *error_word();
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Whether two buffers share a byte.
+inline bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
 
 // Block sizes the kernels take: a block of 32 tokens is read as two 16-token tiles,
 // a 16-token tile spans two blocks of 8
