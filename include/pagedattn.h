@@ -431,7 +431,7 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
  * pa_copy_blocks first).  A block id outside the pool: the row is not copied,
  * PA_ERR_DEVICE_CHECK.
  *   element_bytes  2 (16-bit cache) or 1 (FP8, head_dim 128): rows are moved bit for bit
- *   new_lens       int32 [num_seqs], neither context_lens nor seq_lens itself
+ *   new_lens       int32 [num_seqs], overlapping neither context_lens nor seq_lens
  *   workspace      pa_evict_workspace_size bytes; two calls that can overlap need
  *                  workspaces of their own
  * budget >= sinks + recent, budget >= 1.

@@ -499,8 +499,6 @@ extern "C" PA_API pa_status pa_evict(
     return PA_ERR_INVALID_ARG;
   // the ledgers are both updated in place or both written elsewhere
   if ((scores == scores_out) != (row_pos == row_pos_out)) return PA_ERR_INVALID_ARG;
-  // (every KV head reads the old lengths while one writes the new)
-  if (new_lens == context_lens || new_lens == seq_lens) return PA_ERR_INVALID_ARG;
   const void *ptrs[7] = {k_cache, v_cache, workspace, scores, row_pos, scores_out, row_pos_out};
   for (const void *p : ptrs)
     if (!pa::aligned16(p)) return PA_ERR_INVALID_ARG;
@@ -511,6 +509,16 @@ extern "C" PA_API pa_status pa_evict(
   if ((int64_t)max_blocks_per_seq * block_size >= (int64_t)1 << 30) return PA_ERR_INVALID_ARG;
   if ((int64_t)num_seqs * num_kv_heads >= (int64_t)1 << 31) return PA_ERR_INVALID_ARG;
   if (workspace_bytes < pa_evict_workspace_size(num_seqs, num_kv_heads, budget))
+    return PA_ERR_INVALID_ARG;
+  // every KV head reads the old lengths while one writes the new; ledgers are updated in
+  // place or quite apart
+  const size_t lens = (size_t)num_seqs * sizeof(int32_t);
+  const size_t ledger = (size_t)num_seqs * num_kv_heads * max_blocks_per_seq * block_size * 4;
+  if (pa::overlap(new_lens, lens, context_lens, lens) || pa::overlap(new_lens, lens, seq_lens, lens))
+    return PA_ERR_INVALID_ARG;
+  if (scores != scores_out &&
+      (pa::overlap(scores_out, ledger, scores, ledger) || pa::overlap(row_pos_out, ledger, row_pos, ledger) ||
+       pa::overlap(scores_out, ledger, row_pos, ledger) || pa::overlap(row_pos_out, ledger, scores, ledger)))
     return PA_ERR_INVALID_ARG;
   EvictArgs a;
   a.k_cache = static_cast<uint8_t *>(k_cache);
