@@ -470,7 +470,9 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, float *scores_out, int32
  *   out_tokens    int32 [num_seqs][max_draft + 1]; num_accepted int32 [num_seqs]
  * A draft id outside [0, vocab) is rejected, a draft_lens outside [0, max_draft] is
  * clamped, a target row without any positive entry gives token -1: each sets
- * PA_ERR_DEVICE_CHECK.  Pointers 4-byte aligned.
+ * PA_ERR_DEVICE_CHECK.  Pointers 4-byte aligned; outputs overlap neither one another nor
+ * the int32 inputs (new_lens apart, as said; and new_lens or num_accepted may be
+ * draft_lens itself).
  */
 PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *num_accepted, int32_t *new_lens,
                                   const int32_t *context_lens, const float *target_probs,

@@ -336,6 +336,23 @@ extern "C" PA_API pa_status pa_verify_drafts(
                           draft_probs,  draft_tokens, draft_lens, accept_u,     sample_u};
   for (const void *p : ptrs)
     if (!pa::aligned4(p)) return PA_ERR_INVALID_ARG;
+  // A sequence's thread blocks read its inputs before one of them writes its outputs, but
+  // sequences have no order: an output lies on an input only where every sequence's part
+  // lies on its own (and context_lens is read last).
+  const size_t lens = (size_t)num_seqs * 4, drafts = lens * max_draft, tokens = lens + drafts;
+  auto shared = [](const void *p, size_t p_bytes, const void *q, size_t q_bytes, bool same_is_fine) {
+    return p && q && pa::overlap(p, p_bytes, q, q_bytes) && !(same_is_fine && p == q);
+  };
+  const int32_t *old_lens = new_lens ? context_lens : nullptr;
+  if (shared(new_lens, lens, old_lens, lens, true) || shared(new_lens, lens, draft_lens, lens, true) ||
+      shared(new_lens, lens, draft_tokens, drafts, false) ||
+      shared(num_accepted, lens, draft_lens, lens, true) || shared(num_accepted, lens, old_lens, lens, false) ||
+      shared(num_accepted, lens, draft_tokens, drafts, false) ||
+      shared(out_tokens, tokens, draft_tokens, drafts, num_seqs == 1) ||
+      shared(out_tokens, tokens, draft_lens, lens, false) || shared(out_tokens, tokens, old_lens, lens, false) ||
+      shared(out_tokens, tokens, num_accepted, lens, false) ||
+      shared(out_tokens, tokens, new_lens, lens, false) || shared(num_accepted, lens, new_lens, lens, false))
+    return PA_ERR_INVALID_ARG;
   VerifyArgs a;
   a.out_tokens = out_tokens;
   a.num_accepted = num_accepted;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests.test_abi import FAKE, lib  # noqa: F401  (fixture)
-from tests.test_operators_abi import EVICT, INVALID, SCORED, _call
+from tests.test_operators_abi import EVICT, INVALID, SCORED, VERIFY, _call
 
 AT = 0x1000000  # never used: the calls are refused, or (without a GPU) fail at their first step
 
@@ -55,3 +55,34 @@ def test_evict(lib, kw):  # noqa: F811
                                 beside(so=("sc", 0), po=("rp", 0))])
 def test_evict_beside(lib, kw):  # noqa: F811
     assert _call(lib, "pa_evict", EVICT, kw) != INVALID
+
+
+SEQS, DRAFTS = 2, 3   # of VERIFY
+VERIFY_AT = {**{k: AT + i * 0x10000 for i, k in enumerate(VERIFY) if VERIFY[k] == FAKE}, "dl": AT - 0x10000}
+
+
+def verify(**kw):
+    a = dict(VERIFY_AT)
+    for k, (other, by) in kw.items():
+        a[k] = VERIFY_AT[other] + by
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    verify(nl=("cl", 4)), verify(nl=("cl", -4)), verify(nl=("dl", 4)), verify(acc=("dl", -4)), verify(acc=("cl", 0)),
+    verify(out=("x", 0)), verify(out=("x", 4 * SEQS * DRAFTS - 4)), verify(out=("x", 4 - 4 * SEQS * (DRAFTS + 1))),
+    verify(out=("dl", 0)), verify(out=("cl", 0)), verify(acc=("x", 8)), verify(nl=("x", 0)),
+    verify(acc=("out", 16)), verify(nl=("out", 0)), verify(nl=("acc", 0)),
+    {**verify(out=("x", 4)), "n": 1},
+])
+def test_verify_drafts(lib, kw):  # noqa: F811
+    assert _call(lib, "pa_verify_drafts", VERIFY, kw) == INVALID
+
+
+@accepted
+@pytest.mark.parametrize("kw", [
+    verify(), verify(nl=("cl", 0)), verify(nl=("dl", 0)), verify(acc=("dl", 0)), verify(out=("x", 4 * SEQS * DRAFTS)),
+    {**verify(out=("x", 0)), "n": 1}, {**verify(acc=("cl", 0)), "nl": None}, {**verify(), "nl": None, "cl": None, "dl": None},
+])
+def test_verify_drafts_beside(lib, kw):  # noqa: F811
+    assert _call(lib, "pa_verify_drafts", VERIFY, kw) != INVALID
