@@ -428,8 +428,8 @@ PA_API pa_status pa_decode_scored(void *out, float *scores, int32_t *row_pos, co
  * arrays (not overlapping), rows below new_lens[i] written; rows from there on are
  * left as they were.  With other arrays the call may be repeated with the same result.
  * Blocks of a sequence longer than the budget must be its own (copy shared ones with
- * pa_copy_blocks first).  A block id outside the pool: the row is not copied,
- * PA_ERR_DEVICE_CHECK.
+ * pa_copy_blocks first).  A block id outside the pool, of the hole or of the row that would
+ * fill it: the hole keeps its row, score and position, PA_ERR_DEVICE_CHECK.
  *   element_bytes  2 (16-bit cache) or 1 (FP8, head_dim 128): rows are moved bit for bit
  *   new_lens       int32 [num_seqs], overlapping neither context_lens nor seq_lens
  *   workspace      pa_evict_workspace_size bytes; two calls that can overlap need

@@ -242,10 +242,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a)
   };
   const unsigned below = (1u << lane) - 1u;
   const int32_t *table = a.block_tables + (int64_t)seq * a.max_blocks_per_seq;
-  // move pair p: the ledgers here; the row indices of its copy (-1: no such block)
+  // move pair p: the ledgers here, and the row indices of its copy (-1: a block outside the
+  // pool, and the hole's row and ledger entries stay as they are)
   auto start_move = [&](int2 p, int64_t &rt, int64_t &rf) {
-    scores_out[p.x] = __ldcg(scores + p.y);
-    row_pos_out[p.x] = __ldcg(row_pos + p.y);
+    const float score = __ldcg(scores + p.y);
+    const int pos = __ldcg(row_pos + p.y);
     const int sh = a.block_shift, mask = (1 << sh) - 1;
     const int bt = __ldg(table + (p.x >> sh)), bf = __ldg(table + (p.y >> sh));
     rt = rf = -1;
@@ -253,6 +254,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a)
       pa::record_error(a.err, pa::kErrCheck);
       return;
     }
+    scores_out[p.x] = score;
+    row_pos_out[p.x] = pos;
     rt = (((int64_t)bt * a.num_kv_heads + head) << sh) + (p.x & mask);
     rf = (((int64_t)bf * a.num_kv_heads + head) << sh) + (p.y & mask);
   };
