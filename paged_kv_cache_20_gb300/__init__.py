@@ -28,6 +28,7 @@ import importlib
 import math
 import os
 import threading
+import warnings
 
 import torch
 
@@ -104,6 +105,22 @@ class PagedAttnError(RuntimeError):
         self.status = status
 
 
+def _checked_calls():
+    """csrc/pa_calls.cpp (links the same library), or None where it is missing or was built
+    for another torch: the binding then makes every check and call itself."""
+    try:
+        calls = importlib.import_module("._calls", __package__)
+        version = getattr(calls, "torch_version", "?")
+        if version == torch.__version__:
+            return calls
+        why = f"built for torch {version}, this is {torch.__version__}"
+    except ImportError as e:
+        why = str(e)
+    warnings.warn(f"{__package__}._calls is not used ({why}): short calls take a few microseconds longer; "
+                  "paged_kv_cache_20_gb300._build.build() makes it", RuntimeWarning, stacklevel=3)
+    return None
+
+
 def load(path: str = LIBRARY) -> ctypes.CDLL:
     """Load the library (once).  Raises RuntimeError when it has not been built."""
     global _lib, _fast
@@ -118,7 +135,7 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
                 fn.restype = res
                 fn.argtypes = args
             if path == LIBRARY:
-                _fast = importlib.import_module("._calls", __package__)  # (links the same library)
+                _fast = _checked_calls()
             _lib = lib
         return _lib
 

@@ -4,7 +4,8 @@ Each .cu file compiles to an object in parallel, then one link step produces
 ``paged_kv_cache_20_gb300/libpagedattn.so``.  The library links the shared CUDA
 runtime so it shares one runtime instance with PyTorch in the same process.  The
 binding's checked calls (``csrc/pa_calls.cpp``, host code against torch's headers) go
-into ``paged_kv_cache_20_gb300/_calls.so`` beside it.
+into ``paged_kv_cache_20_gb300/_calls.so`` beside it; where they cannot be built the
+binding makes the same calls without them.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,10 +46,20 @@ def _deps() -> list[str]:
     return files
 
 
+def _calls_record() -> str:
+    """File that says for which torch the checked calls were last built, or tried."""
+    return os.path.join(BUILD_DIR, "calls.txt")
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIBRARY) or not os.path.exists(CALLS):
+    import torch
+    if not os.path.exists(LIBRARY) or not os.path.exists(_calls_record()):
         return True
-    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(CALLS))
+    with open(_calls_record()) as f:
+        outcome, version = f.read().split()
+    if version != torch.__version__ or (outcome == "built" and not os.path.exists(CALLS)):
+        return True
+    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(_calls_record()))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
@@ -57,12 +69,35 @@ def calls_command(out: str) -> list[str]:
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f'-DPA_TORCH_VERSION="{torch.__version__}"',
             "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
             "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
             "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
             os.path.join(CSRC, "pa_calls.cpp"), "-o", out, "-L", os.path.join(root, "lib"),
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", HERE, "-l:libpagedattn.so",
             "-Wl,-rpath,$ORIGIN"]
+
+
+def build_calls() -> None:
+    """The checked calls, after the library.  They only shorten calls: where they cannot be
+    built (no headers of Python or torch) that is a warning, and none are left behind."""
+    import torch
+    tmp = CALLS + ".tmp"
+    cmd = calls_command(tmp)
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        failure = res.stdout + res.stderr if res.returncode != 0 else None
+    except OSError as e:
+        failure = str(e)
+    if failure is None:
+        os.replace(tmp, CALLS)
+    else:
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
+        warnings.warn(f"_calls.so not built, calls are checked in Python: {' '.join(cmd)}\n{failure}",
+                      RuntimeWarning, stacklevel=2)
+    with open(_calls_record(), "w") as f:
+        f.write(f"{'failed' if failure is not None else 'built'} {torch.__version__}\n")
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -89,11 +124,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{res.stdout}{res.stderr}")
     os.replace(tmp, LIBRARY)
-    tmp = CALLS + ".tmp"
-    res = subprocess.run(calls_command(tmp), capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"g++ failed: {' '.join(calls_command(tmp))}\n{res.stdout}{res.stderr}")
-    os.replace(tmp, CALLS)
+    build_calls()
     return LIBRARY
 
 

@@ -283,4 +283,13 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", "Checked calls of libpag
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&kModule); }
+// torch_version: the torch whose headers this was built with; with another one nothing here
+// may be called.
+PyMODINIT_FUNC PyInit__calls(void) {
+  PyObject *m = PyModule_Create(&kModule);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", PA_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
