@@ -26,6 +26,8 @@ def attention64(c):
     share = torch.zeros(c["scores"].shape, dtype=torch.float64, device=DEV)
     biggest = 0.0
     for i, L in enumerate(c["lens"]):
+        if L == 0:
+            continue
         blocks = c["table"][i, :-(-L // c["bs"])].long()
         rows = [x[blocks].transpose(0, 1).reshape(h, -1, d)[:, :L] for x in (k, v)]
         sees = torch.arange(L, device=DEV) <= (L - u + torch.arange(u, device=DEV))[:, None]
