@@ -70,6 +70,18 @@ struct Call {
   void *stream() const { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 };
 
+// The C call itself, without the interpreter's lock: a launch waits where the driver's queue
+// is full, and other threads (or a host function in that queue) may need the interpreter to
+// go on.  (0.03 to 0.13 us a call.)
+template <typename F>
+pa_status unlocked(F call) {
+  struct Lock {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return call();
+}
+
 bool element(const Tensor &t, pa_dtype *dt) {
   if (t.scalar_type() == at::kHalf)
     *dt = PA_FP16;
@@ -153,11 +165,15 @@ pa_status rope_append(Call &c) {
   void *sm = c.dense(7, at::kLong, {n}), *tp = c.dense(8, at::kLong, {half}), *ap = c.dense(9, at::kInt, {half});
   c.ok = c.ok && fits({n, hq, kv.heads, kv.blocks, axes, 2 * half});
   if (!c.ok) return PA_OK;
-  return pa_rope_append(qo, qp, kp, vp, kv.k, kv.v, static_cast<const int32_t *>(pp),
-                        static_cast<const int64_t *>(sm), static_cast<const int64_t *>(tp),
-                        static_cast<const int32_t *>(ap), (int)n, (int)hq, (int)kv.heads, (int)kv.dim,
-                        (int)(2 * half), (int)axes, c.args[10] == Py_True, so, sq, sk, sv, (int)kv.block,
-                        (int)kv.blocks, dt, kv.ks, kv.vs, c.stream());
+  const int adjacent = c.args[10] == Py_True;
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_rope_append(qo, qp, kp, vp, kv.k, kv.v, static_cast<const int32_t *>(pp),
+                          static_cast<const int64_t *>(sm), static_cast<const int64_t *>(tp),
+                          static_cast<const int32_t *>(ap), (int)n, (int)hq, (int)kv.heads, (int)kv.dim,
+                          (int)(2 * half), (int)axes, adjacent, so, sq, sk, sv, (int)kv.block, (int)kv.blocks, dt,
+                          kv.ks, kv.vs, s);
+  });
 }
 
 // out, scores, q, k_cache, v_cache, block_tables, context_lens, scale, q_len, num_splits,
@@ -188,11 +204,16 @@ pa_status decode_scored(Call &c) {
   void *rp = c.maybe(11, at::kInt, {n, kv.heads, rows}), *sl = c.maybe(12, at::kInt, {n});
   c.ok = c.ok && fits({n, hq, kv.heads, kv.blocks, rows});
   if (!c.ok) return PA_OK;
-  return pa_decode_scored(op, static_cast<float *>(sc), static_cast<int32_t *>(rp), qp, kv.k, kv.v, kv.ks,
-                          kv.vs, static_cast<const int32_t *>(tables), static_cast<const int32_t *>(lens),
-                          static_cast<const int32_t *>(sl), (int)n, (int)hq, (int)kv.heads, (int)kv.dim,
-                          (int)kv.block, (float)PyFloat_AS_DOUBLE(c.args[7]), (int)width, (int)kv.blocks,
-                          (int)u, dt, (int)splits, ws->data_ptr(), ws->nbytes(), c.stream());
+  const float scale = (float)PyFloat_AS_DOUBLE(c.args[7]);
+  void *room = ws->data_ptr(), *s = c.stream();
+  const size_t room_bytes = ws->nbytes();
+  return unlocked([&] {
+    return pa_decode_scored(op, static_cast<float *>(sc), static_cast<int32_t *>(rp), qp, kv.k, kv.v, kv.ks, kv.vs,
+                            static_cast<const int32_t *>(tables), static_cast<const int32_t *>(lens),
+                            static_cast<const int32_t *>(sl), (int)n, (int)hq, (int)kv.heads, (int)kv.dim,
+                            (int)kv.block, scale, (int)width, (int)kv.blocks, (int)u, dt, (int)splits, room,
+                            room_bytes, s);
+  });
 }
 
 // k_cache, v_cache, scores, row_pos, block_tables, context_lens, seq_lens, budget, sinks,
@@ -217,12 +238,16 @@ pa_status evict(Call &c) {
   void *seen = c.dense(6, at::kInt, {n}), *nl = c.dense(12, at::kInt, {n});
   c.ok = c.ok && fits({n, h, shape[0], rows});
   if (!c.ok) return PA_OK;
-  return pa_evict(kp, vp, static_cast<float *>(so), static_cast<int32_t *>(po), static_cast<int32_t *>(nl),
-                  static_cast<const float *>(sc), static_cast<const int32_t *>(rp),
-                  static_cast<const int32_t *>(tables), static_cast<const int32_t *>(lens),
-                  static_cast<const int32_t *>(seen), (int)n, (int)h, (int)shape[3], (int)shape[2], (int)width,
-                  (int)shape[0], (int)budget, (int)sinks, (int)recent, bytes, ws->data_ptr(), ws->nbytes(),
-                  c.stream());
+  const int blocks = (int)shape[0], block = (int)shape[2], dim = (int)shape[3];
+  void *room = ws->data_ptr(), *s = c.stream();
+  const size_t room_bytes = ws->nbytes();
+  return unlocked([&] {
+    return pa_evict(kp, vp, static_cast<float *>(so), static_cast<int32_t *>(po), static_cast<int32_t *>(nl),
+                    static_cast<const float *>(sc), static_cast<const int32_t *>(rp),
+                    static_cast<const int32_t *>(tables), static_cast<const int32_t *>(lens),
+                    static_cast<const int32_t *>(seen), (int)n, (int)h, dim, block, (int)width, blocks, (int)budget,
+                    (int)sinks, (int)recent, bytes, room, room_bytes, s);
+  });
 }
 
 // fp32 [n][r][vocab], rows dense and evenly spaced
@@ -249,10 +274,13 @@ pa_status verify_drafts(Call &c) {
   void *out = c.dense(7, at::kInt, {n, k + 1}), *acc = c.dense(8, at::kInt, {n});
   c.ok = c.ok && fits({n, k, vocab});
   if (!c.ok) return PA_OK;
-  return pa_verify_drafts(static_cast<int32_t *>(out), static_cast<int32_t *>(acc), static_cast<int32_t *>(nl),
-                          static_cast<const int32_t *>(cl), pp, qp, static_cast<const int32_t *>(xp),
-                          static_cast<const int32_t *>(dl), static_cast<const float *>(au),
-                          static_cast<const float *>(su), (int)n, (int)k, (int)vocab, ps, qs, c.stream());
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_verify_drafts(static_cast<int32_t *>(out), static_cast<int32_t *>(acc), static_cast<int32_t *>(nl),
+                            static_cast<const int32_t *>(cl), pp, qp, static_cast<const int32_t *>(xp),
+                            static_cast<const int32_t *>(dl), static_cast<const float *>(au),
+                            static_cast<const float *>(su), (int)n, (int)k, (int)vocab, ps, qs, s);
+  });
 }
 
 // (no exception leaves: a tensor that has no plain storage, say, is the binding's business)
