@@ -125,3 +125,70 @@ def test_large_vocabulary(pa, sure):  # noqa: F811
     got = verifies.both(pa, c, sure=sure)
     assert (got[0].max(1).values.cpu() % per_warp(160001) >= 2048).any() or sure
     assert pa.pa_device_error() == 0
+
+
+def test_longest_step(pa):  # noqa: F811
+    """The most query tokens a call takes, over contexts as long, longer and shorter."""
+    u, lens = 4096, [4096, 5001, 300, 4352]
+    c = scoreds.make(51, lens, u, 2, 1, 64, 16, "bf16", False)
+    out, scores, pos = scoreds.run(pa, c)
+    want, share, biggest = attention64(c)
+    _tol.check(ref.f64(out), want, "bf16")
+    rel = 2 * (64 + 2) * 2.0 ** -24 * biggest + (8 + 2 * u + 2) * 2.0 ** -24
+    old, now = ref.f64(c["scores"]), ref.f64(scores)
+    for i, L in enumerate(lens):
+        old[i, :, max(0, L - u):L] = 0.0
+        at = torch.arange(max(0, L - u), L, dtype=torch.int32)
+        assert torch.equal(pos[i, 0, max(0, L - u):L].cpu(), at + int(c["sl"][i]) - L)
+    err = np.abs(now - (old + share))
+    assert not (err > rel * share + 2.0 ** -23 * np.abs(old + share) + 1e-30).any(), float(err.max())
+    assert pa.pa_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_caches_past_four_gigabytes(pa, fp8):  # noqa: F811
+    """Blocks whose bytes and elements lie past 2^32 give what the same blocks give in a
+    small pool, bit for bit."""
+    n, hq, hkv, d, bs, u, drafts = 3, 16, 8, 128, 16, 40, 3
+    lens, width = [700, 333, 40], 50
+    blocks = (1 << 32) // (hkv * bs * d * (1 if fp8 else 2)) + n * width + 8
+    assert blocks * hkv * bs * d > 1 << 31
+    g = torch.Generator().manual_seed(52)
+    spread = torch.randperm(n * width, generator=g).view(n, width).to(torch.int32)
+    small = torch.randint(0, 255 if fp8 else 30000, (2, n * width, hkv, bs, d), generator=g)
+    if fp8:
+        small = torch.where(small % 128 == 127, 0, small).to(torch.uint8)   # (no NaN codes)
+        sc = dict(k_scale=torch.full((hkv,), 0.01, device=DEV), v_scale=torch.full((hkv,), 0.02, device=DEV))
+    else:
+        small, sc = (small / 15000.0 - 1.0).bfloat16(), {}
+    rnd = lambda *s: torch.randn(*s, generator=g).bfloat16()  # noqa: E731
+    steps = [[rnd(n * t, h, d).to(DEV) for h in (hq, hkv, hkv)] for t in (u, 1 + drafts, 1)]
+    turns, axis = pa.rope_table(d, device=DEV)
+    got = []
+    for first in (0, blocks - n * width):
+        pool = torch.empty(2, blocks if first else n * width, hkv, bs, d, dtype=small.dtype, device=DEV)
+        pool[:, first:first + n * width] = small.to(DEV)
+        k, v = pool[0], pool[1]
+        tables = (spread + first).to(DEV).contiguous()
+        scores = torch.ones(n, hkv, width * bs, device=DEV)
+        pos = torch.arange(width * bs, dtype=torch.int32, device=DEV).repeat(n, hkv, 1)
+        ctx = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        outs = []
+        for q, kn, vn in steps:
+            t = q.shape[0] // n
+            place = (ctx[:, None] - t + torch.arange(t, device=DEV)).reshape(1, -1).to(torch.int32)
+            slots = pa.pa_slot_mapping(tables, ctx, bs, t)
+            qr = torch.empty_like(q)
+            pa.pa_rope_append(qr, q, kn, vn, k, v, place, slots, turns, axis, **sc)
+            out = torch.empty(n, t, hq, d, dtype=q.dtype, device=DEV)
+            pa.pa_decode_scored(out, scores, qr.view(n, t, hq, d), k, v, tables, ctx, d ** -0.5, q_len=t,
+                                row_pos=pos, seq_lens=ctx, **sc)
+            outs.append(out)
+        new = pa.pa_evict(k, v, scores, pos, tables, ctx, ctx, 200, 2, 30)
+        torch.cuda.synchronize()
+        assert pa.pa_device_error() == 0
+        got.append([*outs, scores, pos, new, k[first:first + n * width].clone(), v[first:first + n * width].clone()])
+        del pool, k, v
+    for x, y in zip(*got):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert all(torch.isfinite(x.float()).all() for x in got[0][:4]) and got[0][5].tolist() == [200, 200, 40]
