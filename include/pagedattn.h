@@ -455,9 +455,11 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, float *scores_out, int32
  *   weights w(v) = max(p_a(v) - q_a(v), 0) if a < m, else p_m(v); if they sum to zero
  *   (the two rows agree), w = p_a;
  *   token = the first v with w(0) + .. + w(v) > sample_u[i] * sum w.
- * out_tokens[i] = the a standing drafts, the token, then -1.  Products and sums are
- * exact to fp64, so the choice is the formula's.  Weights that are negative, NaN or
- * infinite count as zero.
+ * out_tokens[i] = the a standing drafts, the token, then -1.  Which drafts stand is exact:
+ * u q < p is compared with the exact product.  The sums w are good to about 2^-46 of the
+ * row's total (pairs of fp32; the total within fp32's range and not below 2^-100, as a row
+ * of probabilities is): a sample_u that falls so near a border may take either of the
+ * tokens beside it.  Weights that are negative, NaN or infinite count as zero.
  * draft_probs NULL: drafts that were certain (q_j(x_j) = 1, 0 elsewhere).
  * new_lens (may be NULL, or context_lens itself): context_lens[i] - (max_draft - a), the
  * cache length after a

@@ -14,8 +14,10 @@
 //   * up to kFew (a serving step appends one row, or a few with drafts): that many
 //     times the smallest (key, then higher row) that is larger than the last one found;
 //   * more: the budget-th largest key by a radix select, eight bits at a time, then the
-//     rows in order.  (One row over 1024: 17.5 us by the radix select, 6.9 by the first.)
-// Keys are held in shared memory.
+//     rows in order.
+// 64 sequences x 8 heads, 1, 4, 6 and 8 rows over 1024: 5.3, 9.8, 12.8 and 15.9 us by the
+// first, 12.7, 13.2, 13.7 and 14.1 by the second; 2 x 8 heads, 1, 4 and 8 over 32768:
+// 7.0, 13.7 and 22.8 against 30.1 to 30.4.  Keys are held in shared memory.
 //
 // Moves.  Attention does not depend on the order of cached rows (K rows carry their
 // rotation), so nothing is shifted: with m rows evicted below `budget`, exactly m kept
@@ -452,7 +454,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictArgs a)
   // (distributed shared memory was last read before the barrier above)
 }
 
-// Tables of at most so many rows: CTAs of 256 threads; longer ones: 512.
+// Tables of at most so many rows: CTAs of 256 threads, one per head; longer ones: 512, and
+// clusters of them.  Half the rows kept of 1024, 4096 and 8192, 64 x 8 heads: 42, 129 and
+// 257 us the first way, 46, 137 and 252 the second; 16 x 8 heads: 17.5, 62 and 134 against
+// 19.4, 48 and 78; one row over 1023, 4095 and 8191, 64 x 8 heads: 5.0, 7.3 and 10.6
+// against 8.5, 10.2 and 13.5.  (The table's width stands for the contexts, whose lengths
+// the host does not know: 1025 rows of 64 x 8 heads in tables of 1040 or 4096 rows 5.3 us,
+// 8192 8.1, 32768 12.7.)
 constexpr int kSmallRows = 4096;
 
 template <int NT>

@@ -15,8 +15,10 @@
 // The answer is a token id, so sums decide at borders: with a vocabulary of 10^5
 // tokens an fp32 sum of the weights (error ~1e-7 of the total) lands on the wrong side
 // of one of the borders in about one call in a hundred.  All sums here are pairs of
-// fp32 (the rounded sum and the rounding errors it dropped, by Knuth's two-sum), good to
-// about 2^-46 of the total; the fp64 rate of GB300 is two operations a clock and SM
+// fp32 (the rounded sum and the rounding errors it dropped, by Knuth's two-sum, themselves
+// added in fp32), good to about 2^-46 of the total (2^-47.2 the worst of 40 rows of 32000 and
+// 131071 entries, the same additions redone on the CPU); a uniform that falls so near a border may take either
+// token.  The fp64 rate of GB300 is two operations a clock and SM
 // (scans in fp64 made the search 17 us of 35 in a batch of 64).  u q < p is compared in
 // fp64, where the product of two fp32 is exact.
 //
