@@ -24,7 +24,7 @@ import torch
 own = False
 
 DTYPES = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
-LEAST, MOST = 2.0 ** -64, 2.0 ** 64  # block scales lie between
+LEAST, MOST = 2.0 ** -40, 2.0 ** 40  # block scales lie between
 
 
 # ------------------------------------------------------------------------------ cases
@@ -204,8 +204,8 @@ def _gen(seed):
 def _need(top):
     """The smallest power of two s with top <= 448 s (448 = 0.875 * 2^9), as bits."""
     m, e = torch.frexp(top)
-    e = torch.where(m <= 0.875, e - 9, e - 8).clamp(-64, 64)
-    e = torch.where(top > 0, e, -64)
+    e = torch.where(m <= 0.875, e - 9, e - 8).clamp(-40, 40)
+    e = torch.where(top > 0, e, -40)
     return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
 
 
@@ -602,7 +602,7 @@ def _exact_append(s):
             full = torch.zeros((hi - lo) * bs, x.shape[1], dtype=torch.float64, device="cuda")
             full[first - lo * bs:first - lo * bs + x.shape[0]] = x
             top = full.view(hi - lo, bs, -1).amax(1)
-            need = torch.exp2(torch.ceil(torch.log2(top.clamp_min(1e-300) / 448)).clamp(-64, 64))
+            need = torch.exp2(torch.ceil(torch.log2(top.clamp_min(1e-300) / 448)).clamp(-40, 40))
             if first > lo * bs:
                 need[0] = torch.maximum(need[0], scales[blk[0], :, which])
             scales[blk, :, which] = need
