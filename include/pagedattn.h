@@ -88,7 +88,8 @@ typedef enum {
     PA_ERR_DEVICE_TIMEOUT = -5
 } pa_status;
 
-typedef enum { PA_FP16 = 0, PA_BF16 = 1 } pa_dtype;
+/* PA_FP32: the logits of pa_adjust_logits alone */
+typedef enum { PA_FP16 = 0, PA_BF16 = 1, PA_FP32 = 2 } pa_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 PA_API const char *pa_status_string(pa_status status);
@@ -482,6 +483,166 @@ PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *num_accepted, in
                                   const int32_t *draft_lens, const float *accept_u,
                                   const float *sample_u, int num_seqs, int max_draft, int vocab,
                                   int64_t target_stride, int64_t draft_stride, void *stream);
+
+/*
+ * Block-scaled FP8 cache ([QA] Q4).  A pool of e4m3 codes as for pa_append_kv_fp8, with one
+ * scale for K and one for V of every block and KV head:
+ *   kv_scales  fp32 [num_blocks][num_kv_heads][2]  (K, V), 16-byte aligned
+ * An element stands for code * scale.  The scales come from the data: no calibration, and a
+ * token of large values costs the rows of its own block their small ones, not a head's.
+ * Scales count as clamped to [2^-40, 2^40] (NaN as 2^-40).  head_dim 128 only.  pa_evict moves
+ * rows between blocks and is not for such a pool; pa_copy_pages copies its blocks.
+ *
+ * pa_append_kv_block_scaled -- the last q_len positions of every sequence, rows of k_new and
+ * v_new [num_seqs * q_len][num_kv_heads][head_dim] (16-bit of type new_dtype; tokens k_stride /
+ * v_stride elements apart, multiples of 8, at least a token's width), into their blocks.
+ * For a block that the step writes, one KV head, and K or V:
+ *   need = the least power of two with max |x| <= 448 need over the step's finite x in it,
+ *          clamped as above
+ *   s    = need where the block's first row is one of the step's, else max(scale, need)
+ *   code = e4m3(x / s) (nearest even; magnitudes above 448, infinities among them, to 448) for the
+ *          step's rows; rows before them, if s grew: code = e4m3(code * scale / s)
+ * and s becomes the scale.  Rows past the step's are left as they were: they stand for nothing.  A
+ * power of two moves only exponents: an older row is rounded again only where it becomes
+ * subnormal.  After a rejection the next step overwrites the rejected rows; the scale keeps
+ * what they needed.  Positions < 0 are skipped; positions beyond the table or the pool are
+ * skipped and set PA_ERR_DEVICE_CHECK.  A block that is written must belong to one sequence
+ * (pa_fork_blocks sees to it).  num_seqs == 0 is a no-op.
+ */
+PA_API pa_status pa_append_kv_block_scaled(void *k_cache, void *v_cache, float *kv_scales,
+                                           const void *k_new, const void *v_new,
+                                           const int32_t *block_tables, const int32_t *context_lens,
+                                           int num_seqs, int num_kv_heads, int head_dim,
+                                           int block_size, int max_blocks_per_seq, int num_blocks,
+                                           int q_len, pa_dtype new_dtype, int64_t k_stride,
+                                           int64_t v_stride, void *stream);
+
+/*
+ * pa_decode_block_scaled -- pa_decode (q_len 1..4096, GQA, causal limit, rows that see
+ * nothing) over a block-scaled cache; q and out of type dtype, fp32 arithmetic on
+ * code * scale.  num_splits == 1: one pass, workspace may be NULL; num_splits > 1: split-KV,
+ * workspace of pa_decode_workspace_size bytes, 256-byte aligned, and the combine.  (Its
+ * sections hold what pa_decode_partial writes, with m the running maximum of s_t plus the
+ * base-2 logarithm of V's scale.)  Two calls that can overlap need workspaces of their own.
+ * Weights are rounded to 16 bits, times their V scale relative to the largest such product.
+ */
+PA_API pa_status pa_decode_block_scaled(void *out, const void *q, const void *k_cache,
+                                        const void *v_cache, const float *kv_scales,
+                                        const int32_t *block_tables, const int32_t *context_lens,
+                                        int num_seqs, int num_q_heads, int num_kv_heads,
+                                        int head_dim, int block_size, float scale,
+                                        int max_blocks_per_seq, int num_blocks, int q_len,
+                                        pa_dtype dtype, int num_splits, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * The pool's blocks by reference counts, on the device ([QA] Q2: sequences share blocks until
+ * one of them writes).
+ *   ref_counts    int32 [num_blocks]: table entries that hold the block; 0: the block is free
+ *   block_tables  an entry < 0 holds no block
+ * The calls keep the counts in step with the tables; at the start every entry is -1 and every
+ * count 0, or the counts are the entries' number.  Each call has one result, whatever the order
+ * of its threads.  An entry outside the pool, or one whose block was not counted, sets
+ * PA_ERR_DEVICE_CHECK and counts as none.  None of them touches a cache: with several
+ * layers over one table they run once, and pa_copy_pages once a layer.  Arrays are 4-byte
+ * aligned, block_tables (pa_fork_blocks apart), ref_counts and the workspace 16-byte aligned;
+ * outputs overlap nothing else but where said.
+ * Workspace: pa_pages_workspace_size(num_blocks, num_forks) bytes (num_forks 0 for the others);
+ * two calls that can overlap need workspaces of their own.
+ *
+ * pa_free_blocks -- entries of sequence i at or past ceil(keep_lens[i] / block_size) give
+ * their block up (its count falls by one) and become -1.  keep_lens 0: all of them; the
+ * new lengths of pa_verify_drafts or pa_evict: what these no longer use.
+ *
+ * pa_reserve_blocks -- entries of sequence i before ceil(lens[i] / block_size) that are < 0
+ * take the free blocks in ascending order, in the order of sequences and entries; their counts
+ * become 1.  missing[0] = how many found none; they stay < 0.  lens past the table's width:
+ * the width (PA_ERR_DEVICE_CHECK).
+ *
+ * pa_fork_blocks -- for fork f, sequence dst_seqs[f] becomes a copy of src_seqs[f]: the full
+ * blocks are shared (their counts rise by one), a partial last block is to be copied into a
+ * free one (ascending, in the order of forks), and context_lens[dst] = context_lens[src].  The
+ * copies to make are listed, src_blocks[p] -> dst_blocks[p] for p < counts[0]; entries from
+ * there on are left as they were.  counts[1] = forks that found no free block: these get
+ * their parent's full blocks and that length.  What dst's row held before is overwritten,
+ * not freed.  Every dst_seqs[f] is another sequence, and none of src_seqs (else the result is
+ * undefined); ids outside the batch, or src == dst, set PA_ERR_DEVICE_CHECK and are skipped.
+ *   src_seqs, dst_seqs, src_blocks, dst_blocks  int32 [num_forks <= num_seqs] (num_forks 0:
+ *   counts alone are written); counts int32 [2]
+ *
+ * pa_compact_blocks -- the pool's blocks to its front: with live = blocks of a count other than
+ * 0, the k-th of them at or past `live` gets the id of the k-th free one before it, in
+ * tables and counts; counts[0] = how many, listed as above, counts[1] = live.  After the
+ * copies the blocks from `live` on are free.  tables and counts are updated in place, or
+ * (the _out arrays being others) the inputs are left as they were.
+ *   src_blocks, dst_blocks  int32 [num_blocks / 2]
+ *
+ * pa_copy_pages -- whole blocks src_blocks[p] -> dst_blocks[p], p < min(counts[0], max_pairs),
+ * K, V and (kv_scales non-NULL) their scales, bit for bit; element_bytes 2 (16-bit pools) or 1
+ * (head_dim 128).  Ids outside the pool are skipped and set PA_ERR_DEVICE_CHECK.  A destination
+ * that is also a source or another pair's destination: undefined result.
+ */
+PA_API size_t pa_pages_workspace_size(int num_blocks, int num_forks);
+PA_API pa_status pa_free_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *keep_lens,
+                                int num_seqs, int max_blocks_per_seq, int num_blocks, int block_size,
+                                void *stream);
+PA_API pa_status pa_reserve_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *lens,
+                                   int32_t *missing, int num_seqs, int max_blocks_per_seq,
+                                   int num_blocks, int block_size, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+PA_API pa_status pa_fork_blocks(int32_t *block_tables, int32_t *context_lens, int32_t *ref_counts,
+                                const int32_t *src_seqs, const int32_t *dst_seqs, int32_t *src_blocks,
+                                int32_t *dst_blocks, int32_t *counts, int num_forks, int num_seqs,
+                                int max_blocks_per_seq, int num_blocks, int block_size,
+                                void *workspace, size_t workspace_bytes, void *stream);
+PA_API pa_status pa_compact_blocks(int32_t *block_tables_out, int32_t *ref_counts_out,
+                                   const int32_t *block_tables, const int32_t *ref_counts,
+                                   int32_t *src_blocks, int32_t *dst_blocks, int32_t *counts,
+                                   int num_seqs, int max_blocks_per_seq, int num_blocks,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales,
+                               const int32_t *src_blocks, const int32_t *dst_blocks,
+                               const int32_t *counts, int max_pairs, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, int element_bytes, void *stream);
+
+/*
+ * pa_adjust_logits -- penalties, biases and grammar masks on a step's logits, and the
+ * probabilities that pa_verify_drafts takes.  Row j of sequence i is the one behind its
+ * drafts 0 .. j-1.  Its outputs are history[i][prompt_lens[i] .. history_lens[i]) and
+ * those drafts; count = how often entry v stands there, seen = it stands there or in the
+ * prompt, history[i][0 .. prompt_lens[i]).  Of its logit x:
+ *   y = x > 0 ? x / repetition[i] : x * repetition[i]   if seen, else x
+ *   y = (y - count * frequency[i]) - presence[i]        if count > 0
+ *   y = y + bias_values[i][b]  for every b with bias_ids[i][b] == v, in their order
+ *   y = -inf                   if bit v % 32 of the mask's word v / 32 is 0
+ * each operation rounded to fp32.  probs == 0: out = y, of the logits' type.  probs != 0:
+ * out fp32, softmax(y / temperature[i]); temperature <= 0 (or NaN): 1 at the largest y (the
+ * lowest entry of equals), 0 elsewhere.  There a NaN counts as -inf and +inf as the largest
+ * finite number; a row that its mask leaves empty is all zeros (pa_verify_drafts answers
+ * -1 to it).
+ *   logits       [num_seqs][rows][logits_stride], vocab used; fp16, bf16 or fp32 (dtype)
+ *   out          [num_seqs][rows][out_stride]; may be logits itself where type and stride
+ *                are the same, and overlaps nothing else
+ *   history      int32 [num_seqs][max_history], history_lens, prompt_lens int32 [num_seqs]
+ *                (prompt_lens NULL: no prompt)
+ *   drafts       int32 [num_seqs][rows - 1]
+ *   repetition, presence, frequency, temperature  fp32 [num_seqs] (NULL: 1, 0, 0, 1)
+ *   bias_ids, bias_values  int32, fp32 [num_seqs][num_bias], num_bias <= 1024
+ *   mask         32-bit words; sequences mask_seq_stride and rows mask_row_stride words
+ *                apart (0: shared)
+ * All but out and logits may be NULL.  Negative ids (padding) are ignored, ids >= vocab too,
+ * which set PA_ERR_DEVICE_CHECK, as a history_lens outside [0, max_history] (clamped) does.
+ * vocab <= 2^18.  num_seqs == 0 is a no-op.
+ */
+PA_API pa_status pa_adjust_logits(void *out, const void *logits, const int32_t *history,
+                                  const int32_t *history_lens, const int32_t *prompt_lens,
+                                  const int32_t *drafts, const float *repetition,
+                                  const float *presence, const float *frequency,
+                                  const int32_t *bias_ids, const float *bias_values,
+                                  const int32_t *mask, const float *temperature, int num_seqs,
+                                  int rows, int vocab, int max_history, int num_bias, pa_dtype dtype,
+                                  int probs, int64_t out_stride, int64_t logits_stride,
+                                  int64_t mask_seq_stride, int64_t mask_row_stride, void *stream);
 
 #ifdef __cplusplus
 }

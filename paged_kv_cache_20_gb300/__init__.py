@@ -14,6 +14,8 @@ Layouts match ``include/pagedattn.h``:
   context_lens      int32 [num_seqs]       (count this step's new tokens)
   slot_mapping      int64 [n_tokens]
   scores, row_pos   fp32, int32 [num_seqs, num_kv_heads, max_blocks_per_seq * block_size]
+  kv_scales         fp32 [num_blocks, num_kv_heads, 2]  (K, V; a block-scaled FP8 cache)
+  ref_counts        int32 [num_blocks]
 
 Streams: a call runs on the current stream, or on the one named by ``stream`` (a
 ``torch.cuda.Stream`` or a raw handle; ordering it after the work that makes the
@@ -44,7 +46,9 @@ PA_ERR_DEVICE_CHECK = -4
 PA_ERR_DEVICE_TIMEOUT = -5
 
 PA_FP16, PA_BF16 = 0, 1
+PA_FP32 = 2   # the logits of pa_adjust_logits alone
 _DTYPE = {torch.float16: PA_FP16, torch.bfloat16: PA_BF16}
+_LOGIT_DTYPE = {**_DTYPE, torch.float32: PA_FP32}
 
 _c_int, _c_float, _c_size, _c_vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
 _c_i64 = ctypes.c_int64
@@ -90,6 +94,16 @@ _SIGNATURES = {
     "pa_evict_workspace_size": (_c_size, [_c_int] * 3),
     "pa_evict": (_c_int, [_c_vp] * 10 + [_c_int] * 10 + [_c_vp, _c_size, _c_vp]),
     "pa_verify_drafts": (_c_int, [_c_vp] * 10 + [_c_int] * 3 + [_c_i64, _c_i64, _c_vp]),
+    "pa_append_kv_block_scaled": (_c_int, [_c_vp] * 7 + [_c_int] * 8 + [_c_i64, _c_i64, _c_vp]),
+    "pa_decode_block_scaled": (_c_int, [_c_vp] * 7 + [_c_int] * 5 + [_c_float] + [_c_int] * 5 +
+                               [_c_vp, _c_size, _c_vp]),
+    "pa_pages_workspace_size": (_c_size, [_c_int] * 2),
+    "pa_free_blocks": (_c_int, [_c_vp] * 3 + [_c_int] * 4 + [_c_vp]),
+    "pa_reserve_blocks": (_c_int, [_c_vp] * 4 + [_c_int] * 4 + [_c_vp, _c_size, _c_vp]),
+    "pa_fork_blocks": (_c_int, [_c_vp] * 8 + [_c_int] * 5 + [_c_vp, _c_size, _c_vp]),
+    "pa_compact_blocks": (_c_int, [_c_vp] * 7 + [_c_int] * 3 + [_c_vp, _c_size, _c_vp]),
+    "pa_copy_pages": (_c_int, [_c_vp] * 6 + [_c_int] * 6 + [_c_vp]),
+    "pa_adjust_logits": (_c_int, [_c_vp] * 13 + [_c_int] * 7 + [_c_i64] * 4 + [_c_vp]),
 }
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # PA_NOALLOC_SCRATCH_BYTES
@@ -896,3 +910,380 @@ def pa_verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | Non
     if st != PA_OK:
         raise PagedAttnError("pa_verify_drafts", st)
     return out_tokens, num_accepted, new_lens
+
+
+# ------------------------------------------------------ block-scaled FP8 cache
+def _scaled_caches(k_cache, v_cache, kv_scales, dev: int):
+    """Pointers of a block-scaled pool's codes and scales, and its shape."""
+    cache = _cache_shape(k_cache)
+    dt = k_cache.dtype
+    if dt not in _FP8_CACHE:
+        raise TypeError(f"k_cache must hold e4m3 codes (uint8 or float8_e4m3fn), got {dt}")
+    _shape(v_cache, "v_cache", cache)
+    _shape(kv_scales, "kv_scales", (cache[0], cache[1], 2))
+    return (_ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+            _ptr(kv_scales, "kv_scales", torch.float32, dev), cache)
+
+
+def _tables(block_tables, dev: int) -> tuple:
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    return (_ptr(block_tables, "block_tables", torch.int32, dev), *block_tables.shape)
+
+
+def pa_append_kv_block_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
+                              k_new: torch.Tensor, v_new: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, q_len: int = 1, stream=None) -> None:
+    """Quantise the last q_len positions of every sequence into a block-scaled FP8 cache,
+    each block's scale grown where its rows need it.
+
+    k_new, v_new [num_seqs * q_len, num_kv_heads, head_dim], 16-bit; tokens may be strided.
+    """
+    if stream is None and _fast is not None:
+        st = _fast.append_kv_block_scaled(k_cache, v_cache, kv_scales, k_new, v_new, block_tables,
+                                          context_lens, q_len)
+        if st == PA_OK:
+            return
+        if st is not None:
+            raise PagedAttnError("pa_append_kv_block_scaled", st)
+    dev = _device_of(k_new)
+    kc, vc, sp, (num_blocks, h_kv, block_size, head_dim) = _scaled_caches(k_cache, v_cache, kv_scales, dev)
+    bt, num_seqs, maxb = _tables(block_tables, dev)
+    _shape(context_lens, "context_lens", (num_seqs,))
+    dt = _elt(k_new, "k_new")
+    shape = (num_seqs * q_len, h_kv, head_dim)
+    k_ptr, k_st = _tokens3(k_new, "k_new", k_new.dtype, dev, shape)
+    v_ptr, v_st = _tokens3(v_new, "v_new", k_new.dtype, dev, shape)
+    cl = _ptr(context_lens, "context_lens", torch.int32, dev)
+    if num_seqs == 0:
+        return
+    st = (_lib or load()).pa_append_kv_block_scaled(
+        kc, vc, sp, k_ptr, v_ptr, bt, cl, num_seqs, h_kv, head_dim, block_size, maxb, num_blocks, q_len,
+        dt, k_st, v_st, _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_append_kv_block_scaled", st)
+
+
+def pa_decode_block_scaled(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           kv_scales: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           scale: float, q_len: int = 1, num_splits: int = 1,
+                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Paged attention over a block-scaled FP8 cache; writes and returns ``out`` (shape of
+    q).  num_splits > 1 uses the split-KV pair."""
+    if stream is None and _fast is not None:
+        st = _fast.decode_block_scaled(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, scale,
+                                       q_len, num_splits, workspace)
+        if st == PA_OK:
+            return out
+        if st is not None:
+            raise PagedAttnError("pa_decode_block_scaled", st)
+    dev = _device_of(q)
+    kc, vc, sp, (num_blocks, h_kv, block_size, head_dim) = _scaled_caches(k_cache, v_cache, kv_scales, dev)
+    bt, num_seqs, maxb = _tables(block_tables, dev)
+    dt, elt, q_shape = _elt(q, "q"), q.dtype, q.shape
+    if len(q_shape) < 3:
+        raise ValueError("q must be [num_seqs, q_len, num_q_heads, head_dim]")
+    h_q = q_shape[-2]
+    if q_shape != (num_seqs, q_len, h_q, head_dim) and (q_len != 1 or q_shape != (num_seqs, h_q, head_dim)):
+        raise ValueError("q must be [num_seqs, q_len, num_q_heads, head_dim]")
+    _shape(out, "out", q_shape)
+    _shape(context_lens, "context_lens", (num_seqs,))
+    ws, ws_bytes = None, 0
+    if num_splits > 1:
+        if workspace is None:
+            nbytes = pa_decode_workspace_size(num_seqs, h_q, q_len, head_dim, num_splits)
+            workspace = _made((nbytes,), torch.uint8, q.device, stream)
+        ws, ws_bytes = _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes
+    st = (_lib or load()).pa_decode_block_scaled(
+        _ptr(out, "out", elt, dev), _ptr(q, "q", elt, dev), kc, vc, sp, bt,
+        _ptr(context_lens, "context_lens", torch.int32, dev), num_seqs, h_q, h_kv, head_dim, block_size,
+        scale, maxb, num_blocks, q_len, dt, num_splits, ws, ws_bytes, _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_decode_block_scaled", st)
+    return out
+
+
+# ------------------------------------------------------------ the pool's blocks
+def pa_pages_workspace_size(num_blocks: int, num_forks: int = 0) -> int:
+    """Bytes of the bookkeeping calls' workspace (0 for invalid sizes)."""
+    return int(load().pa_pages_workspace_size(num_blocks, num_forks))
+
+
+def _pool(block_tables, ref_counts) -> tuple:
+    """(device, table pointer, num_seqs, width, counts pointer, num_blocks)"""
+    dev = _device_of(block_tables)
+    if ref_counts.dim() != 1:
+        raise ValueError("ref_counts must be [num_blocks]")
+    return (dev, *_tables(block_tables, dev), _ptr(ref_counts, "ref_counts", torch.int32, dev),
+            ref_counts.shape[0])
+
+
+def _i32(t, name: str, shape: tuple, dev: int) -> int:
+    _shape(t, name, shape)
+    return _ptr(t, name, torch.int32, dev)
+
+
+def _pages_room(workspace, num_blocks: int, num_forks: int, device, stream, dev: int) -> tuple:
+    if workspace is None:
+        workspace = _made((pa_pages_workspace_size(num_blocks, num_forks),), torch.uint8, device, stream)
+    return workspace, _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes
+
+
+def pa_free_blocks(block_tables: torch.Tensor, ref_counts: torch.Tensor, keep_lens: torch.Tensor,
+                   block_size: int, stream=None) -> None:
+    """Give up every sequence's blocks past its first keep_lens[i] tokens: their counts
+    fall by one, their entries become -1."""
+    if stream is None and _fast is not None:
+        st = _fast.free_blocks(block_tables, ref_counts, keep_lens, block_size)
+        if st == PA_OK:
+            return
+        if st is not None:
+            raise PagedAttnError("pa_free_blocks", st)
+    dev, bt, n, width, rc, num_blocks = _pool(block_tables, ref_counts)
+    kl = _i32(keep_lens, "keep_lens", (n,), dev)
+    st = (_lib or load()).pa_free_blocks(bt, rc, kl, n, width, num_blocks, block_size, _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_free_blocks", st)
+
+
+def pa_reserve_blocks(block_tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch.Tensor, block_size: int,
+                      missing: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Blocks for every sequence's first lens[i] tokens where it has none: the lowest free
+    ones, in the order of sequences.  Returns ``missing`` (int32 [1]): entries that found
+    no free block."""
+    if stream is None and _fast is not None:
+        st = _fast.reserve_blocks(block_tables, ref_counts, lens, block_size, missing, workspace)
+        if st == PA_OK:
+            return missing
+        if st is not None:
+            raise PagedAttnError("pa_reserve_blocks", st)
+    dev, bt, n, width, rc, num_blocks = _pool(block_tables, ref_counts)
+    ln = _i32(lens, "lens", (n,), dev)
+    if missing is None:
+        missing = _made((1,), torch.int32, lens.device, stream)
+    mp = _i32(missing, "missing", (1,), dev)
+    workspace, ws, ws_bytes = _pages_room(workspace, num_blocks, 0, lens.device, stream, dev)
+    st = (_lib or load()).pa_reserve_blocks(bt, rc, ln, mp, n, width, num_blocks, block_size, ws, ws_bytes,
+                                            _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_reserve_blocks", st)
+    return missing
+
+
+def pa_fork_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_counts: torch.Tensor,
+                   src_seqs: torch.Tensor, dst_seqs: torch.Tensor, block_size: int,
+                   src_blocks: torch.Tensor | None = None, dst_blocks: torch.Tensor | None = None,
+                   counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Sequences dst_seqs[f] become copies of src_seqs[f]: full blocks shared, partial last
+    blocks to be copied.  Returns (src_blocks, dst_blocks, counts): the copies to make with
+    pa_copy_pages, counts[0] of them; counts[1] forks found no free block."""
+    if stream is None and _fast is not None:
+        st = _fast.fork_blocks(block_tables, context_lens, ref_counts, src_seqs, dst_seqs, block_size, src_blocks,
+                               dst_blocks, counts, workspace)
+        if st == PA_OK:
+            return src_blocks, dst_blocks, counts
+        if st is not None:
+            raise PagedAttnError("pa_fork_blocks", st)
+    dev, bt, n, width, rc, num_blocks = _pool(block_tables, ref_counts)
+    cl = _i32(context_lens, "context_lens", (n,), dev)
+    if src_seqs.dim() != 1:
+        raise ValueError("src_seqs must be [num_forks]")
+    f = src_seqs.shape[0]
+    ss, ds = _i32(src_seqs, "src_seqs", (f,), dev), _i32(dst_seqs, "dst_seqs", (f,), dev)
+    device = block_tables.device
+    if src_blocks is None:
+        src_blocks = _made((f,), torch.int32, device, stream)
+    if dst_blocks is None:
+        dst_blocks = _made((f,), torch.int32, device, stream)
+    if counts is None:
+        counts = _made((2,), torch.int32, device, stream)
+    sb, db = _i32(src_blocks, "src_blocks", (f,), dev), _i32(dst_blocks, "dst_blocks", (f,), dev)
+    cp = _i32(counts, "counts", (2,), dev)
+    workspace, ws, ws_bytes = _pages_room(workspace, num_blocks, f, device, stream, dev)
+    st = (_lib or load()).pa_fork_blocks(bt, cl, rc, ss, ds, sb, db, cp, f, n, width, num_blocks, block_size, ws,
+                                         ws_bytes, _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_fork_blocks", st)
+    return src_blocks, dst_blocks, counts
+
+
+def pa_compact_blocks(block_tables: torch.Tensor, ref_counts: torch.Tensor,
+                      block_tables_out: torch.Tensor | None = None, ref_counts_out: torch.Tensor | None = None,
+                      src_blocks: torch.Tensor | None = None, dst_blocks: torch.Tensor | None = None,
+                      counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Give the blocks in use the pool's lowest ids, in tables and counts (in place unless
+    both outputs are given).  Returns (src_blocks, dst_blocks, counts): the copies to make
+    with pa_copy_pages, counts[0] of them; counts[1] blocks are in use."""
+    if stream is None and _fast is not None:
+        st = _fast.compact_blocks(block_tables, ref_counts, block_tables_out, ref_counts_out, src_blocks,
+                                  dst_blocks, counts, workspace)
+        if st == PA_OK:
+            return src_blocks, dst_blocks, counts
+        if st is not None:
+            raise PagedAttnError("pa_compact_blocks", st)
+    dev, bt, n, width, rc, num_blocks = _pool(block_tables, ref_counts)
+    if (block_tables_out is None) != (ref_counts_out is None):
+        raise ValueError("give both block_tables_out and ref_counts_out, or neither")
+    to, ro = bt, rc
+    if block_tables_out is not None:
+        to = _i32(block_tables_out, "block_tables_out", (n, width), dev)
+        ro = _i32(ref_counts_out, "ref_counts_out", (num_blocks,), dev)
+    device, most = block_tables.device, num_blocks // 2
+    if src_blocks is None:
+        src_blocks = _made((most,), torch.int32, device, stream)
+    if dst_blocks is None:
+        dst_blocks = _made((most,), torch.int32, device, stream)
+    if counts is None:
+        counts = _made((2,), torch.int32, device, stream)
+    sb, db = _i32(src_blocks, "src_blocks", (most,), dev), _i32(dst_blocks, "dst_blocks", (most,), dev)
+    cp = _i32(counts, "counts", (2,), dev)
+    workspace, ws, ws_bytes = _pages_room(workspace, num_blocks, 0, device, stream, dev)
+    st = (_lib or load()).pa_compact_blocks(to, ro, bt, rc, sb, db, cp, n, width, num_blocks, ws, ws_bytes,
+                                            _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_compact_blocks", st)
+    return src_blocks, dst_blocks, counts
+
+
+def pa_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
+                  counts: torch.Tensor, kv_scales: torch.Tensor | None = None, stream=None) -> None:
+    """Copy the first counts[0] listed blocks src_blocks[p] -> dst_blocks[p] of both caches
+    (16-bit or FP8), with their scales where kv_scales is given."""
+    if stream is None and _fast is not None:
+        st = _fast.copy_pages(k_cache, v_cache, src_blocks, dst_blocks, counts, kv_scales)
+        if st == PA_OK:
+            return
+        if st is not None:
+            raise PagedAttnError("pa_copy_pages", st)
+    dev = _device_of(k_cache)
+    cache = num_blocks, h_kv, block_size, head_dim = _cache_shape(k_cache)
+    elt = k_cache.dtype
+    if elt not in _DTYPE and elt not in _FP8_CACHE:
+        raise TypeError(f"k_cache must be 16-bit or hold e4m3 codes, got {elt}")
+    _shape(v_cache, "v_cache", cache)
+    sp = None
+    if kv_scales is not None:
+        _shape(kv_scales, "kv_scales", (num_blocks, h_kv, 2))
+        sp = _ptr(kv_scales, "kv_scales", torch.float32, dev)
+    if src_blocks.dim() != 1:
+        raise ValueError("src_blocks must be [max_pairs]")
+    most = src_blocks.shape[0]
+    sb, db = _i32(src_blocks, "src_blocks", (most,), dev), _i32(dst_blocks, "dst_blocks", (most,), dev)
+    _shape(counts, "counts", (2,))
+    kc, vc = _ptr(k_cache, "k_cache", elt, dev), _ptr(v_cache, "v_cache", elt, dev)
+    cp = _ptr(counts, "counts", torch.int32, dev)
+    if most == 0:
+        return
+    st = (_lib or load()).pa_copy_pages(kc, vc, sp, sb, db, cp, most, h_kv, head_dim, block_size, num_blocks,
+                                        2 if elt in _DTYPE else 1, _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_copy_pages", st)
+
+
+# ---------------------------------------------------------------------- logits
+def _logit_rows(t, name: str, dtype, dev: int) -> tuple[int, int]:
+    """Pointer and row stride of [n, r, vocab], rows dense and evenly spaced (a slice of a
+    padded vocabulary is fine)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{dev}")
+    n, r, vocab = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), vocab
+    s0, s1, s2 = t.stride()
+    row = s1 if r > 1 else s0 if n > 1 else vocab
+    if (vocab > 1 and s2 != 1) or (n > 1 and s0 != r * row):
+        raise ValueError(f"{name}: rows must be dense and evenly spaced")
+    return t.data_ptr(), row
+
+
+def pa_adjust_logits(out: torch.Tensor | None, logits: torch.Tensor, history: torch.Tensor | None = None,
+                     history_lens: torch.Tensor | None = None, prompt_lens: torch.Tensor | None = None,
+                     drafts: torch.Tensor | None = None, repetition: torch.Tensor | None = None,
+                     presence: torch.Tensor | None = None, frequency: torch.Tensor | None = None,
+                     bias_ids: torch.Tensor | None = None, bias_values: torch.Tensor | None = None,
+                     mask: torch.Tensor | None = None, temperature: torch.Tensor | None = None,
+                     probs: bool = False, stream=None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and a grammar's mask on logits [num_seqs, rows,
+    vocab] (fp16, bf16 or fp32), row j behind drafts[:, :j]; with ``probs`` the fp32
+    probabilities at ``temperature`` that pa_verify_drafts takes.
+
+    history int32 [num_seqs, max_history] with history_lens (and prompt_lens: where the
+    prompt ends); drafts int32 [num_seqs, rows - 1]; the penalties and the temperature fp32
+    [num_seqs]; bias_ids, bias_values [num_seqs, num_bias]; mask int32 [num_seqs, rows,
+    ceil(vocab / 32)], which may be expanded over rows or sequences.  ``out`` (logits itself
+    is fine) is made when None.
+    """
+    if stream is None and _fast is not None and out is not None:
+        st = _fast.adjust_logits(out, logits, history, history_lens, prompt_lens, drafts, repetition, presence,
+                                 frequency, bias_ids, bias_values, mask, temperature, probs)
+        if st == PA_OK:
+            return out
+        if st is not None:
+            raise PagedAttnError("pa_adjust_logits", st)
+    dev = _device_of(logits)
+    if logits.dtype not in _LOGIT_DTYPE:
+        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [num_seqs, rows, vocab]")
+    n, r, vocab = logits.shape
+    out_type = torch.float32 if probs else logits.dtype
+    if out is None:
+        out = _made((n, r, vocab), out_type, logits.device, stream)
+    _shape(out, "out", (n, r, vocab))
+    i_ptr, i_st = _logit_rows(logits, "logits", logits.dtype, dev)
+    o_ptr, o_st = _logit_rows(out, "out", out_type, dev)
+    if (history is None) != (history_lens is None):
+        raise ValueError("give both history and history_lens, or neither")
+    if prompt_lens is not None and history is None:
+        raise ValueError("prompt_lens needs history")
+    hp = hl = pl = None
+    longest = 0
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != n:
+            raise ValueError(f"history must be [{n}, max_history]")
+        longest = history.shape[1]
+        hp = _ptr(history, "history", torch.int32, dev)
+        hl = _i32(history_lens, "history_lens", (n,), dev)
+        if prompt_lens is not None:
+            pl = _i32(prompt_lens, "prompt_lens", (n,), dev)
+        if longest == 0:
+            hp = hl = pl = None
+    dp = _i32(drafts, "drafts", (n, r - 1), dev) if drafts is not None else None
+    per = []
+    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency),
+                    ("temperature", temperature)):
+        if t is not None:
+            _shape(t, name, (n,))
+        per.append(None if t is None else _ptr(t, name, torch.float32, dev))
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("give both bias_ids and bias_values, or neither")
+    bi = bv = None
+    num_bias = 0
+    if bias_ids is not None:
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != n:
+            raise ValueError(f"bias_ids must be [{n}, num_bias]")
+        num_bias = bias_ids.shape[1]
+        bi = _ptr(bias_ids, "bias_ids", torch.int32, dev)
+        _shape(bias_values, "bias_values", (n, num_bias))
+        bv = _ptr(bias_values, "bias_values", torch.float32, dev)
+        if num_bias == 0:
+            bi = bv = None
+    mp, m_seq, m_row = None, 0, 0
+    if mask is not None:
+        words = (vocab + 31) // 32
+        _shape(mask, "mask", (n, r, words))
+        if mask.dtype is not torch.int32 or mask.get_device() != dev:
+            raise TypeError(f"mask must be an int32 tensor on cuda:{dev}")
+        m_seq, m_row, one = mask.stride()
+        if one != 1 and words > 1:
+            raise ValueError("mask: the words of a row must be dense")
+        mp, m_seq, m_row = mask.data_ptr(), m_seq if n > 1 else 0, m_row if r > 1 else 0
+    if n == 0 or r == 0:
+        return out
+    st = (_lib or load()).pa_adjust_logits(
+        o_ptr, i_ptr, hp, hl, pl, dp, per[0], per[1], per[2], bi, bv, mp, per[3], n, r, vocab, longest, num_bias,
+        _LOGIT_DTYPE[logits.dtype], 1 if probs else 0, o_st, i_st, m_seq, m_row, _stream_on(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError("pa_adjust_logits", st)
+    return out

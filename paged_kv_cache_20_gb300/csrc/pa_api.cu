@@ -431,6 +431,8 @@ struct Placement {
   float *scores = nullptr;
   int32_t *row_pos = nullptr;
   const int32_t *seq_lens = nullptr;
+  // a block-scaled FP8 cache
+  const float *kv_scales = nullptr;
 };
 
 // CTAs of a cascade's shared-prefix pass: a share of the SMs, so that the tail
@@ -453,7 +455,7 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
                         const Placement &place = Placement()) {
   const int64_t units = (int64_t)num_seqs * num_kv_heads * num_splits;
   if (units >= (int64_t)1 << 31) return PA_ERR_INVALID_ARG;
-  const bool fp8 = k_scale != nullptr;
+  const bool fp8 = k_scale != nullptr || place.kv_scales != nullptr;
   // many query rows (or the shared-prefix pass): the CTA-shared pipeline kernel,
   // over a 16-bit or an FP8 cache
   if (fp8 && place.shared_prefix > 0) return PA_ERR_UNSUPPORTED;
@@ -515,6 +517,7 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
   a.scores = place.scores;
   a.row_pos = place.row_pos;
   a.seq_lens = place.seq_lens;
+  a.kv_scales = reinterpret_cast<const float2 *>(place.kv_scales);
   a.max_rows = max_blocks_per_seq * block_size;
   if (place.stat_m != nullptr) {
     a.ws_m = place.stat_m;
@@ -578,13 +581,18 @@ pa_status decode_common(void *out, float *ws, const WsLayout *lay, const void *q
     } else {
       qmap = kmap;  // unused
     }
-    if (scored)
+    if (place.kv_scales != nullptr)
+      e = pa::launch_prefill8b(kmap, vmap, qmap, a, dtype == PA_FP16, partial, s);
+    else if (scored)
       e = pa::launch_prefill_stats(kmap, vmap, qmap, a, head_dim, dtype == PA_FP16, fp8, s);
     else
       e = block_size == 16
             ? pa::launch_prefill(kmap, vmap, qmap, a, head_dim, dtype == PA_FP16, partial, fp8, s)
             : pa::launch_prefill_bx(kmap, vmap, qmap, a, head_dim, dtype == PA_FP16, partial, fp8, s);
-  } else if (scored)
+  } else if (place.kv_scales != nullptr)
+    e = dtype == PA_FP16 ? pa::launch_decode8b_fp16(kmap, vmap, a, partial, (int)units, s)
+                         : pa::launch_decode8b_bf16(kmap, vmap, a, partial, (int)units, s);
+  else if (scored)
     e = dtype == PA_FP16
             ? pa::launch_decode_scored_fp16(kmap, vmap, a, head_dim, fp8, partial, (int)units, s)
             : pa::launch_decode_scored_bf16(kmap, vmap, a, head_dim, fp8, partial, (int)units, s);
@@ -870,6 +878,40 @@ PA_API pa_status pa_decode_fp8(void *out, const void *q, const void *k_new, cons
                      block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
                      block_size, scale, num_splits, max_blocks_per_seq, num_blocks, q_len, dtype, stream,
                      k_new, v_new, k_scale, v_scale);
+  if (st != PA_OK) return st;
+  return pa_decode_combine(out, workspace, workspace_bytes, num_seqs, num_q_heads, head_dim,
+                           q_len, num_splits, dtype, stream);
+}
+
+PA_API pa_status pa_decode_block_scaled(void *out, const void *q, const void *k_cache,
+                                        const void *v_cache, const float *kv_scales,
+                                        const int32_t *block_tables, const int32_t *context_lens,
+                                        int num_seqs, int num_q_heads, int num_kv_heads,
+                                        int head_dim, int block_size, float scale,
+                                        int max_blocks_per_seq, int num_blocks, int q_len,
+                                        pa_dtype dtype, int num_splits, void *workspace,
+                                        size_t workspace_bytes, void *stream) {
+  if (!out || !aligned16(out) || !kv_scales || !aligned16(kv_scales)) return PA_ERR_INVALID_ARG;
+  if (num_splits <= 0 || num_splits >= (1 << 20)) return PA_ERR_INVALID_ARG;
+  pa_status st = check_decode(q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+                              num_q_heads, num_kv_heads, head_dim, block_size, scale,
+                              max_blocks_per_seq, num_blocks, q_len, dtype);
+  if (st != PA_OK) return st;
+  if (head_dim != 128) return PA_ERR_UNSUPPORTED;
+  Placement place;
+  place.kv_scales = kv_scales;
+  if (num_splits == 1)
+    return decode_common(out, nullptr, nullptr, q, k_cache, v_cache, block_tables, context_lens,
+                         num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, scale, 1,
+                         max_blocks_per_seq, num_blocks, q_len, dtype, stream, nullptr, nullptr,
+                         nullptr, nullptr, place);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PA_ERR_INVALID_ARG;
+  const WsLayout lay = ws_layout(num_seqs, num_q_heads, q_len, head_dim, num_splits);
+  if (workspace_bytes < lay.total) return PA_ERR_INVALID_ARG;
+  st = decode_common(nullptr, static_cast<float *>(workspace), &lay, q, k_cache, v_cache,
+                     block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                     block_size, scale, num_splits, max_blocks_per_seq, num_blocks, q_len, dtype, stream,
+                     nullptr, nullptr, nullptr, nullptr, place);
   if (st != PA_OK) return st;
   return pa_decode_combine(out, workspace, workspace_bytes, num_seqs, num_q_heads, head_dim,
                            q_len, num_splits, dtype, stream);

@@ -1,0 +1,12 @@
+// pa_block_scaled_bf16.cu -- bf16 instantiations of the decode kernels over a block-scaled FP8
+// cache, for all block sizes.
+#include "pa_decode_inst.cuh"
+
+namespace pa {
+cudaError_t launch_decode8b_bf16(const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const DecodeArgs &args, bool partial, int units, cudaStream_t stream) {
+  using T = __nv_bfloat16;
+  return args.block_size == 16 ? launch_decode8_t<16, T, false, true>(kmap, vmap, args, partial, units, stream)
+                               : launch_decode8_t<0, T, false, true>(kmap, vmap, args, partial, units, stream);
+}
+}  // namespace pa

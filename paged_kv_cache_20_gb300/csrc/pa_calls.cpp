@@ -283,6 +283,268 @@ pa_status verify_drafts(Call &c) {
   });
 }
 
+// A block-scaled pool: codes and scales.
+struct ScaledCaches {
+  void *k = nullptr, *v = nullptr;
+  float *scales = nullptr;
+  int64_t blocks = 0, heads = 0, block = 0, dim = 0;
+  ScaledCaches(Call &c, int k_at, int v_at, int s_at) {
+    const Tensor *t = c.ok ? c.tensor(k_at) : nullptr;
+    c.ok = c.ok && t->dim() == 4 && codes(t->scalar_type());
+    if (!c.ok) return;
+    const at::IntArrayRef shape = t->sizes();
+    blocks = shape[0], heads = shape[1], block = shape[2], dim = shape[3];
+    k = c.dense(k_at, t->scalar_type(), shape);
+    v = c.dense(v_at, t->scalar_type(), shape);
+    scales = static_cast<float *>(c.dense(s_at, at::kFloat, {blocks, heads, 2}));
+  }
+};
+
+// k_cache, v_cache, kv_scales, k_new, v_new, block_tables, context_lens, q_len
+pa_status append_kv_block_scaled(Call &c) {
+  const Tensor *x = c.first(3);
+  pa_dtype dt = PA_FP16;
+  c.ok = c.ok && element(*x, &dt);
+  const ScaledCaches kv(c, 0, 1, 2);
+  const long u = c.integer(7);
+  const Tensor *bt = c.ok ? c.tensor(5) : nullptr;
+  c.ok = c.ok && bt->dim() == 2 && bt->size(0) > 0 && u > 0;
+  if (!c.ok) return PA_OK;
+  const int64_t n = bt->size(0), width = bt->size(1);
+  int64_t sk = 0, sv = 0;
+  void *kp = tokens3(c, 3, x->scalar_type(), {n * u, kv.heads, kv.dim}, &sk);
+  void *vp = tokens3(c, 4, x->scalar_type(), {n * u, kv.heads, kv.dim}, &sv);
+  void *tables = c.dense(5, at::kInt, {n, width}), *lens = c.dense(6, at::kInt, {n});
+  c.ok = c.ok && fits({n, width, kv.heads, kv.blocks});
+  if (!c.ok) return PA_OK;
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_append_kv_block_scaled(kv.k, kv.v, kv.scales, kp, vp, static_cast<const int32_t *>(tables),
+                                     static_cast<const int32_t *>(lens), (int)n, (int)kv.heads, (int)kv.dim,
+                                     (int)kv.block, (int)width, (int)kv.blocks, (int)u, dt, sk, sv, s);
+  });
+}
+
+// out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, scale, q_len, num_splits,
+// workspace
+pa_status decode_block_scaled(Call &c) {
+  const Tensor *q = c.first(1);
+  pa_dtype dt = PA_FP16;
+  c.ok = c.ok && element(*q, &dt) && PyFloat_Check(c.args[7]);
+  if (!c.ok) return PA_OK;
+  const ScalarType type = q->scalar_type();
+  const ScaledCaches kv(c, 2, 3, 4);
+  const long u = c.integer(8), splits = c.integer(9);
+  const Tensor *bt = c.ok ? c.tensor(5) : nullptr;
+  c.ok = c.ok && bt->dim() == 2 && q->dim() >= 3 && (splits <= 1 || !c.none(10));
+  if (!c.ok) return PA_OK;
+  void *room = nullptr;
+  size_t room_bytes = 0;
+  if (splits > 1) {
+    const Tensor *ws = c.tensor(10);
+    c.ok = c.ok && ws->is_contiguous();
+    if (!c.ok) return PA_OK;
+    room = ws->data_ptr();
+    room_bytes = ws->nbytes();
+  }
+  const int64_t n = bt->size(0), width = bt->size(1), hq = q->size(-2);
+  void *tables = c.dense(5, at::kInt, {n, width}), *lens = c.dense(6, at::kInt, {n});
+  void *qp, *op;
+  if (q->dim() == 4) {
+    qp = c.dense(1, type, {n, u, hq, kv.dim});
+    op = c.dense(0, type, {n, u, hq, kv.dim});
+  } else {
+    c.ok = c.ok && u == 1;
+    qp = c.dense(1, type, {n, hq, kv.dim});
+    op = c.dense(0, type, {n, hq, kv.dim});
+  }
+  c.ok = c.ok && fits({n, hq, kv.heads, kv.blocks, width});
+  if (!c.ok) return PA_OK;
+  const float scale = (float)PyFloat_AS_DOUBLE(c.args[7]);
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_decode_block_scaled(op, qp, kv.k, kv.v, kv.scales, static_cast<const int32_t *>(tables),
+                                  static_cast<const int32_t *>(lens), (int)n, (int)hq, (int)kv.heads, (int)kv.dim,
+                                  (int)kv.block, scale, (int)width, (int)kv.blocks, (int)u, dt, (int)splits, room,
+                                  room_bytes, s);
+  });
+}
+
+// Block tables and reference counts of a pool.
+struct Pool {
+  int32_t *tables = nullptr, *refs = nullptr;
+  int64_t n = 0, width = 0, blocks = 0;
+  Pool(Call &c, int t_at, int r_at) {
+    const Tensor *t = c.first(t_at), *r = c.ok ? c.tensor(r_at) : nullptr;
+    c.ok = c.ok && t->dim() == 2 && r->dim() == 1;
+    if (!c.ok) return;
+    n = t->size(0), width = t->size(1), blocks = r->size(0);
+    tables = static_cast<int32_t *>(c.dense(t_at, at::kInt, {n, width}));
+    refs = static_cast<int32_t *>(c.dense(r_at, at::kInt, {blocks}));
+    c.ok = c.ok && fits({n, width, blocks});
+  }
+};
+
+int32_t *ints(Call &c, int i, at::IntArrayRef shape) { return static_cast<int32_t *>(c.dense(i, at::kInt, shape)); }
+
+// A workspace that the caller gave.
+void *room_of(Call &c, int i, size_t *bytes) {
+  const Tensor *t = c.ok ? c.tensor(i) : nullptr;
+  c.ok = c.ok && t->is_contiguous();
+  if (!c.ok) return nullptr;
+  *bytes = t->nbytes();
+  return t->data_ptr();
+}
+
+// block_tables, ref_counts, keep_lens, block_size
+pa_status free_blocks(Call &c) {
+  const Pool p(c, 0, 1);
+  const int32_t *keep = ints(c, 2, {p.n});
+  const long block = c.integer(3);
+  if (!c.ok) return PA_OK;
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_free_blocks(p.tables, p.refs, keep, (int)p.n, (int)p.width, (int)p.blocks, (int)block, s);
+  });
+}
+
+// block_tables, ref_counts, lens, block_size, missing, workspace
+pa_status reserve_blocks(Call &c) {
+  const Pool p(c, 0, 1);
+  const int32_t *lens = ints(c, 2, {p.n});
+  const long block = c.integer(3);
+  int32_t *missing = ints(c, 4, {1});
+  size_t room_bytes = 0;
+  void *room = room_of(c, 5, &room_bytes);
+  if (!c.ok) return PA_OK;
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_reserve_blocks(p.tables, p.refs, lens, missing, (int)p.n, (int)p.width, (int)p.blocks, (int)block,
+                             room, room_bytes, s);
+  });
+}
+
+// block_tables, context_lens, ref_counts, src_seqs, dst_seqs, block_size, src_blocks,
+// dst_blocks, counts, workspace
+pa_status fork_blocks(Call &c) {
+  const Pool p(c, 0, 2);
+  int32_t *lens = ints(c, 1, {p.n});
+  const Tensor *t = c.ok ? c.tensor(3) : nullptr;
+  c.ok = c.ok && t->dim() == 1;
+  if (!c.ok) return PA_OK;
+  const int64_t f = t->size(0);
+  const int32_t *src = ints(c, 3, {f}), *dst = ints(c, 4, {f});
+  const long block = c.integer(5);
+  int32_t *sb = ints(c, 6, {f}), *db = ints(c, 7, {f}), *counts = ints(c, 8, {2});
+  size_t room_bytes = 0;
+  void *room = room_of(c, 9, &room_bytes);
+  c.ok = c.ok && fits({f});
+  if (!c.ok) return PA_OK;
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_fork_blocks(p.tables, lens, p.refs, src, dst, sb, db, counts, (int)f, (int)p.n, (int)p.width,
+                          (int)p.blocks, (int)block, room, room_bytes, s);
+  });
+}
+
+// block_tables, ref_counts, block_tables_out, ref_counts_out, src_blocks, dst_blocks, counts,
+// workspace
+pa_status compact_blocks(Call &c) {
+  const Pool p(c, 0, 1);
+  c.ok = c.ok && c.none(2) == c.none(3);
+  if (!c.ok) return PA_OK;
+  int32_t *to = c.none(2) ? p.tables : ints(c, 2, {p.n, p.width});
+  int32_t *ro = c.none(3) ? p.refs : ints(c, 3, {p.blocks});
+  int32_t *sb = ints(c, 4, {p.blocks / 2}), *db = ints(c, 5, {p.blocks / 2}), *counts = ints(c, 6, {2});
+  size_t room_bytes = 0;
+  void *room = room_of(c, 7, &room_bytes);
+  if (!c.ok) return PA_OK;
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_compact_blocks(to, ro, p.tables, p.refs, sb, db, counts, (int)p.n, (int)p.width, (int)p.blocks, room,
+                             room_bytes, s);
+  });
+}
+
+// k_cache, v_cache, src_blocks, dst_blocks, counts, kv_scales
+pa_status copy_pages(Call &c) {
+  const Tensor *k = c.first(0), *t = c.ok ? c.tensor(2) : nullptr;
+  c.ok = c.ok && k->dim() == 4 && t->dim() == 1 && t->size(0) > 0;
+  if (!c.ok) return PA_OK;
+  const ScalarType type = k->scalar_type();
+  const int bytes = type == at::kHalf || type == at::kBFloat16 ? 2 : codes(type) ? 1 : 0;
+  const at::IntArrayRef shape = k->sizes();
+  void *kp = c.dense(0, type, shape), *vp = c.dense(1, type, shape);
+  const int64_t most = t->size(0);
+  const int32_t *sb = ints(c, 2, {most}), *db = ints(c, 3, {most}), *counts = ints(c, 4, {2});
+  void *scales = c.maybe(5, at::kFloat, {shape[0], shape[1], 2});
+  c.ok = c.ok && bytes && fits({most, shape[0], shape[1]});
+  if (!c.ok) return PA_OK;
+  const int blocks = (int)shape[0], heads = (int)shape[1], block = (int)shape[2], dim = (int)shape[3];
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_copy_pages(kp, vp, static_cast<float *>(scales), sb, db, counts, (int)most, heads, dim, block, blocks,
+                         bytes, s);
+  });
+}
+
+// out, logits, history, history_lens, prompt_lens, drafts, repetition, presence, frequency,
+// bias_ids, bias_values, mask, temperature, probs
+pa_status adjust_logits(Call &c) {
+  const Tensor *x = c.first(1);
+  c.ok = c.ok && x->dim() == 3 && PyBool_Check(c.args[13]);
+  if (!c.ok) return PA_OK;
+  const ScalarType type = x->scalar_type();
+  pa_dtype dt = PA_FP32;
+  c.ok = type == at::kFloat || element(*x, &dt);
+  const bool probs = c.args[13] == Py_True;
+  const at::IntArrayRef shape = x->sizes();
+  const int64_t n = shape[0], r = shape[1], vocab = shape[2];
+  void *in = c.dense(1, type, shape), *out = c.dense(0, probs ? at::kFloat : type, shape);
+  c.ok = c.ok && n > 0 && r > 0 && c.none(2) == c.none(3) && !(c.none(2) && !c.none(4)) && c.none(9) == c.none(10);
+  if (!c.ok) return PA_OK;
+  int64_t longest = 0, num_bias = 0, m_seq = 0, m_row = 0;
+  const int32_t *hist = nullptr, *bias = nullptr, *mask = nullptr;
+  if (!c.none(2)) {
+    const Tensor *t = c.tensor(2);
+    c.ok = c.ok && t->dim() == 2 && t->size(1) > 0;
+    if (!c.ok) return PA_OK;
+    longest = t->size(1);
+    hist = ints(c, 2, {n, longest});
+  }
+  if (!c.none(9)) {
+    const Tensor *t = c.ok ? c.tensor(9) : nullptr;
+    c.ok = c.ok && t->dim() == 2 && t->size(1) > 0;
+    if (!c.ok) return PA_OK;
+    num_bias = t->size(1);
+    bias = ints(c, 9, {n, num_bias});
+  }
+  const auto i32 = [&](int i) { return static_cast<const int32_t *>(c.maybe(i, at::kInt, {n})); };
+  const auto f32 = [&](int i) { return static_cast<const float *>(c.maybe(i, at::kFloat, {n})); };
+  const int32_t *hl = i32(3), *pl = i32(4);
+  const int32_t *dr = static_cast<const int32_t *>(c.maybe(5, at::kInt, {n, r - 1}));
+  const float *rep = f32(6), *pres = f32(7), *freq = f32(8), *temp = f32(12);
+  const float *bv = static_cast<const float *>(c.maybe(10, at::kFloat, {n, num_bias}));
+  if (c.ok && !c.none(11)) {
+    const Tensor *t = c.tensor(11);
+    const int64_t words = (vocab + 31) / 32;
+    c.ok = c.ok && t->scalar_type() == at::kInt && t->dim() == 3 && t->size(0) == n && t->size(1) == r &&
+           t->size(2) == words && (t->stride(2) == 1 || words == 1);
+    if (!c.ok) return PA_OK;
+    mask = static_cast<const int32_t *>(t->data_ptr());
+    m_seq = n > 1 ? t->stride(0) : 0;
+    m_row = r > 1 ? t->stride(1) : 0;
+  }
+  c.ok = c.ok && fits({n, r, vocab, longest, num_bias});
+  if (!c.ok) return PA_OK;
+  void *s = c.stream();
+  return unlocked([&] {
+    return pa_adjust_logits(out, in, hist, hl, pl, dr, rep, pres, freq, bias, bv, mask, temp, (int)n, (int)r,
+                            (int)vocab, (int)longest, (int)num_bias, dt, probs ? 1 : 0, vocab, vocab, m_seq, m_row,
+                            s);
+  });
+}
+
 // (no exception leaves: a tensor that has no plain storage, say, is the binding's business)
 template <pa_status (*F)(Call &), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -304,6 +566,14 @@ PyMethodDef kMethods[] = {
     {"decode_scored", (PyCFunction)(void (*)(void))entry<decode_scored, 15>, METH_FASTCALL, nullptr},
     {"evict", (PyCFunction)(void (*)(void))entry<evict, 14>, METH_FASTCALL, nullptr},
     {"verify_drafts", (PyCFunction)(void (*)(void))entry<verify_drafts, 10>, METH_FASTCALL, nullptr},
+    {"append_kv_block_scaled", (PyCFunction)(void (*)(void))entry<append_kv_block_scaled, 8>, METH_FASTCALL, nullptr},
+    {"decode_block_scaled", (PyCFunction)(void (*)(void))entry<decode_block_scaled, 11>, METH_FASTCALL, nullptr},
+    {"free_blocks", (PyCFunction)(void (*)(void))entry<free_blocks, 4>, METH_FASTCALL, nullptr},
+    {"reserve_blocks", (PyCFunction)(void (*)(void))entry<reserve_blocks, 6>, METH_FASTCALL, nullptr},
+    {"fork_blocks", (PyCFunction)(void (*)(void))entry<fork_blocks, 10>, METH_FASTCALL, nullptr},
+    {"compact_blocks", (PyCFunction)(void (*)(void))entry<compact_blocks, 8>, METH_FASTCALL, nullptr},
+    {"copy_pages", (PyCFunction)(void (*)(void))entry<copy_pages, 6>, METH_FASTCALL, nullptr},
+    {"adjust_logits", (PyCFunction)(void (*)(void))entry<adjust_logits, 14>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", "Checked calls of libpagedattn.so.", -1, kMethods,

@@ -118,7 +118,32 @@ struct DecodeArgs {
   int max_rows;
   // Scored prefill: -(m + log2 l) of every query row [num_seqs][num_kv_heads][rows]
   float *row_nlse;
+  // Block-scaled FP8 cache (paths built with BSC): value = code * scale of its block and
+  // KV head, [num_blocks][num_kv_heads][2] (K, V)
+  const float2 *kv_scales;
 };
+
+// Block scales count as clamped to this range (both ends exact): with 80 binary orders
+// between the largest and the smallest V scale, a weight times its scale that underflows
+// (below 2^-126 of the largest such product) is one below 2^-46 of the row's largest weight.
+constexpr float kScaleLeast = 0x1p-40f, kScaleMost = 0x1p40f;
+__device__ __forceinline__ float clamp_scale(float s) {  // (NaN: the least)
+  return fminf(fmaxf(s, kScaleLeast), kScaleMost);
+}
+
+// Softmax over a block-scaled cache.  With x_t = scale * log2(e) * sk q.c_t (sk: K scale of
+// t's block, c_t: codes) and sv the V scale, the pass keeps the running maximum m of
+// x_t + log2 sv, multiplies the V codes by w_t = 2^(x_t + log2 sv - m) <= 1 and sums
+// l = sum w_t / sv:  sum w_t c_t / l  is then  softmax(x) V.  So both scales cost one
+// multiply-add each where a plain pass has a multiply and an add, the product rounded to
+// 16 bits for P V never exceeds 1, and no accumulator is rescaled when a block's scale
+// differs from the last one's.  For sv a power of two log2 sv is exact.
+// What a tile's tokens share, by halves of 8 tokens (the same where a block holds both).
+struct TileScales {
+  float k[2], lv[2], inv[2];  // K scale, log2 and reciprocal of the V scale
+};
+template <bool BSC> struct TileArg { using type = float; };
+template <> struct TileArg<true> { using type = TileScales; };
 
 // The ledger's entry at `at` (cached row t of a sequence of Lc tokens) gains `share`; rows
 // of this step (the last q_len) start with it, and their position is noted.
@@ -272,7 +297,7 @@ __device__ __forceinline__ RowInfo row_info(const DecodeArgs &a, int kvh, int rh
 // CUDA-core path: R rows, K lanes per token.
 template <typename T, int D, int K, int R, bool SC = false>
 struct FmaPath {
-  static constexpr bool kScored = SC;
+  static constexpr bool kScored = SC, kBlockScaled = false;
   static constexpr int RPC = R;                    // rows per CTA
   static constexpr int TPP = 32 / K;               // tokens per pass
   static constexpr int PASSES = kTileTokens / TPP;  // passes per tile
@@ -462,9 +487,10 @@ struct FmaPath {
 
 // ---------------------------------------------------------------------------------
 // Tensor-core path: up to 16 rows (padded), warp-level mma.sync m16n8k16.
-template <typename T, int D, bool SC = false>
+template <typename T, int D, bool SC = false, bool BSC = false>
 struct MmaPath {
-  static constexpr bool kScored = SC;
+  static constexpr bool kScored = SC, kBlockScaled = BSC;
+  using Arg = typename TileArg<BSC>::type;
   static constexpr int RPC = 16;
   static constexpr int KS = D / 16;  // k-steps of S = Q K^T
   static constexpr int NT = D / 8;   // n-tiles (8 dims) of O
@@ -552,9 +578,11 @@ struct MmaPath {
   // lane/4 + 8, tokens nt*8 + (lane%4)*2 + {0,1}), rescaling O and l when a row's
   // maximum grows.  Returns P as the A operand (rows x 16 tokens): pa, and pl for
   // the split.
+  // (Block scales: token half nt of the tile has the scales [nt] of arg, and what comes back
+  // are the weights times their V scale.)
   template <bool MASKED>
   __device__ __forceinline__ void softmax_p(float (&sc)[2][4], int tile_idx, uint32_t (&pa)[4],
-                                            uint32_t (&pl)[4]) {
+                                            uint32_t (&pl)[4], const Arg &arg = Arg()) {
     const int lane = threadIdx.x & 31;
     // scale to base-2 units, mask, row max over the 16 tokens (4 lanes per row)
     float mx[2];
@@ -564,7 +592,11 @@ struct MmaPath {
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = sc[nt][2 * hr + e] * rs[hr];
+          float v;
+          if constexpr (BSC)
+            v = fmaf(sc[nt][2 * hr + e], rs[hr] * arg.k[nt], arg.lv[nt]);
+          else
+            v = sc[nt][2 * hr + e] * rs[hr];
           if (MASKED) {
             const int tg = tile_idx * kTileTokens + nt * 8 + (lane & 3) * 2 + e;
             if (tg >= lim[hr]) v = -INFINITY;
@@ -598,7 +630,10 @@ struct MmaPath {
           else
             p = fast_exp2(v - m[hr]);
           sc[nt][2 * hr + e] = p;
-          l[hr] += p;
+          if constexpr (BSC)
+            l[hr] = fmaf(p, arg.inv[nt], l[hr]);
+          else
+            l[hr] += p;
         }
     }
     // P as the A operand, straight from the S fragments
@@ -676,9 +711,10 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 // [token][row]; one movmatrix transpose per block gives the B fragment of P^T.
 // Thread (g, c) = (lane / 4, lane % 4) holds rows 2c and 2c+1 (P, l, O^T columns) and
 // tokens g and g+8 of each tile.
-template <typename T, int D, bool SC = false>
+template <typename T, int D, bool SC = false, bool BSC = false>
 struct MmaTPath {
-  static constexpr bool kScored = SC;
+  static constexpr bool kScored = SC, kBlockScaled = BSC;
+  using Arg = typename TileArg<BSC>::type;
   static constexpr int RPC = 8;
   static constexpr int KS = D / 16;  // k-steps of S (16 dims each)
   static constexpr int MT = D / 16;  // m-tiles of O^T (16 dims each)
@@ -750,15 +786,20 @@ struct MmaTPath {
 
   // Online-softmax update from this tile's raw S^T (sc[i]: token g + 8 (i >> 1), row
   // 2c + (i & 1)), rescaling O^T and l when a row's maximum grows.  Returns P^T's B
-  // fragments (tokens 0-7 and 8-15, transposed): bh, and bl for the split.
+  // fragments (tokens 0-7 and 8-15, transposed): bh, and bl for the split.  (Block scales:
+  // as in MmaPath.)
   template <bool MASKED>
   __device__ __forceinline__ void softmax_p(float (&sc)[4], int tile_idx, uint32_t (&bh)[2],
-                                            uint32_t (&bl)[2]) {
+                                            uint32_t (&bl)[2], const Arg &arg = Arg()) {
     const int g = (threadIdx.x & 31) >> 2;
     // scale, mask
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float v = sc[i] * rs[i & 1];
+      float v;
+      if constexpr (BSC)
+        v = fmaf(sc[i], rs[i & 1] * arg.k[i >> 1], arg.lv[i >> 1]);
+      else
+        v = sc[i] * rs[i & 1];
       if (MASKED) {
         const int tg = tile_idx * kTileTokens + g + 8 * (i >> 1);
         if (tg >= lim[i & 1]) v = -INFINITY;
@@ -796,7 +837,10 @@ struct MmaTPath {
         else
           p = fast_exp2(v - m[e]);
         sc[2 * h + e] = p;
-        l[e] += p;
+        if constexpr (BSC)
+          l[e] = fmaf(p, arg.inv[h], l[e]);
+        else
+          l[e] += p;
       }
     }
     // P^T B fragments: (tokens 0-7) and (tokens 8-15) blocks, transposed
@@ -897,12 +941,14 @@ __device__ __forceinline__ uint32_t e4m3_hi_f16x2(uint32_t w) {
 // Every load above is conflict-free under the 128-byte swizzle: the 8 lanes of a
 // shared-memory phase hit 8 distinct 16-byte bank groups.  Each q row is scaled by a
 // power of two into fp16's range and the score scale of its S^T column undoes it.
-template <typename T, bool SC = false>
+// BSC: block scales, applied in the softmax.
+template <typename T, bool SC = false, bool BSC = false>
 struct Mma8TPath {
-  static constexpr bool kScored = SC;
+  static constexpr bool kScored = SC, kBlockScaled = BSC;
   static constexpr int D = 128;
   static constexpr int RPC = 8;
-  using Inner = MmaTPath<__half, D, SC>;
+  using Inner = MmaTPath<__half, D, SC, BSC>;
+  using Arg = typename Inner::Arg;
   static constexpr int KS = Inner::KS;
   __device__ __forceinline__ ScoreSink<SC> &sink() { return inner.raw; }
   Inner inner;  // inner.o[b][i]: O^T dim 16g + 2b + (i >> 1), row 2c + (i & 1)
@@ -947,7 +993,7 @@ struct Mma8TPath {
   }
 
   template <bool MASKED>
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, float) {
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, const Arg &arg) {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const uint4 k0a = lds128(kt + sw128_offset_row128(g, 2 * c));
@@ -971,7 +1017,7 @@ struct Mma8TPath {
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] += sd[i];
     uint32_t bh[2], bl[2];
-    inner.template softmax_p<MASKED>(sc, tile_idx, bh, bl);  // fp16 P: no split
+    inner.template softmax_p<MASKED>(sc, tile_idx, bh, bl, arg);  // fp16 P: no split
     // O^T += V^T P^T.  Word j of a lane's V chunk holds dims 16g + 4j .. +3: m-tile
     // 2j takes dims 4j, 4j + 1 (rows g, g + 8), m-tile 2j + 1 dims 4j + 2, 4j + 3.
 #pragma unroll
@@ -1017,9 +1063,11 @@ struct Mma8TPath {
 // FP8 (e4m3) cache, CUDA-core path: head_dim 128, one 128-byte row per token,
 // 4 lanes per token, each lane 2 chunks of 16 codes.  The K scale is folded into q,
 // the V scale into the output.
-template <typename T, int R, bool SC = false>
+// BSC: block scales, applied to the finished dot products and in the softmax.
+template <typename T, int R, bool SC = false, bool BSC = false>
 struct Fma8Path {
-  static constexpr bool kScored = SC;
+  static constexpr bool kScored = SC, kBlockScaled = BSC;
+  using Arg = typename TileArg<BSC>::type;
   static constexpr int D = 128;
   static constexpr int RPC = R;
   static constexpr int K = 4;                        // lanes per token
@@ -1073,7 +1121,7 @@ struct Fma8Path {
   }
 
   template <bool MASKED>
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, float) {
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, const Arg &arg) {
     float s[PASSES][R];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
@@ -1096,6 +1144,13 @@ struct Fma8Path {
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int o = 1; o < K; o <<= 1) s[p][r] += __shfl_xor_sync(0xffffffffu, s[p][r], o);
+    if constexpr (BSC) {
+      static_assert(TPP == 8, "pass p holds token half p");
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[p][r] = fmaf(s[p][r], arg.k[p], arg.lv[p]);
+    }
     if (MASKED) {
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
@@ -1136,7 +1191,10 @@ struct Fma8Path {
         else
           pv = fast_exp2(s[p][r] - m[r]);
         s[p][r] = pv;
-        l[r] += pv;
+        if constexpr (BSC)
+          l[r] = fmaf(pv, arg.inv[p], l[r]);
+        else
+          l[r] += pv;
       }
     }
 #pragma unroll
@@ -1208,12 +1266,14 @@ struct Fma8Path {
 // A bf16 q row is brought into fp16 range by an exact power-of-two factor 2^-e (e:
 // exponent of the row's largest |q|), and 2^e goes into that row's score scale.  P
 // is then fp16 too: no hi/lo split is needed.
-template <typename T, bool SC = false>
+// BSC: block scales, applied in the softmax.
+template <typename T, bool SC = false, bool BSC = false>
 struct Mma8Path {
-  static constexpr bool kScored = SC;
+  static constexpr bool kScored = SC, kBlockScaled = BSC;
   static constexpr int D = 128;
   static constexpr int RPC = 16;
-  using Inner = MmaPath<__half, D, SC>;
+  using Inner = MmaPath<__half, D, SC, BSC>;
+  using Arg = typename Inner::Arg;
   static constexpr int KS = Inner::KS;
   __device__ __forceinline__ ScoreSink<SC> &sink() { return inner.raw; }
   Inner inner;
@@ -1256,7 +1316,7 @@ struct Mma8Path {
   }
 
   template <bool MASKED>
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, float) {
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, const Arg &arg) {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     uint4 kw[2][2];  // [token g, g + 8][dims 32c .. +15, 32c + 16 .. +31]
@@ -1288,7 +1348,7 @@ struct Mma8Path {
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[nt][e] += sd[nt][e];
     uint32_t pa[4], pl[4];
-    inner.template softmax_p<MASKED>(sc, tile_idx, pa, pl);  // fp16 P: no split
+    inner.template softmax_p<MASKED>(sc, tile_idx, pa, pl, arg);  // fp16 P: no split
     // O += P V.  Word j of a lane's V chunk holds dims 16g + 4j .. +3: the B columns
     // g of n-tiles 4j .. 4j + 3.
 #pragma unroll
@@ -1424,8 +1484,10 @@ __global__ void __launch_bounds__(NW * 32)
   const int tb = part.tb, te = part.te;
   const int first_masked = (L - a.q_len + 1) / kTileTokens;  // tiles >= this need masking
   // base-2 score scale (times the K scale of an FP8 cache) and the V scale
-  const float sscale = a.scale_log2 * (KV8 ? __ldg(a.k_scale + kvh) : 1.f);
-  const float vscale = KV8 ? __ldg(a.v_scale + kvh) : 1.f;
+  // (block scales are applied tile by tile)
+  constexpr bool kHeadScale = KV8 && !Path::kBlockScaled;
+  const float sscale = a.scale_log2 * (kHeadScale ? __ldg(a.k_scale + kvh) : 1.f);
+  const float vscale = kHeadScale ? __ldg(a.v_scale + kvh) : 1.f;
 
   // This warp's tiles: the unit's ntiles blocks are visited from a starting offset
   // `rot` that differs between the KV heads of a sequence, tile number
@@ -1447,9 +1509,47 @@ __global__ void __launch_bounds__(NW * 32)
   const uint32_t my_stages = smem_base + warp * NSTAGE * kStageBytes;
   // lane i holds the block-table entries of tile n = window + i
   int tbl = 0, tbl2 = kNoBlock;
+  // Block scales: lane i also holds the scales of tile n = window + i (second 8-token block:
+  // sc2), and of the window before, whose last tiles are worked on while the next window's
+  // tiles are issued.  The scales' loads are waited for only where a tile is worked on.
+  // (Read through L2: an append just before this kernel may have written them.)
+  [[maybe_unused]] float2 sc = make_float2(1.f, 1.f), sc2 = sc, sc_old = sc, sc2_old = sc;
+  [[maybe_unused]] int sc_win = -1;
+  auto scales_of = [&](int id) {
+    return id >= 0 && id < a.num_blocks ? __ldcg(a.kv_scales + (size_t)id * a.num_kv_heads + kvh)
+                                        : make_float2(1.f, 1.f);
+  };
   auto load_window = [&](int n0) {
     if (n0 + lane < n_my)
       tile_entries(table, tile_of(n0 + lane), bsz, a.max_blocks_per_seq, L, tbl, tbl2);
+    if constexpr (Path::kBlockScaled) {
+      sc_old = sc;
+      sc_win = n0 >> 5;
+      if (n0 + lane < n_my) sc = scales_of(tbl);
+      if (BS == 0) {
+        sc2_old = sc2;
+        if (n0 + lane < n_my) sc2 = bsz == 8 ? scales_of(tbl2) : sc;
+      }
+    }
+  };
+  // the scales of this warp's tile n, all lanes
+  auto tile_scales = [&](int n) {
+    TileScales t;
+    const bool cur = (n >> 5) == sc_win;
+#pragma unroll
+    for (int h = 0; h < (BS == 0 ? 2 : 1); ++h) {
+      const float2 from = h == 0 ? (cur ? sc : sc_old) : (cur ? sc2 : sc2_old);
+      t.k[h] = clamp_scale(__shfl_sync(0xffffffffu, from.x, n & 31));
+      const float v = clamp_scale(__shfl_sync(0xffffffffu, from.y, n & 31));
+      t.lv[h] = log2f(v);
+      t.inv[h] = 1.f / v;
+    }
+    if (BS != 0) {
+      t.k[1] = t.k[0];
+      t.lv[1] = t.lv[0];
+      t.inv[1] = t.inv[0];
+    }
+    return t;
   };
 
   auto issue = [&](int n) {
@@ -1499,7 +1599,7 @@ __global__ void __launch_bounds__(NW * 32)
   // (j - tb - rot) mod ntiles, modulo TW.  The table window and q above are already
   // in flight: neither is written here.
   bool reads_new = false;
-  if (a.k_new != nullptr && ntiles > 0) {
+  if (!Path::kBlockScaled && a.k_new != nullptr && ntiles > 0) {
     const int j1 = min(te, (L + kTileTokens - 1) / kTileTokens);  // past the last new tile
     for (int j = max(tb, max(0, L - a.q_len) / kTileTokens); j < j1; ++j) {
       int k = j - tb - rot;
@@ -1572,9 +1672,15 @@ __global__ void __launch_bounds__(NW * 32)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      path.template tile<true>(kt, vt, j, sscale);
+      if constexpr (Path::kBlockScaled)
+        path.template tile<true>(kt, vt, j, tile_scales(n));
+      else
+        path.template tile<true>(kt, vt, j, sscale);
     } else {
-      path.template tile<false>(kt, vt, j, sscale);
+      if constexpr (Path::kBlockScaled)
+        path.template tile<false>(kt, vt, j, tile_scales(n));
+      else
+        path.template tile<false>(kt, vt, j, sscale);
     }
     __syncwarp();
     if (n + NSTAGE < n_my) issue(n + NSTAGE);

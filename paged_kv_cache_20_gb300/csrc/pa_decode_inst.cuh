@@ -141,33 +141,34 @@ static cudaError_t launch_paths(const CUtensorMap &kmap, const CUtensorMap &vmap
   return launch_one<BS, T, D, MmaPath<T, D, SC>, PARTIAL>(kmap, vmap, a, units, groups, st);
 }
 
-template <int BS, typename T, bool PARTIAL, bool SC>
+// BSC: block-scaled cache.
+template <int BS, typename T, bool PARTIAL, bool SC, bool BSC>
 static cudaError_t launch_paths8(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                  const DecodeArgs &a, int units, cudaStream_t st) {
   if constexpr (!PARTIAL) {
-    if (a.rows == 1) return launch_few_units<BS, T, Fma8Path<T, 1, SC>, true, 2, 1>(kmap, vmap, a, units, st);
-    if (a.rows == 2) return launch_few_units<BS, T, Fma8Path<T, 2, SC>, true, 2, 1>(kmap, vmap, a, units, st);
+    if (a.rows == 1) return launch_few_units<BS, T, Fma8Path<T, 1, SC, BSC>, true, 2, 1>(kmap, vmap, a, units, st);
+    if (a.rows == 2) return launch_few_units<BS, T, Fma8Path<T, 2, SC, BSC>, true, 2, 1>(kmap, vmap, a, units, st);
   }
-  if (a.rows == 1) return launch_one<BS, T, 128, Fma8Path<T, 1, SC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
-  if (a.rows == 2) return launch_one<BS, T, 128, Fma8Path<T, 2, SC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
+  if (a.rows == 1) return launch_one<BS, T, 128, Fma8Path<T, 1, SC, BSC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
+  if (a.rows == 2) return launch_one<BS, T, 128, Fma8Path<T, 2, SC, BSC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
   if (a.rows <= 8) {
-    if constexpr (!PARTIAL) return launch_few_units<BS, T, Mma8TPath<T, SC>, true, 3, 2>(kmap, vmap, a, units, st);
-    return launch_one<BS, T, 128, Mma8TPath<T, SC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
+    if constexpr (!PARTIAL) return launch_few_units<BS, T, Mma8TPath<T, SC, BSC>, true, 3, 2>(kmap, vmap, a, units, st);
+    return launch_one<BS, T, 128, Mma8TPath<T, SC, BSC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
   }
   const int groups = (a.rows + 15) / 16;
   if constexpr (!PARTIAL)
-    if (groups == 1) return launch_few_units<BS, T, Mma8Path<T, SC>, true, 2, 1>(kmap, vmap, a, units, st);
-  return launch_one<BS, T, 128, Mma8Path<T, SC>, PARTIAL, true>(kmap, vmap, a, units, groups, st);
+    if (groups == 1) return launch_few_units<BS, T, Mma8Path<T, SC, BSC>, true, 2, 1>(kmap, vmap, a, units, st);
+  return launch_one<BS, T, 128, Mma8Path<T, SC, BSC>, PARTIAL, true>(kmap, vmap, a, units, groups, st);
 }
 
 // FP8 (e4m3) cache, head_dim 128; T is the type of q and out.
 // BS = 16: kernels built for 16-token blocks; BS = 0: kernels that read the block
 // size (8 or 32) from the arguments.
-template <int BS, typename T, bool SC = false>
+template <int BS, typename T, bool SC = false, bool BSC = false>
 static cudaError_t launch_decode8_t(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                     const DecodeArgs &a, bool partial, int units, cudaStream_t st) {
-  return partial ? launch_paths8<BS, T, true, SC>(kmap, vmap, a, units, st)
-                 : launch_paths8<BS, T, false, SC>(kmap, vmap, a, units, st);
+  return partial ? launch_paths8<BS, T, true, SC, BSC>(kmap, vmap, a, units, st)
+                 : launch_paths8<BS, T, false, SC, BSC>(kmap, vmap, a, units, st);
 }
 
 template <int BS, typename T, bool SC = false>

@@ -70,6 +70,14 @@ cudaError_t launch_prefill(const CUtensorMap &kmap, const CUtensorMap &vmap, con
 cudaError_t launch_prefill_bx(const CUtensorMap &kmap, const CUtensorMap &vmap,
                               const CUtensorMap &qmap, const DecodeArgs &args, int head_dim,
                               bool fp16, bool partial, bool kv8, cudaStream_t stream);
+// A block-scaled FP8 cache (args.kv_scales; head_dim 128), any block size: up to 16 query
+// tokens, and more.
+cudaError_t launch_decode8b_fp16(const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const DecodeArgs &args, bool partial, int units, cudaStream_t stream);
+cudaError_t launch_decode8b_bf16(const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const DecodeArgs &args, bool partial, int units, cudaStream_t stream);
+cudaError_t launch_prefill8b(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap,
+                             const DecodeArgs &args, bool fp16, bool partial, cudaStream_t stream);
 cudaError_t launch_combine_fp16(const CombineArgs &args, int head_dim, cudaStream_t stream);
 cudaError_t launch_combine_bf16(const CombineArgs &args, int head_dim, cudaStream_t stream);
 

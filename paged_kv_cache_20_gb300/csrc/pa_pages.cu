@@ -1,0 +1,726 @@
+// pa_pages.cu -- the block pool's bookkeeping on the device: blocks freed, reserved, forked
+// and compacted by reference counts, and the copy of the blocks that those calls list.
+//
+// A block is free while no table entry refers to it (ref_counts[b] == 0).  Every call has
+// one answer whatever the order of its threads: free blocks are taken in ascending order by
+// the entries that want one in (sequence, logical block) order.  Both orders are ranks, and
+// a rank is a prefix sum: each warp counts its contiguous part, the warps' totals are
+// summed over the thread block and over the cluster, and the warp walks its part again with
+// its rank at hand.
+//
+// Bound by latency: a pool of 131,072 blocks has 512 KiB of counts.  One cluster of 8
+// thread blocks of 32 warps walks it, so the sums over all warps cost one cluster barrier
+// instead of a kernel boundary; with 256 warps a warp's part of such a pool is 512 counts,
+// four 16-byte loads a lane.
+#include <algorithm>
+
+#include "../../include/pagedattn.h"
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "pa_launch.h"
+
+namespace pa {
+namespace {
+
+// All threads of the cluster (a warp arrives as one).
+__device__ __forceinline__ void sync_cluster() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
+constexpr int kCluster = 8;
+constexpr int kWarpsPerCta = 32;
+constexpr int kAllWarps = kCluster * kWarpsPerCta;
+
+// A contiguous part of [0, n) for each of the cluster's warps, in whole steps of 128.
+struct Part {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ Part part_of(int64_t n, int gw) {
+  const int64_t steps = (n + 127) / 128;
+  const int64_t per = (steps + kAllWarps - 1) / kAllWarps;
+  Part p;
+  p.lo = min(n, (int64_t)gw * per * 128);
+  p.hi = min(n, p.lo + per * 128);
+  return p;
+}
+
+// Four counts (or entries) at i .. i + 3 of an array of n; `fill` past its end.  Read
+// through L2: these arrays are written by the calls before and by this one.
+__device__ __forceinline__ int4 load4(const int32_t *p, int64_t i, int64_t n, int fill) {
+  if (i + 4 <= n) return __ldcg(reinterpret_cast<const int4 *>(p + i));
+  int4 v = make_int4(fill, fill, fill, fill);
+  if (i < n) v.x = __ldcg(p + i);
+  if (i + 1 < n) v.y = __ldcg(p + i + 1);
+  if (i + 2 < n) v.z = __ldcg(p + i + 2);
+  return v;
+}
+
+__device__ __forceinline__ int warp_sum(int v) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)v); }
+// Sum over the lanes before this one.
+__device__ __forceinline__ int warp_before(int v) {
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) >= o) s += u;
+  }
+  return s - v;
+}
+
+// The totals of the cluster's warps, [which][warp]: each warp leaves its own in its thread
+// block, and after a cluster barrier reads those of the warps before it.
+struct Totals {
+  int of[2][kWarpsPerCta];
+};
+// Sum of totals `which` over the warps before gw (before) and over all (all).
+__device__ __forceinline__ void ranks(Totals &t, int which, int gw, int &before, int &all) {
+  const int lane = threadIdx.x & 31;
+  before = all = 0;
+#pragma unroll
+  for (int c = 0; c < kCluster; ++c) {
+    const int v = dsmem_ld_s32(dsmem_map(smem_u32(&t.of[which][lane]), c));
+    all += v;
+    if (c * kWarpsPerCta + lane < gw) before += v;
+  }
+  before = warp_sum(before);
+  all = warp_sum(all);
+}
+
+// Free blocks of this warp's part of the counts.
+__device__ __forceinline__ int count_free(const int32_t *refs, Part p) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+#pragma unroll 4
+  for (int64_t i = p.lo + 4 * lane; i < p.hi; i += 128) {
+    const int4 v = load4(refs, i, p.hi, 1);
+    n += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+  }
+  return warp_sum(n);
+}
+
+// The first `want` free blocks, ascending, to list (rank of this warp's first: before).
+__device__ __forceinline__ void list_free(const int32_t *refs, Part p, int before, int want, int32_t *list) {
+  const int lane = threadIdx.x & 31;
+  int at = before;
+  for (int64_t i0 = p.lo; i0 < p.hi && at < want; i0 += 128) {
+    const int64_t i = i0 + 4 * lane;
+    const int4 v = load4(refs, i, p.hi, 1);
+    const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
+    const int mine = f[0] + f[1] + f[2] + f[3];
+    int r = at + warp_before(mine);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (f[k]) {
+        if (r < want) list[r] = (int32_t)(i + k);
+        ++r;
+      }
+    at += warp_sum(mine);
+  }
+}
+
+struct PoolArgs {
+  int32_t *tables, *refs;
+  const int32_t *lens;  // reserve: tokens wanted; free: tokens kept
+  int32_t *missing, *list;
+  int num_seqs, width, num_blocks, block_size;
+  unsigned *err;
+};
+
+__device__ __forceinline__ int64_t blocks_of(int len, int block_size) {
+  return len > 0 ? ((int64_t)len + block_size - 1) / block_size : 0;
+}
+
+// ---- free ------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) free_blocks_kernel(const PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t n = (int64_t)a.num_seqs * a.width;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int4 v = load4(a.tables, i, n, -1);
+  const int id[4] = {v.x, v.y, v.z, v.w};
+  int64_t row = i / a.width;
+  int col = (int)(i - row * a.width);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (id[k] >= 0 && col >= blocks_of(__ldg(a.lens + row), a.block_size)) {
+      bool bad = id[k] >= a.num_blocks;
+      if (!bad && atomicSub(a.refs + id[k], 1) <= 0) {  // was not counted: leave the count
+        atomicAdd(a.refs + id[k], 1);
+        bad = true;
+      }
+      if (bad) record_error(a.err, kErrCheck);
+      a.tables[i + k] = -1;
+    }
+    if (++col == a.width) {
+      col = 0;
+      ++row;
+    }
+  }
+}
+
+// ---- reserve ---------------------------------------------------------------------
+// Entries at i .. i + 3 of the tables that want a block, as four bits.
+__device__ __forceinline__ int wants4(const PoolArgs &a, int64_t i, int64_t n, bool rec) {
+  if (i >= n) return 0;
+  const int4 v = load4(a.tables, i, n, 0);
+  if (v.x >= 0 && v.y >= 0 && v.z >= 0 && v.w >= 0) return 0;
+  const int id[4] = {v.x, v.y, v.z, v.w};
+  int64_t row = i / a.width;
+  int col = (int)(i - row * a.width);
+  int f = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (id[k] < 0 && col < blocks_of(__ldg(a.lens + row), a.block_size)) f |= 1 << k;
+    if (++col == a.width) {
+      col = 0;
+      ++row;
+    }
+  }
+  return f;
+}
+
+__global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs a) {
+  __shared__ Totals tot;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
+  const int64_t n = (int64_t)a.num_seqs * a.width;
+  const Part pe = part_of(n, gw), pb = part_of(a.num_blocks, gw);
+  for (int i = gw * 32 + lane; i < a.num_seqs; i += kAllWarps * 32)
+    if (blocks_of(__ldg(a.lens + i), a.block_size) > a.width) record_error(a.err, kErrCheck);
+  int wanted = 0;
+#pragma unroll 2
+  for (int64_t i = pe.lo + 4 * lane; i < pe.hi; i += 128) wanted += __popc(wants4(a, i, pe.hi, false));
+  wanted = warp_sum(wanted);
+  const int free = count_free(a.refs, pb);
+  if (lane == 0) {
+    tot.of[0][warp] = wanted;
+    tot.of[1][warp] = free;
+  }
+  sync_cluster();
+  int want0, wants, free0, frees;
+  ranks(tot, 0, gw, want0, wants);
+  ranks(tot, 1, gw, free0, frees);
+  list_free(a.refs, pb, free0, wants, a.list);
+  sync_cluster();  // the list is written, every count read
+  int at = want0;
+  if (wanted > 0) {
+    for (int64_t i0 = pe.lo; i0 < pe.hi; i0 += 128) {
+      const int64_t i = i0 + 4 * lane;
+      const int f = wants4(a, i, pe.hi, false);
+      const int mine = __popc(f);
+      int r = at + warp_before(mine);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (f >> k & 1) {
+          if (r < frees) {
+            const int id = __ldcg(a.list + r);
+            a.tables[i + k] = id;
+            a.refs[id] = 1;
+          }
+          ++r;
+        }
+      at += warp_sum(mine);
+    }
+  }
+  if (gw == 0 && lane == 0) *a.missing = max(0, wants - frees);
+}
+
+// ---- fork ------------------------------------------------------------------------
+struct ForkArgs {
+  int32_t *tables, *lens, *refs;
+  const int32_t *src, *dst;
+  int32_t *src_blocks, *dst_blocks, *counts, *list, *tail_of;
+  int num_forks, num_seqs, width, num_blocks, block_size;
+  unsigned *err;
+};
+
+// Fork f's parent and child; false: an id outside the batch, or a parent its own child.
+__device__ __forceinline__ bool fork_pair(const ForkArgs &a, int f, int &s, int &d) {
+  s = __ldg(a.src + f);
+  d = __ldg(a.dst + f);
+  return s >= 0 && s < a.num_seqs && d >= 0 && d < a.num_seqs && s != d;
+}
+
+// The partial block at the end of fork f's parent (-1: none, or the fork is skipped).
+__device__ __forceinline__ int parent_tail(const ForkArgs &a, int f, bool rec) {
+  int s, d, id = -1;
+  bool bad = !fork_pair(a, f, s, d);
+  if (!bad) {
+    const int len = max(0, __ldcg(a.lens + s));
+    bad = blocks_of(len, a.block_size) > a.width;
+    if (!bad && len % a.block_size != 0) {
+      id = __ldcg(a.tables + (int64_t)s * a.width + len / a.block_size);
+      bad = id < 0 || id >= a.num_blocks;
+    }
+  }
+  if (bad && rec) record_error(a.err, kErrCheck);
+  return bad ? -1 : id;
+}
+
+__global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) {
+  __shared__ Totals tot;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
+  const Part pb = part_of(a.num_blocks, gw);
+  // forks in parts of whole warps: f = lo + lane, lo + lane + 32, ..
+  const int per = (a.num_forks + kAllWarps * 32 - 1) / (kAllWarps * 32) * 32;
+  const int lo = min(a.num_forks, gw * per), hi = min(a.num_forks, lo + per);
+  int tails = 0;
+  for (int f = lo + lane; f < hi; f += 32) {
+    tails += parent_tail(a, f, true) >= 0;
+  }
+  tails = warp_sum(tails);
+  const int free = count_free(a.refs, pb);
+  if (lane == 0) {
+    tot.of[0][warp] = tails;
+    tot.of[1][warp] = free;
+  }
+  sync_cluster();
+  int tail0, all, free0, frees;
+  ranks(tot, 0, gw, tail0, all);
+  ranks(tot, 1, gw, free0, frees);
+  list_free(a.refs, pb, free0, all, a.list);
+  sync_cluster();  // the list is written, every count and length read that decides
+  int at = tail0;
+  for (int f0 = lo; f0 < hi; f0 += 32) {
+    const int f = f0 + lane;
+    const int t = f < hi ? parent_tail(a, f, false) : -1;
+    const int r = at + warp_before(t >= 0);
+    at += warp_sum(t >= 0);
+    if (f < hi) {
+      int id = -1;
+      if (t >= 0 && r < frees) {
+        id = __ldcg(a.list + r);
+        a.refs[id] = 1;
+        a.src_blocks[r] = t;
+        a.dst_blocks[r] = id;
+      }
+      a.tail_of[f] = id;
+    }
+  }
+  if (gw == 0 && lane == 0) {
+    a.counts[0] = min(all, frees);
+    a.counts[1] = max(0, all - frees);
+  }
+  sync_cluster();
+  // the children's rows
+  const int64_t n = (int64_t)a.num_forks * a.width;
+  for (int64_t i = (int64_t)gw * 32 + lane; i < n; i += kAllWarps * 32) {
+    const int f = (int)(i / a.width), j = (int)(i - (int64_t)f * a.width);
+    int s, d;
+    if (!fork_pair(a, f, s, d)) continue;
+    const int len = max(0, __ldcg(a.lens + s));
+    const int full = min(len / a.block_size, a.width);
+    int id = -1;
+    if (j < full) {
+      id = __ldcg(a.tables + (int64_t)s * a.width + j);
+      if (id < 0 || id >= a.num_blocks) {
+        record_error(a.err, kErrCheck);
+        id = -1;
+      } else {
+        atomicAdd(a.refs + id, 1);
+      }
+    } else if (j == full) {
+      id = __ldcg(a.tail_of + f);
+    }
+    a.tables[(int64_t)d * a.width + j] = id;
+  }
+  sync_cluster();  // every parent's length read
+  for (int f = gw * 32 + lane; f < a.num_forks; f += kAllWarps * 32) {
+    int s, d;
+    if (!fork_pair(a, f, s, d)) continue;
+    const int len = max(0, __ldcg(a.lens + s));
+    const int full = min(len / a.block_size, a.width);
+    a.lens[d] = __ldcg(a.tail_of + f) >= 0 ? len : full * a.block_size;
+  }
+}
+
+// ---- compact ---------------------------------------------------------------------
+struct CompactArgs {
+  int32_t *tables_out, *refs_out;
+  const int32_t *tables, *refs;
+  int32_t *src_blocks, *dst_blocks, *counts;
+  int32_t *name;   // [num_blocks]: new id of a block that moves, -1 for a free one
+  int32_t *moved;  // [num_blocks / 2]: reference counts of the moving blocks
+  int num_seqs, width, num_blocks;
+  unsigned *err;
+};
+
+__global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactArgs a) {
+  __shared__ Totals tot;
+  __shared__ int s_below;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
+  const Part p = part_of(a.num_blocks, gw);
+  if (threadIdx.x == 0) s_below = 0;
+  const int used = (int)(p.hi - p.lo) - count_free(a.refs, p);
+  if (lane == 0) tot.of[0][warp] = used;
+  sync_cluster();
+  int used0, live;
+  ranks(tot, 0, gw, used0, live);
+  // used blocks below `live`: the warp whose part holds that border counts them
+  if (p.lo < live && live <= p.hi) {
+    int below = 0;
+    for (int64_t i = p.lo + lane; i < live; i += 32) below += __ldcg(a.refs + i) != 0;
+    below = warp_sum(below);
+    if (lane == 0) s_below = used0 + below;
+  }
+  sync_cluster();
+  int below = 0;
+#pragma unroll
+  for (int c = 0; c < kCluster; ++c) below += dsmem_ld_s32(dsmem_map(smem_u32(&s_below), c));
+  // the k-th used block at or past `live` goes to the k-th free one before it
+  int at = used0;
+  for (int64_t i0 = p.lo; i0 < p.hi; i0 += 128) {
+    const int64_t i = i0 + 4 * lane;
+    const int4 v = load4(a.refs, i, p.hi, 0);
+    const int ref[4] = {v.x, v.y, v.z, v.w};
+    const int mine = (v.x != 0) + (v.y != 0) + (v.z != 0) + (v.w != 0);
+    int u = at + warp_before(mine);  // used blocks before i + k
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t b = i + k;
+      if (b < p.hi) {
+        if (b < live) {
+          if (ref[k] == 0)
+            a.dst_blocks[b - u] = (int32_t)b;
+          else
+            a.refs_out[b] = ref[k];
+        } else {
+          if (ref[k] != 0) {
+            a.src_blocks[u - below] = (int32_t)b;
+            a.moved[u - below] = ref[k];
+          }
+          a.name[b] = -1;
+          a.refs_out[b] = 0;
+        }
+      }
+      u += ref[k] != 0;
+    }
+    at += warp_sum(mine);
+  }
+  const int moves = live - below;
+  if (gw == 0 && lane == 0) {
+    a.counts[0] = moves;
+    a.counts[1] = live;
+  }
+  sync_cluster();
+  for (int k = gw * 32 + lane; k < moves; k += kAllWarps * 32) {
+    const int to = __ldcg(a.dst_blocks + k);
+    a.name[__ldcg(a.src_blocks + k)] = to;
+    a.refs_out[to] = __ldcg(a.moved + k);
+  }
+  sync_cluster();
+  const int64_t n = (int64_t)a.num_seqs * a.width;
+  for (int64_t i = ((int64_t)gw * 32 + lane) * 4; i < n; i += kAllWarps * 128) {
+    const int4 v = load4(a.tables, i, n, -1);
+    int id[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k >= n) continue;
+      if (id[k] >= live) {
+        id[k] = id[k] < a.num_blocks ? __ldcg(a.name + id[k]) : -1;
+        if (id[k] < 0) record_error(a.err, kErrCheck);  // outside the pool, or counted as free
+      }
+      a.tables_out[i + k] = id[k];
+    }
+  }
+}
+
+// ---- copy ------------------------------------------------------------------------
+// Pieces of 16 KiB, one a step: K's of every listed pair, then V's, the pair's scales with
+// its first piece of K.
+constexpr int kPieceThreads = 256, kPieceLoads = 4;
+constexpr int kPiece = kPieceThreads * kPieceLoads;  // 16-byte chunks
+
+struct CopyArgs {
+  uint4 *cache[2];
+  float *kv_scales;
+  const int32_t *src, *dst, *counts;
+  int64_t chunks;  // 16-byte chunks of a block in one cache
+  int max_pairs, num_blocks, pieces, scales_per_block;
+  unsigned *err;
+};
+
+__global__ void __launch_bounds__(kPieceThreads) copy_pages_kernel(const CopyArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int pairs = min(max(0, __ldcg(a.counts)), a.max_pairs);
+  const int64_t tasks = (int64_t)pairs * 2 * a.pieces;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int piece = (int)(task % a.pieces);
+    const int64_t rest = task / a.pieces;
+    const int kv = (int)(rest & 1), pair = (int)(rest >> 1);
+    const int s = __ldcg(a.src + pair), d = __ldcg(a.dst + pair);
+    if (s < 0 || s >= a.num_blocks || d < 0 || d >= a.num_blocks) {
+      if (piece == 0 && kv == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
+      continue;
+    }
+    const uint4 *from = a.cache[kv] + s * a.chunks;
+    uint4 *to = a.cache[kv] + d * a.chunks;
+    const int64_t c0 = (int64_t)piece * kPiece + threadIdx.x;
+    uint4 v[kPieceLoads];
+#pragma unroll
+    for (int u = 0; u < kPieceLoads; ++u)
+      if (c0 + u * kPieceThreads < a.chunks) v[u] = __ldcs(from + c0 + u * kPieceThreads);
+#pragma unroll
+    for (int u = 0; u < kPieceLoads; ++u)
+      if (c0 + u * kPieceThreads < a.chunks) __stcs(to + c0 + u * kPieceThreads, v[u]);
+    if (a.kv_scales != nullptr && piece == 0 && kv == 0)
+      for (int i = threadIdx.x; i < a.scales_per_block; i += kPieceThreads)
+        a.kv_scales[(int64_t)d * a.scales_per_block + i] = __ldcg(a.kv_scales + (int64_t)s * a.scales_per_block + i);
+  }
+}
+
+// One cluster of kCluster thread blocks, as a dependent of the work before it.
+template <typename A>
+cudaError_t launch_cluster(void (*kern)(A), cudaStream_t st, const A &args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kWarpsPerCta * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args);
+}
+
+// Sizes that the bookkeeping calls share.
+pa_status check_pool(int num_seqs, int max_blocks_per_seq, int num_blocks, int block_size) {
+  if (num_seqs <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0) return PA_ERR_INVALID_ARG;
+  if (!supported_block(block_size)) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t)1 << 30 || num_blocks >= 1 << 30 ||
+      (int64_t)max_blocks_per_seq * block_size >= (int64_t)1 << 31)
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+size_t ints(int64_t n) { return (size_t)n * 4; }
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+PA_API size_t pa_pages_workspace_size(int num_blocks, int num_forks) {
+  if (num_blocks <= 0 || num_forks < 0) return 0;
+  return ((size_t)num_blocks + (size_t)std::max(num_forks, num_blocks / 2) + 4) * 4;
+}
+
+PA_API pa_status pa_free_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *keep_lens,
+                                int num_seqs, int max_blocks_per_seq, int num_blocks, int block_size,
+                                void *stream) {
+  if (!block_tables || !ref_counts || !keep_lens) return PA_ERR_INVALID_ARG;
+  const pa_status st = check_pool(num_seqs, max_blocks_per_seq, num_blocks, block_size);
+  if (st != PA_OK) return st;
+  if (!aligned16(block_tables) || !aligned16(ref_counts) || !aligned4(keep_lens)) return PA_ERR_INVALID_ARG;
+  const size_t table = ints((int64_t)num_seqs * max_blocks_per_seq), refs = ints(num_blocks), lens = ints(num_seqs);
+  if (overlap(block_tables, table, ref_counts, refs) || overlap(block_tables, table, keep_lens, lens) ||
+      overlap(ref_counts, refs, keep_lens, lens))
+    return PA_ERR_INVALID_ARG;
+  PoolArgs a = {};
+  a.tables = block_tables;
+  a.refs = ref_counts;
+  a.lens = keep_lens;
+  a.num_seqs = num_seqs;
+  a.width = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.err = error_word();
+  if (a.err == nullptr) return PA_ERR_CUDA;
+  const unsigned ctas = (unsigned)(((int64_t)num_seqs * max_blocks_per_seq + 1023) / 1024);
+  return launch_dependent(free_blocks_kernel, ctas, 256, static_cast<cudaStream_t>(stream), a) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_reserve_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *lens,
+                                   int32_t *missing, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                                   int block_size, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!block_tables || !ref_counts || !lens || !missing || !workspace) return PA_ERR_INVALID_ARG;
+  const pa_status st = check_pool(num_seqs, max_blocks_per_seq, num_blocks, block_size);
+  if (st != PA_OK) return st;
+  if (!aligned16(block_tables) || !aligned16(ref_counts) || !aligned16(workspace) || !aligned4(lens) ||
+      !aligned4(missing))
+    return PA_ERR_INVALID_ARG;
+  if (workspace_bytes < pa_pages_workspace_size(num_blocks, 0)) return PA_ERR_INVALID_ARG;
+  struct {
+    const void *p;
+    size_t n;
+  } buf[] = {{block_tables, ints((int64_t)num_seqs * max_blocks_per_seq)}, {ref_counts, ints(num_blocks)},
+             {lens, ints(num_seqs)}, {missing, 4}, {workspace, pa_pages_workspace_size(num_blocks, 0)}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(buf[i].p, buf[i].n, buf[j].p, buf[j].n)) return PA_ERR_INVALID_ARG;
+  PoolArgs a = {};
+  a.tables = block_tables;
+  a.refs = ref_counts;
+  a.lens = lens;
+  a.missing = missing;
+  a.list = static_cast<int32_t *>(workspace);
+  a.num_seqs = num_seqs;
+  a.width = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.err = error_word();
+  if (a.err == nullptr) return PA_ERR_CUDA;
+  return launch_cluster(reserve_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
+                                                                                                    : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_fork_blocks(int32_t *block_tables, int32_t *context_lens, int32_t *ref_counts,
+                                const int32_t *src_seqs, const int32_t *dst_seqs, int32_t *src_blocks,
+                                int32_t *dst_blocks, int32_t *counts, int num_forks, int num_seqs,
+                                int max_blocks_per_seq, int num_blocks, int block_size, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+  if (!block_tables || !context_lens || !ref_counts || !counts || !workspace) return PA_ERR_INVALID_ARG;
+  const pa_status st = check_pool(num_seqs, max_blocks_per_seq, num_blocks, block_size);
+  if (st != PA_OK) return st;
+  if (num_forks < 0 || num_forks > num_seqs) return PA_ERR_INVALID_ARG;
+  if (num_forks > 0 && (!src_seqs || !dst_seqs || !src_blocks || !dst_blocks)) return PA_ERR_INVALID_ARG;
+  if (!aligned16(ref_counts) || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+  for (const void *p : {static_cast<const void *>(block_tables), static_cast<const void *>(context_lens),
+                        static_cast<const void *>(src_seqs), static_cast<const void *>(dst_seqs),
+                        static_cast<const void *>(src_blocks), static_cast<const void *>(dst_blocks),
+                        static_cast<const void *>(counts)})
+    if (!aligned4(p)) return PA_ERR_INVALID_ARG;
+  const size_t room = pa_pages_workspace_size(num_blocks, num_forks);
+  if (workspace_bytes < room) return PA_ERR_INVALID_ARG;
+  struct {
+    const void *p;
+    size_t n;
+  } buf[] = {{block_tables, ints((int64_t)num_seqs * max_blocks_per_seq)}, {context_lens, ints(num_seqs)},
+             {ref_counts, ints(num_blocks)}, {src_blocks, ints(num_forks)}, {dst_blocks, ints(num_forks)},
+             {counts, 8}, {workspace, room}, {src_seqs, ints(num_forks)}, {dst_seqs, ints(num_forks)}};
+  for (int i = 0; i < 7; ++i)  // (the inputs, 7 and 8, may be one array)
+    for (int j = i + 1; j < 9; ++j)
+      if (overlap(buf[i].p, buf[i].n, buf[j].p, buf[j].n)) return PA_ERR_INVALID_ARG;
+  if (num_forks == 0)
+    return cudaMemsetAsync(counts, 0, 8, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  ForkArgs a = {};
+  a.tables = block_tables;
+  a.lens = context_lens;
+  a.refs = ref_counts;
+  a.src = src_seqs;
+  a.dst = dst_seqs;
+  a.src_blocks = src_blocks;
+  a.dst_blocks = dst_blocks;
+  a.counts = counts;
+  a.list = static_cast<int32_t *>(workspace);
+  a.tail_of = a.list + num_blocks;
+  a.num_forks = num_forks;
+  a.num_seqs = num_seqs;
+  a.width = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.err = error_word();
+  if (a.err == nullptr) return PA_ERR_CUDA;
+  return launch_cluster(fork_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
+                                                                                                 : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_compact_blocks(int32_t *block_tables_out, int32_t *ref_counts_out,
+                                   const int32_t *block_tables, const int32_t *ref_counts, int32_t *src_blocks,
+                                   int32_t *dst_blocks, int32_t *counts, int num_seqs, int max_blocks_per_seq,
+                                   int num_blocks, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!block_tables_out || !ref_counts_out || !block_tables || !ref_counts || !counts || !workspace)
+    return PA_ERR_INVALID_ARG;
+  if (num_blocks > 1 && (!src_blocks || !dst_blocks)) return PA_ERR_INVALID_ARG;
+  const pa_status st = check_pool(num_seqs, max_blocks_per_seq, num_blocks, 16);
+  if (st != PA_OK) return st;
+  if (!aligned16(block_tables) || !aligned16(ref_counts) || !aligned16(workspace) || !aligned4(block_tables_out) ||
+      !aligned4(ref_counts_out) || !aligned4(src_blocks) || !aligned4(dst_blocks) || !aligned4(counts))
+    return PA_ERR_INVALID_ARG;
+  const size_t room = pa_pages_workspace_size(num_blocks, 0);
+  if (workspace_bytes < room) return PA_ERR_INVALID_ARG;
+  const size_t table = ints((int64_t)num_seqs * max_blocks_per_seq), refs = ints(num_blocks);
+  struct {
+    const void *p;
+    size_t n;
+  } buf[] = {{block_tables_out, table}, {ref_counts_out, refs}, {src_blocks, ints(num_blocks / 2)},
+             {dst_blocks, ints(num_blocks / 2)}, {counts, 8}, {workspace, room}, {block_tables, table},
+             {ref_counts, refs}};
+  for (int i = 0; i < 8; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (!((i == 0 && j == 6 && block_tables_out == block_tables) ||
+            (i == 1 && j == 7 && ref_counts_out == ref_counts)) &&
+          overlap(buf[i].p, buf[i].n, buf[j].p, buf[j].n))
+        return PA_ERR_INVALID_ARG;
+  CompactArgs a = {};
+  a.tables_out = block_tables_out;
+  a.refs_out = ref_counts_out;
+  a.tables = block_tables;
+  a.refs = ref_counts;
+  a.src_blocks = src_blocks;
+  a.dst_blocks = dst_blocks;
+  a.counts = counts;
+  a.name = static_cast<int32_t *>(workspace);
+  a.moved = a.name + num_blocks;
+  a.num_seqs = num_seqs;
+  a.width = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.err = error_word();
+  if (a.err == nullptr) return PA_ERR_CUDA;
+  return launch_cluster(compact_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
+                                                                                                    : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales, const int32_t *src_blocks,
+                               const int32_t *dst_blocks, const int32_t *counts, int max_pairs, int num_kv_heads,
+                               int head_dim, int block_size, int num_blocks, int element_bytes, void *stream) {
+  if (!k_cache || !v_cache || !src_blocks || !dst_blocks || !counts) return PA_ERR_INVALID_ARG;
+  if (max_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(src_blocks) || !aligned4(dst_blocks) ||
+      !aligned4(counts) || !aligned4(kv_scales))
+    return PA_ERR_INVALID_ARG;
+  if (element_bytes != 1 && element_bytes != 2) return PA_ERR_UNSUPPORTED;
+  if (!supported_block(block_size)) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 128 && !(head_dim == 64 && element_bytes == 2)) return PA_ERR_UNSUPPORTED;
+  if (kv_scales && element_bytes != 1) return PA_ERR_INVALID_ARG;
+  if ((int64_t)num_blocks * num_kv_heads * 2 >= (int64_t)1 << 31) return PA_ERR_INVALID_ARG;
+  if (max_pairs == 0) return PA_OK;
+  CopyArgs a = {};
+  a.cache[0] = static_cast<uint4 *>(k_cache);
+  a.cache[1] = static_cast<uint4 *>(v_cache);
+  a.kv_scales = kv_scales;
+  a.src = src_blocks;
+  a.dst = dst_blocks;
+  a.counts = counts;
+  a.chunks = (int64_t)num_kv_heads * block_size * head_dim * element_bytes / 16;
+  a.max_pairs = max_pairs;
+  a.num_blocks = num_blocks;
+  a.pieces = (int)((a.chunks + kPiece - 1) / kPiece);
+  a.scales_per_block = 2 * num_kv_heads;
+  a.err = error_word();
+  if (a.err == nullptr) return PA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PA_ERR_CUDA;
+  // how many pairs there are is known on the device alone: at most a wave of thread blocks
+  const int64_t tasks = (int64_t)max_pairs * 2 * a.pieces;
+  const unsigned ctas = (unsigned)std::min<int64_t>(tasks, (int64_t)sms * 8);
+  return launch_dependent(copy_pages_kernel, ctas, kPieceThreads, static_cast<cudaStream_t>(stream), a) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+}  // extern "C"

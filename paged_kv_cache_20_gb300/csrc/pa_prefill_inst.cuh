@@ -22,13 +22,13 @@ namespace {
 template <int D> constexpr int kRingK = D == 128 ? 3 : 4;
 template <int D> constexpr int kRingV = D == 128 ? 2 : 4;
 
-template <typename T, int D, bool PARTIAL, bool KV8, bool BS16, bool STATS = false>
+template <typename T, int D, bool PARTIAL, bool KV8, bool BS16, bool STATS = false, bool BSC = false>
 cudaError_t launch_prefill_t(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap,
                              const DecodeArgs &a, cudaStream_t st) {
   // the MMA operands are fp16 over an FP8 cache; the layout's sizes match either way
   using TM = typename TcPick<KV8, __half, T>::type;
   constexpr int kSmem = TcLayout<TM, D>::smem_bytes(kRingK<D>, kRingV<D>);
-  auto kern = paged_prefill_tc_kernel<T, D, kRingK<D>, kRingV<D>, PARTIAL, KV8, BS16, STATS>;
+  auto kern = paged_prefill_tc_kernel<T, D, kRingK<D>, kRingV<D>, PARTIAL, KV8, BS16, STATS, BSC>;
   static std::atomic<unsigned long long> opted{0};  // bit per device: smem opt-in done
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

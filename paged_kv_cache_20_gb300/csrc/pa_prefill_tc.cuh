@@ -51,6 +51,13 @@
 // release the stage to the MMA issuers; the MMAs run on fp16 operands.  Each KV
 // head's K scale goes into the score scale and its V scale into the output; a
 // bf16 q row is scaled into fp16 by a power of two that its score scale undoes.
+//
+// Block scales (BSC): the scales of each 16 (or 8) positions go into the softmax, as
+// TileScales of pa_decode.cuh describes.  Their K scale joins the row's score scale in
+// the multiply-add of the exponent, the log2 of their V scale its addend, so a chunk
+// costs no operation per score more than with one scale a head; the row sum is taken by
+// blocks, each times its 1 / V scale.  Every softmax warp looks its half chunk's scales
+// up a chunk ahead (table entry, then scales: two loads that depend on each other).
 #pragma once
 
 #include "pa_decode.cuh"
@@ -320,7 +327,9 @@ __device__ __forceinline__ void tc_widen_e4m3_rows(uint32_t st, int r0, int rows
 // block size (8 or 32) is read from the arguments.
 // STATS (single pass only): also write each row's -(m + log2 l), l the sum of its weights
 // before their rounding for P V, for a second pass that needs the weights themselves.
-template <typename T, int D, int NK, int NV, bool PARTIAL, bool KV8, bool BS16, bool STATS = false>
+// BSC: a block-scaled FP8 cache.
+template <typename T, int D, int NK, int NV, bool PARTIAL, bool KV8, bool BS16, bool STATS = false,
+          bool BSC = false>
 __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap,
@@ -336,6 +345,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
   constexpr int kOCols = D / 2;  // O columns per softmax warp
   static_assert(NK >= 2 && NV >= 2, "ring depth");
   static_assert(!(PARTIAL && STATS), "statistics of a single pass");
+  static_assert(!BSC || (KV8 && !STATS), "block scales: FP8 cache");
   static_assert(D == 64 || D == 128, "head_dim");
 
   extern __shared__ uint8_t smem_raw[];
@@ -360,6 +370,10 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
   __shared__ int s_lens[kLptMaxSeqs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
+  // BSC: per softmax warp, the scales of its half chunk by runs of 8 positions: K scale,
+  // log2 and reciprocal of the V scale
+  constexpr int kRuns = kTcChunk / 2 / 8;
+  __shared__ __align__(16) float4 s_scl[BSC ? kTcSoft : 1][BSC ? 2 : 1][kRuns];
 
   griddep_wait();
   griddep_launch_dependents();
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         // over an FP8 cache the scores carry the unit's K scale; a negative one
         // negates Q K^T as a negative softmax scale does
         uint32_t idS = kIdS;
-        if (KV8 && __ldg(a.k_scale + t.kvh) < 0.f) idS ^= 1u << 13;
+        if (KV8 && !BSC && __ldg(a.k_scale + t.kvh) < 0.f) idS ^= 1u << 13;
         for (int j = 0; ok && j < t.nch; ++j) {
           const int gg = g + j;
           ok = wait_all(&k_full[gg % NK], (gg / NK) & 1);
@@ -702,7 +716,10 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
     uint64_t rs2 = tc::f2pack(rs, rs);
     float vs_u = 1.f;  // the unit's V scale (FP8 cache)
     auto unit_scales = [&](const TcUnit &t, int e_row) {
-      if constexpr (KV8) {
+      if constexpr (BSC) {  // the blocks' scales follow chunk by chunk
+        rs = a.scale_log2 * ldexpf(1.f, e_row);
+        rs = rs > 0.f ? rs : 1e-30f;
+      } else if constexpr (KV8) {
         const float r = a.scale_log2 * fabsf(__ldg(a.k_scale + t.kvh)) * ldexpf(1.f, e_row);
         rs = r > 0.f ? r : 1e-30f;
         rs2 = tc::f2pack(rs, rs);
@@ -860,10 +877,34 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
     constexpr bool kExactSum = STATS && !Lay::kSplitP;
     long long pend_roff = -1;
 
+    // BSC: lanes 0 .. 7 look up the scales of this warp's positions 64 hc + 8 lane .. + 7 of
+    // a chunk: the block id two chunks ahead, its scales one ahead
+    [[maybe_unused]] int id_next = -1;
+    [[maybe_unused]] float2 scl_next = make_float2(1.f, 1.f);
+    auto block_at = [&](const TcUnit &t, int j) -> int {
+      const int tile = t.tb + j * kTcBlocks + 4 * hc + (lane >> 1);
+      if (lane >= kRuns || j >= t.nch || tile >= t.t_end) return -1;
+      const int blk = kBsz == 16 ? tile : kBsz == 32 ? tile >> 1 : 2 * tile + (lane & 1);
+      return blk < a.max_blocks_per_seq ? __ldg(a.block_tables + (size_t)t.tseq * a.max_blocks_per_seq + blk) : -1;
+    };
+    auto scales_at = [&](const TcUnit &t, int id) -> float2 {
+      if (id < 0 || id >= a.num_blocks) return make_float2(1.f, 1.f);
+      return __ldcg(a.kv_scales + (size_t)id * a.num_kv_heads + t.kvh);
+    };
+    auto first_scales = [&](const TcUnit &t) {
+      if constexpr (BSC) {
+        if (!t.valid) return;
+        const int id = block_at(t, 0);
+        id_next = block_at(t, 1);
+        scl_next = scales_at(t, id);
+      }
+    };
+
     int g = 0;   // chunks of this CTA so far (all units)
     int qn = 0;  // Q buffers written (without TMA)
     int e_cur = 0, e_next = 0;  // the row's q exponent (FP8 cache, bf16 q), this unit and next
     TcUnit cu = tc_unit(a, geo, 0, s_order, lens, lane, row, false, kBsz);
+    first_scales(cu);
     if (!a.q_tma && cu.valid && cu.nch > 0) {
       e_cur = write_q(cu);
       qn = 1;
@@ -876,6 +917,19 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         const int gg = g + j;
         const int b = gg % 3;
         const uint32_t ts = trow + Lay::kColS + kTcChunk * b + 64 * hc;  // this warp's columns
+        [[maybe_unused]] const float4 *scl = s_scl[BSC ? warp - kSoft0 : 0][BSC ? j & 1 : 0];
+        if constexpr (BSC) {
+          // this chunk's scales to the warp's rows (the slot's last readers, two chunks ago,
+          // are behind the barriers of the last one), the next chunk's loads on their way
+          if (lane < kRuns) {
+            const float sv1 = clamp_scale(scl_next.y);
+            s_scl[warp - kSoft0][j & 1][lane] =
+                make_float4(clamp_scale(scl_next.x), log2f(sv1), 1.f / sv1, 0.f);
+          }
+          scl_next = scales_at(cu, id_next);
+          id_next = block_at(cu, j + 2);
+          __syncwarp();
+        }
         bool w = mbar_wait_bounded(smem_u32(&s_full[b]), (gg / 3) & 1);
         w = __all_sync(0xffffffffu, w);
         if (!w) {
@@ -893,6 +947,21 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
 #pragma unroll
           for (int c = 0; c < 64; ++c) sv[c] = (c0 + c < lim_row) ? sv[c] : -INFINITY;
         }
+        float mx;
+        if constexpr (BSC) {
+          // by runs of one scale pair: 16 positions (8 where blocks may be that small)
+          constexpr int kRun = BS16 ? 16 : 8;
+          mx = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < 64 / kRun; ++r) {
+            const float *x = sv + r * kRun;
+            float m1 = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+            if constexpr (kRun == 16)
+              m1 = fmax3(m1, fmax3(fmax3(x[8], x[9], x[10]), fmax3(x[11], x[12], x[13]), x[14]), x[15]);
+            const float4 q = scl[r * (kRun / 8)];
+            mx = fmaxf(mx, fmaf(m1, rs * q.x, q.y));
+          }
+        } else {
         float pm[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) pm[i] = fmax3(sv[i], sv[8 + i], sv[16 + i]);  // 0..23
@@ -904,8 +973,9 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         // the eight chains and 56..63
         const float q0 = fmax3(pm[0], pm[1], sv[56]), q1 = fmax3(pm[2], pm[3], sv[57]);
         const float q2 = fmax3(pm[4], pm[5], sv[58]), q3 = fmax3(pm[6], pm[7], sv[59]);
-        float mx = fmax3(fmax3(q0, q1, sv[60]), fmax3(q2, q3, sv[61]), fmaxf(sv[62], sv[63]));
-        mx = exchange(mx * rs, true);  // the whole chunk's row maximum
+        mx = fmax3(fmax3(q0, q1, sv[60]), fmax3(q2, q3, sv[61]), fmaxf(sv[62], sv[63])) * rs;
+        }
+        mx = exchange(mx, true);  // the whole chunk's row maximum
         if (!ok) break;
         const float m_new = fmaxf(m_run, mx);
         const bool need = m_new > m_run + kTcRescale;  // false while both are -inf
@@ -919,7 +989,34 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         const uint64_t nmb2 = tc::f2pack(-mb, -mb);
         uint64_t ps2[2] = {0ull, 0ull};  // packed partial sums (+0.0f, +0.0f)
         uint64_t px2[2] = {0ull, 0ull};  // the same of the unrounded weights
-        {
+        if constexpr (BSC) {
+          constexpr int kRun = BS16 ? 16 : 8;
+          uint32_t hw[32];
+          float sum = 0.f;
+#pragma unroll
+          for (int r = 0; r < 64 / kRun; ++r) {
+            const float4 q = scl[r * (kRun / 8)];
+            const float ks = rs * q.x, add = q.y - mb;
+            const uint64_t ks2 = tc::f2pack(ks, ks), add2 = tc::f2pack(add, add);
+            uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < kRun / 2; ++i) {
+              const int e = r * (kRun / 2) + i;
+              float x0, x1;
+              tc::f2unpack(tc::ffma2(tc::f2pack(sv[2 * e], sv[2 * e + 1]), ks2, add2), x0, x1);
+              const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
+              hw[e] = Elt<TM>::from_f2(p0, p1);
+              // (the sum before rounding: a weight whose V scale is far below the largest
+              // is nothing beside it in 16 bits, and all of its share in the sum)
+              part[i & 1] = tc::fadd2(part[i & 1], tc::f2pack(p0, p1));
+            }
+            float a0, a1;
+            tc::f2unpack(tc::fadd2(part[0], part[1]), a0, a1);
+            sum = fmaf(a0 + a1, q.z, sum);
+          }
+          tc::st32u(ts, hw);
+          l += sum;
+        } else {
           // P over these S columns: hi words in the first 32, lo words (bf16) next
           uint32_t hw[32];
 #pragma unroll
@@ -953,7 +1050,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
             tc::st32u(ts + 32, hw);
           }
         }
-        {
+        if constexpr (!BSC) {
           float a0, a1, b0, b1;
           tc::f2unpack(ps2[0], a0, a1);
           tc::f2unpack(ps2[1], b0, b1);
@@ -1042,6 +1139,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
       // buffer is free once this unit's last S MMA has completed
       const TcUnit nu = tc_unit(a, geo, k + 1, s_order, lens, lane, row, false, kBsz);
       e_next = 0;
+      first_scales(nu);
       if (!a.q_tma && nu.valid && nu.nch > 0) {
         if (qn > 0) {
           bool w = mbar_wait_bounded(smem_u32(&q_free), (qn - 1) & 1);
