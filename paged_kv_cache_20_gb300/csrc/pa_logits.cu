@@ -11,14 +11,19 @@
 // each operation rounded to fp32 by itself, so that the largest y does not depend on how
 // they are fused.
 //
-// Bound by memory: a row is read once and written once.  A cluster of up to 8 thread blocks
-// holds one row in registers, each a slice of the vocabulary; a warp takes its part of the
-// row against its own maximum, and one cluster barrier exchanges every warp's maximum and
-// sum.  The counts of a slice stand in shared memory for all rows of the sequence, each
-// draft added before the next row, beside one bit an entry that says whether anything was
-// counted: the rows' elements read that bit, few of them a count.  A row of an odd
-// vocabulary starts anywhere: a thread's eight elements are aligned to 16 bytes of the row,
-// not to the slice, whose ragged ends go by single elements.
+// Bound by memory: a row is read once and written once.  A cluster of up to 16 thread blocks
+// holds one row in registers, as it was read, each a slice of the vocabulary; a warp takes
+// its part of the row against its own maximum, and one cluster barrier exchanges every
+// warp's maximum and sum.
+// The entries that anything was counted for are few and lie anywhere: a slice keeps their
+// counts in shared memory, a list of them in ascending order, and one bit an entry.  The
+// dense pass masks them out with the grammar's bits, two selects of registers an element;
+// the list's entries are gathered, adjusted and summed apart, a few a thread, and written over
+// the dense pass's zeros.  (With every element testing its own bit and adjusting in place,
+// 64 x 8 rows of 131,071 took 462 us: the slice of the common tokens kept its whole cluster
+// waiting.)  The list serves all rows of a sequence, each draft joining it before the next.
+// A row of an odd vocabulary starts anywhere: a thread's eight elements are aligned to 16
+// bytes of the row, not to the slice, whose ragged ends go by single elements.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -41,9 +46,10 @@ __device__ __forceinline__ void sync_cluster() {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;    // 8 up to kMostSlice * 8 entries; 16 is an opt-in
+constexpr int kMostSlice = 16384;  // entries of a thread block
 constexpr int kMaxBias = 1024;
-constexpr int kMaxVocab = 1 << 18;
+constexpr int kMaxVocab = kMostSlice * kMaxCluster;
 constexpr unsigned kPrompt = 1u << 31, kBias = 1u << 30;  // flags above an entry's count
 
 struct LogitArgs {
@@ -53,28 +59,48 @@ struct LogitArgs {
   const float *repetition, *presence, *frequency, *bias_values, *temperature;
   int num_seqs, rows, vocab, max_history, num_bias;
   int slice;      // entries of a thread block, a multiple of 32
+  int listed;     // room for a slice's counted entries
   int row_groups;  // row groups of a sequence, each of its own cluster
   int64_t out_stride, logits_stride, mask_seq, mask_row;
   unsigned *err;
 };
 
-template <typename T> struct In;
-template <> struct In<__half> {
-  static __device__ __forceinline__ float to_f(uint16_t v) { return __half2float(__ushort_as_half(v)); }
-};
-template <> struct In<__nv_bfloat16> {
-  static __device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-};
-
-// Eight elements from a 16-byte boundary.
+// Eight elements of a row as they are read.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
+struct Eight {  // fp16, bf16: pairs
+  uint32_t w[4];
+  static constexpr uint32_t kNegInf = Elt<T>::kMantBits == 10 ? 0xfc00u : 0xff80u;
+  __device__ __forceinline__ void load(const T *p) {
     const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  // elements i with bit i of `in` alone, -inf for the others
+  __device__ __forceinline__ void load_some(const T *p, unsigned in) {
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = in >> i & 1 ? reinterpret_cast<const uint16_t *>(p)[i] : kNegInf;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = h[2 * i] | h[2 * i + 1] << 16;
+  }
+  // -inf where bit i of `on` is clear
+  __device__ __forceinline__ void keep(unsigned on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = (on >> (2 * i) & 1 ? 0xffffu : 0u) | (on >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+      w[i] = (w[i] & m) | ((kNegInf | kNegInf << 16) & ~m);
+    }
+  }
+  __device__ __forceinline__ void no_nan() {  // NaN to -inf (the other operand is taken)
+    const uint32_t neg = kNegInf | kNegInf << 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (Elt<T>::kMantBits == 10)
+        asm("max.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(neg));
+      else
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(neg));
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = Elt<T>::to_f2(w[i]);
@@ -82,23 +108,38 @@ __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
       x[2 * i + 1] = f.y;
     }
   }
-}
+};
+template <>
+struct Eight<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float *p) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void load_some(const float *p, unsigned in) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = in >> i & 1 ? p[i] : -INFINITY;
+  }
+  __device__ __forceinline__ void keep(unsigned on) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = on >> i & 1 ? v[i] : -INFINITY;
+  }
+  __device__ __forceinline__ void no_nan() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaxf(v[i], -INFINITY);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ float load1(const T *p) {
   if constexpr (sizeof(T) == 4)
     return *p;
   else
-    return In<T>::to_f(*reinterpret_cast<const uint16_t *>(p));
-}
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-  } else {
-    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(Elt<T>::from_f2(x[0], x[1]), Elt<T>::from_f2(x[2], x[3]),
-                                                    Elt<T>::from_f2(x[4], x[5]), Elt<T>::from_f2(x[6], x[7])));
-  }
+    return Elt<T>::to_f2(*reinterpret_cast<const uint16_t *>(p)).x;
 }
 template <typename T>
 __device__ __forceinline__ void store1(T *p, float x) {
@@ -107,8 +148,25 @@ __device__ __forceinline__ void store1(T *p, float x) {
   else
     *reinterpret_cast<uint16_t *>(p) = Elt<T>::from_f(x);
 }
+// Eight values: whole groups at 16-byte boundaries, else the elements of `in`.
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&x)[8], bool whole, unsigned in) {
+  if (whole) {
+    if constexpr (sizeof(T) == 4) {
+      __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+      __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    } else {
+      __stcs(reinterpret_cast<uint4 *>(p), make_uint4(Elt<T>::from_f2(x[0], x[1]), Elt<T>::from_f2(x[2], x[3]),
+                                                      Elt<T>::from_f2(x[4], x[5]), Elt<T>::from_f2(x[6], x[7])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (in >> i & 1) store1(p + i, x[i]);
+  }
+}
 
-// 2^x, subnormal results to zero (a probability below 2^-126 of the warp's largest)
+// 2^x, subnormal results to zero (a probability below 2^-126 of the largest)
 __device__ __forceinline__ float ex2_flush(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -128,15 +186,28 @@ __device__ __forceinline__ unsigned bits8(int v0, int words, Load load) {
   return __funnelshift_r(a, b, s) & 0xffu;
 }
 
+// Elements of the group at v0 that lie in [lo, hi), as bits.
+__device__ __forceinline__ unsigned inside(int v0, int lo, int hi) {
+  unsigned in = 0xffu;
+  if (v0 < lo) in &= 0xffu << min(8, lo - v0);
+  if (v0 + 8 > hi) in &= v0 < hi ? 0xffu >> (v0 + 8 - hi) : 0u;
+  return in & 0xffu;
+}
+
+// Shared memory of a slice: counts [slice], bits [slice / 32], list [listed] (16 bits each),
+// adjusted values [listed], biases (id, value) [num_bias].
+__host__ __device__ __forceinline__ size_t slice_bytes(int slice, int listed, int num_bias) {
+  return (size_t)slice * 4 + slice / 8 + (size_t)listed * 2 + (size_t)listed * 4 + (size_t)num_bias * 8;
+}
+
 // VPT: groups of eight elements a thread holds.
 template <typename T, int VPT, bool PROBS>
-__global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitArgs a) {
   using O = typename std::conditional<PROBS, float, T>::type;
-  extern __shared__ unsigned s_words[];  // counts [slice], then one bit an entry [slice / 32]
+  extern __shared__ unsigned s_words[];
   __shared__ __align__(8) float2 s_stat[2][kMaxCluster * kWarps];
-  __shared__ int s_bias_id[kMaxBias];
-  __shared__ float s_bias_v[kMaxBias];
-  __shared__ int s_bias_n;
+  __shared__ int s_part[kWarps];
+  __shared__ int s_bias_n, s_listed;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -146,13 +217,19 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
   const int j0 = (int)((int64_t)a.rows * group / a.row_groups);
   const int j1 = (int)((int64_t)a.rows * (group + 1) / a.row_groups);
   const int lo = min(a.vocab, crank * a.slice), hi = min(a.vocab, lo + a.slice);
-  unsigned *count = s_words, *touched = s_words + a.slice;
-  const bool counted = a.history != nullptr || a.drafts != nullptr || a.num_bias > 0;
+  unsigned *count = s_words, *touched = count + a.slice;
+  float *adj = reinterpret_cast<float *>(touched + a.slice / 32);
+  float *bias_v = adj + a.listed;
+  int *bias_id = reinterpret_cast<int *>(bias_v + a.num_bias);
+  uint16_t *list = reinterpret_cast<uint16_t *>(bias_id + a.num_bias);
+  const bool counted = a.listed > 0;
 
-  auto touch = [&](int e) { atomicOr(touched + (e >> 5), 1u << (e & 31)); };
+  int entries = 0;  // on the list
   if (counted) {
     for (int i = threadIdx.x; i < a.slice + a.slice / 32; i += kThreads) s_words[i] = 0u;
+    if (threadIdx.x == 0) s_bias_n = 0;
     __syncthreads();
+    auto touch = [&](int e) { atomicOr(touched + (e >> 5), 1u << (e & 31)); };
     if (a.history != nullptr) {
       int n = __ldg(a.history_lens + seq);
       if ((n < 0 || n > a.max_history) && threadIdx.x == 0 && crank == 0) record_error(a.err, kErrCheck);
@@ -181,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
         }
       }
     // the slice's biases, in the list's order
-    if (warp == 0) {
+    if (warp == 0 && a.num_bias > 0) {
       int n = 0;
       for (int i0 = 0; i0 < a.num_bias; i0 += 32) {
         const int i = i0 + lane;
@@ -191,8 +268,8 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
         const unsigned who = __ballot_sync(0xffffffffu, mine);
         if (mine) {
           const int at = n + __popc(who & ((1u << lane) - 1u));
-          s_bias_id[at] = v - lo;
-          s_bias_v[at] = __ldg(a.bias_values + (int64_t)seq * a.num_bias + i);
+          bias_id[at] = v - lo;
+          bias_v[at] = __ldg(a.bias_values + (int64_t)seq * a.num_bias + i);
           atomicOr(count + (v - lo), kBias);
           touch(v - lo);
         }
@@ -200,6 +277,29 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
       }
       if (lane == 0) s_bias_n = n;
     }
+    __syncthreads();
+    // the list, ascending (its order is the order of the row's sums): each thread's words
+    const int words = a.slice / 32, per = (words + kThreads - 1) / kThreads;
+    const int w0 = min(words, (int)threadIdx.x * per), w1 = min(words, w0 + per);
+    int mine = 0;
+    for (int w = w0; w < w1; ++w) mine += __popc(touched[w]);
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += u;
+    }
+    if (lane == 31) s_part[warp] = before;
+    before -= mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_part[w];
+      entries += s_part[w];
+    }
+    for (int w = w0; w < w1; ++w)
+      for (unsigned b = touched[w]; b; b &= b - 1u) list[before++] = (uint16_t)(32 * w + __ffs(b) - 1);
+    if (threadIdx.x == 0) s_listed = entries;
     __syncthreads();
   }
   const float rep = a.repetition ? __ldg(a.repetition + seq) : 1.f;
@@ -217,9 +317,13 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
     if (c > 0u) x = __fsub_rn(__fsub_rn(x, __fmul_rn((float)c, freq)), pres);
     if (w & kBias) {
       for (int i = 0; i < s_bias_n; ++i)
-        if (s_bias_id[i] == e) x = __fadd_rn(x, s_bias_v[i]);
+        if (bias_id[i] == e) x = __fadd_rn(x, bias_v[i]);
     }
     return x;
+  };
+  // 2^((x - m) fac) against a maximum m; with an infinite m the entries that reach it
+  auto weight = [&](float x, float m) {
+    return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : ex2_flush((x - m) * fac);
   };
 
   for (int j = j0; j < j1; ++j) {
@@ -231,66 +335,85 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
     // groups of eight from the 16-byte boundary at or before the slice's first element
     const int shift = (int)((reinterpret_cast<uintptr_t>(in + lo) & (8 * sizeof(T) - 1)) / sizeof(T));
     const bool out8 = ((reinterpret_cast<uintptr_t>(out + lo - shift)) & 15u) == 0;
-    float x[VPT][8];
+    const int first = lo - shift + 8 * (int)threadIdx.x;  // of the thread's group 0
+    constexpr int kStep = 8 * kThreads;
+    Eight<T> x[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v0 = lo - shift + 8 * (k * kThreads + (int)threadIdx.x);
-      if (v0 >= lo && v0 + 8 <= hi) {
-        load8(in + v0, x[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = v0 + i >= lo && v0 + i < hi ? load1(in + v0 + i) : -INFINITY;
-      }
+      const int v0 = first + k * kStep;
+      if (v0 >= lo && v0 + 8 <= hi)
+        x[k].load(in + v0);
+      else
+        x[k].load_some(in + v0, inside(v0, lo, hi));
+    }
+    // the list's entries
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < entries; i += kThreads) {
+      const int e = list[i];
+      float y = adjust(load1(in + lo + e), e);
+      if (mask != nullptr && !(__ldg(mask + ((lo + e) >> 5)) >> ((lo + e) & 31) & 1)) y = -INFINITY;
+      if (PROBS) y = fmaxf(y, -INFINITY);  // NaN counts as -inf
+      adj[i] = y;
+      m = fmaxf(m, y);
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v0 = lo - shift + 8 * (k * kThreads + (int)threadIdx.x);
-      if (v0 >= hi) continue;
-      if (counted) {
-        const unsigned t = bits8(v0 - lo, a.slice / 32, [&](int w) { return touched[w]; });
-        if (t) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (t >> i & 1) x[k][i] = adjust(x[k][i], v0 - lo + i);
-        }
-      }
-      if (mask != nullptr) {
-        const unsigned on = bits8(v0, (a.vocab + 31) / 32, [&](int w) { return __ldg(mask + w); });
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = on >> i & 1 ? x[k][i] : -INFINITY;
+      const int v0 = first + k * kStep;
+      if (v0 < hi) {
+        unsigned on = 0xffu;
+        if (mask != nullptr) on = bits8(v0, (a.vocab + 31) / 32, [&](int w) { return __ldg(mask + w); });
+        if (counted) on &= ~bits8(v0 - lo, a.slice / 32, [&](int w) { return touched[w]; });
+        if (on != 0xffu) x[k].keep(on);
+        if (PROBS) x[k].no_nan();
       }
     }
+    float mul = 0.f, M = -INFINITY;
+    int best = INT_MAX;
     if constexpr (PROBS) {
-      float m = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < VPT; ++k)
+      for (int k = 0; k < VPT; ++k) {
+        float f[8];
+        x[k].get(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          // NaN counts as -inf, +inf as the largest finite number
-          x[k][i] = fminf(fmaxf(x[k][i], -INFINITY), FLT_MAX);
-          m = fmaxf(m, x[k][i]);
-        }
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, f[i]);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       float second = 0.f;  // the warp's sum, or the place of its first largest entry
       if (greedy) {
         int at = INT_MAX;
+        if (m != -INFINITY) {
 #pragma unroll
-        for (int k = VPT - 1; k >= 0; --k)
+          for (int k = VPT - 1; k >= 0; --k) {
+            float f[8];
+            x[k].get(f);
 #pragma unroll
-          for (int i = 7; i >= 0; --i)
-            if (x[k][i] == m) at = lo - shift + 8 * (k * kThreads + (int)threadIdx.x) + i;
-        if (m == -INFINITY) at = INT_MAX;
-        second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
-      } else {
-        const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[k][i] = ex2_flush((x[k][i] - mm) * fac);
-            second += x[k][i];
+            for (int i = 7; i >= 0; --i)
+              if (f[i] == m) at = first + k * kStep + i;
           }
+          for (int i = threadIdx.x; i < entries; i += kThreads)
+            if (adj[i] == m) at = min(at, lo + (int)list[i]);
+        }
+        second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
+      } else if (m != -INFINITY) {
+        for (int i = threadIdx.x; i < entries; i += kThreads) second += weight(adj[i], m);
+        if (m == INFINITY) {
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) {
+            float f[8];
+            x[k].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) second += f[i] == INFINITY ? 1.f : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) {
+            float f[8];
+            x[k].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) second += ex2_flush((f[i] - m) * fac);
+          }
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) second += __shfl_xor_sync(0xffffffffu, second, o);
       }
@@ -299,52 +422,71 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
       float2 *stat = s_stat[j & 1];
       if (lane < csize) dsmem_st_f32x2(dsmem_map(smem_u32(stat + crank * kWarps + warp), lane), m, second);
       sync_cluster();
-      float M = -INFINITY;
       for (int i = lane; i < csize * kWarps; i += 32) M = fmaxf(M, stat[i].x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float mul = 0.f;
-      int best = INT_MAX;
       if (greedy) {
         for (int i = lane; i < csize * kWarps; i += 32)
           if (stat[i].x == M) best = min(best, __float_as_int(stat[i].y));
         best = __reduce_min_sync(0xffffffffu, best);
       } else if (M != -INFINITY) {
         float sum = 0.f;
-        for (int i = lane; i < csize * kWarps; i += 32) sum += stat[i].y * ex2_flush((stat[i].x - M) * fac);
+        for (int i = lane; i < csize * kWarps; i += 32) sum += stat[i].y * weight(stat[i].x, M);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        mul = m == -INFINITY ? 0.f : ex2_flush((m - M) * fac) / sum;
+        mul = 1.f / sum;
       }
-#pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        const int v0 = lo - shift + 8 * (k * kThreads + (int)threadIdx.x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = greedy ? (v0 + i == best ? 1.f : 0.f) : x[k][i] * mul;
-      }
+    } else if (entries > 0) {
+      __syncthreads();  // in place: the list's logits are read before the row is written
     }
+    const bool none = PROBS && M == -INFINITY;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v0 = lo - shift + 8 * (k * kThreads + (int)threadIdx.x);
-      if (out8 && v0 >= lo && v0 + 8 <= hi) {
-        store8(out + v0, x[k]);
-      } else {
+      const int v0 = first + k * kStep;
+      float f[8];
+      x[k].get(f);
+      if constexpr (PROBS) {
+        if (greedy || none) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (v0 + i >= lo && v0 + i < hi) store1(out + v0 + i, x[k][i]);
-      }
-    }
-    if (a.drafts != nullptr && j + 1 < j1) {
-      if (!PROBS) __syncthreads();  // (else the cluster barrier: every count of this row is read)
-      if (threadIdx.x == 0) {
-        const int v = __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + j);
-        if (v >= a.vocab && crank == 0) record_error(a.err, kErrCheck);
-        if (v >= lo && v < hi) {
-          count[v - lo] += 1u;
-          touch(v - lo);
+          for (int i = 0; i < 8; ++i) f[i] = v0 + i == best ? 1.f : 0.f;
+        } else if (M == INFINITY) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = f[i] == INFINITY ? mul : 0.f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = ex2_flush((f[i] - M) * fac) * mul;
         }
       }
-      __syncthreads();
+      if (v0 < hi) {
+        const unsigned part = inside(v0, lo, hi);
+        store8(out + v0, f, out8 && part == 0xffu, part);
+      }
+    }
+    if (entries > 0 || a.drafts != nullptr) {
+      __syncthreads();  // the dense pass is written, and every bit and count of this row read
+      for (int i = threadIdx.x; i < entries; i += kThreads) {
+        const int v = lo + (int)list[i];
+        float y = adj[i];
+        if (PROBS) y = greedy || none ? (v == best ? 1.f : 0.f) : weight(y, M) * mul;
+        store1(out + v, y);
+      }
+      if (a.drafts != nullptr && j + 1 < j1) {
+        if (threadIdx.x == 0) {
+          const int v = __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + j);
+          if (v >= a.vocab && crank == 0) record_error(a.err, kErrCheck);
+          if (v >= lo && v < hi) {
+            const int e = v - lo;
+            count[e] += 1u;
+            if (!(touched[e >> 5] >> (e & 31) & 1)) {
+              touched[e >> 5] |= 1u << (e & 31);
+              list[s_listed] = (uint16_t)e;
+              s_listed += 1;
+            }
+          }
+        }
+        __syncthreads();
+        entries = s_listed;
+      }
     }
   }
   if (PROBS) sync_cluster();  // peers' shared memory stays until every pair has arrived
@@ -353,21 +495,23 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
 template <typename T, int VPT, bool PROBS>
 cudaError_t launch_one(const LogitArgs &a, int cluster, cudaStream_t st) {
   auto kern = adjust_logits_kernel<T, VPT, PROBS>;
-  const size_t smem = ((size_t)a.slice + a.slice / 32) * 4;
+  constexpr int kMost = std::min(VPT * kThreads * 8, kMostSlice);  // entries of this kernel's slices
   static std::atomic<unsigned long long> opted{0};  // bit per device: shared-memory opt-in done
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(opted.load(std::memory_order_acquire) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (VPT * kThreads * 8 + 32) / 32 * 33 * 4);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)slice_bytes(kMost, kMost, kMaxBias));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     opted.fetch_or(1ull << dev, std::memory_order_acq_rel);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.num_seqs * a.row_groups * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = a.listed > 0 ? slice_bytes(a.slice, a.listed, a.num_bias) : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -387,22 +531,24 @@ cudaError_t launch_slices(LogitArgs a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // slices of at most 16384 entries (two thread blocks an SM); smaller ones, and rows apart,
+  // slices of at most kMostSlice entries (two thread blocks an SM); smaller ones, and rows apart,
   // while the clusters do not fill the GPU twice
   int cluster = 1;
-  while (cluster < kMaxCluster && (a.vocab > 16384 * cluster ||
-                                   (a.vocab > 2048 * cluster && (int64_t)a.num_seqs * cluster < 2 * sms)))
+  while (a.vocab > kMostSlice * cluster ||
+         (cluster < 8 && a.vocab > 2048 * cluster && (int64_t)a.num_seqs * cluster < 2 * sms))
     cluster *= 2;
   const int64_t units = (int64_t)a.num_seqs * cluster;
   a.row_groups = (int)std::min<int64_t>(a.rows, std::max<int64_t>(1, (2 * sms + units - 1) / units));
   a.slice = ((a.vocab + cluster - 1) / cluster + 31) / 32 * 32;
   if ((int64_t)units * a.row_groups >= (int64_t)1 << 31) return cudaErrorInvalidConfiguration;
+  // every entry of a slice may be counted, and no more than there are ids
+  const int64_t ids = (int64_t)(a.history ? a.max_history : 0) + (a.drafts ? a.rows - 1 : 0) + a.num_bias;
+  a.listed = (int)std::min<int64_t>(ids, a.slice);
   const int groups = (a.slice + 7) / 8 + 1;  // of eight elements, with a ragged one
   const int vpt = (groups + kThreads - 1) / kThreads;
   if (vpt <= 1) return launch_one<T, 1, PROBS>(a, cluster, st);
   if (vpt <= 3) return launch_one<T, 3, PROBS>(a, cluster, st);
-  if (vpt <= 5) return launch_one<T, 5, PROBS>(a, cluster, st);
-  return launch_one<T, 9, PROBS>(a, cluster, st);
+  return launch_one<T, 5, PROBS>(a, cluster, st);
 }
 
 }  // namespace
@@ -479,7 +625,7 @@ extern "C" PA_API pa_status pa_adjust_logits(
   a.vocab = vocab;
   a.max_history = max_history;
   a.num_bias = num_bias;
-  a.slice = a.row_groups = 0;
+  a.slice = a.row_groups = a.listed = 0;
   a.out_stride = out_stride;
   a.logits_stride = logits_stride;
   a.mask_seq = mask_seq_stride;
