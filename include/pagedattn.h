@@ -617,8 +617,8 @@ PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales,
  *   y = -inf                   if bit v % 32 of the mask's word v / 32 is 0
  * each operation rounded to fp32.  probs == 0: out = y, of the logits' type.  probs != 0:
  * out fp32, softmax(y / temperature[i]); temperature <= 0 (or NaN): 1 at the largest y (the
- * lowest entry of equals), 0 elsewhere.  There a NaN counts as -inf and +inf as the largest
- * finite number; a row that its mask leaves empty is all zeros (pa_verify_drafts answers
+ * lowest entry of equals), 0 elsewhere.  There a NaN counts as -inf, infinite entries share
+ * the whole, and a row that its mask leaves empty is all zeros (pa_verify_drafts answers
  * -1 to it).
  *   logits       [num_seqs][rows][logits_stride], vocab used; fp16, bf16 or fp32 (dtype)
  *   out          [num_seqs][rows][out_stride]; may be logits itself where type and stride

@@ -12,18 +12,20 @@
 // they are fused.
 //
 // Bound by memory: a row is read once and written once.  A cluster of up to 16 thread blocks
-// holds one row in registers, as it was read, each a slice of the vocabulary; a warp takes
-// its part of the row against its own maximum, and one cluster barrier exchanges every
-// warp's maximum and sum.
-// The entries that anything was counted for are few and lie anywhere: a slice keeps their
-// counts in shared memory, a list of them in ascending order, and one bit an entry.  The
-// dense pass masks them out with the grammar's bits, two selects of registers an element;
-// the list's entries are gathered, adjusted and summed apart, a few a thread, and written over
-// the dense pass's zeros.  (With every element testing its own bit and adjusting in place,
-// 64 x 8 rows of 131,071 took 462 us: the slice of the common tokens kept its whole cluster
-// waiting.)  The list serves all rows of a sequence, each draft joining it before the next.
+// takes the rows of a sequence one after the other, each a slice of the vocabulary.  A bulk
+// copy brings the slice of the next row to shared memory while this one is worked on in
+// registers, as it was read; a warp takes its part of the row against its own maximum, and
+// one cluster barrier exchanges every warp's maximum and sum.
+// The entries that anything was counted for are few and lie anywhere: a slice keeps a list of
+// them in ascending order with their counts, and one bit an entry.  The dense pass masks
+// them out with the grammar's bits; the list's entries are gathered, adjusted and summed
+// apart, a few a thread, and written over the dense pass's zeros.  The list serves all rows
+// of a sequence, each draft joining it before the next.
+// 64 x 8 rows of 131,071 bf16 logits: 462 us with every element testing its own bit and
+// adjusting in place (the slice of the common tokens kept its cluster waiting), 212 us with
+// the list but rows loaded when their turn came and 45 instructions an element.
 // A row of an odd vocabulary starts anywhere: a thread's eight elements are aligned to 16
-// bytes of the row, not to the slice, whose ragged ends go by single elements.
+// bytes of the row, not to the slice, whose ragged ends are masked.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -43,6 +45,15 @@ __device__ __forceinline__ void sync_cluster() {
   __syncwarp();
   cluster_sync_all();
 }
+// The two halves of a cluster barrier that orders nothing: every thread block has started.
+__device__ __forceinline__ void cluster_started() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_all_started() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
@@ -50,6 +61,7 @@ constexpr int kMaxCluster = 16;    // 8 up to kMostSlice * 8 entries; 16 is an o
 constexpr int kMostSlice = 16384;  // entries of a thread block
 constexpr int kMaxBias = 1024;
 constexpr int kMaxVocab = kMostSlice * kMaxCluster;
+constexpr int kMostShared = 226 * 1024;  // dynamic, beside less than 1 KiB of static
 constexpr unsigned kPrompt = 1u << 31, kBias = 1u << 30;  // flags above an entry's count
 
 struct LogitArgs {
@@ -60,45 +72,61 @@ struct LogitArgs {
   int num_seqs, rows, vocab, max_history, num_bias;
   int slice;      // entries of a thread block, a multiple of 32
   int listed;     // room for a slice's counted entries
+  int wide;       // their counts may pass 14 bits
+  int late;       // no room for their adjusted values: worked out again where they are used
   int row_groups;  // row groups of a sequence, each of its own cluster
   int64_t out_stride, logits_stride, mask_seq, mask_row;
   unsigned *err;
 };
 
 // Eight elements of a row as they are read.
+// Bits 0-3 and 4-7 of `on` as the top bits of four bytes each (the shifted copies of four
+// bits do not meet); a byte permute then makes each a mask.
+__device__ __forceinline__ uint32_t top_bits(unsigned four) { return four * 0x10204080u; }
+// Bytes whose top bits they are: bytes 0, 0, 1, 1 (low pair) or 2, 2, 3, 3, each all its top bit.
+__device__ __forceinline__ uint32_t pair_mask(uint32_t top, bool high) {
+  uint32_t d;
+  if (high)
+    asm("prmt.b32 %0, %1, %1, 0xbbaa;" : "=r"(d) : "r"(top));
+  else
+    asm("prmt.b32 %0, %1, %1, 0x9988;" : "=r"(d) : "r"(top));
+  return d;
+}
+
 template <typename T>
 struct Eight {  // fp16, bf16: pairs
   uint32_t w[4];
-  static constexpr uint32_t kNegInf = Elt<T>::kMantBits == 10 ? 0xfc00u : 0xff80u;
-  __device__ __forceinline__ void load(const T *p) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+  static constexpr uint32_t kNegInf = Elt<T>::kMantBits == 10 ? 0xfc00fc00u : 0xff80ff80u;
+  __device__ __forceinline__ void load(uint32_t at) {
+    const uint4 v = lds128(at);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   }
-  // elements i with bit i of `in` alone, -inf for the others
-  __device__ __forceinline__ void load_some(const T *p, unsigned in) {
-    uint32_t h[8];
+  __device__ __forceinline__ void nothing() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = in >> i & 1 ? reinterpret_cast<const uint16_t *>(p)[i] : kNegInf;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = h[2 * i] | h[2 * i + 1] << 16;
+    for (int i = 0; i < 4; ++i) w[i] = kNegInf;
   }
   // -inf where bit i of `on` is clear
   __device__ __forceinline__ void keep(unsigned on) {
+    const uint32_t a = top_bits(on & 15u), b = top_bits(on >> 4);
+    const uint32_t m[4] = {pair_mask(a, false), pair_mask(a, true), pair_mask(b, false), pair_mask(b, true)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t m = (on >> (2 * i) & 1 ? 0xffffu : 0u) | (on >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
-      w[i] = (w[i] & m) | ((kNegInf | kNegInf << 16) & ~m);
-    }
+    for (int i = 0; i < 4; ++i) w[i] = (w[i] & m[i]) | (kNegInf & ~m[i]);
   }
-  __device__ __forceinline__ void no_nan() {  // NaN to -inf (the other operand is taken)
-    const uint32_t neg = kNegInf | kNegInf << 16;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // (of a NaN, the other)
+    uint32_t d;
+    if constexpr (Elt<T>::kMantBits == 10)
+      asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ __forceinline__ void no_nan() {  // NaN to -inf
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (Elt<T>::kMantBits == 10)
-        asm("max.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(neg));
-      else
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(neg));
-    }
+    for (int i = 0; i < 4; ++i) w[i] = max2(w[i], kNegInf);
+  }
+  __device__ __forceinline__ float largest() const {
+    const float2 f = Elt<T>::to_f2(max2(max2(w[0], w[1]), max2(w[2], w[3])));
+    return fmaxf(f.x, f.y);
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
@@ -112,13 +140,15 @@ struct Eight {  // fp16, bf16: pairs
 template <>
 struct Eight<float> {
   float v[8];
-  __device__ __forceinline__ void load(const float *p) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-  __device__ __forceinline__ void load_some(const float *p, unsigned in) {
+  __device__ __forceinline__ void load(uint32_t at) {
+    const uint4 a = lds128(at), b = lds128(at + 16);
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = in >> i & 1 ? p[i] : -INFINITY;
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+  }
+  __device__ __forceinline__ void nothing() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = -INFINITY;
   }
   __device__ __forceinline__ void keep(unsigned on) {
 #pragma unroll
@@ -127,6 +157,9 @@ struct Eight<float> {
   __device__ __forceinline__ void no_nan() {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaxf(v[i], -INFINITY);
+  }
+  __device__ __forceinline__ float largest() const {
+    return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
@@ -139,7 +172,7 @@ __device__ __forceinline__ float load1(const T *p) {
   if constexpr (sizeof(T) == 4)
     return *p;
   else
-    return Elt<T>::to_f2(*reinterpret_cast<const uint16_t *>(p)).x;
+    return Elt<T>::to_f2(*reinterpret_cast<const uint16_t *>(p)).x;  // (the pair's upper half zero)
 }
 template <typename T>
 __device__ __forceinline__ void store1(T *p, float x) {
@@ -177,15 +210,6 @@ __device__ __forceinline__ void dsmem_st_f32x2(uint32_t addr, float a, float b) 
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
-// Bits v0 .. v0 + 7 of a bit array of `words` words (bits outside: 0).
-template <typename Load>
-__device__ __forceinline__ unsigned bits8(int v0, int words, Load load) {
-  const int w = v0 >> 5, s = v0 & 31;  // (v0 may be negative: w = -1)
-  const unsigned a = w >= 0 && w < words ? load(w) : 0u;
-  const unsigned b = s > 24 && w + 1 < words ? load(w + 1) : 0u;
-  return __funnelshift_r(a, b, s) & 0xffu;
-}
-
 // Elements of the group at v0 that lie in [lo, hi), as bits.
 __device__ __forceinline__ unsigned inside(int v0, int lo, int hi) {
   unsigned in = 0xffu;
@@ -194,41 +218,87 @@ __device__ __forceinline__ unsigned inside(int v0, int lo, int hi) {
   return in & 0xffu;
 }
 
-// Shared memory of a slice: counts [slice], bits [slice / 32], list [listed] (16 bits each),
-// adjusted values [listed], biases (id, value) [num_bias].
-__host__ __device__ __forceinline__ size_t slice_bytes(int slice, int listed, int num_bias) {
-  return (size_t)slice * 4 + slice / 8 + (size_t)listed * 2 + (size_t)listed * 4 + (size_t)num_bias * 8;
+// Shared memory of a slice, in this order: a region that holds the counts while the list is
+// made (16 bits an entry, 32 where a history is too long for them) and the next row's logits
+// after that; the warps' statistics [2][cluster * kWarps]; bits [slice / 32] of counted entries, and of
+// a row's dense ones with a word before and behind; adjusted values (but where every entry of a
+// large slice may be listed, which leaves no room for them: late), counts and places of the
+// listed entries; biases (id, value).
+struct Room {
+  int region, stat, touched, on, adj, cnt, bias_v, bias_id, list, total;
+};
+__host__ __device__ inline Room room_of(int slice, int listed, int num_bias, int cluster, int elt, bool wide,
+                                        bool late) {
+  const int counts = listed > 0 ? slice * (wide ? 4 : 2) : 0;
+  const int stage = slice * elt + 64;  // (whole groups around the slice's ragged ends)
+  Room r;
+  int at = 0;
+  auto take = [&](int bytes) {
+    const int was = at;
+    at += (bytes + 15) / 16 * 16;
+    return was;
+  };
+  r.region = take(counts > stage ? counts : stage);
+  r.stat = take(2 * cluster * kWarps * 8);
+  r.touched = take(slice / 8);
+  r.on = take(slice / 8 + 8);
+  r.adj = take(late ? 0 : listed * 4);
+  r.cnt = take(listed * 4);
+  r.bias_v = take(num_bias * 4);
+  r.bias_id = take(num_bias * 4);
+  r.list = take(listed * 2);
+  r.total = at;
+  return r;
 }
+constexpr int kNarrowMost = (1 << 14) - 1;  // counts of 16 bits: 14 and two flags
 
 // VPT: groups of eight elements a thread holds.
 template <typename T, int VPT, bool PROBS>
 __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitArgs a) {
   using O = typename std::conditional<PROBS, float, T>::type;
-  extern __shared__ unsigned s_words[];
-  __shared__ __align__(8) float2 s_stat[2][kMaxCluster * kWarps];
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  __shared__ __align__(8) uint64_t s_bar;
   __shared__ int s_part[kWarps];
-  __shared__ int s_bias_n, s_listed;
+  __shared__ int s_bias_n;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&s_bar), 1);
+    fence_mbar_init();
+    s_bias_n = 0;
+  }
+  if (PROBS) cluster_started();
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int csize = (int)cluster_nctarank(), crank = (int)cluster_ctarank();
   const int unit = blockIdx.x / csize;
   const int seq = unit / a.row_groups, group = unit % a.row_groups;
   const int j0 = (int)((int64_t)a.rows * group / a.row_groups);
   const int j1 = (int)((int64_t)a.rows * (group + 1) / a.row_groups);
   const int lo = min(a.vocab, crank * a.slice), hi = min(a.vocab, lo + a.slice);
-  unsigned *count = s_words, *touched = count + a.slice;
-  float *adj = reinterpret_cast<float *>(touched + a.slice / 32);
-  float *bias_v = adj + a.listed;
-  int *bias_id = reinterpret_cast<int *>(bias_v + a.num_bias);
-  uint16_t *list = reinterpret_cast<uint16_t *>(bias_id + a.num_bias);
+  const Room room = room_of(a.slice, a.listed, a.num_bias, csize, (int)sizeof(T), a.wide != 0,
+                            a.late != 0);
+  unsigned *region = reinterpret_cast<unsigned *>(s_raw + room.region);
+  float2 *stats = reinterpret_cast<float2 *>(s_raw + room.stat);
+  unsigned *touched = reinterpret_cast<unsigned *>(s_raw + room.touched);
+  unsigned *on = reinterpret_cast<unsigned *>(s_raw + room.on) + 1;
+  float *adj = reinterpret_cast<float *>(s_raw + room.adj);
+  unsigned *cnt = reinterpret_cast<unsigned *>(s_raw + room.cnt);
+  float *bias_v = reinterpret_cast<float *>(s_raw + room.bias_v);
+  int *bias_id = reinterpret_cast<int *>(s_raw + room.bias_id);
+  uint16_t *list = reinterpret_cast<uint16_t *>(s_raw + room.list);
+  const int words = a.slice / 32;  // at most kThreads: a word a thread
   const bool counted = a.listed > 0;
 
   int entries = 0;  // on the list
   if (counted) {
-    for (int i = threadIdx.x; i < a.slice + a.slice / 32; i += kThreads) s_words[i] = 0u;
-    if (threadIdx.x == 0) s_bias_n = 0;
+    const int dense = a.wide ? a.slice : a.slice / 2;
+    for (int i = threadIdx.x; i < dense; i += kThreads) region[i] = 0u;
+    if (threadIdx.x < words) touched[threadIdx.x] = 0u;
     __syncthreads();
+    // an entry's count (in the low bits) or flag; narrow: two entries a word
+    const unsigned prompt_bit = a.wide ? kPrompt : kPrompt >> 16, bias_bit = a.wide ? kBias : kBias >> 16;
+    auto at_of = [&](int e) { return region + (a.wide ? e : e >> 1); };
+    auto up_of = [&](int e) { return a.wide ? 0 : (e & 1) * 16; };
     auto touch = [&](int e) { atomicOr(touched + (e >> 5), 1u << (e & 31)); };
     if (a.history != nullptr) {
       int n = __ldg(a.history_lens + seq);
@@ -241,11 +311,12 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         const int v = __ldg(ids + i);
         if (v >= a.vocab && crank == 0) record_error(a.err, kErrCheck);
         if (v >= lo && v < hi) {
+          const int e = v - lo;
           if (i < prompt)
-            atomicOr(count + (v - lo), kPrompt);
+            atomicOr(at_of(e), prompt_bit << up_of(e));
           else
-            atomicAdd(count + (v - lo), 1u);
-          touch(v - lo);
+            atomicAdd(at_of(e), 1u << up_of(e));
+          touch(e);
         }
       }
     }
@@ -253,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       for (int i = threadIdx.x; i < j0; i += kThreads) {
         const int v = __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + i);
         if (v >= lo && v < hi) {
-          atomicAdd(count + (v - lo), 1u);
+          atomicAdd(at_of(v - lo), 1u << up_of(v - lo));
           touch(v - lo);
         }
       }
@@ -270,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
           const int at = n + __popc(who & ((1u << lane) - 1u));
           bias_id[at] = v - lo;
           bias_v[at] = __ldg(a.bias_values + (int64_t)seq * a.num_bias + i);
-          atomicOr(count + (v - lo), kBias);
+          atomicOr(at_of(v - lo), bias_bit << up_of(v - lo));
           touch(v - lo);
         }
         n += __popc(who);
@@ -278,30 +349,33 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       if (lane == 0) s_bias_n = n;
     }
     __syncthreads();
-    // the list, ascending (its order is the order of the row's sums): each thread's words
-    const int words = a.slice / 32, per = (words + kThreads - 1) / kThreads;
-    const int w0 = min(words, (int)threadIdx.x * per), w1 = min(words, w0 + per);
-    int mine = 0;
-    for (int w = w0; w < w1; ++w) mine += __popc(touched[w]);
-    int before = mine;
+    // the list, ascending (its order is the order of the row's sums): a word a thread
+    const unsigned mine = threadIdx.x < words ? touched[threadIdx.x] : 0u;
+    int before = __popc(mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, before, o);
       if (lane >= o) before += u;
     }
     if (lane == 31) s_part[warp] = before;
-    before -= mine;
+    before -= __popc(mine);
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += s_part[w];
       entries += s_part[w];
     }
-    for (int w = w0; w < w1; ++w)
-      for (unsigned b = touched[w]; b; b &= b - 1u) list[before++] = (uint16_t)(32 * w + __ffs(b) - 1);
-    if (threadIdx.x == 0) s_listed = entries;
-    __syncthreads();
+    for (unsigned b = mine; b; b &= b - 1u) {
+      const int e = 32 * (int)threadIdx.x + __ffs(b) - 1;
+      unsigned c = *at_of(e) >> up_of(e);
+      if (!a.wide) c = (c & (bias_bit - 1u)) | (c & prompt_bit ? kPrompt : 0u) | (c & bias_bit ? kBias : 0u);
+      list[before] = (uint16_t)e;
+      cnt[before++] = c;
+    }
+    // the region is read: ordered before the copies that come to it
+    fence_proxy_async_smem();
   }
+  if (threadIdx.x < 2) on[threadIdx.x == 0 ? -1 : words] = 0u;
   const float rep = a.repetition ? __ldg(a.repetition + seq) : 1.f;
   const float pres = a.presence ? __ldg(a.presence + seq) : 0.f;
   const float freq = a.frequency ? __ldg(a.frequency + seq) : 0.f;
@@ -309,9 +383,53 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   const bool greedy = PROBS && !(temp > 0.f);
   // the exponent's factor; kept finite and above zero, so that -inf stays -inf
   const float fac = fminf(fmaxf(1.4426950408889634f / temp, 1e-38f), FLT_MAX);
+  const bool some = counted || a.mask != nullptr;  // any element may drop out of the dense pass
 
-  auto adjust = [&](float x, int e) {
-    const unsigned w = count[e];
+  // A row's slice in shared memory: byte addr - base of the region, base the 32-byte (fp32; else
+  // 16-byte) boundary at or before the slice.  Copied in whole 16-byte pieces, also around
+  // the slice's ends, but nothing outside the logits.
+  constexpr uintptr_t kAlign = 8 * sizeof(T);
+  const uintptr_t all0 = (reinterpret_cast<uintptr_t>(a.logits) + 15) & ~(uintptr_t)15;
+  const uintptr_t all1 =
+      reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) +
+                                  ((int64_t)a.num_seqs * a.rows - 1) * a.logits_stride + a.vocab) &
+      ~(uintptr_t)15;
+  auto row_of = [&](int j) {
+    return static_cast<const T *>(a.logits) + ((int64_t)seq * a.rows + j) * a.logits_stride;
+  };
+  auto copied = [&](const T *in, uintptr_t &c0, uintptr_t &c1) {
+    c0 = reinterpret_cast<uintptr_t>(in + lo) & ~(uintptr_t)15;
+    c1 = (reinterpret_cast<uintptr_t>(in + hi) + 15) & ~(uintptr_t)15;
+    c0 = c0 > all0 ? c0 : all0;
+    c1 = c1 < all1 ? c1 : all1;
+    if (c1 < c0 || lo >= hi) c1 = c0;
+  };
+  auto fetch = [&](int j) {  // (one thread)
+    const T *in = row_of(j);
+    uintptr_t c0, c1;
+    copied(in, c0, c1);
+    const uintptr_t base = reinterpret_cast<uintptr_t>(in + lo) & ~(kAlign - 1);
+    const uint32_t bar = smem_u32(&s_bar);
+    mbar_arrive_expect_tx(bar, (uint32_t)(c1 - c0));
+    if (c1 > c0)
+      bulk_load(smem_u32(region) + (uint32_t)(c0 - base), reinterpret_cast<const void *>(c0), (uint32_t)(c1 - c0),
+                bar);
+  };
+  auto mask_word = [&](int j) -> unsigned {
+    if (a.mask == nullptr || threadIdx.x >= words) return 0xffffffffu;
+    const int w = (lo >> 5) + (int)threadIdx.x;
+    return w < (a.vocab + 31) / 32
+               ? __ldg(reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + j * a.mask_row + w)
+               : 0u;
+  };
+  __syncthreads();  // the barrier, the list; the region is free
+  unsigned mw = 0u;
+  if (j0 < j1) {
+    if (threadIdx.x == 0) fetch(j0);
+    mw = mask_word(j0);
+  }
+
+  auto adjust = [&](float x, int e, unsigned w) {
     const unsigned c = w & (kBias - 1u);
     if (c > 0u || (w & kPrompt)) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
     if (c > 0u) x = __fsub_rn(__fsub_rn(x, __fmul_rn((float)c, freq)), pres);
@@ -326,57 +444,90 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : ex2_flush((x - m) * fac);
   };
 
+  if (PROBS) cluster_all_started();  // before the first pair goes to a peer
   for (int j = j0; j < j1; ++j) {
-    const int64_t row = (int64_t)seq * a.rows + j;
-    const T *in = static_cast<const T *>(a.logits) + row * a.logits_stride;
-    O *out = static_cast<O *>(a.out) + row * a.out_stride;
-    const unsigned *mask = a.mask ? reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + j * a.mask_row
-                                  : nullptr;
-    // groups of eight from the 16-byte boundary at or before the slice's first element
-    const int shift = (int)((reinterpret_cast<uintptr_t>(in + lo) & (8 * sizeof(T) - 1)) / sizeof(T));
+    const T *in = row_of(j);
+    O *out = static_cast<O *>(a.out) + ((int64_t)seq * a.rows + j) * a.out_stride;
+    // groups of eight from the boundary at or before the slice's first element
+    const int shift = (int)((reinterpret_cast<uintptr_t>(in + lo) & (kAlign - 1)) / sizeof(T));
     const bool out8 = ((reinterpret_cast<uintptr_t>(out + lo - shift)) & 15u) == 0;
     const int first = lo - shift + 8 * (int)threadIdx.x;  // of the thread's group 0
     constexpr int kStep = 8 * kThreads;
+    // the dense pass's bits: the mask's, but for the listed entries
+    if (some) {
+      if (threadIdx.x < words) on[threadIdx.x] = counted ? mw & ~touched[threadIdx.x] : mw;
+      __syncthreads();
+      if (j + 1 < j1) mw = mask_word(j + 1);
+    }
+    // the draft behind this row, and whether it is on the list already
+    int draft = -1;
+    bool listed = false;
+    if (counted && a.drafts != nullptr && j + 1 < j1) {
+      const int v = __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + j);
+      if (v >= a.vocab && crank == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
+      if (v >= lo && v < hi) {
+        draft = v - lo;
+        listed = touched[draft >> 5] >> (draft & 31) & 1;
+      }
+    }
+    if (!mbar_wait_bounded(smem_u32(&s_bar), (j - j0) & 1)) record_error(a.err, kErrTimeout);
+    {  // elements beside what was copied: the logits' own ragged ends
+      uintptr_t c0, c1;
+      copied(in, c0, c1);
+      const uintptr_t p0 = reinterpret_cast<uintptr_t>(in + lo), p1 = reinterpret_cast<uintptr_t>(in + hi);
+      if (lo < hi && (c0 > p0 || c1 < p1)) {
+        const int e = threadIdx.x < 16 ? (int)threadIdx.x : hi - lo - 1 - ((int)threadIdx.x - 16);
+        if (threadIdx.x < 32 && e >= 0 && e < hi - lo) {
+          const uintptr_t g = reinterpret_cast<uintptr_t>(in + lo + e);
+          if (g < c0 || g >= c1) reinterpret_cast<T *>(region)[shift + e] = in[lo + e];
+        }
+        __syncthreads();
+      }
+    }
+    const uint32_t base = smem_u32(region) + 8 * (uint32_t)sizeof(T) * threadIdx.x;
+    const uint32_t bit0 = 32u + (uint32_t)(8 * (int)threadIdx.x - shift);  // of group 0, from the word before `on`
     Eight<T> x[VPT];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int v0 = first + k * kStep;
-      if (v0 >= lo && v0 + 8 <= hi)
-        x[k].load(in + v0);
-      else
-        x[k].load_some(in + v0, inside(v0, lo, hi));
-    }
-    // the list's entries
     float m = -INFINITY;
-    for (int i = threadIdx.x; i < entries; i += kThreads) {
-      const int e = list[i];
-      float y = adjust(load1(in + lo + e), e);
-      if (mask != nullptr && !(__ldg(mask + ((lo + e) >> 5)) >> ((lo + e) & 31) & 1)) y = -INFINITY;
-      if (PROBS) y = fmaxf(y, -INFINITY);  // NaN counts as -inf
-      adj[i] = y;
-      m = fmaxf(m, y);
-    }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v0 = first + k * kStep;
       if (v0 < hi) {
-        unsigned on = 0xffu;
-        if (mask != nullptr) on = bits8(v0, (a.vocab + 31) / 32, [&](int w) { return __ldg(mask + w); });
-        if (counted) on &= ~bits8(v0 - lo, a.slice / 32, [&](int w) { return touched[w]; });
-        if (on != 0xffu) x[k].keep(on);
-        if (PROBS) x[k].no_nan();
+        unsigned keep = 0xffu;
+        x[k].load(base + k * (kStep * (uint32_t)sizeof(T)));
+        if (v0 < lo || v0 + 8 > hi) keep = inside(v0, lo, hi);
+        if (some) {
+          const uint32_t b = bit0 + k * kStep;
+          keep &= __funnelshift_r(on[(int)(b >> 5) - 1], on[b >> 5], b);
+        }
+        if (keep != 0xffu) x[k].keep(keep);
+        if constexpr (PROBS) {
+          x[k].no_nan();
+          m = fmaxf(m, x[k].largest());
+        }
+      } else {
+        x[k].nothing();
       }
     }
+    // the list's entries
+    auto adjusted = [&](int i) {
+      const int e = list[i];
+      float y = adjust(load1(reinterpret_cast<const T *>(region) + shift + e), e, cnt[i]);
+      if (a.mask != nullptr &&
+          !(__ldg(reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + j * a.mask_row + ((lo + e) >> 5)) >>
+                ((lo + e) & 31) & 1))
+        y = -INFINITY;
+      return PROBS ? fmaxf(y, -INFINITY) : y;  // NaN counts as -inf
+    };
+    for (int i = threadIdx.x; i < entries; i += kThreads) {
+      const float y = adjusted(i);
+      if (!a.late) adj[i] = y;
+      m = fmaxf(m, y);
+    }
+    auto listed_y = [&](int i) { return a.late ? adjusted(i) : adj[i]; };
+    fence_proxy_async_smem();  // the region is read: before the copy of the next row
     float mul = 0.f, M = -INFINITY;
     int best = INT_MAX;
     if constexpr (PROBS) {
-#pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        float f[8];
-        x[k].get(f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, f[i]);
-      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       float second = 0.f;  // the warp's sum, or the place of its first largest entry
@@ -392,11 +543,11 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
               if (f[i] == m) at = first + k * kStep + i;
           }
           for (int i = threadIdx.x; i < entries; i += kThreads)
-            if (adj[i] == m) at = min(at, lo + (int)list[i]);
+            if (listed_y(i) == m) at = min(at, lo + (int)list[i]);
         }
         second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
       } else if (m != -INFINITY) {
-        for (int i = threadIdx.x; i < entries; i += kThreads) second += weight(adj[i], m);
+        for (int i = threadIdx.x; i < entries; i += kThreads) second += weight(listed_y(i), m);
         if (m == INFINITY) {
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
@@ -408,20 +559,23 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         } else {
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
+            if (first + k * kStep >= hi) continue;
             float f[8];
             x[k].get(f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) second += ex2_flush((f[i] - m) * fac);
           }
         }
+        __syncwarp();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) second += __shfl_xor_sync(0xffffffffu, second, o);
       }
       // every warp's pair to every thread block of the cluster; rows take turns with two
       // buffers, so a pair is read before the row after next overwrites it
-      float2 *stat = s_stat[j & 1];
+      float2 *stat = stats + (j & 1) * csize * kWarps;
       if (lane < csize) dsmem_st_f32x2(dsmem_map(smem_u32(stat + crank * kWarps + warp), lane), m, second);
       sync_cluster();
+      if (threadIdx.x == 0 && j + 1 < j1 && !a.late) fetch(j + 1);
       for (int i = lane; i < csize * kWarps; i += 32) M = fmaxf(M, stat[i].x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -436,13 +590,15 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         mul = 1.f / sum;
       }
-    } else if (entries > 0) {
-      __syncthreads();  // in place: the list's logits are read before the row is written
+    } else {
+      __syncthreads();  // the region is read
+      if (threadIdx.x == 0 && j + 1 < j1 && !a.late) fetch(j + 1);
     }
     const bool none = PROBS && M == -INFINITY;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v0 = first + k * kStep;
+      if (v0 >= hi) continue;
       float f[8];
       x[k].get(f);
       if constexpr (PROBS) {
@@ -457,35 +613,30 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
           for (int i = 0; i < 8; ++i) f[i] = ex2_flush((f[i] - M) * fac) * mul;
         }
       }
-      if (v0 < hi) {
-        const unsigned part = inside(v0, lo, hi);
-        store8(out + v0, f, out8 && part == 0xffu, part);
-      }
+      const bool whole = v0 >= lo && v0 + 8 <= hi;
+      store8(out + v0, f, out8 && whole, whole ? 0xffu : inside(v0, lo, hi));
     }
-    if (entries > 0 || a.drafts != nullptr) {
-      __syncthreads();  // the dense pass is written, and every bit and count of this row read
+    if (counted) {
+      __syncthreads();  // the dense pass is written, every bit of this row read
       for (int i = threadIdx.x; i < entries; i += kThreads) {
-        const int v = lo + (int)list[i];
-        float y = adj[i];
-        if (PROBS) y = greedy || none ? (v == best ? 1.f : 0.f) : weight(y, M) * mul;
-        store1(out + v, y);
+        const int e = list[i];
+        float y = listed_y(i);
+        if (PROBS) y = greedy || none ? (lo + e == best ? 1.f : 0.f) : weight(y, M) * mul;
+        store1(out + lo + e, y);
+        if (draft == e) cnt[i] += 1u;
       }
-      if (a.drafts != nullptr && j + 1 < j1) {
-        if (threadIdx.x == 0) {
-          const int v = __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + j);
-          if (v >= a.vocab && crank == 0) record_error(a.err, kErrCheck);
-          if (v >= lo && v < hi) {
-            const int e = v - lo;
-            count[e] += 1u;
-            if (!(touched[e >> 5] >> (e & 31) & 1)) {
-              touched[e >> 5] |= 1u << (e & 31);
-              list[s_listed] = (uint16_t)e;
-              s_listed += 1;
-            }
-          }
+      if (draft >= 0 && !listed) {  // (its word's thread takes its bits of the next row)
+        if (threadIdx.x == draft >> 5) {
+          touched[threadIdx.x] |= 1u << (draft & 31);
+          list[entries] = (uint16_t)draft;
+          cnt[entries] = 1u;
         }
+        ++entries;
+      }
+      if (a.late && j + 1 < j1) {
+        fence_proxy_async_smem();
         __syncthreads();
-        entries = s_listed;
+        if (threadIdx.x == 0) fetch(j + 1);
       }
     }
   }
@@ -502,8 +653,9 @@ cudaError_t launch_one(const LogitArgs &a, int cluster, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(opted.load(std::memory_order_acquire) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)slice_bytes(kMost, kMost, kMaxBias));
+    // the most that any sizes of this kernel ask for
+    const int most = room_of(kMost, kMost, kMaxBias, kMaxCluster, sizeof(T), true, false).total;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, std::min(most, kMostShared));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     opted.fetch_or(1ull << dev, std::memory_order_acq_rel);
@@ -511,7 +663,7 @@ cudaError_t launch_one(const LogitArgs &a, int cluster, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.num_seqs * a.row_groups * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.listed > 0 ? slice_bytes(a.slice, a.listed, a.num_bias) : 0;
+  cfg.dynamicSmemBytes = room_of(a.slice, a.listed, a.num_bias, cluster, sizeof(T), a.wide != 0, a.late != 0).total;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -544,6 +696,8 @@ cudaError_t launch_slices(LogitArgs a, cudaStream_t st) {
   // every entry of a slice may be counted, and no more than there are ids
   const int64_t ids = (int64_t)(a.history ? a.max_history : 0) + (a.drafts ? a.rows - 1 : 0) + a.num_bias;
   a.listed = (int)std::min<int64_t>(ids, a.slice);
+  a.wide = ids > kNarrowMost;
+  a.late = room_of(a.slice, a.listed, a.num_bias, cluster, sizeof(T), a.wide, false).total > kMostShared;
   const int groups = (a.slice + 7) / 8 + 1;  // of eight elements, with a ragged one
   const int vpt = (groups + kThreads - 1) / kThreads;
   if (vpt <= 1) return launch_one<T, 1, PROBS>(a, cluster, st);
@@ -625,7 +779,7 @@ extern "C" PA_API pa_status pa_adjust_logits(
   a.vocab = vocab;
   a.max_history = max_history;
   a.num_bias = num_bias;
-  a.slice = a.row_groups = a.listed = 0;
+  a.slice = a.row_groups = a.listed = a.wide = a.late = 0;
   a.out_stride = out_stride;
   a.logits_stride = logits_stride;
   a.mask_seq = mask_seq_stride;

@@ -188,13 +188,15 @@ def adjusted(x, history, prompt, drafts, rep, pres, freq, bias, allowed):
 
 
 def probabilities(y, t):
-    y = np.where(np.isnan(y), -np.inf, np.minimum(y.astype(np.float64), np.finfo(np.float32).max))
+    y = np.where(np.isnan(y), -np.inf, y.astype(np.float64))
     if y.max() == -np.inf:
         return np.zeros_like(y)
     if not t > 0:
         p = np.zeros_like(y)
         p[int(np.argmax(y))] = 1
         return p
+    if y.max() == np.inf:
+        return (y == np.inf) / (y == np.inf).sum()
     with np.errstate(over="ignore"):
         p = np.exp((y - y.max()) / float(t))
     return p / p.sum()

@@ -159,7 +159,7 @@ def test_rows_that_the_mask_leaves_empty(pa, v):
 
 @pytest.mark.parametrize("v", [9, 50001])
 def test_special_logits(pa, v):
-    """NaN counts as -inf, +inf as the largest finite number; one at the lowest of equals."""
+    """NaN counts as -inf, infinite entries share the whole; one at the lowest of equals."""
     x = torch.full((5, 1, v), -2.0, device=DEV)
     x[0, 0, 3], x[0, 0, 5] = math.nan, 1.0
     x[1, 0, 2], x[1, 0, v - 1] = math.inf, math.inf
@@ -171,6 +171,11 @@ def test_special_logits(pa, v):
     assert p[1, 0, 2] == 0.5 and p[1, 0, v - 1] == 0.5
     assert bool((p[2] == 0).all())
     assert bool(((p[4] * v - 1).abs() < 2.0 ** -17).all())
+    # an infinite entry beside counted ones, in 16 bits too
+    for dt in (torch.float16, torch.float32):
+        q = pa.pa_adjust_logits(None, x.to(dt), history=i32([[2, 3, v - 1]] * 5), history_lens=i32([3] * 5),
+                                frequency=f32([0.5] * 5), probs=True).cpu()
+        assert q[1, 0, 2] == 0.5 and q[1, 0, v - 1] == 0.5 and float(q[1].sum()) == 1
     for t in (0.0, -1.0, math.nan):
         g = pa.pa_adjust_logits(None, x, temperature=f32([t] * 5), probs=True).cpu()
         assert [int(g[i, 0].argmax()) for i in (0, 1, 3, 4)] == [5, 2, v // 2, 0]
@@ -208,6 +213,36 @@ def test_rows_apart(pa):
         p = pa.pa_adjust_logits(None, wide.to(dt)[:, :, 1:v + 1], probs=True)
         want = wide.to(dt)[:, :, 1:v + 1].double().softmax(-1)
         assert float((p.double() / want - 1).abs().max()) < 2.0 ** -16
+
+
+@pytest.mark.parametrize("hist,v", [(16383, 40000), (16384, 40000), (40000, 9000), (70000, 262144)])
+def test_long_histories(pa, hist, v):
+    """Counts that pass 14 and 16 bits, every entry of a slice counted."""
+    rng = np.random.default_rng(hist)
+    c = Case(rng, 2, 3, v, "bf16", hist, 5, True)
+    c.hist[0, :hist // 2] = 7
+    c.hist[1] = np.arange(hist) % v
+    c.hl[:], c.pl[:] = hist, (0, hist // 3)
+    x = c.x.to(DEV)
+    got = pa.pa_adjust_logits(None, x, **c.args()).cpu()
+    for i in range(2):
+        for j in range(3):
+            assert torch.equal(got[i, j], torch.from_numpy(c.adjusted(i, j)).to(torch.bfloat16))
+    c.check_probs(pa.pa_adjust_logits(None, x, temperature=f32(c.temp), probs=True, **c.args()), c.temp.astype(np.float32))
+    assert pa.pa_device_error() == 0
+
+
+def test_drafts_on_the_list_and_off_it(pa):
+    """The same token drafted again and again, one of the history, one of the biases."""
+    rng = np.random.default_rng(8)
+    c = Case(rng, 3, 8, 33000, "fp16", 20, 4, False)
+    c.drafts[0] = 32999
+    c.drafts[1] = [c.hist[1, 0], 5, 5, -1, 5, c.bias[0][1, 0], 0]
+    c.drafts[2] = [0, 1, 2, 3, 31, 32, 33]
+    out = pa.pa_adjust_logits(None, c.x.to(DEV), **c.args()).cpu()
+    for i in range(3):
+        for j in range(8):
+            assert torch.equal(out[i, j], torch.from_numpy(c.adjusted(i, j)).to(torch.float16)), (i, j)
 
 
 def test_ids_outside_the_vocabulary(pa):
