@@ -11,19 +11,20 @@
 // each operation rounded to fp32 by itself, so that the largest y does not depend on how
 // they are fused.
 //
-// Bound by memory: a row is read once and written once.  A cluster of up to 16 thread blocks
-// takes the rows of a sequence one after the other, each a slice of the vocabulary.  A bulk
-// copy brings the slice of the next row to shared memory while this one is worked on in
-// registers, as it was read; a warp takes its part of the row against its own maximum, and
-// one cluster barrier exchanges every warp's maximum and sum.
+// Bound by memory: a row is read from it once and written once.  A cluster of up to 16 thread
+// blocks takes the rows of a sequence, each a slice of the vocabulary.  The softmax needs a
+// row's maximum and sum over all slices, and exchanging them row by row left the GPU waiting
+// (182 us for 64 x 8 rows of 131,071 bf16 logits, whether one thread block an SM held two
+// rows in registers or two held one each).  So a thread block first reads up to kBatch rows
+// and sums them, the cluster exchanges the sums of them all at once, and the rows are taken
+// again, last ones first: the last are in shared memory still, the others come from L2 (8
+// rows of every resident thread block are 80 MB of its 129).  Bulk copies bring the rows.
 // The entries that anything was counted for are few and lie anywhere: a slice keeps a list of
 // them in ascending order with their counts, and one bit an entry.  The dense pass masks
 // them out with the grammar's bits; the list's entries are gathered, adjusted and summed
 // apart, a few a thread, and written over the dense pass's zeros.  The list serves all rows
-// of a sequence, each draft joining it before the next.
-// 64 x 8 rows of 131,071 bf16 logits: 462 us with every element testing its own bit and
-// adjusting in place (the slice of the common tokens kept its cluster waiting), 212 us with
-// the list but rows loaded when their turn came and 45 instructions an element.
+// of a sequence: each draft joins it before the row behind it, and leaves it again on the
+// way back.  (With every element testing its own bit and adjusting in place: 462 us.)
 // A row of an odd vocabulary starts anywhere: a thread's eight elements are aligned to 16
 // bytes of the row, not to the slice, whose ragged ends are masked.
 #include <algorithm>
@@ -36,6 +37,7 @@
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_launch.h"
+#include "pa_tc.cuh"
 
 namespace pa {
 namespace {
@@ -45,35 +47,33 @@ __device__ __forceinline__ void sync_cluster() {
   __syncwarp();
   cluster_sync_all();
 }
-// The two halves of a cluster barrier that orders nothing: every thread block has started.
-__device__ __forceinline__ void cluster_started() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_all_started() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-}
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;    // 8 up to kMostSlice * 8 entries; 16 is an opt-in
 constexpr int kMostSlice = 16384;  // entries of a thread block
+constexpr int kMaxStages = 2;
+constexpr int kBatch = 8;  // rows that are summed before the exchange
 constexpr int kMaxBias = 1024;
 constexpr int kMaxVocab = kMostSlice * kMaxCluster;
 constexpr int kMostShared = 226 * 1024;  // dynamic, beside less than 1 KiB of static
 constexpr unsigned kPrompt = 1u << 31, kBias = 1u << 30;  // flags above an entry's count
 
+// How a slice's shared memory is used (Room, below).
+struct Modes {
+  int wide, shared, stages;
+};
+
 struct LogitArgs {
   void *out;
   const void *logits;
+  uint64_t logits_end;  // address past the last element
   const int32_t *history, *history_lens, *prompt_lens, *drafts, *bias_ids, *mask;
   const float *repetition, *presence, *frequency, *bias_values, *temperature;
   int num_seqs, rows, vocab, max_history, num_bias;
   int slice;      // entries of a thread block, a multiple of 32
   int listed;     // room for a slice's counted entries
-  int wide;       // their counts may pass 14 bits
-  int late;       // no room for their adjusted values: worked out again where they are used
+  Modes modes;    // wide: their counts may pass 14 bits
   int row_groups;  // row groups of a sequence, each of its own cluster
   int64_t out_stride, logits_stride, mask_seq, mask_row;
   unsigned *err;
@@ -100,10 +100,6 @@ struct Eight {  // fp16, bf16: pairs
   __device__ __forceinline__ void load(uint32_t at) {
     const uint4 v = lds128(at);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  }
-  __device__ __forceinline__ void nothing() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = kNegInf;
   }
   // -inf where bit i of `on` is clear
   __device__ __forceinline__ void keep(unsigned on) {
@@ -145,10 +141,6 @@ struct Eight<float> {
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
-  }
-  __device__ __forceinline__ void nothing() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = -INFINITY;
   }
   __device__ __forceinline__ void keep(unsigned on) {
 #pragma unroll
@@ -218,19 +210,18 @@ __device__ __forceinline__ unsigned inside(int v0, int lo, int hi) {
   return in & 0xffu;
 }
 
-// Shared memory of a slice, in this order: a region that holds the counts while the list is
-// made (16 bits an entry, 32 where a history is too long for them) and the next row's logits
-// after that; the warps' statistics [2][cluster * kWarps]; bits [slice / 32] of counted entries, and of
-// a row's dense ones with a word before and behind; adjusted values (but where every entry of a
-// large slice may be listed, which leaves no room for them: late), counts and places of the
-// listed entries; biases (id, value).
+// Shared memory of a slice: rows' logits, a stage each; the counts that the list is made from
+// (16 bits an entry, 32 where a history is too long for them), in the logits' place where
+// that leaves room for another thread block (shared); a batch's statistics by warp, and by thread
+// block; bits of counted entries, and of a row's mask and its dense elements, these with a
+// word before and behind; counts and places of the listed entries; biases (id,
+// value).
 struct Room {
-  int region, stat, touched, on, adj, cnt, bias_v, bias_id, list, total;
+  int stage, step, counts, warps, blocks, touched, mask, on, cnt, bias_v, bias_id, list, total;
 };
-__host__ __device__ inline Room room_of(int slice, int listed, int num_bias, int cluster, int elt, bool wide,
-                                        bool late) {
-  const int counts = listed > 0 ? slice * (wide ? 4 : 2) : 0;
-  const int stage = slice * elt + 64;  // (whole groups around the slice's ragged ends)
+__host__ __device__ inline Room room_of(int slice, int listed, int num_bias, int cluster, int elt, Modes m) {
+  const int counts = listed > 0 ? slice * (m.wide ? 4 : 2) : 0;
+  const int stage = (slice * elt + 64 + 15) / 16 * 16;  // (whole groups around the slice's ragged ends)
   Room r;
   int at = 0;
   auto take = [&](int bytes) {
@@ -238,11 +229,14 @@ __host__ __device__ inline Room room_of(int slice, int listed, int num_bias, int
     at += (bytes + 15) / 16 * 16;
     return was;
   };
-  r.region = take(counts > stage ? counts : stage);
-  r.stat = take(2 * cluster * kWarps * 8);
+  r.step = stage;
+  r.stage = r.counts = take(m.shared && counts > m.stages * stage ? counts : m.stages * stage);
+  if (!m.shared) r.counts = take(counts);
+  r.warps = take(kBatch * kWarps * 8);
+  r.blocks = take(kBatch * cluster * 8);
   r.touched = take(slice / 8);
+  r.mask = take(slice / 8);
   r.on = take(slice / 8 + 8);
-  r.adj = take(late ? 0 : listed * 4);
   r.cnt = take(listed * 4);
   r.bias_v = take(num_bias * 4);
   r.bias_id = take(num_bias * 4);
@@ -257,16 +251,17 @@ template <typename T, int VPT, bool PROBS>
 __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitArgs a) {
   using O = typename std::conditional<PROBS, float, T>::type;
   extern __shared__ __align__(16) uint8_t s_raw[];
-  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ __align__(8) uint64_t s_bar[kMaxStages];
   __shared__ int s_part[kWarps];
   __shared__ int s_bias_n;
+  __shared__ float2 s_row[kBatch];  // of a batch's rows: the maximum, and the weights' factor or the one's place
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&s_bar), 1);
+#pragma unroll
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(smem_u32(&s_bar[i]), 1);
     fence_mbar_init();
     s_bias_n = 0;
   }
-  if (PROBS) cluster_started();
   griddep_wait();
   griddep_launch_dependents();
   const int csize = (int)cluster_nctarank(), crank = (int)cluster_ctarank();
@@ -275,30 +270,72 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   const int j0 = (int)((int64_t)a.rows * group / a.row_groups);
   const int j1 = (int)((int64_t)a.rows * (group + 1) / a.row_groups);
   const int lo = min(a.vocab, crank * a.slice), hi = min(a.vocab, lo + a.slice);
-  const Room room = room_of(a.slice, a.listed, a.num_bias, csize, (int)sizeof(T), a.wide != 0,
-                            a.late != 0);
-  unsigned *region = reinterpret_cast<unsigned *>(s_raw + room.region);
-  float2 *stats = reinterpret_cast<float2 *>(s_raw + room.stat);
+  const Room room = room_of(a.slice, a.listed, a.num_bias, csize, (int)sizeof(T), a.modes);
+  const int stages = a.modes.stages;
+  float2 *warp_stats = reinterpret_cast<float2 *>(s_raw + room.warps);    // [kBatch][kWarps]
+  float2 *block_stats = reinterpret_cast<float2 *>(s_raw + room.blocks);  // [kBatch][cluster]
   unsigned *touched = reinterpret_cast<unsigned *>(s_raw + room.touched);
+  unsigned *mask = reinterpret_cast<unsigned *>(s_raw + room.mask);
   unsigned *on = reinterpret_cast<unsigned *>(s_raw + room.on) + 1;
-  float *adj = reinterpret_cast<float *>(s_raw + room.adj);
   unsigned *cnt = reinterpret_cast<unsigned *>(s_raw + room.cnt);
   float *bias_v = reinterpret_cast<float *>(s_raw + room.bias_v);
   int *bias_id = reinterpret_cast<int *>(s_raw + room.bias_id);
   uint16_t *list = reinterpret_cast<uint16_t *>(s_raw + room.list);
   const int words = a.slice / 32;  // at most kThreads: a word a thread
   const bool counted = a.listed > 0;
+  const bool some = counted || a.mask != nullptr;  // any element may drop out of the dense pass
 
-  int entries = 0;  // on the list
+  // ---- a row's slice in shared memory: byte addr - base of the stage, base the boundary of
+  // eight elements at or before the slice.  Copied in whole 16-byte pieces, also around
+  // the slice's ends, but nothing outside the logits.
+  constexpr uintptr_t kAlign = 8 * sizeof(T);
+  const uintptr_t all0 = (reinterpret_cast<uintptr_t>(a.logits) + 15) & ~(uintptr_t)15;
+  const uintptr_t all1 = (uintptr_t)a.logits_end & ~(uintptr_t)15;
+  auto row_of = [&](int j) {
+    return static_cast<const T *>(a.logits) + ((int64_t)seq * a.rows + j) * a.logits_stride;
+  };
+  auto copied = [&](const T *in, uintptr_t &c0, uintptr_t &c1) {
+    c0 = reinterpret_cast<uintptr_t>(in + lo) & ~(uintptr_t)15;
+    c1 = (reinterpret_cast<uintptr_t>(in + hi) + 15) & ~(uintptr_t)15;
+    c0 = c0 > all0 ? c0 : all0;
+    c1 = c1 < all1 ? c1 : all1;
+    if (c1 < c0 || lo >= hi) c1 = c0;
+  };
+  auto fetch = [&](int j, int slot) {  // (one thread)
+    const T *in = row_of(j);
+    uintptr_t c0, c1;
+    copied(in, c0, c1);
+    const uintptr_t base = reinterpret_cast<uintptr_t>(in + lo) & ~(kAlign - 1);
+    const uint32_t bar = smem_u32(&s_bar[slot]);
+    mbar_arrive_expect_tx(bar, (uint32_t)(c1 - c0));
+    if (c1 > c0)
+      bulk_load(smem_u32(s_raw + room.stage + slot * room.step) + (uint32_t)(c0 - base), reinterpret_cast<const void *>(c0), (uint32_t)(c1 - c0), bar);
+  };
+  auto mask_row = [&](int j) {
+    return reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + j * a.mask_row;
+  };
+  auto mask_word = [&](int j) -> unsigned {
+    if (a.mask == nullptr || threadIdx.x >= words) return 0xffffffffu;
+    const int w = (lo >> 5) + (int)threadIdx.x;
+    return w < (a.vocab + 31) / 32 ? __ldg(mask_row(j) + w) : 0u;
+  };
+  auto fetch_first = [&](int j) {  // (one thread) the first rows of those from j on
+    for (int i = 0; i < min(j1 - j, stages); ++i) fetch(j + i, i);
+  };
+  if (threadIdx.x == 0 && !a.modes.shared) fetch_first(j0);
+
+  // ---- the list of counted entries
+  int entries = 0;
   if (counted) {
-    const int dense = a.wide ? a.slice : a.slice / 2;
-    for (int i = threadIdx.x; i < dense; i += kThreads) region[i] = 0u;
+    unsigned *dense = reinterpret_cast<unsigned *>(s_raw + room.counts);
+    const bool wide = a.modes.wide != 0;
+    for (int i = threadIdx.x; i < (wide ? a.slice : a.slice / 2); i += kThreads) dense[i] = 0u;
     if (threadIdx.x < words) touched[threadIdx.x] = 0u;
     __syncthreads();
     // an entry's count (in the low bits) or flag; narrow: two entries a word
-    const unsigned prompt_bit = a.wide ? kPrompt : kPrompt >> 16, bias_bit = a.wide ? kBias : kBias >> 16;
-    auto at_of = [&](int e) { return region + (a.wide ? e : e >> 1); };
-    auto up_of = [&](int e) { return a.wide ? 0 : (e & 1) * 16; };
+    const unsigned prompt_bit = wide ? kPrompt : kPrompt >> 16, bias_bit = wide ? kBias : kBias >> 16;
+    auto at_of = [&](int e) { return dense + (wide ? e : e >> 1); };
+    auto up_of = [&](int e) { return wide ? 0 : (e & 1) * 16; };
     auto touch = [&](int e) { atomicOr(touched + (e >> 5), 1u << (e & 31)); };
     if (a.history != nullptr) {
       int n = __ldg(a.history_lens + seq);
@@ -349,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       if (lane == 0) s_bias_n = n;
     }
     __syncthreads();
-    // the list, ascending (its order is the order of the row's sums): a word a thread
+    // ascending (its order is the order of the row's sums): a word a thread
     const unsigned mine = threadIdx.x < words ? touched[threadIdx.x] : 0u;
     int before = __popc(mine);
 #pragma unroll
@@ -360,20 +397,23 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     if (lane == 31) s_part[warp] = before;
     before -= __popc(mine);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_part[w];
-      entries += s_part[w];
-    }
+    const int part = lane < kWarps ? s_part[lane] : 0;
+    before += (int)__reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)part : 0u);
+    entries = (int)__reduce_add_sync(0xffffffffu, (unsigned)part);
     for (unsigned b = mine; b; b &= b - 1u) {
       const int e = 32 * (int)threadIdx.x + __ffs(b) - 1;
       unsigned c = *at_of(e) >> up_of(e);
-      if (!a.wide) c = (c & (bias_bit - 1u)) | (c & prompt_bit ? kPrompt : 0u) | (c & bias_bit ? kBias : 0u);
+      if (!wide) c = (c & (bias_bit - 1u)) | (c & prompt_bit ? kPrompt : 0u) | (c & bias_bit ? kBias : 0u);
       list[before] = (uint16_t)e;
       cnt[before++] = c;
     }
-    // the region is read: ordered before the copies that come to it
-    fence_proxy_async_smem();
+    if (a.modes.shared) {  // the counts are read: their place may be copied to
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (threadIdx.x == 0) fetch_first(j0);
+    }
+  } else if (a.modes.shared && threadIdx.x == 0) {
+    fetch_first(j0);
   }
   if (threadIdx.x < 2) on[threadIdx.x == 0 ? -1 : words] = 0u;
   const float rep = a.repetition ? __ldg(a.repetition + seq) : 1.f;
@@ -383,51 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   const bool greedy = PROBS && !(temp > 0.f);
   // the exponent's factor; kept finite and above zero, so that -inf stays -inf
   const float fac = fminf(fmaxf(1.4426950408889634f / temp, 1e-38f), FLT_MAX);
-  const bool some = counted || a.mask != nullptr;  // any element may drop out of the dense pass
-
-  // A row's slice in shared memory: byte addr - base of the region, base the 32-byte (fp32; else
-  // 16-byte) boundary at or before the slice.  Copied in whole 16-byte pieces, also around
-  // the slice's ends, but nothing outside the logits.
-  constexpr uintptr_t kAlign = 8 * sizeof(T);
-  const uintptr_t all0 = (reinterpret_cast<uintptr_t>(a.logits) + 15) & ~(uintptr_t)15;
-  const uintptr_t all1 =
-      reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) +
-                                  ((int64_t)a.num_seqs * a.rows - 1) * a.logits_stride + a.vocab) &
-      ~(uintptr_t)15;
-  auto row_of = [&](int j) {
-    return static_cast<const T *>(a.logits) + ((int64_t)seq * a.rows + j) * a.logits_stride;
-  };
-  auto copied = [&](const T *in, uintptr_t &c0, uintptr_t &c1) {
-    c0 = reinterpret_cast<uintptr_t>(in + lo) & ~(uintptr_t)15;
-    c1 = (reinterpret_cast<uintptr_t>(in + hi) + 15) & ~(uintptr_t)15;
-    c0 = c0 > all0 ? c0 : all0;
-    c1 = c1 < all1 ? c1 : all1;
-    if (c1 < c0 || lo >= hi) c1 = c0;
-  };
-  auto fetch = [&](int j) {  // (one thread)
-    const T *in = row_of(j);
-    uintptr_t c0, c1;
-    copied(in, c0, c1);
-    const uintptr_t base = reinterpret_cast<uintptr_t>(in + lo) & ~(kAlign - 1);
-    const uint32_t bar = smem_u32(&s_bar);
-    mbar_arrive_expect_tx(bar, (uint32_t)(c1 - c0));
-    if (c1 > c0)
-      bulk_load(smem_u32(region) + (uint32_t)(c0 - base), reinterpret_cast<const void *>(c0), (uint32_t)(c1 - c0),
-                bar);
-  };
-  auto mask_word = [&](int j) -> unsigned {
-    if (a.mask == nullptr || threadIdx.x >= words) return 0xffffffffu;
-    const int w = (lo >> 5) + (int)threadIdx.x;
-    return w < (a.vocab + 31) / 32
-               ? __ldg(reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + j * a.mask_row + w)
-               : 0u;
-  };
-  __syncthreads();  // the barrier, the list; the region is free
-  unsigned mw = 0u;
-  if (j0 < j1) {
-    if (threadIdx.x == 0) fetch(j0);
-    mw = mask_word(j0);
-  }
+  __syncthreads();  // the copies' barriers and the list
 
   auto adjust = [&](float x, int e, unsigned w) {
     const unsigned c = w & (kBias - 1u);
@@ -443,219 +439,372 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   auto weight = [&](float x, float m) {
     return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : ex2_flush((x - m) * fac);
   };
+  // the same of a pair, m finite
+  const uint64_t fac2 = tc::f2pack(fac, fac);
+  auto weight2 = [&](float x0, float x1, uint64_t neg_m2, float &w0, float &w1) {
+    float z0, z1;
+    tc::f2unpack(tc::fmul2(tc::fadd2(tc::f2pack(x0, x1), neg_m2), fac2), z0, z1);
+    w0 = ex2_flush(z0);
+    w1 = ex2_flush(z1);
+  };
 
-  if (PROBS) cluster_all_started();  // before the first pair goes to a peer
-  for (int j = j0; j < j1; ++j) {
-    const T *in = row_of(j);
-    O *out = static_cast<O *>(a.out) + ((int64_t)seq * a.rows + j) * a.out_stride;
-    // groups of eight from the boundary at or before the slice's first element
-    const int shift = (int)((reinterpret_cast<uintptr_t>(in + lo) & (kAlign - 1)) / sizeof(T));
-    const bool out8 = ((reinterpret_cast<uintptr_t>(out + lo - shift)) & 15u) == 0;
-    const int first = lo - shift + 8 * (int)threadIdx.x;  // of the thread's group 0
-    constexpr int kStep = 8 * kThreads;
-    // the dense pass's bits: the mask's, but for the listed entries
-    if (some) {
-      if (threadIdx.x < words) on[threadIdx.x] = counted ? mw & ~touched[threadIdx.x] : mw;
-      __syncthreads();
-      if (j + 1 < j1) mw = mask_word(j + 1);
-    }
-    // the draft behind this row, and whether it is on the list already
-    int draft = -1;
-    bool listed = false;
-    if (counted && a.drafts != nullptr && j + 1 < j1) {
-      const int v = __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + j);
-      if (v >= a.vocab && crank == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
-      if (v >= lo && v < hi) {
-        draft = v - lo;
-        listed = touched[draft >> 5] >> (draft & 31) & 1;
+  // ---- the rows, one after the other in either direction
+  constexpr int kStep = 8 * kThreads;
+  unsigned phase = 0u;  // of each stage's next copy, a bit a stage
+  auto draft_of = [&](int j) {  // the draft behind row j
+    return a.drafts != nullptr && j >= j0 && j + 1 < j1 ? __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + j) : -1;
+  };
+  // A draft joins the list: `known` says that it is on it.  (Read by others behind the row's
+  // barrier.)
+  auto join = [&](int e, bool known) {
+    if (known) {
+      for (int i = threadIdx.x; i < entries; i += kThreads)
+        if (list[i] == e) cnt[i] += 1u;
+    } else {
+      if (threadIdx.x == e >> 5) {
+        touched[threadIdx.x] |= 1u << (e & 31);
+        list[entries] = (uint16_t)e;
+        cnt[entries] = 1u;
       }
+      ++entries;
     }
-    if (!mbar_wait_bounded(smem_u32(&s_bar), (j - j0) & 1)) record_error(a.err, kErrTimeout);
-    {  // elements beside what was copied: the logits' own ragged ends
+  };
+  // ... and leaves it: the last one that joined first.  One that brought its entry along left
+  // it at the list's end with a count of one and no flag, which nothing else can have there.
+  // (`last`, read before a barrier: it is such a one.)
+  auto leave = [&](int e, bool last) {
+    if (last) {
+      if (threadIdx.x == e >> 5) touched[threadIdx.x] &= ~(1u << (e & 31));
+      --entries;
+    } else {
+      for (int i = threadIdx.x; i < entries; i += kThreads)
+        if (list[i] == e) cnt[i] -= 1u;
+    }
+  };
+  struct Row {
+    const T *in;
+    const uint8_t *stage;
+    int shift, first;  // groups of eight start `shift` before the slice; the thread's group 0
+  };
+  // Row j in stage `slot` (landed: it is there already), with mask word mw: to be worked on.
+  auto begin = [&](int j, int slot, bool landed, unsigned mw) {
+    Row r;
+    r.in = row_of(j);
+    uint8_t *stage = s_raw + room.stage + slot * room.step;
+    r.stage = stage;
+    r.shift = (int)((reinterpret_cast<uintptr_t>(r.in + lo) & (kAlign - 1)) / sizeof(T));
+    r.first = lo - r.shift + 8 * (int)threadIdx.x;
+    if (some && threadIdx.x < words) {
+      on[threadIdx.x] = counted ? mw & ~touched[threadIdx.x] : mw;
+      mask[threadIdx.x] = mw;
+    }
+    // (one warp asks the copies' barrier: all of them asking take the scheduler's turns)
+    if (!landed) {
+      if (warp == 0 && !mbar_wait_bounded(smem_u32(&s_bar[slot]), phase >> slot & 1u)) record_error(a.err, kErrTimeout);
+      phase ^= 1u << slot;
+    }
+    __syncthreads();
+    // elements beside what was copied: the logits' own ragged ends
+    const uintptr_t p0 = reinterpret_cast<uintptr_t>(r.in + lo), p1 = reinterpret_cast<uintptr_t>(r.in + hi);
+    if (!landed && lo < hi && (p0 < all0 || p1 > all1)) {
       uintptr_t c0, c1;
-      copied(in, c0, c1);
-      const uintptr_t p0 = reinterpret_cast<uintptr_t>(in + lo), p1 = reinterpret_cast<uintptr_t>(in + hi);
-      if (lo < hi && (c0 > p0 || c1 < p1)) {
-        const int e = threadIdx.x < 16 ? (int)threadIdx.x : hi - lo - 1 - ((int)threadIdx.x - 16);
-        if (threadIdx.x < 32 && e >= 0 && e < hi - lo) {
-          const uintptr_t g = reinterpret_cast<uintptr_t>(in + lo + e);
-          if (g < c0 || g >= c1) reinterpret_cast<T *>(region)[shift + e] = in[lo + e];
-        }
-        __syncthreads();
+      copied(r.in, c0, c1);
+      const int e = threadIdx.x < 16 ? (int)threadIdx.x : hi - lo - 1 - ((int)threadIdx.x - 16);
+      if (threadIdx.x < 32 && e >= 0 && e < hi - lo) {
+        const uintptr_t g = reinterpret_cast<uintptr_t>(r.in + lo + e);
+        if (g < c0 || g >= c1) reinterpret_cast<T *>(stage)[r.shift + e] = r.in[lo + e];
       }
+      fence_proxy_async_smem();  // before the copy of another row
+      __syncthreads();
     }
-    const uint32_t base = smem_u32(region) + 8 * (uint32_t)sizeof(T) * threadIdx.x;
-    const uint32_t bit0 = 32u + (uint32_t)(8 * (int)threadIdx.x - shift);  // of group 0, from the word before `on`
-    Eight<T> x[VPT];
-    float m = -INFINITY;
+    return r;
+  };
+  // The thread's group k of a row (it starts before the slice's end), -inf for what is not dense.
+  auto dense = [&](const Row &r, int k) {
+    const int v0 = r.first + k * kStep;
+    Eight<T> x;
+    x.load(smem_u32(r.stage) + (8 * threadIdx.x + k * kStep) * (uint32_t)sizeof(T));
+    unsigned keep = 0xffu;
+    if (v0 < lo || v0 + 8 > hi) keep = inside(v0, lo, hi);
+    if (some) {
+      const uint32_t b = 32u + (uint32_t)(v0 - lo);  // from the word before `on`
+      keep &= __funnelshift_r(on[(int)(b >> 5) - 1], on[b >> 5], b);
+    }
+    if (keep != 0xffu) x.keep(keep);
+    if (PROBS) x.no_nan();
+    return x;
+  };
+  // Entry i of the list, adjusted.
+  auto adjusted = [&](const Row &r, int i) {
+    const int e = list[i];
+    float y = adjust(load1(reinterpret_cast<const T *>(r.stage) + r.shift + e), e, cnt[i]);
+    if (a.mask != nullptr && !(mask[e >> 5] >> (e & 31) & 1u)) y = -INFINITY;
+    return PROBS ? fmaxf(y, -INFINITY) : y;  // NaN counts as -inf
+  };
+  auto put = [&](const Row &r, O *out, int k, const float (&f)[8]) {
+    const int v0 = r.first + k * kStep;
+    const bool whole = v0 >= lo && v0 + 8 <= hi;
+    store8(out + v0, f, whole && (reinterpret_cast<uintptr_t>(out + v0) & 15u) == 0, whole ? 0xffu : inside(v0, lo, hi));
+  };
+  // The stage of a row that was worked on: another row may come.
+  auto release = [&](int slot, int next, bool more) {
+    __syncthreads();
+    if (threadIdx.x == 0 && more) fetch(next, slot);
+  };
+
+  if constexpr (!PROBS) {
+    unsigned mw = mask_word(j0);
+    int behind = draft_of(j0), slot = 0;
+    for (int j = j0; j < j1; ++j) {
+      const Row r = begin(j, slot, false, mw);
+      if (j + 1 < j1) mw = mask_word(j + 1);
+      const int e = behind >= lo && behind < hi ? behind - lo : -1;
+      if (behind >= a.vocab && crank == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
+      const bool known = e >= 0 && (touched[e >> 5] >> (e & 31) & 1u);
+      behind = draft_of(j + 1);
+      O *out = static_cast<O *>(a.out) + ((int64_t)seq * a.rows + j) * a.out_stride;
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int v0 = first + k * kStep;
-      if (v0 < hi) {
-        unsigned keep = 0xffu;
-        x[k].load(base + k * (kStep * (uint32_t)sizeof(T)));
-        if (v0 < lo || v0 + 8 > hi) keep = inside(v0, lo, hi);
-        if (some) {
-          const uint32_t b = bit0 + k * kStep;
-          keep &= __funnelshift_r(on[(int)(b >> 5) - 1], on[b >> 5], b);
-        }
-        if (keep != 0xffu) x[k].keep(keep);
-        if constexpr (PROBS) {
-          x[k].no_nan();
-          m = fmaxf(m, x[k].largest());
-        }
-      } else {
-        x[k].nothing();
+      for (int k = 0; k < VPT; ++k) {
+        if (r.first + k * kStep >= hi) continue;
+        float f[8];
+        dense(r, k).get(f);
+        put(r, out, k, f);
       }
+      if (counted) {
+        __syncthreads();  // the dense pass is written
+        for (int i = threadIdx.x; i < entries; i += kThreads) store1(out + lo + list[i], adjusted(r, i));
+      }
+      release(slot, j + stages, j + stages < j1);
+      if (e >= 0) join(e, known);
+      if (++slot == stages) slot = 0;
     }
-    // the list's entries
-    auto adjusted = [&](int i) {
-      const int e = list[i];
-      float y = adjust(load1(reinterpret_cast<const T *>(region) + shift + e), e, cnt[i]);
-      if (a.mask != nullptr &&
-          !(__ldg(reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + j * a.mask_row + ((lo + e) >> 5)) >>
-                ((lo + e) & 31) & 1))
-        y = -INFINITY;
-      return PROBS ? fmaxf(y, -INFINITY) : y;  // NaN counts as -inf
-    };
-    for (int i = threadIdx.x; i < entries; i += kThreads) {
-      const float y = adjusted(i);
-      if (!a.late) adj[i] = y;
-      m = fmaxf(m, y);
-    }
-    auto listed_y = [&](int i) { return a.late ? adjusted(i) : adj[i]; };
-    fence_proxy_async_smem();  // the region is read: before the copy of the next row
-    float mul = 0.f, M = -INFINITY;
-    int best = INT_MAX;
-    if constexpr (PROBS) {
+  } else {
+    for (int b0 = j0; b0 < j1; b0 += kBatch) {
+      const int b1 = min(j1, b0 + kBatch);
+      // ---- forward: every warp's maximum of its part of a row, and the sum against it (or the
+      // place of its first largest entry)
+      if (b0 > j0) {
+        if (threadIdx.x == 0)
+          for (int i = 0; i < min(b1 - b0, stages); ++i) fetch(b0 + i, i);
+      }
+      unsigned mw = mask_word(b0);
+      int behind = draft_of(b0), slot = 0;
+      for (int j = b0; j < b1; ++j) {
+        const Row r = begin(j, slot, false, mw);
+        if (j + 1 < b1) mw = mask_word(j + 1);
+        const int e = behind >= lo && behind < hi ? behind - lo : -1;
+        if (behind >= a.vocab && crank == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
+        const bool known = e >= 0 && (touched[e >> 5] >> (e & 31) & 1u);
+        behind = draft_of(j + 1);
+        // (16-bit groups are kept for the second look, fp32 ones are taken again)
+        constexpr bool kKeep = sizeof(T) == 2;
+        Eight<T> x[kKeep ? VPT : 1];
+        float m = -INFINITY;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float second = 0.f;  // the warp's sum, or the place of its first largest entry
-      if (greedy) {
+        for (int k = 0; k < VPT; ++k)
+          if (r.first + k * kStep < hi) {
+            const Eight<T> g = dense(r, k);
+            m = fmaxf(m, g.largest());
+            if constexpr (kKeep) x[k] = g;
+          }
+        auto again = [&](int k, float (&f)[8]) {
+          if constexpr (kKeep)
+            x[k].get(f);
+          else
+            dense(r, k).get(f);
+        };
+        // the list's entries, as they come: their maximum, sum and place
+        float ms = -INFINITY, ss = 0.f;
         int at = INT_MAX;
-        if (m != -INFINITY) {
-#pragma unroll
-          for (int k = VPT - 1; k >= 0; --k) {
-            float f[8];
-            x[k].get(f);
-#pragma unroll
-            for (int i = 7; i >= 0; --i)
-              if (f[i] == m) at = first + k * kStep + i;
-          }
-          for (int i = threadIdx.x; i < entries; i += kThreads)
-            if (listed_y(i) == m) at = min(at, lo + (int)list[i]);
-        }
-        second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
-      } else if (m != -INFINITY) {
-        for (int i = threadIdx.x; i < entries; i += kThreads) second += weight(listed_y(i), m);
-        if (m == INFINITY) {
-#pragma unroll
-          for (int k = 0; k < VPT; ++k) {
-            float f[8];
-            x[k].get(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) second += f[i] == INFINITY ? 1.f : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < VPT; ++k) {
-            if (first + k * kStep >= hi) continue;
-            float f[8];
-            x[k].get(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) second += ex2_flush((f[i] - m) * fac);
+        for (int i = threadIdx.x; i < entries; i += kThreads) {
+          const float y = adjusted(r, i);
+          if (y == -INFINITY) continue;
+          if (greedy) {
+            const int v = lo + (int)list[i];
+            if (y > ms || (y == ms && v < at)) at = v;
+            ms = fmaxf(ms, y);
+          } else if (y > ms) {
+            ss = ss * weight(ms, y) + 1.f;
+            ms = y;
+          } else {
+            ss += weight(y, ms);
           }
         }
         __syncwarp();
+        m = fmaxf(m, ms);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) second += __shfl_xor_sync(0xffffffffu, second, o);
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float second = 0.f;
+        if (greedy) {
+          if (ms != m || m == -INFINITY) at = INT_MAX;
+          if (m != -INFINITY) {
+#pragma unroll
+            for (int k = VPT - 1; k >= 0; --k) {
+              if (r.first + k * kStep >= hi) continue;
+              float f[8];
+              again(k, f);
+#pragma unroll
+              for (int i = 7; i >= 0; --i)
+                if (f[i] == m) at = min(at, r.first + k * kStep + i);
+            }
+          }
+          __syncwarp();
+          second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
+        } else {
+          if (ms != -INFINITY) second = ss * weight(ms, m);
+          if (m == INFINITY) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+              if (r.first + k * kStep >= hi) continue;
+              float f[8];
+              again(k, f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) second += f[i] == INFINITY ? 1.f : 0.f;
+            }
+          } else if (m != -INFINITY) {
+            const uint64_t neg = tc::f2pack(-m, -m);
+            uint64_t sum = 0ull;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+              if (r.first + k * kStep >= hi) continue;
+              float f[8];
+              again(k, f);
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                float w0, w1;
+                weight2(f[i], f[i + 1], neg, w0, w1);
+                sum = tc::fadd2(sum, tc::f2pack(w0, w1));
+              }
+            }
+            float s0, s1;
+            tc::f2unpack(sum, s0, s1);
+            second += s0 + s1;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) second += __shfl_xor_sync(0xffffffffu, second, o);
+        }
+        if (lane == 0) warp_stats[(j - b0) * kWarps + warp] = make_float2(m, second);
+        release(slot, j + stages, j + stages < b1);
+        if (e >= 0 && j + 1 < b1) join(e, known);
+        if (++slot == stages) slot = 0;
       }
-      // every warp's pair to every thread block of the cluster; rows take turns with two
-      // buffers, so a pair is read before the row after next overwrites it
-      float2 *stat = stats + (j & 1) * csize * kWarps;
-      if (lane < csize) dsmem_st_f32x2(dsmem_map(smem_u32(stat + crank * kWarps + warp), lane), m, second);
-      sync_cluster();
-      if (threadIdx.x == 0 && j + 1 < j1 && !a.late) fetch(j + 1);
-      for (int i = lane; i < csize * kWarps; i += 32) M = fmaxf(M, stat[i].x);
+      // ---- the sums of all slices: warp r takes row r of the batch
+      // of a warp's 32 pairs: the maximum, and the sum against it (or the least place of it)
+      auto merged = [&](float2 v, float &M) {
+        M = v.x;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      if (greedy) {
-        for (int i = lane; i < csize * kWarps; i += 32)
-          if (stat[i].x == M) best = min(best, __float_as_int(stat[i].y));
-        best = __reduce_min_sync(0xffffffffu, best);
-      } else if (M != -INFINITY) {
-        float sum = 0.f;
-        for (int i = lane; i < csize * kWarps; i += 32) sum += stat[i].y * weight(stat[i].x, M);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (greedy)
+          return __int_as_float(__reduce_min_sync(0xffffffffu, v.x == M ? __float_as_int(v.y) : INT_MAX));
+        float sum = M == -INFINITY ? 0.f : v.y * weight(v.x, M);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        mul = 1.f / sum;
+        return sum;
+      };
+      const float2 none = make_float2(-INFINITY, greedy ? __int_as_float(INT_MAX) : 0.f);
+      static_assert(kBatch <= kWarps && kWarps <= 32 && kMaxCluster <= 32, "a warp a row");
+      // (the peers run, and have read the last batch's)
+      sync_cluster();
+      const bool mine = warp < b1 - b0;
+      if (mine) {
+        float m;
+        const float second = merged(lane < kWarps ? warp_stats[warp * kWarps + lane] : none, m);
+        if (lane < csize) dsmem_st_f32x2(dsmem_map(smem_u32(block_stats + warp * csize + crank), lane), m, second);
       }
-    } else {
-      __syncthreads();  // the region is read
-      if (threadIdx.x == 0 && j + 1 < j1 && !a.late) fetch(j + 1);
-    }
-    const bool none = PROBS && M == -INFINITY;
+      sync_cluster();
+      if (mine) {
+        float m;
+        const float second = merged(lane < csize ? block_stats[warp * csize + lane] : none, m);
+        if (lane == 0)
+          s_row[warp] = make_float2(m, !greedy ? 1.f / second : m == -INFINITY ? __int_as_float(INT_MAX) : second);
+      }
+      // ---- back: the last rows are in their stages still (s_row is read behind a row's barrier)
+      mw = mask_word(b1 - 1);
+      behind = draft_of(b1 - 2);
+      for (int j = b1 - 1; j >= b0; --j) {
+        slot = (j - b0) % stages;
+        const Row r = begin(j, slot, j >= b1 - stages, mw);
+        if (j > b0) mw = mask_word(j - 1);
+        const int before = behind;  // the draft before this row, which leaves with it
+        behind = draft_of(j - 2);
+        const float2 stat = s_row[j - b0];
+        const float M = stat.x, mul = stat.y;
+        const int best = greedy ? __float_as_int(stat.y) : INT_MAX;
+        float *out = static_cast<float *>(a.out) + ((int64_t)seq * a.rows + j) * a.out_stride;
+        if (!greedy && fabsf(M) != INFINITY) {
+          const uint64_t neg = tc::f2pack(-M, -M), mul2 = tc::f2pack(mul, mul);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int v0 = first + k * kStep;
-      if (v0 >= hi) continue;
-      float f[8];
-      x[k].get(f);
-      if constexpr (PROBS) {
-        if (greedy || none) {
+          for (int k = 0; k < VPT; ++k) {
+            if (r.first + k * kStep >= hi) continue;
+            float f[8];
+            dense(r, k).get(f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = v0 + i == best ? 1.f : 0.f;
-        } else if (M == INFINITY) {
+            for (int i = 0; i < 8; i += 2) {
+              float w0, w1;
+              weight2(f[i], f[i + 1], neg, w0, w1);
+              tc::f2unpack(tc::fmul2(tc::f2pack(w0, w1), mul2), f[i], f[i + 1]);
+            }
+            put(r, out, k, f);
+          }
+        } else {  // one, none, or the infinite ones
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = f[i] == INFINITY ? mul : 0.f;
-        } else {
+          for (int k = 0; k < VPT; ++k) {
+            const int v0 = r.first + k * kStep;
+            if (v0 >= hi) continue;
+            float f[8];
+            dense(r, k).get(f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = ex2_flush((f[i] - M) * fac) * mul;
+            for (int i = 0; i < 8; ++i)
+              f[i] = M == INFINITY && !greedy ? (f[i] == INFINITY ? mul : 0.f) : v0 + i == best ? 1.f : 0.f;
+            put(r, out, k, f);
+          }
         }
-      }
-      const bool whole = v0 >= lo && v0 + 8 <= hi;
-      store8(out + v0, f, out8 && whole, whole ? 0xffu : inside(v0, lo, hi));
-    }
-    if (counted) {
-      __syncthreads();  // the dense pass is written, every bit of this row read
-      for (int i = threadIdx.x; i < entries; i += kThreads) {
-        const int e = list[i];
-        float y = listed_y(i);
-        if (PROBS) y = greedy || none ? (lo + e == best ? 1.f : 0.f) : weight(y, M) * mul;
-        store1(out + lo + e, y);
-        if (draft == e) cnt[i] += 1u;
-      }
-      if (draft >= 0 && !listed) {  // (its word's thread takes its bits of the next row)
-        if (threadIdx.x == draft >> 5) {
-          touched[threadIdx.x] |= 1u << (draft & 31);
-          list[entries] = (uint16_t)draft;
-          cnt[entries] = 1u;
+        if (counted) {
+          __syncthreads();  // the dense pass is written
+          for (int i = threadIdx.x; i < entries; i += kThreads) {
+            const int e = list[i];
+            float p;
+            if (greedy || M == -INFINITY)
+              p = lo + e == best ? 1.f : 0.f;
+            else
+              p = weight(adjusted(r, i), M) * mul;
+            store1(out + lo + e, p);
+          }
         }
-        ++entries;
+        const int e = j > b0 && before >= lo && before < hi ? before - lo : -1;
+        const bool last = e >= 0 && list[entries - 1] == e && cnt[entries - 1] == 1u;
+        release(slot, j - stages, j - stages >= b0);
+        if (e >= 0) leave(e, last);
       }
-      if (a.late && j + 1 < j1) {
-        fence_proxy_async_smem();
+      // the next batch stands behind this one's drafts
+      if (b1 < j1) {
+        for (int j = b0; j < b1; ++j) {
+          const int v = draft_of(j);
+          if (v >= lo && v < hi) {
+            const int e = v - lo;
+            __syncthreads();
+            const bool known = touched[e >> 5] >> (e & 31) & 1u;
+            __syncthreads();
+            join(e, known);
+          }
+        }
         __syncthreads();
-        if (threadIdx.x == 0) fetch(j + 1);
       }
     }
   }
-  if (PROBS) sync_cluster();  // peers' shared memory stays until every pair has arrived
 }
 
 template <typename T, int VPT, bool PROBS>
 cudaError_t launch_one(const LogitArgs &a, int cluster, cudaStream_t st) {
   auto kern = adjust_logits_kernel<T, VPT, PROBS>;
-  constexpr int kMost = std::min(VPT * kThreads * 8, kMostSlice);  // entries of this kernel's slices
   static std::atomic<unsigned long long> opted{0};  // bit per device: shared-memory opt-in done
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(opted.load(std::memory_order_acquire) & (1ull << dev))) {
-    // the most that any sizes of this kernel ask for
-    const int most = room_of(kMost, kMost, kMaxBias, kMaxCluster, sizeof(T), true, false).total;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, std::min(most, kMostShared));
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     opted.fetch_or(1ull << dev, std::memory_order_acq_rel);
@@ -663,7 +812,7 @@ cudaError_t launch_one(const LogitArgs &a, int cluster, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.num_seqs * a.row_groups * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = room_of(a.slice, a.listed, a.num_bias, cluster, sizeof(T), a.wide != 0, a.late != 0).total;
+  cfg.dynamicSmemBytes = room_of(a.slice, a.listed, a.num_bias, cluster, sizeof(T), a.modes).total;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -683,8 +832,8 @@ cudaError_t launch_slices(LogitArgs a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // slices of at most kMostSlice entries (two thread blocks an SM); smaller ones, and rows apart,
-  // while the clusters do not fill the GPU twice
+  // slices of at most kMostSlice entries ; smaller ones, and rows apart, while the
+  // clusters do not fill the GPU twice
   int cluster = 1;
   while (a.vocab > kMostSlice * cluster ||
          (cluster < 8 && a.vocab > 2048 * cluster && (int64_t)a.num_seqs * cluster < 2 * sms))
@@ -696,8 +845,20 @@ cudaError_t launch_slices(LogitArgs a, cudaStream_t st) {
   // every entry of a slice may be counted, and no more than there are ids
   const int64_t ids = (int64_t)(a.history ? a.max_history : 0) + (a.drafts ? a.rows - 1 : 0) + a.num_bias;
   a.listed = (int)std::min<int64_t>(ids, a.slice);
-  a.wide = ids > kNarrowMost;
-  a.late = room_of(a.slice, a.listed, a.num_bias, cluster, sizeof(T), a.wide, false).total > kMostShared;
+  const int wide = ids > kNarrowMost;
+  const int per = (a.rows + a.row_groups - 1) / a.row_groups;
+  // two thread blocks an SM where they fit, with a row ahead if that fits too
+  const struct {
+    Modes m;
+    int most;
+  } choice[] = {{{wide, 0, 2}, kMostShared / 2}, {{wide, 1, 2}, kMostShared / 2}, {{wide, 0, 1}, kMostShared / 2},
+                {{wide, 1, 1}, kMostShared / 2}, {{wide, 0, 2}, kMostShared},     {{wide, 1, 2}, kMostShared},
+                {{wide, 1, 1}, kMostShared}};
+  for (const auto &c : choice) {
+    if (c.m.stages > 1 && per == 1) continue;  // (a thread block has no second row)
+    a.modes = c.m;
+    if (room_of(a.slice, a.listed, a.num_bias, cluster, sizeof(T), c.m).total <= c.most) break;
+  }
   const int groups = (a.slice + 7) / 8 + 1;  // of eight elements, with a ragged one
   const int vpt = (groups + kThreads - 1) / kThreads;
   if (vpt <= 1) return launch_one<T, 1, PROBS>(a, cluster, st);
@@ -763,6 +924,7 @@ extern "C" PA_API pa_status pa_adjust_logits(
   LogitArgs a;
   a.out = out;
   a.logits = logits;
+  a.logits_end = reinterpret_cast<uintptr_t>(logits) + in_n;
   a.history = max_history > 0 ? history : nullptr;
   a.history_lens = history_lens;
   a.prompt_lens = prompt_lens;
@@ -779,7 +941,8 @@ extern "C" PA_API pa_status pa_adjust_logits(
   a.vocab = vocab;
   a.max_history = max_history;
   a.num_bias = num_bias;
-  a.slice = a.row_groups = a.listed = a.wide = a.late = 0;
+  a.slice = a.row_groups = a.listed = 0;
+  a.modes = Modes{0, 0, 1};
   a.out_stride = out_stride;
   a.logits_stride = logits_stride;
   a.mask_seq = mask_seq_stride;

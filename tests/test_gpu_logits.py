@@ -101,7 +101,8 @@ CASES = [(1, 1, 1, "fp32", 1, 1, False), (3, 2, 7, "fp16", 5, 0, True), (2, 1, 3
          (1, 1, 32000, "fp16", 700, 4, False), (2, 9, 32001, "bf16", 5000, 300, True),
          (2, 2, 131071, "bf16", 4096, 1024, True), (1, 2, 131071, "fp32", 64, 3, True),
          (1, 1, 262144, "fp16", 10, 0, True), (1, 2, 262143, "fp32", 10, 7, False), (200, 2, 777, "fp16", 3, 1, True),
-         (300, 1, 20000, "bf16", 50, 0, False)]
+         (300, 1, 20000, "bf16", 50, 0, False), (3, 21, 40001, "bf16", 40, 6, True), (40, 19, 3001, "fp32", 30, 3, True),
+         (70, 17, 131070, "fp16", 100, 5, False)]
 
 
 @pytest.mark.parametrize("n,r,v,dtype,hist,bias,masked", CASES)
@@ -233,16 +234,24 @@ def test_long_histories(pa, hist, v):
 
 
 def test_drafts_on_the_list_and_off_it(pa):
-    """The same token drafted again and again, one of the history, one of the biases."""
+    """The same token drafted again and again, one of the history, one of the biases; more
+    rows than are summed at once."""
     rng = np.random.default_rng(8)
-    c = Case(rng, 3, 8, 33000, "fp16", 20, 4, False)
+    c = Case(rng, 3, 27, 33000, "fp16", 20, 4, False)
     c.drafts[0] = 32999
-    c.drafts[1] = [c.hist[1, 0], 5, 5, -1, 5, c.bias[0][1, 0], 0]
-    c.drafts[2] = [0, 1, 2, 3, 31, 32, 33]
+    c.drafts[1] = [c.hist[1, 0], 5, 5, -1, 5, c.bias[0][1, 0], 0, 5, 32998, 32998, 7, 32998, 32999] * 2
+    c.drafts[2] = [0, 1, 2, 3, 31, 32, 33, 3, 2, 1, 0, 0, 16000] * 2
     out = pa.pa_adjust_logits(None, c.x.to(DEV), **c.args()).cpu()
     for i in range(3):
-        for j in range(8):
+        for j in range(27):
             assert torch.equal(out[i, j], torch.from_numpy(c.adjusted(i, j)).to(torch.float16)), (i, j)
+    # (a batch of its own for each sequence, and several sequences' rows in one thread block)
+    for n in (3, 300):
+        x = c.x.repeat(n // 3, 1, 1).to(DEV)
+        args = {k: v.repeat(*([n // 3] + [1] * (v.dim() - 1))) for k, v in c.args().items()}
+        p = pa.pa_adjust_logits(None, x, temperature=f32(np.tile(c.temp, n // 3)), probs=True, **args)
+        c.check_probs(p[:3], c.temp.astype(np.float32))
+        c.check_probs(p[n - 3:], c.temp.astype(np.float32))
 
 
 def test_ids_outside_the_vocabulary(pa):
