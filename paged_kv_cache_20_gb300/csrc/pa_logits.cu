@@ -37,7 +37,6 @@
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_launch.h"
-#include "pa_tc.cuh"
 
 namespace pa {
 namespace {
@@ -173,21 +172,15 @@ __device__ __forceinline__ void store1(T *p, float x) {
   else
     *reinterpret_cast<uint16_t *>(p) = Elt<T>::from_f(x);
 }
-// Eight values: whole groups at 16-byte boundaries, else the elements of `in`.
+// Eight values to a 16-byte boundary.
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&x)[8], bool whole, unsigned in) {
-  if (whole) {
-    if constexpr (sizeof(T) == 4) {
-      __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
-      __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-    } else {
-      __stcs(reinterpret_cast<uint4 *>(p), make_uint4(Elt<T>::from_f2(x[0], x[1]), Elt<T>::from_f2(x[2], x[3]),
-                                                      Elt<T>::from_f2(x[4], x[5]), Elt<T>::from_f2(x[6], x[7])));
-    }
+__device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (in >> i & 1) store1(p + i, x[i]);
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(Elt<T>::from_f2(x[0], x[1]), Elt<T>::from_f2(x[2], x[3]),
+                                                    Elt<T>::from_f2(x[4], x[5]), Elt<T>::from_f2(x[6], x[7])));
   }
 }
 
@@ -202,20 +195,13 @@ __device__ __forceinline__ void dsmem_st_f32x2(uint32_t addr, float a, float b) 
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
-// Elements of the group at v0 that lie in [lo, hi), as bits.
-__device__ __forceinline__ unsigned inside(int v0, int lo, int hi) {
-  unsigned in = 0xffu;
-  if (v0 < lo) in &= 0xffu << min(8, lo - v0);
-  if (v0 + 8 > hi) in &= v0 < hi ? 0xffu >> (v0 + 8 - hi) : 0u;
-  return in & 0xffu;
-}
-
 // Shared memory of a slice: rows' logits, a stage each; the counts that the list is made from
 // (16 bits an entry, 32 where a history is too long for them), in the logits' place where
 // that leaves room for another thread block (shared); a batch's statistics by warp, and by thread
-// block; bits of counted entries, and of a row's mask and its dense elements, these with a
-// word before and behind; counts and places of the listed entries; biases (id,
+// block; bits of counted entries, and of a row's mask and its dense elements, these with
+// zeros before and behind (a warp's last group may start 248 elements past the slice); counts and places of the listed entries; biases (id,
 // value).
+constexpr int kOnBehind = 9;  // words
 struct Room {
   int stage, step, counts, warps, blocks, touched, mask, on, cnt, bias_v, bias_id, list, total;
 };
@@ -236,7 +222,7 @@ __host__ __device__ inline Room room_of(int slice, int listed, int num_bias, int
   r.blocks = take(kBatch * cluster * 8);
   r.touched = take(slice / 8);
   r.mask = take(slice / 8);
-  r.on = take(slice / 8 + 8);
+  r.on = take(slice / 8 + 4 + kOnBehind * 4);
   r.cnt = take(listed * 4);
   r.bias_v = take(num_bias * 4);
   r.bias_id = take(num_bias * 4);
@@ -283,7 +269,6 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   uint16_t *list = reinterpret_cast<uint16_t *>(s_raw + room.list);
   const int words = a.slice / 32;  // at most kThreads: a word a thread
   const bool counted = a.listed > 0;
-  const bool some = counted || a.mask != nullptr;  // any element may drop out of the dense pass
 
   // ---- a row's slice in shared memory: byte addr - base of the stage, base the boundary of
   // eight elements at or before the slice.  Copied in whole 16-byte pieces, also around
@@ -311,14 +296,11 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     if (c1 > c0)
       bulk_load(smem_u32(s_raw + room.stage + slot * room.step) + (uint32_t)(c0 - base), reinterpret_cast<const void *>(c0), (uint32_t)(c1 - c0), bar);
   };
-  auto mask_row = [&](int j) {
-    return reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + j * a.mask_row;
-  };
-  auto mask_word = [&](int j) -> unsigned {
-    if (a.mask == nullptr || threadIdx.x >= words) return 0xffffffffu;
-    const int w = (lo >> 5) + (int)threadIdx.x;
-    return w < (a.vocab + 31) / 32 ? __ldg(mask_row(j) + w) : 0u;
-  };
+  // the thread's word of a row's mask (entries past the vocabulary are not the slice's)
+  const unsigned *mask_at = nullptr;
+  if (a.mask != nullptr && lo + 32 * (int)threadIdx.x < hi)
+    mask_at = reinterpret_cast<const unsigned *>(a.mask) + seq * a.mask_seq + (lo >> 5) + threadIdx.x;
+  auto mask_word = [&](int j) { return mask_at != nullptr ? __ldg(mask_at + j * a.mask_row) : 0xffffffffu; };
   auto fetch_first = [&](int j) {  // (one thread) the first rows of those from j on
     for (int i = 0; i < min(j1 - j, stages); ++i) fetch(j + i, i);
   };
@@ -415,7 +397,10 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   } else if (a.modes.shared && threadIdx.x == 0) {
     fetch_first(j0);
   }
-  if (threadIdx.x < 2) on[threadIdx.x == 0 ? -1 : words] = 0u;
+  if (threadIdx.x <= kOnBehind) on[threadIdx.x == 0 ? -1 : words + (int)threadIdx.x - 1] = 0u;
+  // which of the word's entries are the slice's
+  const int ahead = hi - lo - 32 * (int)threadIdx.x;
+  const unsigned valid = ahead >= 32 ? ~0u : ahead <= 0 ? 0u : (1u << ahead) - 1u;
   const float rep = a.repetition ? __ldg(a.repetition + seq) : 1.f;
   const float pres = a.presence ? __ldg(a.presence + seq) : 0.f;
   const float freq = a.frequency ? __ldg(a.frequency + seq) : 0.f;
@@ -435,24 +420,27 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     }
     return x;
   };
-  // 2^((x - m) fac) against a maximum m; with an infinite m the entries that reach it
-  auto weight = [&](float x, float m) {
+  // Weights are 2^(x fac - c) with c = m fac rounded once: the same c in a sum and in what the
+  // sum divides leaves no error of its rounding, and the product x fac is not rounded at all.
+  // A maximum whose product is that large that differences are lost in it, or infinite, goes
+  // by 2^((x - m) fac); with an infinite m the entries that reach it count.
+  auto far = [&](float m) { return !(fabsf(m) * fac < 1e30f); };
+  auto far_weight = [&](float x, float m) {
     return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : ex2_flush((x - m) * fac);
   };
-  // the same of a pair, m finite
-  const uint64_t fac2 = tc::f2pack(fac, fac);
-  auto weight2 = [&](float x0, float x1, uint64_t neg_m2, float &w0, float &w1) {
-    float z0, z1;
-    tc::f2unpack(tc::fmul2(tc::fadd2(tc::f2pack(x0, x1), neg_m2), fac2), z0, z1);
-    w0 = ex2_flush(z0);
-    w1 = ex2_flush(z1);
+  auto weight = [&](float x, float m) {  // of x against the maximum m
+    return far(m) ? far_weight(x, m) : ex2_flush(fmaf(x, fac, -__fmul_rn(m, fac)));
+  };
+  auto rescaled = [&](float m1, float m) {  // of a sum against m1, against m
+    return far(m) || far(m1) ? far_weight(m1, m) : ex2_flush(__fmul_rn(m1, fac) - __fmul_rn(m, fac));
   };
 
   // ---- the rows, one after the other in either direction
   constexpr int kStep = 8 * kThreads;
   unsigned phase = 0u;  // of each stage's next copy, a bit a stage
+  const int32_t *drafts = a.drafts != nullptr ? a.drafts + (int64_t)seq * (a.rows - 1) : nullptr;
   auto draft_of = [&](int j) {  // the draft behind row j
-    return a.drafts != nullptr && j >= j0 && j + 1 < j1 ? __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + j) : -1;
+    return drafts != nullptr && j >= j0 && j + 1 < j1 ? __ldg(drafts + j) : -1;
   };
   // A draft joins the list: `known` says that it is on it.  (Read by others behind the row's
   // barrier.)
@@ -481,21 +469,27 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         if (list[i] == e) cnt[i] -= 1u;
     }
   };
+  const bool ragged = lo < hi && (reinterpret_cast<uintptr_t>(row_of(j0) + lo) < all0 ||
+                                  reinterpret_cast<uintptr_t>(row_of(j1 - 1) + hi) > all1);
   struct Row {
-    const T *in;
     const uint8_t *stage;
-    int shift, first;  // groups of eight start `shift` before the slice; the thread's group 0
+    int shift, first;      // groups of eight start `shift` before the slice; the thread's group 0
+    uint32_t base, up;     // its address, and its bits' place in the first word of
+    const unsigned *bits;  // two that hold them
   };
-  // Row j in stage `slot` (landed: it is there already), with mask word mw: to be worked on.
-  auto begin = [&](int j, int slot, bool landed, unsigned mw) {
+  // The row at `in`, in stage `slot` (landed: it is there already), with mask word mw: to be worked on.
+  auto begin = [&](const T *in, int slot, bool landed, unsigned mw) {
     Row r;
-    r.in = row_of(j);
     uint8_t *stage = s_raw + room.stage + slot * room.step;
     r.stage = stage;
-    r.shift = (int)((reinterpret_cast<uintptr_t>(r.in + lo) & (kAlign - 1)) / sizeof(T));
+    r.shift = (int)((reinterpret_cast<uintptr_t>(in + lo) & (kAlign - 1)) / sizeof(T));
     r.first = lo - r.shift + 8 * (int)threadIdx.x;
-    if (some && threadIdx.x < words) {
-      on[threadIdx.x] = counted ? mw & ~touched[threadIdx.x] : mw;
+    r.base = smem_u32(stage) + 8 * (uint32_t)sizeof(T) * threadIdx.x;
+    r.up = 32u + (uint32_t)(r.first - lo);  // (from the word before `on`)
+    r.bits = on + (int)(r.up >> 5) - 1;
+    r.up &= 31u;
+    if (threadIdx.x < words) {
+      on[threadIdx.x] = valid & (counted ? mw & ~touched[threadIdx.x] : mw);
       mask[threadIdx.x] = mw;
     }
     // (one warp asks the copies' barrier: all of them asking take the scheduler's turns)
@@ -505,35 +499,30 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     }
     __syncthreads();
     // elements beside what was copied: the logits' own ragged ends
-    const uintptr_t p0 = reinterpret_cast<uintptr_t>(r.in + lo), p1 = reinterpret_cast<uintptr_t>(r.in + hi);
-    if (!landed && lo < hi && (p0 < all0 || p1 > all1)) {
+    if (ragged && !landed) {
       uintptr_t c0, c1;
-      copied(r.in, c0, c1);
+      copied(in, c0, c1);
       const int e = threadIdx.x < 16 ? (int)threadIdx.x : hi - lo - 1 - ((int)threadIdx.x - 16);
       if (threadIdx.x < 32 && e >= 0 && e < hi - lo) {
-        const uintptr_t g = reinterpret_cast<uintptr_t>(r.in + lo + e);
-        if (g < c0 || g >= c1) reinterpret_cast<T *>(stage)[r.shift + e] = r.in[lo + e];
+        const uintptr_t g = reinterpret_cast<uintptr_t>(in + lo + e);
+        if (g < c0 || g >= c1) reinterpret_cast<T *>(stage)[r.shift + e] = in[lo + e];
       }
       fence_proxy_async_smem();  // before the copy of another row
       __syncthreads();
     }
     return r;
   };
-  // The thread's group k of a row (it starts before the slice's end), -inf for what is not dense.
+  // The thread's group k of a row, -inf for what is not dense or not the slice's; whether any
+  // of the warp's groups k starts in the slice.
   auto dense = [&](const Row &r, int k) {
-    const int v0 = r.first + k * kStep;
     Eight<T> x;
-    x.load(smem_u32(r.stage) + (8 * threadIdx.x + k * kStep) * (uint32_t)sizeof(T));
-    unsigned keep = 0xffu;
-    if (v0 < lo || v0 + 8 > hi) keep = inside(v0, lo, hi);
-    if (some) {
-      const uint32_t b = 32u + (uint32_t)(v0 - lo);  // from the word before `on`
-      keep &= __funnelshift_r(on[(int)(b >> 5) - 1], on[b >> 5], b);
-    }
-    if (keep != 0xffu) x.keep(keep);
+    x.load(r.base + k * (kStep * (uint32_t)sizeof(T)));
+    x.keep(__funnelshift_r(r.bits[k * (kStep / 32)], r.bits[k * (kStep / 32) + 1], r.up) & 0xffu);
     if (PROBS) x.no_nan();
     return x;
   };
+  const int warp_first = lo + 8 * 32 * __shfl_sync(0xffffffffu, warp, 0);
+  auto there = [&](const Row &r, int k) { return warp_first + k * kStep < hi + r.shift; };
   // Entry i of the list, adjusted.
   auto adjusted = [&](const Row &r, int i) {
     const int e = list[i];
@@ -541,10 +530,53 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     if (a.mask != nullptr && !(mask[e >> 5] >> (e & 31) & 1u)) y = -INFINITY;
     return PROBS ? fmaxf(y, -INFINITY) : y;  // NaN counts as -inf
   };
-  auto put = [&](const Row &r, O *out, int k, const float (&f)[8]) {
-    const int v0 = r.first + k * kStep;
-    const bool whole = v0 >= lo && v0 + 8 <= hi;
-    store8(out + v0, f, whole && (reinterpret_cast<uintptr_t>(out + v0) & 15u) == 0, whole ? 0xffu : inside(v0, lo, hi));
+  // The dense elements of a row, each group through `value`, to out (of the row): whole groups
+  // with wide stores, if they lie on 16-byte boundaries there; the slice's ragged ends, at
+  // most seven elements each, by a thread each.  (With both in one loop a group's eight
+  // single stores are predicated off one by one: 5 instructions an element.)
+  auto write = [&](const Row &r, O *out, auto value) {
+    O *o = out + r.first;
+    if ((reinterpret_cast<uintptr_t>(out + lo - r.shift) & 15u) == 0) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        if (!there(r, k)) continue;
+        const int v0 = r.first + k * kStep;
+        float f[8];
+        dense(r, k).get(f);
+        value(v0, f);
+        if (v0 >= lo && v0 + 8 <= hi) store8(o + k * kStep, f);
+      }
+      // groups 0 and the last, unless they are whole
+      const int n = hi - lo + r.shift;  // elements from group 0 on
+      const bool head = r.shift > 0, tail = (n & 7) != 0 && (n > 8 || !head);
+      if (threadIdx.x < 2 && (threadIdx.x == 0 ? head : tail)) {
+        const int at = threadIdx.x == 0 ? 0 : n & ~7;  // elements from group 0 on
+        Eight<T> x;
+        x.load(smem_u32(r.stage) + at * (uint32_t)sizeof(T));
+        const uint32_t b = 32u + (uint32_t)(at - r.shift);
+        x.keep(__funnelshift_r(on[(int)(b >> 5) - 1], on[b >> 5], b) & 0xffu);
+        if (PROBS) x.no_nan();
+        const int v0 = lo - r.shift + at;
+        float f[8];
+        x.get(f);
+        value(v0, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (v0 + i >= lo && v0 + i < hi) store1(out + v0 + i, f[i]);
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < VPT; ++k) {
+        if (!there(r, k)) continue;
+        const int v0 = r.first + k * kStep;
+        float f[8];
+        dense(r, k).get(f);
+        value(v0, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (v0 + i >= lo && v0 + i < hi) store1(o + k * kStep + i, f[i]);
+      }
+    }
   };
   // The stage of a row that was worked on: another row may come.
   auto release = [&](int slot, int next, bool more) {
@@ -555,21 +587,16 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   if constexpr (!PROBS) {
     unsigned mw = mask_word(j0);
     int behind = draft_of(j0), slot = 0;
-    for (int j = j0; j < j1; ++j) {
-      const Row r = begin(j, slot, false, mw);
+    const T *in = row_of(j0);
+    O *out = static_cast<O *>(a.out) + ((int64_t)seq * a.rows + j0) * a.out_stride;
+    for (int j = j0; j < j1; ++j, in += a.logits_stride, out += a.out_stride) {
+      const Row r = begin(in, slot, false, mw);
       if (j + 1 < j1) mw = mask_word(j + 1);
       const int e = behind >= lo && behind < hi ? behind - lo : -1;
       if (behind >= a.vocab && crank == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
       const bool known = e >= 0 && (touched[e >> 5] >> (e & 31) & 1u);
       behind = draft_of(j + 1);
-      O *out = static_cast<O *>(a.out) + ((int64_t)seq * a.rows + j) * a.out_stride;
-#pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        if (r.first + k * kStep >= hi) continue;
-        float f[8];
-        dense(r, k).get(f);
-        put(r, out, k, f);
-      }
+      write(r, out, [](int, float (&)[8]) {});
       if (counted) {
         __syncthreads();  // the dense pass is written
         for (int i = threadIdx.x; i < entries; i += kThreads) store1(out + lo + list[i], adjusted(r, i));
@@ -589,8 +616,9 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       }
       unsigned mw = mask_word(b0);
       int behind = draft_of(b0), slot = 0;
-      for (int j = b0; j < b1; ++j) {
-        const Row r = begin(j, slot, false, mw);
+      const T *in = row_of(b0);
+      for (int j = b0; j < b1; ++j, in += a.logits_stride) {
+        const Row r = begin(in, slot, false, mw);
         if (j + 1 < b1) mw = mask_word(j + 1);
         const int e = behind >= lo && behind < hi ? behind - lo : -1;
         if (behind >= a.vocab && crank == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
@@ -602,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         float m = -INFINITY;
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-          if (r.first + k * kStep < hi) {
+          if (there(r, k)) {
             const Eight<T> g = dense(r, k);
             m = fmaxf(m, g.largest());
             if constexpr (kKeep) x[k] = g;
@@ -624,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
             if (y > ms || (y == ms && v < at)) at = v;
             ms = fmaxf(ms, y);
           } else if (y > ms) {
-            ss = ss * weight(ms, y) + 1.f;
+            ss = ss * rescaled(ms, y) + 1.f;
             ms = y;
           } else {
             ss += weight(y, ms);
@@ -640,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
           if (m != -INFINITY) {
 #pragma unroll
             for (int k = VPT - 1; k >= 0; --k) {
-              if (r.first + k * kStep >= hi) continue;
+              if (!there(r, k)) continue;
               float f[8];
               again(k, f);
 #pragma unroll
@@ -651,34 +679,30 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
           __syncwarp();
           second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
         } else {
-          if (ms != -INFINITY) second = ss * weight(ms, m);
-          if (m == INFINITY) {
+          if (ms != -INFINITY) second = ss * rescaled(ms, m);
+          if (far(m)) {
+            if (m != -INFINITY) {
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-              if (r.first + k * kStep >= hi) continue;
-              float f[8];
-              again(k, f);
+              for (int k = 0; k < VPT; ++k) {
+                if (!there(r, k)) continue;
+                float f[8];
+                again(k, f);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) second += f[i] == INFINITY ? 1.f : 0.f;
-            }
-          } else if (m != -INFINITY) {
-            const uint64_t neg = tc::f2pack(-m, -m);
-            uint64_t sum = 0ull;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-              if (r.first + k * kStep >= hi) continue;
-              float f[8];
-              again(k, f);
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                float w0, w1;
-                weight2(f[i], f[i + 1], neg, w0, w1);
-                sum = tc::fadd2(sum, tc::f2pack(w0, w1));
+                for (int i = 0; i < 8; ++i) second += far_weight(f[i], m);
               }
             }
-            float s0, s1;
-            tc::f2unpack(sum, s0, s1);
-            second += s0 + s1;
+          } else {
+            const float c = __fmul_rn(m, fac);
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+              if (!there(r, k)) continue;
+              float f[8];
+              again(k, f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sum[i & 1] += ex2_flush(fmaf(f[i], fac, -c));
+            }
+            second += sum[0] + sum[1];
           }
           __syncwarp();
 #pragma unroll
@@ -697,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         if (greedy)
           return __int_as_float(__reduce_min_sync(0xffffffffu, v.x == M ? __float_as_int(v.y) : INT_MAX));
-        float sum = M == -INFINITY ? 0.f : v.y * weight(v.x, M);
+        float sum = M == -INFINITY || v.x == -INFINITY ? 0.f : v.y * rescaled(v.x, M);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         return sum;
@@ -722,43 +746,29 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       // ---- back: the last rows are in their stages still (s_row is read behind a row's barrier)
       mw = mask_word(b1 - 1);
       behind = draft_of(b1 - 2);
-      for (int j = b1 - 1; j >= b0; --j) {
-        slot = (j - b0) % stages;
-        const Row r = begin(j, slot, j >= b1 - stages, mw);
+      float *out = static_cast<float *>(a.out) + ((int64_t)seq * a.rows + b1 - 1) * a.out_stride;
+      for (int j = b1 - 1; j >= b0; --j, out -= a.out_stride) {
+        in -= a.logits_stride;
+        slot = slot == 0 ? stages - 1 : slot - 1;
+        const Row r = begin(in, slot, j >= b1 - stages, mw);
         if (j > b0) mw = mask_word(j - 1);
         const int before = behind;  // the draft before this row, which leaves with it
         behind = draft_of(j - 2);
         const float2 stat = s_row[j - b0];
         const float M = stat.x, mul = stat.y;
         const int best = greedy ? __float_as_int(stat.y) : INT_MAX;
-        float *out = static_cast<float *>(a.out) + ((int64_t)seq * a.rows + j) * a.out_stride;
-        if (!greedy && fabsf(M) != INFINITY) {
-          const uint64_t neg = tc::f2pack(-M, -M), mul2 = tc::f2pack(mul, mul);
+        if (!greedy && !far(M)) {
+          const float c = __fmul_rn(M, fac);
+          write(r, out, [&](int, float (&f)[8]) {
 #pragma unroll
-          for (int k = 0; k < VPT; ++k) {
-            if (r.first + k * kStep >= hi) continue;
-            float f[8];
-            dense(r, k).get(f);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              float w0, w1;
-              weight2(f[i], f[i + 1], neg, w0, w1);
-              tc::f2unpack(tc::fmul2(tc::f2pack(w0, w1), mul2), f[i], f[i + 1]);
-            }
-            put(r, out, k, f);
-          }
-        } else {  // one, none, or the infinite ones
-#pragma unroll
-          for (int k = 0; k < VPT; ++k) {
-            const int v0 = r.first + k * kStep;
-            if (v0 >= hi) continue;
-            float f[8];
-            dense(r, k).get(f);
+            for (int i = 0; i < 8; ++i) f[i] = ex2_flush(fmaf(f[i], fac, -c)) * mul;
+          });
+        } else {  // one, none, or the far ones
+          write(r, out, [&](int v0, float (&f)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              f[i] = M == INFINITY && !greedy ? (f[i] == INFINITY ? mul : 0.f) : v0 + i == best ? 1.f : 0.f;
-            put(r, out, k, f);
-          }
+              f[i] = greedy || M == -INFINITY ? (v0 + i == best ? 1.f : 0.f) : far_weight(f[i], M) * mul;
+          });
         }
         if (counted) {
           __syncthreads();  // the dense pass is written
