@@ -33,21 +33,21 @@ constexpr int kWarpsPerCta = 32;
 constexpr int kAllWarps = kCluster * kWarpsPerCta;
 
 // A contiguous part of [0, n) for each of the cluster's warps, in whole steps of 128.
+// (n < 2^30: check_pool)
 struct Part {
-  int64_t lo, hi;
+  int lo, hi;
 };
-__device__ __forceinline__ Part part_of(int64_t n, int gw) {
-  const int64_t steps = (n + 127) / 128;
-  const int64_t per = (steps + kAllWarps - 1) / kAllWarps;
+__device__ __forceinline__ Part part_of(int n, int gw) {
+  const int per = (n + 128 * kAllWarps - 1) / (128 * kAllWarps);
   Part p;
-  p.lo = min(n, (int64_t)gw * per * 128);
+  p.lo = min(n, gw * per * 128);
   p.hi = min(n, p.lo + per * 128);
   return p;
 }
 
 // Four counts (or entries) at i .. i + 3 of an array of n; `fill` past its end.  Read
 // through L2: these arrays are written by the calls before and by this one.
-__device__ __forceinline__ int4 load4(const int32_t *p, int64_t i, int64_t n, int fill) {
+__device__ __forceinline__ int4 load4(const int32_t *p, int i, int n, int fill) {
   if (i + 4 <= n) return __ldcg(reinterpret_cast<const int4 *>(p + i));
   int4 v = make_int4(fill, fill, fill, fill);
   if (i < n) v.x = __ldcg(p + i);
@@ -87,35 +87,57 @@ __device__ __forceinline__ void ranks(Totals &t, int which, int gw, int &before,
   all = warp_sum(all);
 }
 
-// Free blocks of this warp's part of the counts.
-__device__ __forceinline__ int count_free(const int32_t *refs, Part p) {
-  const int lane = threadIdx.x & 31;
+// Four of a warp's steps at once: lane l holds the counts lo + 128 u + 4 l .. + 3 of step u,
+// `fill` past the part's end.  A part of no more than that stays in registers between the
+// counting and the walk with ranks.
+constexpr int kSteps = 4;
+struct Counts {
+  int4 v[kSteps];
+  __device__ __forceinline__ void load(const int32_t *refs, int lo, int hi, int fill) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) v[u] = load4(refs, lo + 128 * u + 4 * lane, hi, fill);
+  }
+  __device__ __forceinline__ int zeros() const {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) n += (v[u].x == 0) + (v[u].y == 0) + (v[u].z == 0) + (v[u].w == 0);
+    return n;
+  }
+};
+
+// Free blocks of this warp's part of the counts; c: its last steps.
+__device__ __forceinline__ int count_free(const int32_t *refs, Part p, Counts &c) {
   int n = 0;
-#pragma unroll 4
-  for (int64_t i = p.lo + 4 * lane; i < p.hi; i += 128) {
-    const int4 v = load4(refs, i, p.hi, 1);
-    n += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+  for (int lo = p.lo; lo < p.hi; lo += 128 * kSteps) {
+    c.load(refs, lo, p.hi, 1);
+    n += c.zeros();
   }
   return warp_sum(n);
 }
 
 // The first `want` free blocks, ascending, to list (rank of this warp's first: before).
-__device__ __forceinline__ void list_free(const int32_t *refs, Part p, int before, int want, int32_t *list) {
+__device__ __forceinline__ void list_free(const int32_t *refs, Part p, Counts &c, int before, int want,
+                                          int32_t *list) {
   const int lane = threadIdx.x & 31;
+  const bool kept = p.hi - p.lo <= 128 * kSteps;
   int at = before;
-  for (int64_t i0 = p.lo; i0 < p.hi && at < want; i0 += 128) {
-    const int64_t i = i0 + 4 * lane;
-    const int4 v = load4(refs, i, p.hi, 1);
-    const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
-    const int mine = f[0] + f[1] + f[2] + f[3];
-    int r = at + warp_before(mine);
+  for (int lo = p.lo; lo < p.hi && at < want; lo += 128 * kSteps) {
+    if (!kept) c.load(refs, lo, p.hi, 1);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (f[k]) {
-        if (r < want) list[r] = (int32_t)(i + k);
-        ++r;
-      }
-    at += warp_sum(mine);
+    for (int u = 0; u < kSteps; ++u) {
+      const int4 v = c.v[u];
+      const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
+      const int mine = f[0] + f[1] + f[2] + f[3];
+      int r = at + warp_before(mine);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (f[k]) {
+          if (r < want) list[r] = lo + 128 * u + 4 * lane + k;
+          ++r;
+        }
+      at += warp_sum(mine);
+    }
   }
 }
 
@@ -123,28 +145,28 @@ struct PoolArgs {
   int32_t *tables, *refs;
   const int32_t *lens;  // reserve: tokens wanted; free: tokens kept
   int32_t *missing, *list;
-  int num_seqs, width, num_blocks, block_size;
+  int num_seqs, width, num_blocks, shift;  // blocks of 2^shift tokens
   unsigned *err;
 };
 
-__device__ __forceinline__ int64_t blocks_of(int len, int block_size) {
-  return len > 0 ? ((int64_t)len + block_size - 1) / block_size : 0;
+__device__ __forceinline__ unsigned blocks_of(int len, int shift) {
+  return len > 0 ? ((unsigned)len + (1u << shift) - 1u) >> shift : 0u;
 }
 
 // ---- free ------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) free_blocks_kernel(const PoolArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t n = (int64_t)a.num_seqs * a.width;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int n = a.num_seqs * a.width;
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;
   const int4 v = load4(a.tables, i, n, -1);
   const int id[4] = {v.x, v.y, v.z, v.w};
-  int64_t row = i / a.width;
-  int col = (int)(i - row * a.width);
+  int row = i / a.width;
+  int col = i - row * a.width;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    if (id[k] >= 0 && col >= blocks_of(__ldg(a.lens + row), a.block_size)) {
+    if (id[k] >= 0 && (unsigned)col >= blocks_of(__ldg(a.lens + row), a.shift)) {
       bool bad = id[k] >= a.num_blocks;
       if (!bad && atomicSub(a.refs + id[k], 1) <= 0) {  // was not counted: leave the count
         atomicAdd(a.refs + id[k], 1);
@@ -161,21 +183,20 @@ __global__ void __launch_bounds__(256) free_blocks_kernel(const PoolArgs a) {
 }
 
 // ---- reserve ---------------------------------------------------------------------
-// Entries at i .. i + 3 of the tables that want a block, as four bits.
-__device__ __forceinline__ int wants4(const PoolArgs &a, int64_t i, int64_t n, bool rec) {
-  if (i >= n) return 0;
-  const int4 v = load4(a.tables, i, n, 0);
-  if (v.x >= 0 && v.y >= 0 && v.z >= 0 && v.w >= 0) return 0;
+// Of entries v at i .. i + 3 of the tables, those that want a block, as four bits.
+__device__ __forceinline__ int wants4(const PoolArgs &a, int4 v, int i, int hi) {
+  if ((v.x | v.y | v.z | v.w) >= 0) return 0;  // (no negative one; past hi they are 0)
   const int id[4] = {v.x, v.y, v.z, v.w};
-  int64_t row = i / a.width;
-  int col = (int)(i - row * a.width);
+  int row = i / a.width;
+  int col = i - row * a.width;
+  unsigned need = blocks_of(__ldg(a.lens + row), a.shift);
   int f = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    if (id[k] < 0 && col < blocks_of(__ldg(a.lens + row), a.block_size)) f |= 1 << k;
-    if (++col == a.width) {
+    if (id[k] < 0 && (unsigned)col < need) f |= 1 << k;
+    if (++col == a.width && k < 3 && i + k + 1 < hi) {
       col = 0;
-      ++row;
+      need = blocks_of(__ldg(a.lens + ++row), a.shift);
     }
   }
   return f;
@@ -187,15 +208,27 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
-  const int64_t n = (int64_t)a.num_seqs * a.width;
-  const Part pe = part_of(n, gw), pb = part_of(a.num_blocks, gw);
+  const Part pe = part_of(a.num_seqs * a.width, gw), pb = part_of(a.num_blocks, gw);
   for (int i = gw * 32 + lane; i < a.num_seqs; i += kAllWarps * 32)
-    if (blocks_of(__ldg(a.lens + i), a.block_size) > a.width) record_error(a.err, kErrCheck);
+    if (blocks_of(__ldg(a.lens + i), a.shift) > (unsigned)a.width) record_error(a.err, kErrCheck);
+  Counts c;
+  const int free = count_free(a.refs, pb, c);
+  // the entries that want one; of the first steps the flags are kept, four bits a step
+  constexpr int kFlagged = 8;
+  unsigned flags = 0u;
   int wanted = 0;
-#pragma unroll 2
-  for (int64_t i = pe.lo + 4 * lane; i < pe.hi; i += 128) wanted += __popc(wants4(a, i, pe.hi, false));
+  for (int lo = pe.lo; lo < pe.hi; lo += 128 * kSteps) {
+    Counts e;
+    e.load(a.tables, lo, pe.hi, 0);
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const unsigned f = wants4(a, e.v[u], lo + 128 * u + 4 * lane, pe.hi);
+      const int step = (lo - pe.lo) / 128 + u;
+      if (step < kFlagged) flags |= f << (4 * step);
+      wanted += __popc(f);
+    }
+  }
   wanted = warp_sum(wanted);
-  const int free = count_free(a.refs, pb);
   if (lane == 0) {
     tot.of[0][warp] = wanted;
     tot.of[1][warp] = free;
@@ -204,18 +237,20 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
   int want0, wants, free0, frees;
   ranks(tot, 0, gw, want0, wants);
   ranks(tot, 1, gw, free0, frees);
-  list_free(a.refs, pb, free0, wants, a.list);
+  list_free(a.refs, pb, c, free0, wants, a.list);
   sync_cluster();  // the list is written, every count read
   int at = want0;
   if (wanted > 0) {
-    for (int64_t i0 = pe.lo; i0 < pe.hi; i0 += 128) {
-      const int64_t i = i0 + 4 * lane;
-      const int f = wants4(a, i, pe.hi, false);
+    for (int i0 = pe.lo; i0 < pe.hi; i0 += 128) {
+      const int i = i0 + 4 * lane, step = (i0 - pe.lo) / 128;
+      const unsigned f = step < kFlagged ? flags >> (4 * step) & 15u
+                                         : wants4(a, load4(a.tables, i, pe.hi, 0), i, pe.hi);
       const int mine = __popc(f);
+      if (!__any_sync(0xffffffffu, mine > 0)) continue;
       int r = at + warp_before(mine);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (f >> k & 1) {
+        if (f >> k & 1u) {
           if (r < frees) {
             const int id = __ldcg(a.list + r);
             a.tables[i + k] = id;
@@ -234,7 +269,7 @@ struct ForkArgs {
   int32_t *tables, *lens, *refs;
   const int32_t *src, *dst;
   int32_t *src_blocks, *dst_blocks, *counts, *list, *tail_of;
-  int num_forks, num_seqs, width, num_blocks, block_size;
+  int num_forks, num_seqs, width, num_blocks, shift;
   unsigned *err;
 };
 
@@ -251,9 +286,9 @@ __device__ __forceinline__ int parent_tail(const ForkArgs &a, int f, bool rec) {
   bool bad = !fork_pair(a, f, s, d);
   if (!bad) {
     const int len = max(0, __ldcg(a.lens + s));
-    bad = blocks_of(len, a.block_size) > a.width;
-    if (!bad && len % a.block_size != 0) {
-      id = __ldcg(a.tables + (int64_t)s * a.width + len / a.block_size);
+    bad = blocks_of(len, a.shift) > (unsigned)a.width;
+    if (!bad && (len & ((1 << a.shift) - 1)) != 0) {
+      id = __ldcg(a.tables + s * a.width + (len >> a.shift));
       bad = id < 0 || id >= a.num_blocks;
     }
   }
@@ -276,7 +311,8 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
     tails += parent_tail(a, f, true) >= 0;
   }
   tails = warp_sum(tails);
-  const int free = count_free(a.refs, pb);
+  Counts c;
+  const int free = count_free(a.refs, pb, c);
   if (lane == 0) {
     tot.of[0][warp] = tails;
     tot.of[1][warp] = free;
@@ -285,7 +321,7 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
   int tail0, all, free0, frees;
   ranks(tot, 0, gw, tail0, all);
   ranks(tot, 1, gw, free0, frees);
-  list_free(a.refs, pb, free0, all, a.list);
+  list_free(a.refs, pb, c, free0, all, a.list);
   sync_cluster();  // the list is written, every count and length read that decides
   int at = tail0;
   for (int f0 = lo; f0 < hi; f0 += 32) {
@@ -310,16 +346,16 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
   }
   sync_cluster();
   // the children's rows
-  const int64_t n = (int64_t)a.num_forks * a.width;
-  for (int64_t i = (int64_t)gw * 32 + lane; i < n; i += kAllWarps * 32) {
-    const int f = (int)(i / a.width), j = (int)(i - (int64_t)f * a.width);
+  const int n = a.num_forks * a.width;  // (no more forks than rows)
+  for (int i = gw * 32 + lane; i < n; i += kAllWarps * 32) {
+    const int f = i / a.width, j = i - f * a.width;
     int s, d;
     if (!fork_pair(a, f, s, d)) continue;
     const int len = max(0, __ldcg(a.lens + s));
-    const int full = min(len / a.block_size, a.width);
+    const int full = min(len >> a.shift, a.width);
     int id = -1;
     if (j < full) {
-      id = __ldcg(a.tables + (int64_t)s * a.width + j);
+      id = __ldcg(a.tables + s * a.width + j);
       if (id < 0 || id >= a.num_blocks) {
         record_error(a.err, kErrCheck);
         id = -1;
@@ -329,15 +365,15 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
     } else if (j == full) {
       id = __ldcg(a.tail_of + f);
     }
-    a.tables[(int64_t)d * a.width + j] = id;
+    a.tables[d * a.width + j] = id;
   }
   sync_cluster();  // every parent's length read
   for (int f = gw * 32 + lane; f < a.num_forks; f += kAllWarps * 32) {
     int s, d;
     if (!fork_pair(a, f, s, d)) continue;
     const int len = max(0, __ldcg(a.lens + s));
-    const int full = min(len / a.block_size, a.width);
-    a.lens[d] = __ldcg(a.tail_of + f) >= 0 ? len : full * a.block_size;
+    const int full = min(len >> a.shift, a.width);
+    a.lens[d] = __ldcg(a.tail_of + f) >= 0 ? len : full << a.shift;
   }
 }
 
@@ -361,7 +397,9 @@ __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactAr
   const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
   const Part p = part_of(a.num_blocks, gw);
   if (threadIdx.x == 0) s_below = 0;
-  const int used = (int)(p.hi - p.lo) - count_free(a.refs, p);
+  Counts c;
+  const int used = p.hi - p.lo - count_free(a.refs, p, c);
+  const bool kept = p.hi - p.lo <= 128 * kSteps;
   if (lane == 0) tot.of[0][warp] = used;
   sync_cluster();
   int used0, live;
@@ -369,7 +407,7 @@ __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactAr
   // used blocks below `live`: the warp whose part holds that border counts them
   if (p.lo < live && live <= p.hi) {
     int below = 0;
-    for (int64_t i = p.lo + lane; i < live; i += 32) below += __ldcg(a.refs + i) != 0;
+    for (int i = p.lo + lane; i < live; i += 32) below += __ldcg(a.refs + i) != 0;
     below = warp_sum(below);
     if (lane == 0) s_below = used0 + below;
   }
@@ -379,33 +417,38 @@ __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactAr
   for (int c = 0; c < kCluster; ++c) below += dsmem_ld_s32(dsmem_map(smem_u32(&s_below), c));
   // the k-th used block at or past `live` goes to the k-th free one before it
   int at = used0;
-  for (int64_t i0 = p.lo; i0 < p.hi; i0 += 128) {
-    const int64_t i = i0 + 4 * lane;
-    const int4 v = load4(a.refs, i, p.hi, 0);
-    const int ref[4] = {v.x, v.y, v.z, v.w};
-    const int mine = (v.x != 0) + (v.y != 0) + (v.z != 0) + (v.w != 0);
-    int u = at + warp_before(mine);  // used blocks before i + k
+  for (int lo = p.lo; lo < p.hi; lo += 128 * kSteps) {
+    if (!kept) c.load(a.refs, lo, p.hi, 0);  // (kept ones are 1 past the part's end)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t b = i + k;
-      if (b < p.hi) {
-        if (b < live) {
-          if (ref[k] == 0)
-            a.dst_blocks[b - u] = (int32_t)b;
-          else
-            a.refs_out[b] = ref[k];
-        } else {
-          if (ref[k] != 0) {
-            a.src_blocks[u - below] = (int32_t)b;
-            a.moved[u - below] = ref[k];
+    for (int t = 0; t < kSteps; ++t) {
+      const int i = lo + 128 * t + 4 * lane;
+      const int ref[4] = {c.v[t].x, c.v[t].y, c.v[t].z, c.v[t].w};
+      int mine = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine += i + k < p.hi && ref[k] != 0;
+      int u = at + warp_before(mine);  // used blocks before i + k
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int b = i + k;
+        if (b < p.hi) {
+          if (b < live) {
+            if (ref[k] == 0)
+              a.dst_blocks[b - u] = b;
+            else
+              a.refs_out[b] = ref[k];
+          } else {
+            if (ref[k] != 0) {
+              a.src_blocks[u - below] = b;
+              a.moved[u - below] = ref[k];
+            }
+            a.name[b] = -1;
+            a.refs_out[b] = 0;
           }
-          a.name[b] = -1;
-          a.refs_out[b] = 0;
+          u += ref[k] != 0;
         }
       }
-      u += ref[k] != 0;
+      at += warp_sum(mine);
     }
-    at += warp_sum(mine);
   }
   const int moves = live - below;
   if (gw == 0 && lane == 0) {
@@ -419,8 +462,9 @@ __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactAr
     a.refs_out[to] = __ldcg(a.moved + k);
   }
   sync_cluster();
-  const int64_t n = (int64_t)a.num_seqs * a.width;
-  for (int64_t i = ((int64_t)gw * 32 + lane) * 4; i < n; i += kAllWarps * 128) {
+  const int n = a.num_seqs * a.width;
+#pragma unroll 4
+  for (int i = (gw * 32 + lane) * 4; i < n; i += kAllWarps * 128) {
     const int4 v = load4(a.tables, i, n, -1);
     int id[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -436,8 +480,8 @@ __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactAr
 }
 
 // ---- copy ------------------------------------------------------------------------
-// Pieces of 16 KiB, one a step: K's of every listed pair, then V's, the pair's scales with
-// its first piece of K.
+// x: a 16 KiB piece of the block's K or V; y: the pairs (further pairs loop).  A pair's scales
+// go with its first piece of K.
 constexpr int kPieceThreads = 256, kPieceLoads = 4;
 constexpr int kPiece = kPieceThreads * kPieceLoads;  // 16-byte chunks
 
@@ -454,11 +498,8 @@ __global__ void __launch_bounds__(kPieceThreads) copy_pages_kernel(const CopyArg
   griddep_wait();
   griddep_launch_dependents();
   const int pairs = min(max(0, __ldcg(a.counts)), a.max_pairs);
-  const int64_t tasks = (int64_t)pairs * 2 * a.pieces;
-  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int piece = (int)(task % a.pieces);
-    const int64_t rest = task / a.pieces;
-    const int kv = (int)(rest & 1), pair = (int)(rest >> 1);
+  const int piece = blockIdx.x >> 1, kv = blockIdx.x & 1;
+  for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
     const int s = __ldcg(a.src + pair), d = __ldcg(a.dst + pair);
     if (s < 0 || s >= a.num_blocks || d < 0 || d >= a.num_blocks) {
       if (piece == 0 && kv == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
@@ -509,6 +550,9 @@ pa_status check_pool(int num_seqs, int max_blocks_per_seq, int num_blocks, int b
   return PA_OK;
 }
 
+// (8, 16 or 32)
+int shift_of(int block_size) { return block_size == 8 ? 3 : block_size == 16 ? 4 : 5; }
+
 size_t ints(int64_t n) { return (size_t)n * 4; }
 
 }  // namespace
@@ -541,7 +585,7 @@ PA_API pa_status pa_free_blocks(int32_t *block_tables, int32_t *ref_counts, cons
   a.num_seqs = num_seqs;
   a.width = max_blocks_per_seq;
   a.num_blocks = num_blocks;
-  a.block_size = block_size;
+  a.shift = shift_of(block_size);
   a.err = error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
   const unsigned ctas = (unsigned)(((int64_t)num_seqs * max_blocks_per_seq + 1023) / 1024);
@@ -577,7 +621,7 @@ PA_API pa_status pa_reserve_blocks(int32_t *block_tables, int32_t *ref_counts, c
   a.num_seqs = num_seqs;
   a.width = max_blocks_per_seq;
   a.num_blocks = num_blocks;
-  a.block_size = block_size;
+  a.shift = shift_of(block_size);
   a.err = error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
   return launch_cluster(reserve_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
@@ -628,7 +672,7 @@ PA_API pa_status pa_fork_blocks(int32_t *block_tables, int32_t *context_lens, in
   a.num_seqs = num_seqs;
   a.width = max_blocks_per_seq;
   a.num_blocks = num_blocks;
-  a.block_size = block_size;
+  a.shift = shift_of(block_size);
   a.err = error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
   return launch_cluster(fork_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
@@ -715,9 +759,9 @@ PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales, c
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PA_ERR_CUDA;
   // how many pairs there are is known on the device alone: at most a wave of thread blocks
-  const int64_t tasks = (int64_t)max_pairs * 2 * a.pieces;
-  const unsigned ctas = (unsigned)std::min<int64_t>(tasks, (int64_t)sms * 8);
-  return launch_dependent(copy_pages_kernel, ctas, kPieceThreads, static_cast<cudaStream_t>(stream), a) ==
+  const int x = 2 * a.pieces;
+  const int y = std::min(std::min(max_pairs, 65535), std::max(1, sms * 8 / x));
+  return launch_dependent(copy_pages_kernel, dim3((unsigned)x, (unsigned)y, 1), kPieceThreads, static_cast<cudaStream_t>(stream), a) ==
                  cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
