@@ -183,20 +183,27 @@ __global__ void __launch_bounds__(256) free_blocks_kernel(const PoolArgs a) {
 }
 
 // ---- reserve ---------------------------------------------------------------------
+// The blocks that the rows of a thread block's part need, from its first row on, in shared
+// memory: read once, with the first loads under way (a part of more rows reads on).
+constexpr int kNeeds = 1024;
+__device__ __forceinline__ unsigned need_of(const PoolArgs &a, const unsigned *needs, int row0, int row) {
+  return row - row0 < kNeeds ? needs[row - row0] : blocks_of(__ldg(a.lens + row), a.shift);
+}
+
 // Of entries v at i .. i + 3 of the tables, those that want a block, as four bits.
-__device__ __forceinline__ int wants4(const PoolArgs &a, int4 v, int i, int hi) {
+__device__ __forceinline__ int wants4(const PoolArgs &a, const unsigned *needs, int row0, int4 v, int i, int hi) {
   if ((v.x | v.y | v.z | v.w) >= 0) return 0;  // (no negative one; past hi they are 0)
   const int id[4] = {v.x, v.y, v.z, v.w};
   int row = i / a.width;
   int col = i - row * a.width;
-  unsigned need = blocks_of(__ldg(a.lens + row), a.shift);
+  unsigned need = need_of(a, needs, row0, row);
   int f = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (id[k] < 0 && (unsigned)col < need) f |= 1 << k;
     if (++col == a.width && k < 3 && i + k + 1 < hi) {
       col = 0;
-      need = blocks_of(__ldg(a.lens + ++row), a.shift);
+      need = need_of(a, needs, row0, ++row);
     }
   }
   return f;
@@ -204,15 +211,20 @@ __device__ __forceinline__ int wants4(const PoolArgs &a, int4 v, int i, int hi) 
 
 __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs a) {
   __shared__ Totals tot;
+  __shared__ unsigned needs[kNeeds];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
   const Part pe = part_of(a.num_seqs * a.width, gw), pb = part_of(a.num_blocks, gw);
-  for (int i = gw * 32 + lane; i < a.num_seqs; i += kAllWarps * 32)
-    if (blocks_of(__ldg(a.lens + i), a.shift) > (unsigned)a.width) record_error(a.err, kErrCheck);
+  const int row0 = part_of(a.num_seqs * a.width, gw - warp).lo / a.width;
+  if (row0 + (int)threadIdx.x < a.num_seqs) {
+    const unsigned need = blocks_of(__ldg(a.lens + row0 + threadIdx.x), a.shift);
+    needs[threadIdx.x] = need;
+  }
   Counts c;
   const int free = count_free(a.refs, pb, c);
+  __syncthreads();
   // the entries that want one; of the first steps the flags are kept, four bits a step
   constexpr int kFlagged = 8;
   unsigned flags = 0u;
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
     e.load(a.tables, lo, pe.hi, 0);
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      const unsigned f = wants4(a, e.v[u], lo + 128 * u + 4 * lane, pe.hi);
+      const unsigned f = wants4(a, needs, row0, e.v[u], lo + 128 * u + 4 * lane, pe.hi);
       const int step = (lo - pe.lo) / 128 + u;
       if (step < kFlagged) flags |= f << (4 * step);
       wanted += __popc(f);
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
     for (int i0 = pe.lo; i0 < pe.hi; i0 += 128) {
       const int i = i0 + 4 * lane, step = (i0 - pe.lo) / 128;
       const unsigned f = step < kFlagged ? flags >> (4 * step) & 15u
-                                         : wants4(a, load4(a.tables, i, pe.hi, 0), i, pe.hi);
+                                         : wants4(a, needs, row0, load4(a.tables, i, pe.hi, 0), i, pe.hi);
       const int mine = __popc(f);
       if (!__any_sync(0xffffffffu, mine > 0)) continue;
       int r = at + warp_before(mine);
@@ -262,6 +274,8 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
     }
   }
   if (gw == 0 && lane == 0) *a.missing = max(0, wants - frees);
+  for (int i = gw * 32 + lane; i < a.num_seqs; i += kAllWarps * 32)
+    if (blocks_of(__ldg(a.lens + i), a.shift) > (unsigned)a.width) record_error(a.err, kErrCheck);
 }
 
 // ---- fork ------------------------------------------------------------------------
@@ -306,13 +320,15 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
   // forks in parts of whole warps: f = lo + lane, lo + lane + 32, ..
   const int per = (a.num_forks + kAllWarps * 32 - 1) / (kAllWarps * 32) * 32;
   const int lo = min(a.num_forks, gw * per), hi = min(a.num_forks, lo + per);
-  int tails = 0;
-  for (int f = lo + lane; f < hi; f += 32) {
-    tails += parent_tail(a, f, true) >= 0;
-  }
-  tails = warp_sum(tails);
   Counts c;
   const int free = count_free(a.refs, pb, c);
+  int tail = -1, tails = 0;  // (tail: of the lane's last fork; of its only one where a part is a warp)
+  for (int f = lo + lane; f < hi; f += 32) {
+    tail = parent_tail(a, f, true);
+    tails += tail >= 0;
+  }
+  __syncwarp();
+  tails = warp_sum(tails);
   if (lane == 0) {
     tot.of[0][warp] = tails;
     tot.of[1][warp] = free;
@@ -322,11 +338,11 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
   ranks(tot, 0, gw, tail0, all);
   ranks(tot, 1, gw, free0, frees);
   list_free(a.refs, pb, c, free0, all, a.list);
-  sync_cluster();  // the list is written, every count and length read that decides
+  sync_cluster();  // the list is written, every count read
   int at = tail0;
   for (int f0 = lo; f0 < hi; f0 += 32) {
     const int f = f0 + lane;
-    const int t = f < hi ? parent_tail(a, f, false) : -1;
+    const int t = f >= hi ? -1 : per == 32 ? tail : parent_tail(a, f, false);
     const int r = at + warp_before(t >= 0);
     at += warp_sum(t >= 0);
     if (f < hi) {
@@ -344,36 +360,37 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
     a.counts[0] = min(all, frees);
     a.counts[1] = max(0, all - frees);
   }
-  sync_cluster();
-  // the children's rows
-  const int n = a.num_forks * a.width;  // (no more forks than rows)
-  for (int i = gw * 32 + lane; i < n; i += kAllWarps * 32) {
-    const int f = i / a.width, j = i - f * a.width;
-    int s, d;
-    if (!fork_pair(a, f, s, d)) continue;
-    const int len = max(0, __ldcg(a.lens + s));
-    const int full = min(len >> a.shift, a.width);
-    int id = -1;
-    if (j < full) {
-      id = __ldcg(a.tables + s * a.width + j);
-      if (id < 0 || id >= a.num_blocks) {
-        record_error(a.err, kErrCheck);
-        id = -1;
-      } else {
-        atomicAdd(a.refs + id, 1);
+  // the children's rows: so many warps a fork that every warp has one, each the same share of
+  // the row.  What they read of a fork is on its way while the cluster meets.
+  const int share = max(1, kAllWarps / a.num_forks), part = gw % share;
+  int f = gw / share, s = 0, d = 0, len = 0;
+  bool ok = f < a.num_forks && fork_pair(a, f, s, d);
+  if (ok) len = max(0, __ldcg(a.lens + s));
+  sync_cluster();  // the tails' new blocks
+  while (f < a.num_forks) {
+    if (ok) {
+      const int full = min(len >> a.shift, a.width), fresh = __ldcg(a.tail_of + f);
+      const int32_t *from = a.tables + s * a.width;
+      int32_t *to = a.tables + d * a.width;
+#pragma unroll 4
+      for (int j = part * 32 + lane; j < a.width; j += share * 32) {
+        int id = j < full ? __ldcg(from + j) : j == full ? fresh : -1;
+        if (j < full) {
+          if (id < 0 || id >= a.num_blocks) {
+            record_error(a.err, kErrCheck);
+            id = -1;
+          } else {
+            atomicAdd(a.refs + id, 1);
+          }
+        }
+        to[j] = id;
       }
-    } else if (j == full) {
-      id = __ldcg(a.tail_of + f);
+      // (no parent is a child: its length is read by no one else)
+      if (part == 0 && lane == 0) a.lens[d] = fresh >= 0 ? len : full << a.shift;
     }
-    a.tables[d * a.width + j] = id;
-  }
-  sync_cluster();  // every parent's length read
-  for (int f = gw * 32 + lane; f < a.num_forks; f += kAllWarps * 32) {
-    int s, d;
-    if (!fork_pair(a, f, s, d)) continue;
-    const int len = max(0, __ldcg(a.lens + s));
-    const int full = min(len >> a.shift, a.width);
-    a.lens[d] = __ldcg(a.tail_of + f) >= 0 ? len : full << a.shift;
+    f += max(1, kAllWarps / share);
+    ok = f < a.num_forks && fork_pair(a, f, s, d);
+    if (ok) len = max(0, __ldcg(a.lens + s));
   }
 }
 
@@ -508,13 +525,15 @@ __global__ void __launch_bounds__(kPieceThreads) copy_pages_kernel(const CopyArg
     const uint4 *from = a.cache[kv] + s * a.chunks;
     uint4 *to = a.cache[kv] + d * a.chunks;
     const int64_t c0 = (int64_t)piece * kPiece + threadIdx.x;
-    uint4 v[kPieceLoads];
+    if (c0 + (kPieceLoads - 1) * kPieceThreads < a.chunks) {  // all loads before the first store
+      uint4 v[kPieceLoads];
 #pragma unroll
-    for (int u = 0; u < kPieceLoads; ++u)
-      if (c0 + u * kPieceThreads < a.chunks) v[u] = __ldcs(from + c0 + u * kPieceThreads);
+      for (int u = 0; u < kPieceLoads; ++u) v[u] = __ldcs(from + c0 + u * kPieceThreads);
 #pragma unroll
-    for (int u = 0; u < kPieceLoads; ++u)
-      if (c0 + u * kPieceThreads < a.chunks) __stcs(to + c0 + u * kPieceThreads, v[u]);
+      for (int u = 0; u < kPieceLoads; ++u) __stcs(to + c0 + u * kPieceThreads, v[u]);
+    } else {
+      for (int64_t c = c0; c < a.chunks; c += kPieceThreads) __stcs(to + c, __ldcs(from + c));
+    }
     if (a.kv_scales != nullptr && piece == 0 && kv == 0)
       for (int i = threadIdx.x; i < a.scales_per_block; i += kPieceThreads)
         a.kv_scales[(int64_t)d * a.scales_per_block + i] = __ldcg(a.kv_scales + (int64_t)s * a.scales_per_block + i);
