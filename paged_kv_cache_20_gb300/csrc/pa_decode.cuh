@@ -139,9 +139,20 @@ __device__ __forceinline__ float clamp_scale(float s) {  // (NaN: the least)
 // 16 bits for P V never exceeds 1, and no accumulator is rescaled when a block's scale
 // differs from the last one's.  For sv a power of two log2 sv is exact.
 // What a tile's tokens share, by halves of 8 tokens (the same where a block holds both).
+// (Both to 2^-22: what counts is that the one is taken off again by the other.)
 struct TileScales {
   float k[2], lv[2], inv[2];  // K scale, log2 and reciprocal of the V scale
 };
+__device__ __forceinline__ float log2_of_scale(float s) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+__device__ __forceinline__ float inverse_of_scale(float s) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
 template <bool BSC> struct TileArg { using type = float; };
 template <> struct TileArg<true> { using type = TileScales; };
 
@@ -297,6 +308,7 @@ __device__ __forceinline__ RowInfo row_info(const DecodeArgs &a, int kvh, int rh
 // CUDA-core path: R rows, K lanes per token.
 template <typename T, int D, int K, int R, bool SC = false>
 struct FmaPath {
+  static constexpr bool kPairs = false;
   static constexpr bool kScored = SC, kBlockScaled = false;
   static constexpr int RPC = R;                    // rows per CTA
   static constexpr int TPP = 32 / K;               // tokens per pass
@@ -489,6 +501,7 @@ struct FmaPath {
 // Tensor-core path: up to 16 rows (padded), warp-level mma.sync m16n8k16.
 template <typename T, int D, bool SC = false, bool BSC = false>
 struct MmaPath {
+  static constexpr bool kPairs = false;
   static constexpr bool kScored = SC, kBlockScaled = BSC;
   using Arg = typename TileArg<BSC>::type;
   static constexpr int RPC = 16;
@@ -713,6 +726,7 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 // tokens g and g+8 of each tile.
 template <typename T, int D, bool SC = false, bool BSC = false>
 struct MmaTPath {
+  static constexpr bool kPairs = false;
   static constexpr bool kScored = SC, kBlockScaled = BSC;
   using Arg = typename TileArg<BSC>::type;
   static constexpr int RPC = 8;
@@ -857,6 +871,58 @@ struct MmaTPath {
     }
   }
 
+  // softmax_p of two tiles at once (block scales): one maximum and one rescale for 32 tokens.
+  template <bool MASKED>
+  __device__ __forceinline__ void softmax_p2(float (&sa)[4], float (&sb)[4], int ja, int jb, const Arg &aa,
+                                             const Arg &ab, uint32_t (&ba)[2], uint32_t (&bb)[2]) {
+    static_assert(BSC && !SC && Elt<T>::kMantBits >= 10, "block scales, P not split");
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float va = fmaf(sa[i], rs[i & 1] * aa.k[i >> 1], aa.lv[i >> 1]);
+      float vb = fmaf(sb[i], rs[i & 1] * ab.k[i >> 1], ab.lv[i >> 1]);
+      if (MASKED) {
+        if (ja * kTileTokens + g + 8 * (i >> 1) >= lim[i & 1]) va = -INFINITY;
+        if (jb * kTileTokens + g + 8 * (i >> 1) >= lim[i & 1]) vb = -INFINITY;
+      }
+      sa[i] = va;
+      sb[i] = vb;
+    }
+    float mx[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(sa[e], sa[2 + e]), fmaxf(sb[e], sb[2 + e]));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (mx[e] > m[e]) {
+        const float f = fast_exp2(m[e] - mx[e]);  // m = -inf -> 0
+        l[e] *= f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          o[mt][e] *= f;
+          o[mt][2 + e] *= f;
+        }
+        m[e] = mx[e];
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = i & 1;
+      const float pa = MASKED && sa[i] == -INFINITY ? 0.f : fast_exp2(sa[i] - m[e]);
+      const float pb = MASKED && sb[i] == -INFINITY ? 0.f : fast_exp2(sb[i] - m[e]);
+      sa[i] = pa;
+      sb[i] = pb;
+      l[e] = fmaf(pa, aa.inv[i >> 1], fmaf(pb, ab.inv[i >> 1], l[e]));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ba[h] = movmatrix_trans(Elt<T>::from_f2(sa[2 * h], sa[2 * h + 1]));
+      bb[h] = movmatrix_trans(Elt<T>::from_f2(sb[2 * h], sb[2 * h + 1]));
+    }
+  }
+
   // softmax_p, then O^T += V^T P^T with V^T fragments from the 16-bit tile at vt.
   template <bool MASKED>
   __device__ __forceinline__ void softmax_pv(float (&sc)[4], uint32_t vt, int tile_idx) {
@@ -949,6 +1015,7 @@ struct Mma8TPath {
   static constexpr int RPC = 8;
   using Inner = MmaTPath<__half, D, SC, BSC>;
   using Arg = typename Inner::Arg;
+  static constexpr bool kPairs = BSC;  // takes two tiles at a time
   static constexpr int KS = Inner::KS;
   __device__ __forceinline__ ScoreSink<SC> &sink() { return inner.raw; }
   Inner inner;  // inner.o[b][i]: O^T dim 16g + 2b + (i >> 1), row 2c + (i & 1)
@@ -992,20 +1059,17 @@ struct Mma8TPath {
     }
   }
 
-  template <bool MASKED>
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, const Arg &arg) {
+  // S^T of a tile (two independent chains, even and odd k-steps, then added).
+  __device__ __forceinline__ void scores(uint32_t kt, float (&sc)[4]) {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const uint4 k0a = lds128(kt + sw128_offset_row128(g, 2 * c));
     const uint4 k0b = lds128(kt + sw128_offset_row128(g, 2 * c + 1));
     const uint4 k8a = lds128(kt + sw128_offset_row128(g + 8, 2 * c));
     const uint4 k8b = lds128(kt + sw128_offset_row128(g + 8, 2 * c + 1));
-    const uint4 v0 = lds128(vt + sw128_offset_row128(2 * c, g));
-    const uint4 v1 = lds128(vt + sw128_offset_row128(2 * c + 1, g));
-    const uint4 v8 = lds128(vt + sw128_offset_row128(2 * c + 8, g));
-    const uint4 v9 = lds128(vt + sw128_offset_row128(2 * c + 9, g));
-    // S^T: two independent chains (even and odd k-steps), then added
-    float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+    float sd[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[i] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const uint32_t w0 = word_of(ks < 4 ? k0a : k0b, ks & 3);
@@ -1016,14 +1080,30 @@ struct Mma8TPath {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] += sd[i];
-    uint32_t bh[2], bl[2];
-    inner.template softmax_p<MASKED>(sc, tile_idx, bh, bl, arg);  // fp16 P: no split
-    // O^T += V^T P^T.  Word j of a lane's V chunk holds dims 16g + 4j .. +3: m-tile
-    // 2j takes dims 4j, 4j + 1 (rows g, g + 8), m-tile 2j + 1 dims 4j + 2, 4j + 3.
+  }
+
+  // V's codes of a tile, as a lane needs them: dims 16g .. 16g + 15 of its four tokens.
+  struct VTile {
+    uint4 v0, v1, v8, v9;
+  };
+  __device__ __forceinline__ VTile load_v(uint32_t vt) {
+    const int lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;
+    VTile v;
+    v.v0 = lds128(vt + sw128_offset_row128(2 * c, g));
+    v.v1 = lds128(vt + sw128_offset_row128(2 * c + 1, g));
+    v.v8 = lds128(vt + sw128_offset_row128(2 * c + 8, g));
+    v.v9 = lds128(vt + sw128_offset_row128(2 * c + 9, g));
+    return v;
+  }
+
+  // O^T += V^T P^T.  Word j of a lane's V chunk holds dims 16g + 4j .. +3: m-tile
+  // 2j takes dims 4j, 4j + 1 (rows g, g + 8), m-tile 2j + 1 dims 4j + 2, 4j + 3.
+  __device__ __forceinline__ void pv(const VTile &v, const uint32_t (&bh)[2]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t x0 = word_of(v0, j), x1 = word_of(v1, j);
-      const uint32_t x8 = word_of(v8, j), x9 = word_of(v9, j);
+      const uint32_t x0 = word_of(v.v0, j), x1 = word_of(v.v1, j);
+      const uint32_t x8 = word_of(v.v8, j), x9 = word_of(v.v9, j);
       const uint32_t p01 = __byte_perm(x0, x1, 0x5140), q01 = __byte_perm(x0, x1, 0x7362);
       const uint32_t p89 = __byte_perm(x8, x9, 0x5140), q89 = __byte_perm(x8, x9, 0x7362);
       const uint32_t va[4] = {e4m3_lo_f16x2(p01), e4m3_hi_f16x2(p01), e4m3_lo_f16x2(p89),
@@ -1033,6 +1113,31 @@ struct Mma8TPath {
       Elt<__half>::mma16816(inner.o[2 * j], va, bh[0], bh[1]);
       Elt<__half>::mma16816(inner.o[2 * j + 1], vb, bh[0], bh[1]);
     }
+  }
+
+  template <bool MASKED>
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, const Arg &arg) {
+    float sc[4];
+    const VTile v = load_v(vt);
+    scores(kt, sc);
+    uint32_t bh[2], bl[2];
+    inner.template softmax_p<MASKED>(sc, tile_idx, bh, bl, arg);  // fp16 P: no split
+    pv(v, bh);
+  }
+
+  // Two tiles with one softmax update (block scales): of the 444 instructions a tile that the
+  // path takes one by one, the two maxima with their shuffles and the rescale are shared,
+  // and the two tiles' matrix products hide one another's latency.
+  template <bool MASKED>
+  __device__ __forceinline__ void tile2(uint32_t kta, uint32_t vta, int ja, const Arg &aa, uint32_t ktb,
+                                        uint32_t vtb, int jb, const Arg &ab) {
+    float sa[4], sb[4];
+    scores(kta, sa);
+    scores(ktb, sb);
+    uint32_t ba[2], bb[2];
+    inner.template softmax_p2<MASKED>(sa, sb, ja, jb, aa, ab, ba, bb);
+    pv(load_v(vta), ba);
+    pv(load_v(vtb), bb);
   }
 
   template <int STRIDE>
@@ -1066,6 +1171,7 @@ struct Mma8TPath {
 // BSC: block scales, applied to the finished dot products and in the softmax.
 template <typename T, int R, bool SC = false, bool BSC = false>
 struct Fma8Path {
+  static constexpr bool kPairs = false;
   static constexpr bool kScored = SC, kBlockScaled = BSC;
   using Arg = typename TileArg<BSC>::type;
   static constexpr int D = 128;
@@ -1269,6 +1375,7 @@ struct Fma8Path {
 // BSC: block scales, applied in the softmax.
 template <typename T, bool SC = false, bool BSC = false>
 struct Mma8Path {
+  static constexpr bool kPairs = false;
   static constexpr bool kScored = SC, kBlockScaled = BSC;
   static constexpr int D = 128;
   static constexpr int RPC = 16;
@@ -1541,8 +1648,8 @@ __global__ void __launch_bounds__(NW * 32)
       const float2 from = h == 0 ? (cur ? sc : sc_old) : (cur ? sc2 : sc2_old);
       t.k[h] = clamp_scale(__shfl_sync(0xffffffffu, from.x, n & 31));
       const float v = clamp_scale(__shfl_sync(0xffffffffu, from.y, n & 31));
-      t.lv[h] = log2f(v);
-      t.inv[h] = 1.f / v;
+      t.lv[h] = log2_of_scale(v);
+      t.inv[h] = inverse_of_scale(v);
     }
     if (BS != 0) {
       t.k[1] = t.k[0];
@@ -1648,7 +1755,45 @@ __global__ void __launch_bounds__(NW * 32)
 
   bool failed = false;
   int n = 0;
-  for (; n < n_my; ++n) {
+  // rows of a tile past the context hold anything: V's become zeros (0 * NaN would be NaN)
+  auto clear_rows = [&](int j, uint32_t vt) {
+    const int nvalid = L - j * kTileTokens;  // rows >= nvalid are past the context
+    if (nvalid < kTileTokens) {
+      for (int idx = lane; idx < (kTileTokens - nvalid) * kRowChunks; idx += 32) {
+        const int row = nvalid + idx / kRowChunks, ch = idx % kRowChunks;
+        sts128_zero(vt + (KV8 ? sw128_offset_row128(row, ch) : sw128_offset<kTileTokens>(row, ch)));
+      }
+      // order these generic-proxy stores before any later TMA (async proxy) write
+      // into the same stage
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+  };
+  if constexpr (Path::kPairs) {
+    for (; n + 1 < n_my; n += 2) {
+      const int s0 = n % NSTAGE, s1 = (n + 1) % NSTAGE;
+      const bool ok = mbar_wait_bounded(smem_u32(&bars[warp * NSTAGE + s0]), (n / NSTAGE) & 1) &&
+                      mbar_wait_bounded(smem_u32(&bars[warp * NSTAGE + s1]), ((n + 1) / NSTAGE) & 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        failed = true;
+        break;
+      }
+      const int j0 = tile_of(n), j1 = tile_of(n + 1);
+      const uint32_t k0 = my_stages + s0 * kStageBytes, k1 = my_stages + s1 * kStageBytes;
+      const TileScales t0 = tile_scales(n), t1 = tile_scales(n + 1);
+      if (j0 >= first_masked || j1 >= first_masked) {
+        clear_rows(j0, k0 + kTileBytes);
+        clear_rows(j1, k1 + kTileBytes);
+        path.template tile2<true>(k0, k0 + kTileBytes, j0, t0, k1, k1 + kTileBytes, j1, t1);
+      } else {
+        path.template tile2<false>(k0, k0 + kTileBytes, j0, t0, k1, k1 + kTileBytes, j1, t1);
+      }
+      __syncwarp();
+      if (n + NSTAGE < n_my) issue(n + NSTAGE);
+      if (n + 1 + NSTAGE < n_my) issue(n + 1 + NSTAGE);
+    }
+  }
+  for (; n < n_my && !failed; ++n) {
     const int s = n % NSTAGE;
     const uint32_t bar = smem_u32(&bars[warp * NSTAGE + s]);
     const bool ok = mbar_wait_bounded(bar, (n / NSTAGE) & 1);
@@ -1661,17 +1806,7 @@ __global__ void __launch_bounds__(NW * 32)
     const uint32_t vt = kt + kTileBytes;
     if constexpr (Path::kScored) path.sink().tile(j);
     if (j >= first_masked) {
-      const int nvalid = L - j * kTileTokens;  // rows >= nvalid are past the context
-      if (nvalid < kTileTokens) {
-        for (int idx = lane; idx < (kTileTokens - nvalid) * kRowChunks; idx += 32) {
-          const int row = nvalid + idx / kRowChunks, ch = idx % kRowChunks;
-          sts128_zero(vt + (KV8 ? sw128_offset_row128(row, ch) : sw128_offset<kTileTokens>(row, ch)));
-        }
-        // order these generic-proxy stores before any later TMA (async proxy) write
-        // into the same stage
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
+      clear_rows(j, vt);
       if constexpr (Path::kBlockScaled)
         path.template tile<true>(kt, vt, j, tile_scales(n));
       else

@@ -153,6 +153,14 @@ static cudaError_t launch_paths8(const CUtensorMap &kmap, const CUtensorMap &vma
   if (a.rows == 2) return launch_one<BS, T, 128, Fma8Path<T, 2, SC, BSC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
   if (a.rows <= 8) {
     if constexpr (!PARTIAL) return launch_few_units<BS, T, Mma8TPath<T, SC, BSC>, true, 3, 2>(kmap, vmap, a, units, st);
+    if constexpr (BSC) {
+      // partitions that fit one wave of 3-warp CTAs and not one of 4-warp ones
+      long long slots3 = 0;
+      const cudaError_t e = resident_slots<BS, T, 128, Mma8TPath<T, SC, BSC>, PARTIAL, true, 3>(slots3);
+      if (e != cudaSuccess) return e;
+      if (units <= slots3)
+        return launch_one<BS, T, 128, Mma8TPath<T, SC, BSC>, PARTIAL, true, 3>(kmap, vmap, a, units, 1, st);
+    }
     return launch_one<BS, T, 128, Mma8TPath<T, SC, BSC>, PARTIAL, true>(kmap, vmap, a, units, 1, st);
   }
   const int groups = (a.rows + 15) / 16;

@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
           if (lane < kRuns) {
             const float sv1 = clamp_scale(scl_next.y);
             s_scl[warp - kSoft0][j & 1][lane] =
-                make_float4(clamp_scale(scl_next.x), log2f(sv1), 1.f / sv1, 0.f);
+                make_float4(clamp_scale(scl_next.x), log2_of_scale(sv1), inverse_of_scale(sv1), 0.f);
           }
           scl_next = scales_at(cu, id_next);
           id_next = block_at(cu, j + 2);
