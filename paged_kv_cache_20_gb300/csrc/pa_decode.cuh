@@ -1059,21 +1059,30 @@ struct Mma8TPath {
     }
   }
 
-  // S^T of a tile (two independent chains, even and odd k-steps, then added).
-  __device__ __forceinline__ void scores(uint32_t kt, float (&sc)[4]) {
+  // K's codes of a tile, as a lane needs them: dims 32c .. 32c + 31 of tokens g and g + 8.
+  struct KTile {
+    uint4 k0a, k0b, k8a, k8b;
+  };
+  __device__ __forceinline__ KTile load_k(uint32_t kt) {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    const uint4 k0a = lds128(kt + sw128_offset_row128(g, 2 * c));
-    const uint4 k0b = lds128(kt + sw128_offset_row128(g, 2 * c + 1));
-    const uint4 k8a = lds128(kt + sw128_offset_row128(g + 8, 2 * c));
-    const uint4 k8b = lds128(kt + sw128_offset_row128(g + 8, 2 * c + 1));
+    KTile k;
+    k.k0a = lds128(kt + sw128_offset_row128(g, 2 * c));
+    k.k0b = lds128(kt + sw128_offset_row128(g, 2 * c + 1));
+    k.k8a = lds128(kt + sw128_offset_row128(g + 8, 2 * c));
+    k.k8b = lds128(kt + sw128_offset_row128(g + 8, 2 * c + 1));
+    return k;
+  }
+
+  // S^T of a tile (two independent chains, even and odd k-steps, then added).
+  __device__ __forceinline__ void scores(const KTile &k, float (&sc)[4]) {
     float sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const uint32_t w0 = word_of(ks < 4 ? k0a : k0b, ks & 3);
-      const uint32_t w8 = word_of(ks < 4 ? k8a : k8b, ks & 3);
+      const uint32_t w0 = word_of(ks < 4 ? k.k0a : k.k0b, ks & 3);
+      const uint32_t w8 = word_of(ks < 4 ? k.k8a : k.k8b, ks & 3);
       const uint32_t ka[4] = {e4m3_lo_f16x2(w0), e4m3_lo_f16x2(w8), e4m3_hi_f16x2(w0),
                               e4m3_hi_f16x2(w8)};
       Elt<__half>::mma16816((ks & 1) ? sd : sc, ka, inner.qb[ks][0], inner.qb[ks][1]);
@@ -1117,9 +1126,10 @@ struct Mma8TPath {
 
   template <bool MASKED>
   __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, int tile_idx, const Arg &arg) {
-    float sc[4];
+    const KTile k = load_k(kt);
     const VTile v = load_v(vt);
-    scores(kt, sc);
+    float sc[4];
+    scores(k, sc);
     uint32_t bh[2], bl[2];
     inner.template softmax_p<MASKED>(sc, tile_idx, bh, bl, arg);  // fp16 P: no split
     pv(v, bh);
@@ -1132,8 +1142,8 @@ struct Mma8TPath {
   __device__ __forceinline__ void tile2(uint32_t kta, uint32_t vta, int ja, const Arg &aa, uint32_t ktb,
                                         uint32_t vtb, int jb, const Arg &ab) {
     float sa[4], sb[4];
-    scores(kta, sa);
-    scores(ktb, sb);
+    scores(load_k(kta), sa);
+    scores(load_k(ktb), sb);
     uint32_t ba[2], bb[2];
     inner.template softmax_p2<MASKED>(sa, sb, ja, jb, aa, ab, ba, bb);
     pv(load_v(vta), ba);
