@@ -420,19 +420,12 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     }
     return x;
   };
-  // Weights are 2^(x fac - c) with c = m fac rounded once: the same c in a sum and in what the
-  // sum divides leaves no error of its rounding, and the product x fac is not rounded at all.
-  // A maximum whose product is that large that differences are lost in it, or infinite, goes
-  // by 2^((x - m) fac); with an infinite m the entries that reach it count.
-  auto far = [&](float m) { return !(fabsf(m) * fac < 1e30f); };
-  auto far_weight = [&](float x, float m) {
+  // 2^((x - m) fac) against a maximum m; with an infinite m the entries that reach it.  (One
+  // multiply-add with m fac rounded beforehand saves an instruction an element and no time,
+  // and the largest weights, exact here, carry exp2's error there: 5e-7 of a row against
+  // 1e-7.)
+  auto weight = [&](float x, float m) {
     return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : ex2_flush((x - m) * fac);
-  };
-  auto weight = [&](float x, float m) {  // of x against the maximum m
-    return far(m) ? far_weight(x, m) : ex2_flush(fmaf(x, fac, -__fmul_rn(m, fac)));
-  };
-  auto rescaled = [&](float m1, float m) {  // of a sum against m1, against m
-    return far(m) || far(m1) ? far_weight(m1, m) : ex2_flush(__fmul_rn(m1, fac) - __fmul_rn(m, fac));
   };
 
   // ---- the rows, one after the other in either direction
@@ -652,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
             if (y > ms || (y == ms && v < at)) at = v;
             ms = fmaxf(ms, y);
           } else if (y > ms) {
-            ss = ss * rescaled(ms, y) + 1.f;
+            ss = ss * weight(ms, y) + 1.f;
             ms = y;
           } else {
             ss += weight(y, ms);
@@ -679,20 +672,17 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
           __syncwarp();
           second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
         } else {
-          if (ms != -INFINITY) second = ss * rescaled(ms, m);
-          if (far(m)) {
-            if (m != -INFINITY) {
+          if (ms != -INFINITY) second = ss * weight(ms, m);
+          if (m == INFINITY) {
 #pragma unroll
-              for (int k = 0; k < VPT; ++k) {
-                if (!there(r, k)) continue;
-                float f[8];
-                again(k, f);
+            for (int k = 0; k < VPT; ++k) {
+              if (!there(r, k)) continue;
+              float f[8];
+              again(k, f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) second += far_weight(f[i], m);
-              }
+              for (int i = 0; i < 8; ++i) second += weight(f[i], m);
             }
-          } else {
-            const float c = __fmul_rn(m, fac);
+          } else if (m != -INFINITY) {
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
@@ -700,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
               float f[8];
               again(k, f);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) sum[i & 1] += ex2_flush(fmaf(f[i], fac, -c));
+              for (int i = 0; i < 8; ++i) sum[i & 1] += ex2_flush((f[i] - m) * fac);
             }
             second += sum[0] + sum[1];
           }
@@ -721,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         if (greedy)
           return __int_as_float(__reduce_min_sync(0xffffffffu, v.x == M ? __float_as_int(v.y) : INT_MAX));
-        float sum = M == -INFINITY || v.x == -INFINITY ? 0.f : v.y * rescaled(v.x, M);
+        float sum = M == -INFINITY ? 0.f : v.y * weight(v.x, M);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         return sum;
@@ -757,17 +747,16 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         const float2 stat = s_row[j - b0];
         const float M = stat.x, mul = stat.y;
         const int best = greedy ? __float_as_int(stat.y) : INT_MAX;
-        if (!greedy && !far(M)) {
-          const float c = __fmul_rn(M, fac);
+        if (!greedy && fabsf(M) != INFINITY) {
           write(r, out, [&](int, float (&f)[8]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = ex2_flush(fmaf(f[i], fac, -c)) * mul;
+            for (int i = 0; i < 8; ++i) f[i] = ex2_flush((f[i] - M) * fac) * mul;
           });
-        } else {  // one, none, or the far ones
+        } else {  // one, none, or the infinite ones
           write(r, out, [&](int v0, float (&f)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              f[i] = greedy || M == -INFINITY ? (v0 + i == best ? 1.f : 0.f) : far_weight(f[i], M) * mul;
+              f[i] = greedy || M == -INFINITY ? (v0 + i == best ? 1.f : 0.f) : weight(f[i], M) * mul;
           });
         }
         if (counted) {

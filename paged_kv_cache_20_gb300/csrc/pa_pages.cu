@@ -218,20 +218,18 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
   const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
   const Part pe = part_of(a.num_seqs * a.width, gw), pb = part_of(a.num_blocks, gw);
   const int row0 = part_of(a.num_seqs * a.width, gw - warp).lo / a.width;
-  if (row0 + (int)threadIdx.x < a.num_seqs) {
-    const unsigned need = blocks_of(__ldg(a.lens + row0 + threadIdx.x), a.shift);
-    needs[threadIdx.x] = need;
-  }
-  Counts c;
+  const int len = row0 + (int)threadIdx.x < a.num_seqs ? __ldg(a.lens + row0 + threadIdx.x) : 0;
+  Counts c, e;
+  e.load(a.tables, pe.lo, pe.hi, 0);  // (all three loads under way before the first wait)
   const int free = count_free(a.refs, pb, c);
+  needs[threadIdx.x] = blocks_of(len, a.shift);
   __syncthreads();
   // the entries that want one; of the first steps the flags are kept, four bits a step
   constexpr int kFlagged = 8;
   unsigned flags = 0u;
   int wanted = 0;
   for (int lo = pe.lo; lo < pe.hi; lo += 128 * kSteps) {
-    Counts e;
-    e.load(a.tables, lo, pe.hi, 0);
+    if (lo > pe.lo) e.load(a.tables, lo, pe.hi, 0);
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
       const unsigned f = wants4(a, needs, row0, e.v[u], lo + 128 * u + 4 * lane, pe.hi);
@@ -274,8 +272,12 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
     }
   }
   if (gw == 0 && lane == 0) *a.missing = max(0, wants - frees);
-  for (int i = gw * 32 + lane; i < a.num_seqs; i += kAllWarps * 32)
-    if (blocks_of(__ldg(a.lens + i), a.shift) > (unsigned)a.width) record_error(a.err, kErrCheck);
+  // rows longer than the table, among those at hand and (parts of very many rows) the rest
+  const int rows_hi = part_of(a.num_seqs * a.width, gw - warp + kWarpsPerCta).lo / a.width;
+  bool over = needs[threadIdx.x] > (unsigned)a.width;
+  for (int i = row0 + kNeeds + (int)threadIdx.x; i <= min(rows_hi, a.num_seqs - 1); i += 1024)
+    over |= blocks_of(__ldg(a.lens + i), a.shift) > (unsigned)a.width;
+  if (over) record_error(a.err, kErrCheck);
 }
 
 // ---- fork ------------------------------------------------------------------------

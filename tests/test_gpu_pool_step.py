@@ -266,3 +266,31 @@ def test_without_the_compiled_calls(pa):
         pa._fast = fast
     for a in STATE:
         assert torch.equal(got[a], want[a]), a
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_rotated_heads_of_one_projection(pa, dtype):
+    """q and k heads of a fused projection's output rotated in place, without cache rows, then
+    k and v appended from their slices: as q, k and v apart."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    n, u, hq, h, bs = 3, 5, 8, 2, 16
+    t = n * u
+    qkv = torch.randn(t, hq + 2 * h, 128, generator=g, device=DEV).to(dtype)
+    pos = torch.randint(0, 10000, (1, t), generator=g, device=DEV, dtype=torch.int32)
+    turns, axis = pa.rope_table(128)
+    nowhere = torch.full((t,), -1, dtype=torch.int64, device=DEV)
+    ones = torch.ones(h, device=DEV)
+    codes = [torch.zeros(12, h, bs, 128, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    scales = [torch.zeros(12, h, 2, device=DEV) for _ in range(2)]
+    tables, lens = i32(np.arange(12).reshape(3, 4)), i32([5, 20, 37])
+    apart = [x.contiguous() for x in (qkv[:, :hq], qkv[:, hq:hq + h], qkv[:, hq + h:])]
+    for x in apart[:2]:
+        pa.pa_rope_append(x, x, apart[1], apart[2], codes[0], codes[1], pos, nowhere, turns, axis, k_scale=ones,
+                          v_scale=ones)
+    pa.pa_append_kv_block_scaled(codes[0], codes[1], scales[0], apart[1], apart[2], tables, lens, q_len=u)
+    qk, k, v = qkv[:, :hq + h], qkv[:, hq:hq + h], qkv[:, hq + h:]
+    pa.pa_rope_append(qk, qk, k, v, codes[2], codes[3], pos, nowhere, turns, axis, k_scale=ones, v_scale=ones)
+    pa.pa_append_kv_block_scaled(codes[2], codes[3], scales[1], k, v, tables, lens, q_len=u)
+    assert torch.equal(qkv[:, :hq], apart[0])
+    assert torch.equal(codes[0], codes[2]) and torch.equal(codes[1], codes[3]) and torch.equal(scales[0], scales[1])
+    assert bool((codes[0] != 0).any()) and pa.pa_device_error() == 0
