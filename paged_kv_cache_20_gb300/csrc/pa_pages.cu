@@ -9,9 +9,11 @@
 // its rank at hand.
 //
 // Bound by latency: a pool of 131,072 blocks has 512 KiB of counts.  One cluster of 8
-// thread blocks of 32 warps walks it, so the sums over all warps cost one cluster barrier
+// thread blocks of 32 warps walks it, so the sums over all warps cost a cluster barrier
 // instead of a kernel boundary; with 256 warps a warp's part of such a pool is 512 counts,
-// four 16-byte loads a lane.
+// four 16-byte loads a lane, which stay in registers between the two walks.  (16 thread
+// blocks: no faster there, 3 us slower for small pools.  64-bit index arithmetic and the
+// tables' entries read twice: 31 us against 18 for 256 sequences in such a pool.)
 #include <algorithm>
 
 #include "../../include/pagedattn.h"
@@ -22,22 +24,28 @@
 namespace pa {
 namespace {
 
-// All threads of the cluster (a warp arrives as one).
-__device__ __forceinline__ void sync_cluster() {
-  __syncwarp();
-  cluster_sync_all();
+// All threads of the cluster of C thread blocks (a warp arrives as one).
+template <int C>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (C == 1) {
+    __syncthreads();
+  } else {
+    __syncwarp();
+    cluster_sync_all();
+  }
 }
 
-constexpr int kCluster = 8;
 constexpr int kWarpsPerCta = 32;
-constexpr int kAllWarps = kCluster * kWarpsPerCta;
+constexpr int kMaxCluster = 8;
 
 // A contiguous part of [0, n) for each of the cluster's warps, in whole steps of 128.
 // (n < 2^30: check_pool)
 struct Part {
   int lo, hi;
 };
+template <int C>
 __device__ __forceinline__ Part part_of(int n, int gw) {
+  constexpr int kAllWarps = C * kWarpsPerCta;
   const int per = (n + 128 * kAllWarps - 1) / (128 * kAllWarps);
   Part p;
   p.lo = min(n, gw * per * 128);
@@ -74,12 +82,13 @@ struct Totals {
   int of[2][kWarpsPerCta];
 };
 // Sum of totals `which` over the warps before gw (before) and over all (all).
+template <int C>
 __device__ __forceinline__ void ranks(Totals &t, int which, int gw, int &before, int &all) {
   const int lane = threadIdx.x & 31;
   before = all = 0;
 #pragma unroll
-  for (int c = 0; c < kCluster; ++c) {
-    const int v = dsmem_ld_s32(dsmem_map(smem_u32(&t.of[which][lane]), c));
+  for (int c = 0; c < C; ++c) {
+    const int v = C == 1 ? t.of[which][lane] : dsmem_ld_s32(dsmem_map(smem_u32(&t.of[which][lane]), c));
     all += v;
     if (c * kWarpsPerCta + lane < gw) before += v;
   }
@@ -191,11 +200,11 @@ __device__ __forceinline__ unsigned need_of(const PoolArgs &a, const unsigned *n
 }
 
 // Of entries v at i .. i + 3 of the tables, those that want a block, as four bits.
-__device__ __forceinline__ int wants4(const PoolArgs &a, const unsigned *needs, int row0, int4 v, int i, int hi) {
+// (i is column col of row `row`.)
+__device__ __forceinline__ int wants4(const PoolArgs &a, const unsigned *needs, int row0, int4 v, int i, int hi,
+                                      int row, int col) {
   if ((v.x | v.y | v.z | v.w) >= 0) return 0;  // (no negative one; past hi they are 0)
   const int id[4] = {v.x, v.y, v.z, v.w};
-  int row = i / a.width;
-  int col = i - row * a.width;
   unsigned need = need_of(a, needs, row0, row);
   int f = 0;
 #pragma unroll
@@ -209,15 +218,16 @@ __device__ __forceinline__ int wants4(const PoolArgs &a, const unsigned *needs, 
   return f;
 }
 
+template <int C>
 __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs a) {
   __shared__ Totals tot;
   __shared__ unsigned needs[kNeeds];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
-  const Part pe = part_of(a.num_seqs * a.width, gw), pb = part_of(a.num_blocks, gw);
-  const int row0 = part_of(a.num_seqs * a.width, gw - warp).lo / a.width;
+  const int gw = (C == 1 ? 0 : (int)cluster_ctarank()) * kWarpsPerCta + warp;
+  const Part pe = part_of<C>(a.num_seqs * a.width, gw), pb = part_of<C>(a.num_blocks, gw);
+  const int row0 = part_of<C>(a.num_seqs * a.width, gw - warp).lo / a.width;
   const int len = row0 + (int)threadIdx.x < a.num_seqs ? __ldg(a.lens + row0 + threadIdx.x) : 0;
   Counts c, e;
   e.load(a.tables, pe.lo, pe.hi, 0);  // (all three loads under way before the first wait)
@@ -227,12 +237,13 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
   // the entries that want one; of the first steps the flags are kept, four bits a step
   constexpr int kFlagged = 8;
   unsigned flags = 0u;
-  int wanted = 0;
+  int wanted = 0, row = (pe.lo + 4 * lane) / a.width, col = pe.lo + 4 * lane - row * a.width;
   for (int lo = pe.lo; lo < pe.hi; lo += 128 * kSteps) {
     if (lo > pe.lo) e.load(a.tables, lo, pe.hi, 0);
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      const unsigned f = wants4(a, needs, row0, e.v[u], lo + 128 * u + 4 * lane, pe.hi);
+      const unsigned f = wants4(a, needs, row0, e.v[u], lo + 128 * u + 4 * lane, pe.hi, row, col);
+      for (col += 128; col >= a.width; col -= a.width) ++row;
       const int step = (lo - pe.lo) / 128 + u;
       if (step < kFlagged) flags |= f << (4 * step);
       wanted += __popc(f);
@@ -243,18 +254,19 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
     tot.of[0][warp] = wanted;
     tot.of[1][warp] = free;
   }
-  sync_cluster();
+  sync_all<C>();
   int want0, wants, free0, frees;
-  ranks(tot, 0, gw, want0, wants);
-  ranks(tot, 1, gw, free0, frees);
+  ranks<C>(tot, 0, gw, want0, wants);
+  ranks<C>(tot, 1, gw, free0, frees);
   list_free(a.refs, pb, c, free0, wants, a.list);
-  sync_cluster();  // the list is written, every count read
+  sync_all<C>();  // the list is written, every count read
   int at = want0;
   if (wanted > 0) {
     for (int i0 = pe.lo; i0 < pe.hi; i0 += 128) {
       const int i = i0 + 4 * lane, step = (i0 - pe.lo) / 128;
       const unsigned f = step < kFlagged ? flags >> (4 * step) & 15u
-                                         : wants4(a, needs, row0, load4(a.tables, i, pe.hi, 0), i, pe.hi);
+                                         : wants4(a, needs, row0, load4(a.tables, i, pe.hi, 0), i, pe.hi,
+                                                  i / a.width, i % a.width);
       const int mine = __popc(f);
       if (!__any_sync(0xffffffffu, mine > 0)) continue;
       int r = at + warp_before(mine);
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(1024, 1) reserve_blocks_kernel(const PoolArgs 
   }
   if (gw == 0 && lane == 0) *a.missing = max(0, wants - frees);
   // rows longer than the table, among those at hand and (parts of very many rows) the rest
-  const int rows_hi = part_of(a.num_seqs * a.width, gw - warp + kWarpsPerCta).lo / a.width;
+  const int rows_hi = part_of<C>(a.num_seqs * a.width, gw - warp + kWarpsPerCta).lo / a.width;
   bool over = needs[threadIdx.x] > (unsigned)a.width;
   for (int i = row0 + kNeeds + (int)threadIdx.x; i <= min(rows_hi, a.num_seqs - 1); i += 1024)
     over |= blocks_of(__ldg(a.lens + i), a.shift) > (unsigned)a.width;
@@ -312,13 +324,15 @@ __device__ __forceinline__ int parent_tail(const ForkArgs &a, int f, bool rec) {
   return bad ? -1 : id;
 }
 
+template <int C>
 __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) {
+  constexpr int kAllWarps = C * kWarpsPerCta;
   __shared__ Totals tot;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
-  const Part pb = part_of(a.num_blocks, gw);
+  const int gw = (C == 1 ? 0 : (int)cluster_ctarank()) * kWarpsPerCta + warp;
+  const Part pb = part_of<C>(a.num_blocks, gw);
   // forks in parts of whole warps: f = lo + lane, lo + lane + 32, ..
   const int per = (a.num_forks + kAllWarps * 32 - 1) / (kAllWarps * 32) * 32;
   const int lo = min(a.num_forks, gw * per), hi = min(a.num_forks, lo + per);
@@ -335,12 +349,12 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
     tot.of[0][warp] = tails;
     tot.of[1][warp] = free;
   }
-  sync_cluster();
+  sync_all<C>();
   int tail0, all, free0, frees;
-  ranks(tot, 0, gw, tail0, all);
-  ranks(tot, 1, gw, free0, frees);
+  ranks<C>(tot, 0, gw, tail0, all);
+  ranks<C>(tot, 1, gw, free0, frees);
   list_free(a.refs, pb, c, free0, all, a.list);
-  sync_cluster();  // the list is written, every count read
+  sync_all<C>();  // the list is written, every count read
   int at = tail0;
   for (int f0 = lo; f0 < hi; f0 += 32) {
     const int f = f0 + lane;
@@ -368,7 +382,7 @@ __global__ void __launch_bounds__(1024, 1) fork_blocks_kernel(const ForkArgs a) 
   int f = gw / share, s = 0, d = 0, len = 0;
   bool ok = f < a.num_forks && fork_pair(a, f, s, d);
   if (ok) len = max(0, __ldcg(a.lens + s));
-  sync_cluster();  // the tails' new blocks
+  sync_all<C>();  // the tails' new blocks
   while (f < a.num_forks) {
     if (ok) {
       const int full = min(len >> a.shift, a.width), fresh = __ldcg(a.tail_of + f);
@@ -407,22 +421,24 @@ struct CompactArgs {
   unsigned *err;
 };
 
+template <int C>
 __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactArgs a) {
+  constexpr int kAllWarps = C * kWarpsPerCta;
   __shared__ Totals tot;
   __shared__ int s_below;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int gw = (int)cluster_ctarank() * kWarpsPerCta + warp;
-  const Part p = part_of(a.num_blocks, gw);
+  const int gw = (C == 1 ? 0 : (int)cluster_ctarank()) * kWarpsPerCta + warp;
+  const Part p = part_of<C>(a.num_blocks, gw);
   if (threadIdx.x == 0) s_below = 0;
   Counts c;
   const int used = p.hi - p.lo - count_free(a.refs, p, c);
   const bool kept = p.hi - p.lo <= 128 * kSteps;
   if (lane == 0) tot.of[0][warp] = used;
-  sync_cluster();
+  sync_all<C>();
   int used0, live;
-  ranks(tot, 0, gw, used0, live);
+  ranks<C>(tot, 0, gw, used0, live);
   // used blocks below `live`: the warp whose part holds that border counts them
   if (p.lo < live && live <= p.hi) {
     int below = 0;
@@ -430,10 +446,10 @@ __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactAr
     below = warp_sum(below);
     if (lane == 0) s_below = used0 + below;
   }
-  sync_cluster();
+  sync_all<C>();
   int below = 0;
 #pragma unroll
-  for (int c = 0; c < kCluster; ++c) below += dsmem_ld_s32(dsmem_map(smem_u32(&s_below), c));
+  for (int c = 0; c < C; ++c) below += C == 1 ? s_below : dsmem_ld_s32(dsmem_map(smem_u32(&s_below), c));
   // the k-th used block at or past `live` goes to the k-th free one before it
   int at = used0;
   for (int lo = p.lo; lo < p.hi; lo += 128 * kSteps) {
@@ -474,13 +490,13 @@ __global__ void __launch_bounds__(1024, 1) compact_blocks_kernel(const CompactAr
     a.counts[0] = moves;
     a.counts[1] = live;
   }
-  sync_cluster();
+  sync_all<C>();
   for (int k = gw * 32 + lane; k < moves; k += kAllWarps * 32) {
     const int to = __ldcg(a.dst_blocks + k);
     a.name[__ldcg(a.src_blocks + k)] = to;
     a.refs_out[to] = __ldcg(a.moved + k);
   }
-  sync_cluster();
+  sync_all<C>();
   const int n = a.num_seqs * a.width;
 #pragma unroll 4
   for (int i = (gw * 32 + lane) * 4; i < n; i += kAllWarps * 128) {
@@ -542,24 +558,29 @@ __global__ void __launch_bounds__(kPieceThreads) copy_pages_kernel(const CopyArg
   }
 }
 
-// One cluster of kCluster thread blocks, as a dependent of the work before it.
-template <typename A>
+// One cluster of C thread blocks, as a dependent of the work before it.
+template <int C, typename A>
 cudaError_t launch_cluster(void (*kern)(A), cudaStream_t st, const A &args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(C);
   cfg.blockDim = dim3(kWarpsPerCta * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.x = C;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = C > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args);
 }
+
+// Whether one thread block alone is faster, whose barriers cost nothing.  Reserving in a
+// pool of 2048 blocks took it 7.1 us and the cluster 9.1, of 16,384 blocks both 9.7, of 65,536
+// 31 and 12; a fork in 8192 blocks 17 and 11, a compaction of 16,384 25 and 13.
+bool one_block(int num_blocks, int64_t entries) { return num_blocks <= 4096 && entries <= 4096; }
 
 // Sizes that the bookkeeping calls share.
 pa_status check_pool(int num_seqs, int max_blocks_per_seq, int num_blocks, int block_size) {
@@ -645,8 +666,11 @@ PA_API pa_status pa_reserve_blocks(int32_t *block_tables, int32_t *ref_counts, c
   a.shift = shift_of(block_size);
   a.err = error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
-  return launch_cluster(reserve_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
-                                                                                                    : PA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = one_block(num_blocks, (int64_t)num_seqs * max_blocks_per_seq)
+                            ? launch_cluster<1>(reserve_blocks_kernel<1>, s, a)
+                            : launch_cluster<kMaxCluster>(reserve_blocks_kernel<kMaxCluster>, s, a);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_fork_blocks(int32_t *block_tables, int32_t *context_lens, int32_t *ref_counts,
@@ -696,8 +720,11 @@ PA_API pa_status pa_fork_blocks(int32_t *block_tables, int32_t *context_lens, in
   a.shift = shift_of(block_size);
   a.err = error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
-  return launch_cluster(fork_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
-                                                                                                 : PA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = one_block(num_blocks, (int64_t)num_forks * max_blocks_per_seq)
+                            ? launch_cluster<1>(fork_blocks_kernel<1>, s, a)
+                            : launch_cluster<kMaxCluster>(fork_blocks_kernel<kMaxCluster>, s, a);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_compact_blocks(int32_t *block_tables_out, int32_t *ref_counts_out,
@@ -742,8 +769,11 @@ PA_API pa_status pa_compact_blocks(int32_t *block_tables_out, int32_t *ref_count
   a.num_blocks = num_blocks;
   a.err = error_word();
   if (a.err == nullptr) return PA_ERR_CUDA;
-  return launch_cluster(compact_blocks_kernel, static_cast<cudaStream_t>(stream), a) == cudaSuccess ? PA_OK
-                                                                                                    : PA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = one_block(num_blocks, (int64_t)num_seqs * max_blocks_per_seq)
+                            ? launch_cluster<1>(compact_blocks_kernel<1>, s, a)
+                            : launch_cluster<kMaxCluster>(compact_blocks_kernel<kMaxCluster>, s, a);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales, const int32_t *src_blocks,
