@@ -11,14 +11,17 @@
 // each operation rounded to fp32 by itself, so that the largest y does not depend on how
 // they are fused.
 //
-// Bound by memory: a row is read from it once and written once.  A cluster of up to 16 thread
-// blocks takes the rows of a sequence, each a slice of the vocabulary.  The softmax needs a
-// row's maximum and sum over all slices, and exchanging them row by row left the GPU waiting
-// (182 us for 64 x 8 rows of 131,071 bf16 logits, whether one thread block an SM held two
-// rows in registers or two held one each).  So a thread block first reads up to kBatch rows
-// and sums them, the cluster exchanges the sums of them all at once, and the rows are taken
-// again, last ones first: the last are in shared memory still, the others come from L2 (8
-// rows of every resident thread block are 80 MB of its 129).  Bulk copies bring the rows.
+// A row is read from memory once and written once.  A cluster of up to 16 thread blocks takes
+// the rows of a sequence, each a slice of the vocabulary.  The softmax needs a row's maximum
+// and sum over all slices, and exchanging them row by row left the GPU waiting (183 us for
+// 64 x 8 rows of 131,071 bf16 logits, 289 with one thread block of twice the threads an SM
+// and two rows in registers).  So a thread block first reads up to kBatch rows and sums them,
+// the cluster exchanges the sums of them all at once, and the rows are taken again, last ones
+// first: the last are in shared memory still, the others come from L2 (8 rows of every
+// resident thread block are 80 MB of its 129).  Bulk copies bring the rows.  174 us, where
+// the bytes take 61: the schedulers issue in 47 % of the clocks, between barriers, and the
+// reading and the writing half of all thread blocks fall together.  Batches of 4 rows 181,
+// of 2 196, of 4 and 8 by turns 181; 256 threads 185, three thread blocks of them an SM 207.
 // The entries that anything was counted for are few and lie anywhere: a slice keeps a list of
 // them in ascending order with their counts, and one bit an entry.  The dense pass masks
 // them out with the grammar's bits; the list's entries are gathered, adjusted and summed
@@ -227,7 +230,10 @@ __host__ __device__ inline Room room_of(int slice, int listed, int num_bias, int
   r.bias_v = take(num_bias * 4);
   r.bias_id = take(num_bias * 4);
   r.list = take(listed * 2);
-  r.total = at;
+  // a warp that any of its groups concerns reads them all: up to 255 elements and a shift of 7
+  // past the slice, in the last stage past its end
+  const int read = (m.stages - 1) * stage + (slice + 262) * elt;
+  r.total = at > read ? at : (read + 15) / 16 * 16;
   return r;
 }
 constexpr int kNarrowMost = (1 << 14) - 1;  // counts of 16 bits: 14 and two flags
