@@ -18,7 +18,7 @@
 // and two rows in registers).  So a thread block first reads up to kBatch rows and sums them,
 // the cluster exchanges the sums of them all at once, and the rows are taken again, last ones
 // first: the last are in shared memory still, the others come from L2 (8 rows of every
-// resident thread block are 80 MB of its 129).  Bulk copies bring the rows.  174 us, where
+// resident thread block are 80 MB of its 129).  Bulk copies bring the rows.  170 us, where
 // the bytes take 61: the schedulers issue in 47 % of the clocks, between barriers, and the
 // reading and the writing half of all thread blocks fall together.  Batches of 4 rows 181,
 // of 2 196, of 4 and 8 by turns 181; 256 threads 185, three thread blocks of them an SM 207.
@@ -48,6 +48,16 @@ namespace {
 __device__ __forceinline__ void sync_cluster() {
   __syncwarp();
   cluster_sync_all();
+}
+
+// The two halves of a cluster barrier that orders nothing: every thread block has started.
+__device__ __forceinline__ void cluster_started() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_all_started() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 constexpr int kThreads = 512;
@@ -202,8 +212,8 @@ __device__ __forceinline__ void dsmem_st_f32x2(uint32_t addr, float a, float b) 
 // (16 bits an entry, 32 where a history is too long for them), in the logits' place where
 // that leaves room for another thread block (shared); a batch's statistics by warp, and by thread
 // block; bits of counted entries, and of a row's mask and its dense elements, these with
-// zeros before and behind (a warp's last group may start 248 elements past the slice); counts and places of the listed entries; biases (id,
-// value).
+// zeros before and behind (a warp's last group may start 248 elements past the slice); counts
+// and places of the listed entries; biases (id, value).
 constexpr int kOnBehind = 9;  // words
 struct Room {
   int stage, step, counts, warps, blocks, touched, mask, on, cnt, bias_v, bias_id, list, total;
@@ -254,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     fence_mbar_init();
     s_bias_n = 0;
   }
+  if (PROBS) cluster_started();
   griddep_wait();
   griddep_launch_dependents();
   const int csize = (int)cluster_nctarank(), crank = (int)cluster_ctarank();
@@ -724,8 +735,12 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       };
       const float2 none = make_float2(-INFINITY, greedy ? __int_as_float(INT_MAX) : 0.f);
       static_assert(kBatch <= kWarps && kWarps <= 32 && kMaxCluster <= 32, "a warp a row");
-      // (the peers run, and have read the last batch's)
-      sync_cluster();
+      if (b0 == j0) {
+        cluster_all_started();
+        __syncthreads();  // the warps' pairs
+      } else {
+        sync_cluster();  // ... and the peers have read the last batch's
+      }
       const bool mine = warp < b1 - b0;
       if (mine) {
         float m;
