@@ -542,10 +542,12 @@ PA_API pa_status pa_decode_block_scaled(void *out, const void *q, const void *k_
  *   block_tables  an entry < 0 holds no block
  * The calls keep the counts in step with the tables; at the start every entry is -1 and every
  * count 0, or the counts are the entries' number.  Each call has one result, whatever the order
- * of its threads.  An entry outside the pool, or one whose block was not counted, sets
- * PA_ERR_DEVICE_CHECK and counts as none.  None of them touches a cache: with several
- * layers over one table they run once, and pa_copy_pages once a layer.  Arrays are 4-byte
- * aligned, block_tables (pa_fork_blocks apart), ref_counts and the workspace 16-byte aligned;
+ * of its threads.  An entry outside the pool that a call gives up, shares, copies or
+ * renames sets PA_ERR_DEVICE_CHECK and counts as none; so does one whose block has a count of
+ * 0 that is given up (pa_free_blocks) or stands past the pool's new front
+ * (pa_compact_blocks).  None of them touches a cache: with several layers over one table
+ * they run once, and pa_copy_pages once a layer.  A batch has at least one sequence.  Arrays
+ * are 4-byte aligned, block_tables (pa_fork_blocks apart), ref_counts and the workspace 16-byte aligned;
  * outputs overlap nothing else but where said.
  * Workspace: pa_pages_workspace_size(num_blocks, num_forks) bytes (num_forks 0 for the others);
  * two calls that can overlap need workspaces of their own.

@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     if (a.drafts != nullptr)
       for (int i = threadIdx.x; i < j0; i += kThreads) {
         const int v = __ldg(a.drafts + (int64_t)seq * (a.rows - 1) + i);
+        if (v >= a.vocab && crank == 0) record_error(a.err, kErrCheck);
         if (v >= lo && v < hi) {
           atomicAdd(at_of(v - lo), 1u << up_of(v - lo));
           touch(v - lo);
@@ -852,7 +853,7 @@ cudaError_t launch_slices(LogitArgs a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // slices of at most kMostSlice entries ; smaller ones, and rows apart, while the
+  // slices of at most kMostSlice entries; smaller ones, and rows apart, while the
   // clusters do not fill the GPU twice
   int cluster = 1;
   while (a.vocab > kMostSlice * cluster ||

@@ -265,3 +265,16 @@ def test_ids_outside_the_vocabulary(pa):
                dict(history_lens=i32([-1]), history=i32([[-1, -1, -1]]))):
         pa.pa_adjust_logits(None, x, **{**clean, **kw})
         assert pa.pa_device_error() == pa.PA_ERR_DEVICE_CHECK, kw
+
+
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("n", [1, 700])   # rows of their own thread blocks, and all rows in one
+@pytest.mark.parametrize("at", [0, 1, 3])
+def test_drafts_outside_the_vocabulary(pa, n, probs, at):
+    x = torch.ones(n, 5, 10, device=DEV)
+    drafts = torch.full((n, 4), 9, dtype=torch.int32, device=DEV)
+    pa.pa_adjust_logits(None, x, drafts=drafts, probs=probs)
+    assert pa.pa_device_error() == 0
+    drafts[n - 1, at] = 10
+    pa.pa_adjust_logits(None, x, drafts=drafts, probs=probs)
+    assert pa.pa_device_error() == pa.PA_ERR_DEVICE_CHECK
