@@ -18,7 +18,7 @@
 // and two rows in registers).  So a thread block first reads up to kBatch rows and sums them,
 // the cluster exchanges the sums of them all at once, and the rows are taken again, last ones
 // first: the last are in shared memory still, the others come from L2 (8 rows of every
-// resident thread block are 80 MB of its 129).  Bulk copies bring the rows.  170 us, where
+// resident thread block are 80 MB of its 129).  Bulk copies bring the rows.  148 us, where
 // the bytes take 61: the schedulers issue in 47 % of the clocks, between barriers, and the
 // reading and the writing half of all thread blocks fall together.  Batches of 4 rows 181,
 // of 2 196, of 4 and 8 by turns 181; 256 threads 185, three thread blocks of them an SM 207.
@@ -91,7 +91,6 @@ struct LogitArgs {
   unsigned *err;
 };
 
-// Eight elements of a row as they are read.
 // Bits 0-3 and 4-7 of `on` as the top bits of four bytes each (the shifted copies of four
 // bits do not meet); a byte permute then makes each a mask.
 __device__ __forceinline__ uint32_t top_bits(unsigned four) { return four * 0x10204080u; }
@@ -105,6 +104,7 @@ __device__ __forceinline__ uint32_t pair_mask(uint32_t top, bool high) {
   return d;
 }
 
+// Eight elements of a row as they are read.
 template <typename T>
 struct Eight {  // fp16, bf16: pairs
   uint32_t w[4];
@@ -171,6 +171,50 @@ struct Eight<float> {
   }
 };
 
+// Four, with what writing them to fp32 takes.
+template <typename T>
+struct Four {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(uint32_t at) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+  }
+  __device__ __forceinline__ void keep(unsigned on) {
+    constexpr uint32_t inf = Eight<T>::kNegInf;
+    const uint32_t a = top_bits(on & 15u), m0 = pair_mask(a, false), m1 = pair_mask(a, true);
+    w[0] = (w[0] & m0) | (inf & ~m0);
+    w[1] = (w[1] & m1) | (inf & ~m1);
+  }
+  __device__ __forceinline__ void no_nan() {
+    w[0] = Eight<T>::max2(w[0], Eight<T>::kNegInf);
+    w[1] = Eight<T>::max2(w[1], Eight<T>::kNegInf);
+  }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    const float2 f = Elt<T>::to_f2(w[0]), g = Elt<T>::to_f2(w[1]);
+    x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
+  }
+};
+template <>
+struct Four<float> {
+  float v[4];
+  __device__ __forceinline__ void load(uint32_t at) {
+    const uint4 a = lds128(at);
+    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y);
+    v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+  }
+  __device__ __forceinline__ void keep(unsigned on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = on >> i & 1 ? v[i] : -INFINITY;
+  }
+  __device__ __forceinline__ void no_nan() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaxf(v[i], -INFINITY);
+  }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v[i];
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ float load1(const T *p) {
   if constexpr (sizeof(T) == 4)
@@ -188,13 +232,9 @@ __device__ __forceinline__ void store1(T *p, float x) {
 // Eight values to a 16-byte boundary.
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-  } else {
-    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(Elt<T>::from_f2(x[0], x[1]), Elt<T>::from_f2(x[2], x[3]),
-                                                    Elt<T>::from_f2(x[4], x[5]), Elt<T>::from_f2(x[6], x[7])));
-  }
+  static_assert(sizeof(T) == 2, "fp32 is written in fours");
+  __stcs(reinterpret_cast<uint4 *>(p), make_uint4(Elt<T>::from_f2(x[0], x[1]), Elt<T>::from_f2(x[2], x[3]),
+                                                  Elt<T>::from_f2(x[4], x[5]), Elt<T>::from_f2(x[6], x[7])));
 }
 
 // 2^x, subnormal results to zero (a probability below 2^-126 of the largest)
@@ -542,20 +582,45 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     return PROBS ? fmaxf(y, -INFINITY) : y;  // NaN counts as -inf
   };
   // The dense elements of a row, each group through `value`, to out (of the row): whole groups
-  // with wide stores, if they lie on 16-byte boundaries there; the slice's ragged ends, at
+  // with wide stores, if they lie on 16-byte boundaries there (fp32 in fours, so that a warp's
+  // store fills whole 32-byte sectors; two stores of a thread's eight, half a sector each, took
+  // 171 us for 64 x 8 rows of 131,071 where this takes 148); the slice's ragged ends, at
   // most seven elements each, by a thread each.  (With both in one loop a group's eight
   // single stores are predicated off one by one: 5 instructions an element.)
   auto write = [&](const Row &r, O *out, auto value) {
     O *o = out + r.first;
     if ((reinterpret_cast<uintptr_t>(out + lo - r.shift) & 15u) == 0) {
+      if constexpr (sizeof(O) == 4) {
+        const int in_warp = 4 * lane - 8 * lane;  // (from the thread's eight)
+        const uint32_t at = r.base + in_warp * (int)sizeof(T);
+        const uint32_t b = 32u + (uint32_t)(r.first + in_warp - lo);
+        const unsigned *bits = on + (int)(b >> 5) - 1;
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        if (!there(r, k)) continue;
-        const int v0 = r.first + k * kStep;
-        float f[8];
-        dense(r, k).get(f);
-        value(v0, f);
-        if (v0 >= lo && v0 + 8 <= hi) store8(o + k * kStep, f);
+        for (int k = 0; k < VPT; ++k) {
+          if (!there(r, k)) continue;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int past = k * kStep + 128 * q, v0 = r.first + in_warp + past;
+            Four<T> x;
+            x.load(at + past * (uint32_t)sizeof(T));
+            x.keep(__funnelshift_r(bits[past / 32], bits[past / 32 + 1], b));
+            if (PROBS) x.no_nan();
+            float f[4];
+            x.get(f);
+            value(v0, f);
+            if (v0 >= lo && v0 + 4 <= hi) __stcs(reinterpret_cast<float4 *>(out + v0), make_float4(f[0], f[1], f[2], f[3]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          if (!there(r, k)) continue;
+          const int v0 = r.first + k * kStep;
+          float f[8];
+          dense(r, k).get(f);
+          value(v0, f);
+          if (v0 >= lo && v0 + 8 <= hi) store8(o + k * kStep, f);
+        }
       }
       // groups 0 and the last, unless they are whole
       const int n = hi - lo + r.shift;  // elements from group 0 on
@@ -607,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       if (behind >= a.vocab && crank == 0 && threadIdx.x == 0) record_error(a.err, kErrCheck);
       const bool known = e >= 0 && (touched[e >> 5] >> (e & 31) & 1u);
       behind = draft_of(j + 1);
-      write(r, out, [](int, float (&)[8]) {});
+      write(r, out, [](int, auto &) {});
       if (counted) {
         __syncthreads();  // the dense pass is written
         for (int i = threadIdx.x; i < entries; i += kThreads) store1(out + lo + list[i], adjusted(r, i));
@@ -770,14 +835,14 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         const float M = stat.x, mul = stat.y;
         const int best = greedy ? __float_as_int(stat.y) : INT_MAX;
         if (!greedy && fabsf(M) != INFINITY) {
-          write(r, out, [&](int, float (&f)[8]) {
+          write(r, out, [&](int, auto &f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = ex2_flush((f[i] - M) * fac) * mul;
+            for (int i = 0; i < (int)(sizeof(f) / 4); ++i) f[i] = ex2_flush((f[i] - M) * fac) * mul;
           });
         } else {  // one, none, or the infinite ones
-          write(r, out, [&](int v0, float (&f)[8]) {
+          write(r, out, [&](int v0, auto &f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < (int)(sizeof(f) / 4); ++i)
               f[i] = greedy || M == -INFINITY ? (v0 + i == best ? 1.f : 0.f) : weight(f[i], M) * mul;
           });
         }
