@@ -270,7 +270,10 @@ __host__ __device__ inline Room room_of(int slice, int listed, int num_bias, int
   };
   r.step = stage;
   r.stage = r.counts = take(m.shared && counts > m.stages * stage ? counts : m.stages * stage);
-  if (!m.shared) r.counts = take(counts);
+  if (!m.shared)
+    r.counts = take(counts);
+  else if (m.stages > 1 && counts <= stage)
+    r.counts += stage;  // the second row's: the first is on its way while the list is made
   r.warps = take(kBatch * kWarps * 8);
   r.blocks = take(kBatch * cluster * 8);
   r.touched = take(slice / 8);
@@ -361,7 +364,40 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   auto fetch_first = [&](int j) {  // (one thread) the first rows of those from j on
     for (int i = 0; i < min(j1 - j, stages); ++i) fetch(j + i, i);
   };
-  if (threadIdx.x == 0 && !a.modes.shared) fetch_first(j0);
+  // (of those that counts stand in the place of: all, or all but the first)
+  const bool whole = a.modes.shared && room.counts == room.stage;
+  auto fetch_rest = [&] {
+    for (int i = whole ? 0 : 1; i < min(j1 - j0, stages); ++i) fetch(j0 + i, i);
+  };
+  if (threadIdx.x == 0) {
+    if (!a.modes.shared)
+      fetch_first(j0);
+    else if (!whole)
+      fetch(j0, 0);
+  }
+  // what the list and the rows take of the sequence is all on its way at once; of the history
+  // also what may be past its length
+  constexpr int kAhead = 8;
+  int ids_ahead[kAhead], hist_n = 0, prompt = 0, bias_ahead = -1;
+  float bias_v_ahead = 0.f;
+  const int32_t *ids = a.history + (int64_t)seq * a.max_history;
+  if (a.history != nullptr) {
+    hist_n = __ldg(a.history_lens + seq);
+    if (a.prompt_lens) prompt = __ldg(a.prompt_lens + seq);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = threadIdx.x + u * kThreads;
+      ids_ahead[u] = i < a.max_history ? __ldg(ids + i) : -1;
+    }
+  }
+  if (warp == 0 && lane < a.num_bias) {
+    bias_ahead = __ldg(a.bias_ids + (int64_t)seq * a.num_bias + lane);
+    bias_v_ahead = __ldg(a.bias_values + (int64_t)seq * a.num_bias + lane);
+  }
+  const float rep = a.repetition ? __ldg(a.repetition + seq) : 1.f;
+  const float pres = a.presence ? __ldg(a.presence + seq) : 0.f;
+  const float freq = a.frequency ? __ldg(a.frequency + seq) : 0.f;
+  const float temp = a.temperature ? __ldg(a.temperature + seq) : 1.f;
 
   // ---- the list of counted entries
   int entries = 0;
@@ -377,14 +413,9 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     auto up_of = [&](int e) { return wide ? 0 : (e & 1) * 16; };
     auto touch = [&](int e) { atomicOr(touched + (e >> 5), 1u << (e & 31)); };
     if (a.history != nullptr) {
-      int n = __ldg(a.history_lens + seq);
-      if ((n < 0 || n > a.max_history) && threadIdx.x == 0 && crank == 0) record_error(a.err, kErrCheck);
-      n = min(max(n, 0), a.max_history);
-      const int prompt = a.prompt_lens ? __ldg(a.prompt_lens + seq) : 0;
-      const int32_t *ids = a.history + (int64_t)seq * a.max_history;
-#pragma unroll 4
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int v = __ldg(ids + i);
+      if ((hist_n < 0 || hist_n > a.max_history) && threadIdx.x == 0 && crank == 0) record_error(a.err, kErrCheck);
+      const int n = min(max(hist_n, 0), a.max_history);
+      auto put = [&](int i, int v) {
         if (v >= a.vocab && crank == 0) record_error(a.err, kErrCheck);
         if (v >= lo && v < hi) {
           const int e = v - lo;
@@ -394,7 +425,12 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
             atomicAdd(at_of(e), 1u << up_of(e));
           touch(e);
         }
-      }
+      };
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if ((int)threadIdx.x + u * kThreads < n) put(threadIdx.x + u * kThreads, ids_ahead[u]);
+#pragma unroll 4
+      for (int i = threadIdx.x + kAhead * kThreads; i < n; i += kThreads) put(i, __ldg(ids + i));
     }
     if (a.drafts != nullptr)
       for (int i = threadIdx.x; i < j0; i += kThreads) {
@@ -410,14 +446,15 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
       int n = 0;
       for (int i0 = 0; i0 < a.num_bias; i0 += 32) {
         const int i = i0 + lane;
-        const int v = i < a.num_bias ? __ldg(a.bias_ids + (int64_t)seq * a.num_bias + i) : -1;
+        int v = bias_ahead;
+        if (i0 > 0) v = i < a.num_bias ? __ldg(a.bias_ids + (int64_t)seq * a.num_bias + i) : -1;
         if (v >= a.vocab && crank == 0) record_error(a.err, kErrCheck);
         const bool mine = v >= lo && v < hi;
         const unsigned who = __ballot_sync(0xffffffffu, mine);
         if (mine) {
           const int at = n + __popc(who & ((1u << lane) - 1u));
           bias_id[at] = v - lo;
-          bias_v[at] = __ldg(a.bias_values + (int64_t)seq * a.num_bias + i);
+          bias_v[at] = i0 == 0 ? bias_v_ahead : __ldg(a.bias_values + (int64_t)seq * a.num_bias + i);
           atomicOr(at_of(v - lo), bias_bit << up_of(v - lo));
           touch(v - lo);
         }
@@ -450,19 +487,15 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     if (a.modes.shared) {  // the counts are read: their place may be copied to
       fence_proxy_async_smem();
       __syncthreads();
-      if (threadIdx.x == 0) fetch_first(j0);
+      if (threadIdx.x == 0) fetch_rest();
     }
   } else if (a.modes.shared && threadIdx.x == 0) {
-    fetch_first(j0);
+    fetch_rest();
   }
   if (threadIdx.x <= kOnBehind) on[threadIdx.x == 0 ? -1 : words + (int)threadIdx.x - 1] = 0u;
   // which of the word's entries are the slice's
   const int ahead = hi - lo - 32 * (int)threadIdx.x;
   const unsigned valid = ahead >= 32 ? ~0u : ahead <= 0 ? 0u : (1u << ahead) - 1u;
-  const float rep = a.repetition ? __ldg(a.repetition + seq) : 1.f;
-  const float pres = a.presence ? __ldg(a.presence + seq) : 0.f;
-  const float freq = a.frequency ? __ldg(a.frequency + seq) : 0.f;
-  const float temp = a.temperature ? __ldg(a.temperature + seq) : 1.f;
   const bool greedy = PROBS && !(temp > 0.f);
   // the exponent's factor; kept finite and above zero, so that -inf stays -inf
   const float fac = fminf(fmaxf(1.4426950408889634f / temp, 1e-38f), FLT_MAX);
