@@ -34,6 +34,7 @@
 #include <atomic>
 #include <cfloat>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include "../../include/pagedattn.h"
@@ -951,20 +952,33 @@ cudaError_t launch_slices(LogitArgs a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // slices of at most kMostSlice entries; smaller ones, and rows apart, while the
-  // clusters do not fill the GPU twice
+  // slices of at most kMostSlice entries; smaller ones while the clusters do not fill the GPU
+  // twice
   int cluster = 1;
   while (a.vocab > kMostSlice * cluster ||
          (cluster < 8 && a.vocab > 2048 * cluster && (int64_t)a.num_seqs * cluster < 2 * sms))
     cluster *= 2;
-  const int64_t units = (int64_t)a.num_seqs * cluster;
-  a.row_groups = (int)std::min<int64_t>(a.rows, std::max<int64_t>(1, (2 * sms + units - 1) / units));
   a.slice = ((a.vocab + cluster - 1) / cluster + 31) / 32 * 32;
-  if ((int64_t)units * a.row_groups >= (int64_t)1 << 31) return cudaErrorInvalidConfiguration;
   // every entry of a slice may be counted, and no more than there are ids
   const int64_t ids = (int64_t)(a.history ? a.max_history : 0) + (a.drafts ? a.rows - 1 : 0) + a.num_bias;
   a.listed = (int)std::min<int64_t>(ids, a.slice);
   const int wide = ids > kNarrowMost;
+  // Row groups: so many that the rounds of clusters take least, each of a group's rows and what a
+  // thread block starts and ends with (as long as a row).  Places for clusters: nine tenths
+  // of the SMs' (the GPU's parts hold whole ones: 34 of 8, two thread blocks an SM, were
+  // counted).  A single round takes its time however few clusters are in it, since two share
+  // their SMs all the same; of further rounds a part of the last one's gap (fitted to 1 to 128
+  // sequences).  (As many groups as give every SM two thread blocks: 52 us for 16 x 8 rows of
+  // 131,071, this 41; 32 and 25 for 8 x 8, 78 and 73 for 32 x 8, 111 and 96 for 40 x 8.)
+  const bool two = room_of(a.slice, a.listed, a.num_bias, cluster, sizeof(T), Modes{wide, 1, 1}).total <= kMostShared / 2;
+  const double places = std::max(1, sms * (two ? 18 : 9) / 10 / cluster);
+  double least = 0.;
+  for (int g = 1; g <= std::min(a.rows, 64); ++g) {
+    const double w = (double)a.num_seqs * g / places, c = std::ceil(w);
+    const double time = (c <= 1. ? 1. : w + (c - w) / (c * c - 1.)) * ((a.rows + g - 1) / g + 1);
+    if (g == 1 || time < least) least = time, a.row_groups = g;
+  }
+  if ((int64_t)a.num_seqs * cluster * a.row_groups >= (int64_t)1 << 31) return cudaErrorInvalidConfiguration;
   const int per = (a.rows + a.row_groups - 1) / a.row_groups;
   // two thread blocks an SM where they fit, with a row ahead if that fits too
   const struct {
