@@ -14,7 +14,9 @@
 // Bound by memory: two bytes read and one written an element.  One warp takes the rows of
 // one (block, KV head) of K or of V: it holds the new rows in registers (16 of 16 tokens:
 // 32 registers a lane) between the maximum and the rounding, so they are read once, with
-// every 16-byte load under way before the first use.
+// every 16-byte load under way before the first use.  16 x 512 tokens of 32 heads take 35.1 us,
+// 5.75 TB/s or 0.85 of a plain copy's rate; one token of 64 sequences and 8 heads 7.0 with the
+// call, a chain of dependent loads (length, table, scale).
 #include <algorithm>
 
 #include "../../include/pagedattn.h"

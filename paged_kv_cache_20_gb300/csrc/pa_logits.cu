@@ -11,17 +11,19 @@
 // each operation rounded to fp32 by itself, so that the largest y does not depend on how
 // they are fused.
 //
-// A row is read from memory once and written once.  A cluster of up to 16 thread blocks takes
-// the rows of a sequence, each a slice of the vocabulary.  The softmax needs a row's maximum
-// and sum over all slices, and exchanging them row by row left the GPU waiting (183 us for
-// 64 x 8 rows of 131,071 bf16 logits, 289 with one thread block of twice the threads an SM
-// and two rows in registers).  So a thread block first reads up to kBatch rows and sums them,
-// the cluster exchanges the sums of them all at once, and the rows are taken again, last ones
-// first: the last are in shared memory still, the others come from L2 (8 rows of every
-// resident thread block are 80 MB of its 129).  Bulk copies bring the rows.  148 us, where
-// the bytes take 61: the schedulers issue in 47 % of the clocks, between barriers, and the
-// reading and the writing half of all thread blocks fall together.  Batches of 4 rows 181,
-// of 2 196, of 4 and 8 by turns 181; 256 threads 185, three thread blocks of them an SM 207.
+// A cluster of up to 16 thread blocks takes the rows of a sequence, each a slice of the
+// vocabulary.  The softmax needs a row's maximum and sum over all slices, and exchanging them
+// row by row left the GPU waiting.  So a thread block first reads up to kBatch rows and sums
+// them, the cluster exchanges the sums of them all at once, and the rows are taken again, last
+// ones first: the last are in shared memory still, the others are read again, in part from
+// L2 (keeping them there by a cache hint: no faster).  Bulk copies bring the rows.  64 x 8
+// rows of 131,071 bf16 logits take 144 us, where the bytes read and written once take 61: the
+// schedulers issue in 60 % of the clocks, and 34 clusters of 8 run at once, so that these are
+// two rounds.  Against 174 us (before fp32 was stored in whole sectors, 26 us, and the list's
+// inputs loaded at once): an exchange a row 183, batches of 4 rows 181, of 2 196, of 4 and 8
+// by turns 181; 256 threads 185, three thread blocks of them an SM 207; one thread block of
+// 1024 threads an SM and two rows in registers 289; one barrier a row, with the bits of two
+// rows side by side, 178 against 171 (registers).
 // The entries that anything was counted for are few and lie anywhere: a slice keeps a list of
 // them in ascending order with their counts, and one bit an entry.  The dense pass masks
 // them out with the grammar's bits; the list's entries are gathered, adjusted and summed
