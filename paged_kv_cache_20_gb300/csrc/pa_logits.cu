@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     const uint32_t bar = smem_u32(&s_bar[slot]);
     mbar_arrive_expect_tx(bar, (uint32_t)(c1 - c0));
     if (c1 > c0)
-      bulk_load(smem_u32(s_raw + room.stage + slot * room.step) + (uint32_t)(c0 - base), reinterpret_cast<const void *>(c0), (uint32_t)(c1 - c0), bar);
+      bulk_load(smem_u32(s_raw + room.stage + slot * room.step) + (uint32_t)(c0 - base),
+                reinterpret_cast<const void *>(c0), (uint32_t)(c1 - c0), bar);
   };
   // the thread's word of a row's mask (entries past the vocabulary are not the slice's)
   const unsigned *mask_at = nullptr;
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     O *o = out + r.first;
     if ((reinterpret_cast<uintptr_t>(out + lo - r.shift) & 15u) == 0) {
       if constexpr (sizeof(O) == 4) {
-        const int in_warp = 4 * lane - 8 * lane;  // (from the thread's eight)
+        const int in_warp = -4 * lane;  // its four from its eight: the warp's start and 4 lane
         const uint32_t at = r.base + in_warp * (int)sizeof(T);
         const uint32_t b = 32u + (uint32_t)(r.first + in_warp - lo);
         const unsigned *bits = on + (int)(b >> 5) - 1;

@@ -812,10 +812,9 @@ PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales, c
   // how many pairs there are is known on the device alone: at most a wave of thread blocks
   const int x = 2 * a.pieces;
   const int y = std::min(std::min(max_pairs, 65535), std::max(1, sms * 8 / x));
-  return launch_dependent(copy_pages_kernel, dim3((unsigned)x, (unsigned)y, 1), kPieceThreads, static_cast<cudaStream_t>(stream), a) ==
-                 cudaSuccess
-             ? PA_OK
-             : PA_ERR_CUDA;
+  const cudaError_t e = launch_dependent(copy_pages_kernel, dim3((unsigned)x, (unsigned)y, 1), kPieceThreads,
+                                         static_cast<cudaStream_t>(stream), a);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"
