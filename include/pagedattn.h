@@ -507,7 +507,8 @@ PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *num_accepted, in
  * subnormal.  After a rejection the next step overwrites the rejected rows; the scale keeps
  * what they needed.  Positions < 0 are skipped; positions beyond the table or the pool are
  * skipped and set PA_ERR_DEVICE_CHECK.  A block that is written must belong to one sequence
- * (pa_fork_blocks sees to it).  num_seqs == 0 is a no-op.
+ * (pa_fork_blocks sees to it).  Caches and scales overlap nothing else.  num_seqs == 0 is a
+ * no-op.
  */
 PA_API pa_status pa_append_kv_block_scaled(void *k_cache, void *v_cache, float *kv_scales,
                                            const void *k_new, const void *v_new,

@@ -196,6 +196,22 @@ extern "C" PA_API pa_status pa_append_kv_block_scaled(
       (int64_t)num_seqs * q_len * num_kv_heads >= (int64_t)1 << 31)
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return PA_OK;
+  const int64_t tokens = (int64_t)num_seqs * q_len;
+  for (const int64_t st : {k_stride, v_stride})
+    if (st > ((int64_t)1 << 58) / tokens) return PA_ERR_INVALID_ARG;  // (past every address)
+  // the caches and their scales apart from one another and from what is read (k_new and v_new may
+  // be slices of one array)
+  const size_t cache = (size_t)num_blocks * num_kv_heads * block_size * head_dim;
+  struct {
+    const void *p;
+    size_t n;
+  } buf[] = {{k_cache, cache}, {v_cache, cache}, {kv_scales, (size_t)num_blocks * num_kv_heads * 8},
+             {k_new, (size_t)((tokens - 1) * k_stride + width) * 2},
+             {v_new, (size_t)((tokens - 1) * v_stride + width) * 2},
+             {block_tables, (size_t)num_seqs * max_blocks_per_seq * 4}, {context_lens, (size_t)num_seqs * 4}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 7; ++j)
+      if (overlap(buf[i].p, buf[i].n, buf[j].p, buf[j].n)) return PA_ERR_INVALID_ARG;
   AppendArgs a;
   a.cache[0] = static_cast<uint8_t *>(k_cache);
   a.cache[1] = static_cast<uint8_t *>(v_cache);
