@@ -582,8 +582,9 @@ PA_API pa_status pa_decode_block_scaled(void *out, const void *q, const void *k_
  *
  * pa_copy_pages -- whole blocks src_blocks[p] -> dst_blocks[p], p < min(counts[0], max_pairs),
  * K, V and (kv_scales non-NULL) their scales, bit for bit; element_bytes 2 (16-bit pools) or 1
- * (head_dim 128).  Ids outside the pool are skipped and set PA_ERR_DEVICE_CHECK.  A destination
- * that is also a source or another pair's destination: undefined result.
+ * (head_dim 128).  Caches and scales overlap nothing else.  Ids outside the pool are skipped
+ * and set PA_ERR_DEVICE_CHECK.  A destination that is also a source or another pair's
+ * destination: undefined result.
  */
 PA_API size_t pa_pages_workspace_size(int num_blocks, int num_forks);
 PA_API pa_status pa_free_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *keep_lens,

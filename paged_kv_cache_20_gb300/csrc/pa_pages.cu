@@ -791,6 +791,17 @@ PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales, c
   if (kv_scales && element_bytes != 1) return PA_ERR_INVALID_ARG;
   if ((int64_t)num_blocks * num_kv_heads * 2 >= (int64_t)1 << 31) return PA_ERR_INVALID_ARG;
   if (max_pairs == 0) return PA_OK;
+  // the caches and their scales apart from one another and from the lists (which may be one array)
+  const size_t cache = (size_t)num_blocks * num_kv_heads * block_size * head_dim * element_bytes;
+  const size_t scales = kv_scales ? (size_t)num_blocks * num_kv_heads * 8 : 0;
+  struct {
+    const void *p;
+    size_t n;
+  } buf[] = {{k_cache, cache}, {v_cache, cache}, {kv_scales, scales}, {src_blocks, ints(max_pairs)},
+             {dst_blocks, ints(max_pairs)}, {counts, 8}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 6; ++j)
+      if (buf[i].n && buf[j].n && overlap(buf[i].p, buf[i].n, buf[j].p, buf[j].n)) return PA_ERR_INVALID_ARG;
   CopyArgs a = {};
   a.cache[0] = static_cast<uint4 *>(k_cache);
   a.cache[1] = static_cast<uint4 *>(v_cache);

@@ -1,15 +1,16 @@
-"""Arguments of the block-scaled append that overlap: refused before a launch (no GPU needed)."""
+"""Arguments of the block-scaled append and of the pages' copy that overlap: refused before a
+launch (no GPU needed)."""
 import pytest
 import torch
 
 from tests.test_abi import lib  # noqa: F401  (fixture)
-from tests.test_pool_abi import APPEND, INVALID, _call
+from tests.test_pool_abi import APPEND, COPY, INVALID, _call
 
 AT = 0x1000000  # never used: the calls are refused, or (without a GPU) fail at their first step
 
 accepted = pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call would use its pointers")
 
-SEQS, TOKENS, HEADS, BLOCKS, WIDTH = 2, 3, 2, 8, 4
+SEQS, TOKENS, HEADS, BLOCKS, WIDTH, PAIRS = 2, 3, 2, 8, 4, 5
 CACHE, SCALES = BLOCKS * HEADS * 16 * 128, BLOCKS * HEADS * 8
 ROWS = SEQS * TOKENS * HEADS * 128 * 2
 TABLE, LENS = SEQS * WIDTH * 4, SEQS * 4
@@ -28,6 +29,7 @@ def placed(base, names, **sizes):
 
 
 append = placed(APPEND, ("kc", "vc", "sc", "k", "v", "bt", "cl"), n=SEQS, u=TOKENS, hkv=HEADS, nb=BLOCKS, maxb=WIDTH)
+copy = placed(COPY, ("kc", "vc", "sc", "sb", "db", "cnt"), most=PAIRS, hkv=HEADS, nb=BLOCKS)
 
 
 @pytest.mark.parametrize("kw", [
@@ -51,3 +53,24 @@ def test_append(lib, kw):  # noqa: F811
 ])
 def test_append_beside(lib, kw):  # noqa: F811
     assert _call(lib, "pa_append_kv_block_scaled", APPEND, kw) != INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    copy(vc=("kc", 0)), copy(vc=("kc", CACHE - 16)), copy(kc=("vc", CACHE - 16)), copy(sc=("kc", CACHE - 4)),
+    copy(sc=("vc", 4 - SCALES)), copy(sb=("kc", 0)), copy(sb=("vc", CACHE - 4)), copy(db=("kc", 4 - 4 * PAIRS)),
+    copy(db=("sc", 0)), copy(sb=("sc", SCALES - 4)), copy(cnt=("kc", 16)), copy(cnt=("vc", -4)), copy(cnt=("sc", -4)),
+    {**copy(vc=("kc", CACHE)), "sc": None, "eb": 2},                  # pages of 16 bits
+])
+def test_copy(lib, kw):  # noqa: F811
+    assert _call(lib, "pa_copy_pages", COPY, kw) == INVALID
+
+
+@accepted
+@pytest.mark.parametrize("kw", [
+    copy(), copy(vc=("kc", CACHE)), copy(kc=("vc", CACHE)), copy(sc=("kc", CACHE)), copy(sc=("vc", -SCALES)),
+    copy(sb=("kc", CACHE)), copy(db=("kc", -4 * PAIRS)), copy(sb=("sc", SCALES)), copy(cnt=("vc", -8)),
+    copy(sb=("db", 0)), copy(cnt=("sb", 4)), {**copy(vc=("kc", 2 * CACHE)), "sc": None, "eb": 2},
+    {**copy(sb=("kc", 0)), "sc": None, "most": 0},                    # (nothing listed: a no-op)
+])
+def test_copy_beside(lib, kw):  # noqa: F811
+    assert _call(lib, "pa_copy_pages", COPY, kw) != INVALID
