@@ -501,8 +501,11 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   const int ahead = hi - lo - 32 * (int)threadIdx.x;
   const unsigned valid = ahead >= 32 ? ~0u : ahead <= 0 ? 0u : (1u << ahead) - 1u;
   const bool greedy = PROBS && !(temp > 0.f);
-  // the exponent's factor; kept finite and above zero, so that -inf stays -inf
-  const float fac = fminf(fmaxf(1.4426950408889634f / temp, 1e-38f), FLT_MAX);
+  // The exponent (x - m) / temp log2(e) from half the difference, which does not overflow where
+  // logits of both signs lie near fp32's ends (under temperatures as large that counts), and twice
+  // the factor, kept finite and above zero (the least subnormal for an infinite temperature), so
+  // that -inf stays -inf.
+  const float fac = fminf(fmaxf(2.8853900817779268f / temp, 1e-45f), FLT_MAX);
   __syncthreads();  // the copies' barriers and the list
 
   auto adjust = [&](float x, int e, unsigned w) {
@@ -515,12 +518,14 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     }
     return x;
   };
-  // 2^((x - m) fac) against a maximum m; with an infinite m the entries that reach it.  (One
+  // 2^((x/2 - hm) fac), hm = m/2: the halves are exact, the difference is rounded once.  (One
   // multiply-add with m fac rounded beforehand saves an instruction an element and no time,
   // and the largest weights, exact here, carry exp2's error there: 5e-7 of a row against
   // 1e-7.)
+  auto expo = [&](float x, float hm) { return ex2_flush(fmaf(x, 0.5f, -hm) * fac); };
+  // ... against a maximum m; with an infinite m the entries that reach it.
   auto weight = [&](float x, float m) {
-    return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : ex2_flush((x - m) * fac);
+    return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : expo(x, 0.5f * m);
   };
 
   // ---- the rows, one after the other in either direction
@@ -804,13 +809,14 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
             }
           } else if (m != -INFINITY) {
             float sum[2] = {0.f, 0.f};
+            const float hm = 0.5f * m;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
               if (!there(r, k)) continue;
               float f[8];
               again(k, f);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) sum[i & 1] += ex2_flush((f[i] - m) * fac);
+              for (int i = 0; i < 8; ++i) sum[i & 1] += expo(f[i], hm);
             }
             second += sum[0] + sum[1];
           }
@@ -872,9 +878,10 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         const float M = stat.x, mul = stat.y;
         const int best = greedy ? __float_as_int(stat.y) : INT_MAX;
         if (!greedy && fabsf(M) != INFINITY) {
+          const float hm = 0.5f * M;
           write(r, out, [&](int, auto &f) {
 #pragma unroll
-            for (int i = 0; i < (int)(sizeof(f) / 4); ++i) f[i] = ex2_flush((f[i] - M) * fac) * mul;
+            for (int i = 0; i < (int)(sizeof(f) / 4); ++i) f[i] = expo(f[i], hm) * mul;
           });
         } else {  // one, none, or the infinite ones
           write(r, out, [&](int v0, auto &f) {
