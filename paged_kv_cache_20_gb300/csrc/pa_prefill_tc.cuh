@@ -919,13 +919,14 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
         const int gg = g + j;
         const int b = gg % 3;
         const uint32_t ts = trow + Lay::kColS + kTcChunk * b + 64 * hc;  // this warp's columns
-        [[maybe_unused]] const float4 *scl = s_scl[BSC ? warp - kSoft0 : 0][BSC ? j & 1 : 0];
+        [[maybe_unused]] const float4 *scl = s_scl[BSC ? warp - kSoft0 : 0][BSC ? gg & 1 : 0];
         if constexpr (BSC) {
-          // this chunk's scales to the warp's rows (the slot's last readers, two chunks ago,
-          // are behind the barriers of the last one), the next chunk's loads on their way
+          // this chunk's scales to the warp's rows (the slot's last readers, the warp's own lanes two
+          // chunks ago, in this unit or the last, are behind the exchange of the chunk between),
+          // the next chunk's loads on their way
           if (lane < kRuns) {
             const float sv1 = clamp_scale(scl_next.y);
-            s_scl[warp - kSoft0][j & 1][lane] =
+            s_scl[warp - kSoft0][gg & 1][lane] =
                 make_float4(clamp_scale(scl_next.x), log2_of_scale(sv1), inverse_of_scale(sv1), 0.f);
           }
           scl_next = scales_at(cu, id_next);
