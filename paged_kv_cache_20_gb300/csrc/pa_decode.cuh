@@ -990,6 +990,11 @@ __device__ __forceinline__ uint32_t e4m3_lo_f16x2(uint32_t w) {
 __device__ __forceinline__ uint32_t e4m3_hi_f16x2(uint32_t w) {
   return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
 }
+// The power of two that brings a q row of largest magnitude mx into fp16's range: times 2^-e it is
+// below 2.  (Not below -126: of a row of subnormal bf16 values 2^-e has to be finite.)
+__device__ __forceinline__ int q_exponent(float mx) {
+  return mx > 0.f && isfinite(mx) ? max(ilogbf(mx), -126) : 0;
+}
 
 // ---------------------------------------------------------------------------------
 // FP8 (e4m3) cache, tensor-core path with swapped operands for 3..8 rows per KV
@@ -1044,7 +1049,7 @@ struct Mma8TPath {
     // the 4 lanes holding row g agree on its maximum
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const int e_row = (mx > 0.f && isfinite(mx)) ? ilogbf(mx) : 0;
+    const int e_row = q_exponent(mx);
     const float down = ldexpf(1.f, -e_row);  // |q| * down < 2: well inside fp16
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -1419,7 +1424,7 @@ struct Mma8Path {
     float down[2];
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
-      const int e = (mx[hr] > 0.f && isfinite(mx[hr])) ? ilogbf(mx[hr]) : 0;
+      const int e = q_exponent(mx[hr]);
       down[hr] = ldexpf(1.f, -e);           // |q| * down < 2: well inside fp16
       inner.rs[hr] = sscale * ldexpf(1.f, e);
     }

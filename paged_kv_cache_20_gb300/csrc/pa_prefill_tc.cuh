@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(KV8 ? kTcThreads8 : kTcThreads, 1)
             }
           }
         }
-        e_row = (mx > 0.f && isfinite(mx)) ? ilogbf(mx) : 0;
+        e_row = q_exponent(mx);
         down = ldexpf(1.f, -e_row);  // |q| * down < 2: well inside fp16
       }
 #pragma unroll
