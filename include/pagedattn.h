@@ -507,7 +507,7 @@ PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *num_accepted, in
  * subnormal.  After a rejection the next step overwrites the rejected rows; the scale keeps
  * what they needed.  Positions < 0 are skipped; positions beyond the table or the pool are
  * skipped and set PA_ERR_DEVICE_CHECK.  A block that is written must belong to one sequence
- * (pa_fork_blocks sees to it).  Caches and scales overlap nothing else.  num_seqs == 0 is a
+ * (pa_fork_blocks sees to it, unless a length is taken back into a block that was shared).  Caches and scales overlap nothing else.  num_seqs == 0 is a
  * no-op.
  */
 PA_API pa_status pa_append_kv_block_scaled(void *k_cache, void *v_cache, float *kv_scales,
@@ -569,7 +569,8 @@ PA_API pa_status pa_decode_block_scaled(void *out, const void *q, const void *k_
  * there on are left as they were.  counts[1] = forks that found no free block: these get
  * their parent's full blocks and that length.  What dst's row held before is overwritten,
  * not freed.  Every dst_seqs[f] is another sequence, and none of src_seqs (else the result is
- * undefined); ids outside the batch, or src == dst, set PA_ERR_DEVICE_CHECK and are skipped.
+ * undefined); ids outside the batch, or src == dst, set PA_ERR_DEVICE_CHECK and are skipped.  A
+ * parent's length past its table sets it too and counts as the table's.
  *   src_seqs, dst_seqs, src_blocks, dst_blocks  int32 [num_forks <= num_seqs] (num_forks 0:
  *   counts alone are written); counts int32 [2]
  *
@@ -626,9 +627,11 @@ PA_API pa_status pa_copy_pages(void *k_cache, void *v_cache, float *kv_scales,
  * -1 to it).
  *   logits       [num_seqs][rows][logits_stride], vocab used; fp16, bf16 or fp32 (dtype)
  *   out          [num_seqs][rows][out_stride]; may be logits itself where type and stride
- *                are the same, and overlaps nothing else
+ *                are the same, and overlaps nothing else.  (Fastest with equal strides: a row
+ *                whose start in out, modulo the elements of 16 bytes there, is another than
+ *                that of its logits is stored element by element.)
  *   history      int32 [num_seqs][max_history], history_lens, prompt_lens int32 [num_seqs]
- *                (prompt_lens NULL: no prompt)
+ *                (prompt_lens NULL: no prompt; max_history 0: none of the three is read)
  *   drafts       int32 [num_seqs][rows - 1]
  *   repetition, presence, frequency, temperature  fp32 [num_seqs] (NULL: 1, 0, 0, 1)
  *   bias_ids, bias_values  int32, fp32 [num_seqs][num_bias], num_bias <= 1024

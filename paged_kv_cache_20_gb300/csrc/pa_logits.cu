@@ -18,12 +18,12 @@
 // ones first: the last are in shared memory still, the others are read again, in part from
 // L2 (keeping them there by a cache hint: no faster).  Bulk copies bring the rows.  64 x 8
 // rows of 131,071 bf16 logits take 144 us, where the bytes read and written once take 61: the
-// schedulers issue in 60 % of the clocks, and 34 clusters of 8 run at once, so that these are
-// two rounds.  Against 174 us (before fp32 was stored in whole sectors, 26 us, and the list's
-// inputs loaded at once): an exchange a row 183, batches of 4 rows 181, of 2 196, of 4 and 8
-// by turns 181; 256 threads 185, three thread blocks of them an SM 207; one thread block of
-// 1024 threads an SM and two rows in registers 289; one barrier a row, with the bits of two
-// rows side by side, 178 against 171 (registers).
+// schedulers issue in 59 % of the clocks, 346 warp instructions for 32 x 8 elements, and 34 clusters
+// of 8 run at once, so that these are two rounds.  Against 174 us (before fp32 was stored in
+// whole sectors, 26 us, and the list's inputs loaded at once): an exchange a row 183, batches of
+// 4 rows 181, of 2 196, of 4 and 8 by turns 181; 256 threads 185, three thread blocks of them an
+// SM 207; one thread block of 1024 threads an SM and two rows in registers 289; one barrier a
+// row, with the bits of two rows side by side, 178 against 171 (registers).
 // The entries that anything was counted for are few and lie anywhere: a slice keeps a list of
 // them in ascending order with their counts, and one bit an entry.  The dense pass masks
 // them out with the grammar's bits; the list's entries are gathered, adjusted and summed
@@ -31,7 +31,11 @@
 // of a sequence: each draft joins it before the row behind it, and leaves it again on the
 // way back.  (With every element testing its own bit and adjusting in place: 462 us.)
 // A row of an odd vocabulary starts anywhere: a thread's eight elements are aligned to 16
-// bytes of the row, not to the slice, whose ragged ends are masked.
+// bytes of the row, not to the slice, whose ragged ends are masked.  Where the output's row does not
+// start at the same element of 16 bytes, it is stored element by element: padded rows to dense
+// ones of 131,071 take 311 us so, padded to padded 143.
+// Above 131,072 entries 16 thread blocks a row: 64 x 8 of 151,936 take 238 us (floor 70), of
+// 262,144 297 (121).
 #include <algorithm>
 #include <atomic>
 #include <cfloat>

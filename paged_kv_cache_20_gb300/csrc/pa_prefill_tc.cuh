@@ -58,8 +58,10 @@
 // costs no operation per score more than with one scale a head; the row sum is taken by
 // blocks, each times its 1 / V scale.  Every softmax warp looks its half chunk's scales
 // up a chunk ahead (table entry, then scales: two loads that depend on each other).
-// 4 x 1024 query tokens over up to 8192, 32/8 heads, bf16: 451 us, 708 TFLOP/s, 0.37 of the
-// measured bf16 rate; the tensor pipe is active in 30 % of the clocks, the softmax warps bound.
+// 4 x 1024 query tokens over up to 8192, 32/8 heads, bf16: 455 us, 703 TFLOP/s, 0.37 of the
+// measured bf16 rate; the tensor pipe is active in 30 % of the clocks.  The softmax warps bound: of
+// 3,393 cycles a chunk they wait 116 for scores, while the widening warps work 963 (V) to 1,028
+// (K) and wait for codes the rest.  (One scale a head: 2,755, 180, 1,044 and 1,277.)
 #pragma once
 
 #include "pa_decode.cuh"
