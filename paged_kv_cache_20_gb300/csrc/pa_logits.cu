@@ -17,8 +17,8 @@
 // them, the cluster exchanges the sums of them all at once, and the rows are taken again, last
 // ones first: the last are in shared memory still, the others are read again, in part from
 // L2 (keeping them there by a cache hint: no faster).  Bulk copies bring the rows.  64 x 8
-// rows of 131,071 bf16 logits take 144 us, where the bytes read and written once take 61: the
-// schedulers issue in 59 % of the clocks, 346 warp instructions for 32 x 8 elements, and 34 clusters
+// rows of 131,071 bf16 logits take 145 us, where the bytes read and written once take 61: the
+// schedulers issue in 59 % of the clocks, 344 warp instructions for 32 x 8 elements, and 34 clusters
 // of 8 run at once, so that these are two rounds.  Against 174 us (before fp32 was stored in
 // whole sectors, 26 us, and the list's inputs loaded at once): an exchange a row 183, batches of
 // 4 rows 181, of 2 196, of 4 and 8 by turns 181; 256 threads 185, three thread blocks of them an
@@ -505,11 +505,9 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
   const int ahead = hi - lo - 32 * (int)threadIdx.x;
   const unsigned valid = ahead >= 32 ? ~0u : ahead <= 0 ? 0u : (1u << ahead) - 1u;
   const bool greedy = PROBS && !(temp > 0.f);
-  // The exponent (x - m) / temp log2(e) from half the difference, which does not overflow where
-  // logits of both signs lie near fp32's ends (under temperatures as large that counts), and twice
-  // the factor, kept finite and above zero (the least subnormal for an infinite temperature), so
-  // that -inf stays -inf.
-  const float fac = fminf(fmaxf(2.8853900817779268f / temp, 1e-45f), FLT_MAX);
+  // the exponent's factor; kept finite and above zero (the least subnormal for an infinite
+  // temperature), so that -inf stays -inf
+  const float fac = fminf(fmaxf(1.4426950408889634f / temp, 1e-45f), FLT_MAX);
   __syncthreads();  // the copies' barriers and the list
 
   auto adjust = [&](float x, int e, unsigned w) {
@@ -522,14 +520,20 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
     }
     return x;
   };
-  // 2^((x/2 - hm) fac), hm = m/2: the halves are exact, the difference is rounded once.  (One
-  // multiply-add with m fac rounded beforehand saves an instruction an element and no time,
-  // and the largest weights, exact here, carry exp2's error there: 5e-7 of a row against
-  // 1e-7.)
-  auto expo = [&](float x, float hm) { return ex2_flush(fmaf(x, 0.5f, -hm) * fac); };
-  // ... against a maximum m; with an infinite m the entries that reach it.
+  // 2^((x - m) fac) against a maximum m.  (One multiply-add with m fac rounded beforehand saves an
+  // instruction an element and no time, and the largest weights, exact here, carry exp2's error
+  // there: 5e-7 of a row against 1e-7.)
+  auto near = [&](float x, float m) { return ex2_flush((x - m) * fac); };
+  // The same of any m.  Above kFar x - m may overflow where logits of both signs lie near fp32's ends
+  // (under temperatures as large that counts), half of it does not (a step that every element
+  // would pay for: 64 x 8 rows of 131,071 146.0 us against 144.8); with an infinite m the entries
+  // that reach it share the whole.
+  constexpr float kFar = 1e30f;
   auto weight = [&](float x, float m) {
-    return m == INFINITY ? (x == INFINITY ? 1.f : 0.f) : expo(x, 0.5f * m);
+    if (m <= kFar) return near(x, m);
+    if (m == INFINITY) return x == INFINITY ? 1.f : 0.f;
+    const float half = fmaf(x, 0.5f, -0.5f * m) * fac;
+    return ex2_flush(half + half);
   };
 
   // ---- the rows, one after the other in either direction
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
           second = __int_as_float(__reduce_min_sync(0xffffffffu, at));
         } else {
           if (ms != -INFINITY) second = ss * weight(ms, m);
-          if (m == INFINITY) {
+          if (m > kFar) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
               if (!there(r, k)) continue;
@@ -813,14 +817,13 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
             }
           } else if (m != -INFINITY) {
             float sum[2] = {0.f, 0.f};
-            const float hm = 0.5f * m;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
               if (!there(r, k)) continue;
               float f[8];
               again(k, f);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) sum[i & 1] += expo(f[i], hm);
+              for (int i = 0; i < 8; ++i) sum[i & 1] += near(f[i], m);
             }
             second += sum[0] + sum[1];
           }
@@ -881,13 +884,12 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_logits_kernel(const LogitA
         const float2 stat = s_row[j - b0];
         const float M = stat.x, mul = stat.y;
         const int best = greedy ? __float_as_int(stat.y) : INT_MAX;
-        if (!greedy && fabsf(M) != INFINITY) {
-          const float hm = 0.5f * M;
+        if (!greedy && M <= kFar && M != -INFINITY) {
           write(r, out, [&](int, auto &f) {
 #pragma unroll
-            for (int i = 0; i < (int)(sizeof(f) / 4); ++i) f[i] = expo(f[i], hm) * mul;
+            for (int i = 0; i < (int)(sizeof(f) / 4); ++i) f[i] = near(f[i], M) * mul;
           });
-        } else {  // one, none, or the infinite ones
+        } else {  // one, none, or those of a far maximum
           write(r, out, [&](int v0, auto &f) {
 #pragma unroll
             for (int i = 0; i < (int)(sizeof(f) / 4); ++i)

@@ -29,10 +29,10 @@ TEMPS = (1e-44, 1e-30, 0.7, 1.0, 1.5, 1e36, 7e37, 3.3e38, math.inf)
 def test_differences_past_the_largest_number(pa, v, dtype):
     """Logits of both signs near the type's ends (a mask of its lowest value among them), where
     x - max overflows and x / temperature does not.  Tolerance: exp2's argument is a difference, a
-    factor (one rounding; 2^-23.5 where it is subnormal, at 3.3e38) and a product, each half a step
-    of itself: below 2^-22 of |z| together; exp2 and the sum of a row 2^-17 (up to 86 chained
-    terms); a factor that is the least subnormal where 0 is meant (temperature inf) moves
-    an argument by 3.4e38 * 1.4e-45 = 2^-20.9."""
+    factor (one rounding) and a product, each half a step of itself: below 2^-22 of |z|
+    together; exp2 and the sum of a row 2^-17 (up to 86 chained terms).  Within the latter also what
+    a subnormal factor adds: 2^-22.6 of |z| < 3 at 3.3e38, and the least subnormal where 0 is
+    meant (temperature inf) moves an argument by 6.8e38 * 1.4e-45 = 2^-20."""
     rng = np.random.default_rng(v)
     x = torch.from_numpy(rng.standard_normal((len(TEMPS), 1, v))).to(dtype)
     low = torch.finfo(dtype).min
